@@ -239,6 +239,117 @@ int mla_decode_sparse_bf16(const uint16_t* q_absorbed, const uint16_t* q_rope,
                            uint16_t* out, float* lse, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/* Cache rows: write new tokens into a paged cache, and read tokens back.
+ *
+ * Packed rows.  cu_rows [batch+1] int32 (device, non-decreasing, cu_rows[0] =
+ * 0): sequence b owns packed rows [cu_rows[b], cu_rows[b+1]), which are the
+ * LAST n_b = cu_rows[b+1] - cu_rows[b] of its seq_lens[b] tokens; packed row
+ * i is token seq_lens[b] - cu_rows[b+1] + i, in page block_table[b][t/64],
+ * slot t%64.  seq_lens is therefore the length after the append, the one a
+ * decode call over the same cache takes.  Packed rows past cu_rows[batch]
+ * are left alone.  A row whose token lies outside [0, max_pages*64) sets
+ * MLA_STATUS_BAD_SEQ_LEN, one whose page lies outside [0, num_pages) sets
+ * MLA_STATUS_BAD_PAGE; such a row is not written (append) or reads as zeros
+ * (gather).  Two rows of one append must not share a cache slot (block
+ * tables that share the page of a written token): which bytes the slot then
+ * holds is not defined.
+ *
+ * append: c_kv [rows, 512] bf16 with a row stride of c_stride values, k_rope
+ * [rows, 64] bf16 with a row stride of r_stride values (strides and bases
+ * multiples of 16 bytes).  bf16 rows are stored as they are.  The quantised
+ * rows hold, per group of 32 (e4m3) or 16 (e2m1) values, the scale 2^k with
+ * the smallest k such that the group's largest magnitude is at most 448 * 2^k
+ * (6 * 2^k); k = 0 for a group of zeros; codes are rounded to nearest, ties
+ * to even.  k is kept in [-127, 119] ([-127, 125]), where codes saturate, so
+ * that every stored value is finite in bf16.  A group that holds an infinity
+ * or a NaN takes the NaN scale (255) and reads back as NaN.  The V4.1 rows
+ * store c_kv's first 448 values; its last 64 are ignored.
+ *
+ * gather: out [rows, 576] bf16, [latent 512 | RoPE 64] (V4.1 rows: dims
+ * 448..511 are 0), each value rounded to bf16 (exact in bf16's normal range).
+ *
+ * workspace: at least 256 bytes, zeroed before its first use, 256-byte
+ * aligned; only its status word is used.  Errors as for the decode. */
+int mla_cache_append_bf16(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                          uint16_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          void* workspace, size_t workspace_bytes, void* stream);
+int mla_cache_gather_bf16(const uint16_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+int mla_cache_append_fp8(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                          uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          void* workspace, size_t workspace_bytes, void* stream);
+int mla_cache_gather_fp8(const uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+int mla_cache_append_fp4(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                          uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          void* workspace, size_t workspace_bytes, void* stream);
+int mla_cache_gather_fp4(const uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+int mla_cache_append_fp8_v41(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                          uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          void* workspace, size_t workspace_bytes, void* stream);
+int mla_cache_gather_fp8_v41(const uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+int mla_cache_append_fp4_v41(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                          uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          void* workspace, size_t workspace_bytes, void* stream);
+int mla_cache_gather_fp4_v41(const uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Keys and values of the expanded form ("DeepSeek R1 Architecture &
+ * Deployment Guide", section 1.1, before absorption):
+ *   k_nope[t][h][:] = W_uk[h] . c_t,   v[t][h][:] = W_uv[h] . c_t,
+ * c_t the 512 latent values of row t.  latent [rows, 512] bf16 with a row
+ * stride of row_stride values (a gathered row's first 512; stride and base
+ * multiples of 16 bytes); w_uk, w_uv [128, 128, 512] bf16; k_nope, v
+ * [rows, 128, 128] bf16 (fp32 accumulation, rounded to nearest), 32-byte
+ * aligned.  num_heads and d_v must be 128; rows at most 2^24.
+ * workspace: at least 256 bytes, zeroed before its first use, 256-byte
+ * aligned (status word; after MLA_STATUS_TIMEOUT read it with mla_get_status
+ * before the workspace is used again). */
+int mla_expand_kv(const uint16_t* latent, size_t row_stride, const uint16_t* w_uk, const uint16_t* w_uv, int rows,
+                  int num_heads, int d_v, uint16_t* k_nope, uint16_t* v, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/* Attention of the expanded form over ragged sequences (prefill).  Sequence
+ * b has the packed queries [cu_q[b], cu_q[b+1]) and the packed keys [cu_k[b],
+ * cu_k[b+1]) (cu_q, cu_k: [batch+1] int32, device, non-decreasing, within
+ * [0, num_q] and [0, num_k]).  For query i of n_q, key j of n_k and head h:
+ *   s_ij  = scale * (q_nope[i][h] . k_nope[j][h] + q_rope[i][h] . k_rope[j])
+ *   out   = sum_j softmax_j(s) v[j][h],   lse = ln sum_j exp(s_ij)
+ * over all keys, or with causal != 0 over j <= i + n_k - n_q: the queries are
+ * the sequence's last n_q tokens, so a prompt's next chunk attends to what
+ * is cached before it.  A query that sees no key gets out = 0, lse = -inf.
+ * Queries past cu_q[batch] are left alone.  A sequence whose bounds are out
+ * of order or out of range is skipped and sets MLA_STATUS_BAD_SEQ_LEN.
+ * A masked key's K never matters, whatever it holds, nor does another
+ * sequence's K or V; a non-finite V value of a masked key of the same
+ * sequence may reach the queries within 255 tokens before it.
+ * q_nope [num_q, 128, 128], q_rope [num_q, 128, 64], k_nope [num_k, 128,
+ * 128], k_rope [num_k, 64] (shared by the heads), v [num_k, 128, 128], all
+ * bf16 with their last dimension contiguous; strides (host memory, values,
+ * each a positive multiple of 8): token and head stride of q_nope, of q_rope,
+ * of k_nope, token stride of k_rope, token and head stride of v.  Bases are
+ * 16-byte aligned.  out [num_q, 128, 128] bf16 contiguous, 32-byte aligned;
+ * lse [num_q, 128] fp32.  num_heads must be 128; num_q, num_k at most 2^24.
+ * workspace: mla_workspace_size_prefill(...) bytes, zeroed before its first
+ * use, 256-byte aligned, not shared with a call that may run concurrently. */
+int mla_workspace_size_prefill(int batch, int num_q, size_t* bytes);
+int mla_prefill_bf16(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* k_nope, const uint16_t* k_rope,
+                     const uint16_t* v, const size_t* strides, const int32_t* cu_q, const int32_t* cu_k, int batch,
+                     int num_q, int num_k, int num_heads, int causal, float softmax_scale, uint16_t* out, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
 /* Up-projection of latent attention outputs through W^UV ("DeepSeek R1
  * Architecture & Deployment Guide", section 1.1: the value up-projection is
  * folded out of the attention, which returns the 512-value latent output

@@ -24,6 +24,7 @@ _STATUS = {
 # Exported entry points and their C signatures (restype, argtypes).
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_Z = ctypes.c_size_t
 SIGNATURES = {
     "mla_workspace_size": (_I, [_I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
     "mla_decode_bf16": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P,
@@ -42,6 +43,14 @@ SIGNATURES = {
     "mla_decode_sparse_bf16": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P,
                                     ctypes.c_size_t, _P]),
     "mla_up_project_wuv": (_I, [_P, _P, _I, _I, _I, _P, _P, ctypes.c_size_t, _P]),
+    **{"mla_cache_append_" + f: (_I, [_P, _Z, _P, _Z, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _Z, _P])
+       for f in ("bf16", "fp8", "fp4", "fp8_v41", "fp4_v41")},
+    **{"mla_cache_gather_" + f: (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _Z, _P])
+       for f in ("bf16", "fp8", "fp4", "fp8_v41", "fp4_v41")},
+    "mla_expand_kv": (_I, [_P, _Z, _P, _P, _I, _I, _I, _P, _P, _P, _Z, _P]),
+    "mla_workspace_size_prefill": (_I, [_I, _I, ctypes.POINTER(_Z)]),
+    "mla_prefill_bf16": (_I, [_P, _P, _P, _P, _P, ctypes.POINTER(_Z), _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P,
+                              _P, _P, _Z, _P]),
     "mla_combine_splits": (_I, [_P, _P, _P, _I, _I, _P, _P, _P]),
     "mla_get_status": (_I, [_P, _P]),
     "mla_profile_next_decode": (_I, [_P, _P]),
@@ -326,6 +335,239 @@ def mla_up_project_wuv(latent, w_uv, out=None, workspace=None, stream=None):
     if rc != MLA_OK:
         raise MLAError(rc, "mla_up_project_wuv")
     return out
+
+
+def _check_rows(t: torch.Tensor, name: str, tail: tuple, rows: int | None = None):
+    """A bf16 tensor [rows, *tail] whose last dimension is contiguous and whose
+    other strides and base are multiples of 16 bytes (it may be a view)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 1 + len(tail) or tuple(t.shape[1:]) != tuple(tail) or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{'rows' if rows is None else rows}, "
+                         f"{', '.join(map(str, tail))}]")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if any(t.shape[d] > 1 and (t.stride(d) <= 0 or t.stride(d) % 8) for d in range(t.dim() - 1)) or t.data_ptr() % 16:
+        raise ValueError(f"{name} must start on 16 bytes with strides that are positive multiples of 16 bytes")
+
+
+def _stride(t, dim: int, default: int) -> int:
+    """Stride of a dimension; of one that holds a single entry, `default`."""
+    return int(t.stride(dim)) if t.shape[dim] > 1 else default
+
+
+def _status_workspace(device) -> torch.Tensor:
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+_ROW_WIDTH = {"bf16": 576, "fp8": 594, "fp4": 324, "fp8_v41": 528, "fp4_v41": 288}
+
+
+def _check_cache(fmt, kv_cache, block_table, seq_lens, cu_rows):
+    _check(kv_cache, "kv_cache", torch.bfloat16 if fmt == "bf16" else torch.uint8)
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != _ROW_WIDTH[fmt]:
+        raise ValueError(f"kv_cache must be [num_pages, page_size, {_ROW_WIDTH[fmt]}], got {tuple(kv_cache.shape)}")
+    _check(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    _check(seq_lens, "seq_lens", torch.int32, (block_table.shape[0],))
+    _check(cu_rows, "cu_rows", torch.int32, (block_table.shape[0] + 1,))
+
+
+def _append(fmt, c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace, stream):
+    name = "mla_cache_append_" + fmt
+    _check_rows(c_kv, "c_kv", (512,))
+    rows = int(c_kv.shape[0])
+    _check_rows(k_rope, "k_rope", (64,), rows)
+    _check_cache(fmt, kv_cache, block_table, seq_lens, cu_rows)
+    if workspace is None:
+        workspace = _status_workspace(kv_cache.device)
+    _check(workspace, "workspace", torch.uint8)
+    _same_device(dict(kv_cache=kv_cache, c_kv=c_kv, k_rope=k_rope, block_table=block_table, seq_lens=seq_lens,
+                      cu_rows=cu_rows, workspace=workspace), torch.cuda.current_device())
+    rc = getattr(load(), name)(
+        _ptr(c_kv), _stride(c_kv, 0, 512), _ptr(k_rope), _stride(k_rope, 0, 64), _ptr(kv_cache), _ptr(block_table),
+        _ptr(seq_lens), _ptr(cu_rows), int(block_table.shape[0]), rows, int(kv_cache.shape[0]),
+        int(kv_cache.shape[1]), int(block_table.shape[1]), _ptr(workspace), ctypes.c_size_t(workspace.numel()),
+        _stream(stream))
+    if rc != MLA_OK and rows:       # empty tensors have null pointers: nothing to do
+        raise MLAError(rc, name)
+    return kv_cache
+
+
+def _gather(fmt, kv_cache, block_table, seq_lens, cu_rows, n_rows, out, workspace, stream):
+    name = "mla_cache_gather_" + fmt
+    _check_cache(fmt, kv_cache, block_table, seq_lens, cu_rows)
+    rows = int(n_rows)
+    if rows < 0:
+        raise ValueError("n_rows must not be negative")
+    if out is None:
+        out = torch.empty((rows, 576), dtype=torch.bfloat16, device=kv_cache.device)
+    _check(out, "out", torch.bfloat16, (rows, 576))
+    if workspace is None:
+        workspace = _status_workspace(kv_cache.device)
+    _check(workspace, "workspace", torch.uint8)
+    _same_device(dict(kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, cu_rows=cu_rows, out=out,
+                      workspace=workspace), torch.cuda.current_device())
+    rc = getattr(load(), name)(
+        _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens), _ptr(cu_rows), int(block_table.shape[0]), rows,
+        int(kv_cache.shape[0]), int(kv_cache.shape[1]), int(block_table.shape[1]), _ptr(out), _ptr(workspace),
+        ctypes.c_size_t(workspace.numel()), _stream(stream))
+    if rc != MLA_OK and rows:
+        raise MLAError(rc, name)
+    return out
+
+
+def mla_cache_append_bf16(c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace=None, stream=None):
+    """Write packed new tokens (c_kv [n, 512], k_rope [n, 64] bf16, views with
+    16-byte row strides allowed) into a bf16 cache [num_pages, 64, 576] in
+    place: sequence b's rows [cu_rows[b], cu_rows[b+1]) are the last of its
+    seq_lens[b] tokens.  Returns kv_cache."""
+    return _append("bf16", c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace, stream)
+
+
+def mla_cache_append_fp8(c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace=None, stream=None):
+    """mla_cache_append_bf16 into an FP8 cache [num_pages, 64, 594]: e4m3 codes
+    with the smallest power-of-two scale per 32 values that clips nothing."""
+    return _append("fp8", c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace, stream)
+
+
+def mla_cache_append_fp4(c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace=None, stream=None):
+    """mla_cache_append_bf16 into an FP4 cache [num_pages, 64, 324]: e2m1 codes
+    with the smallest power-of-two scale per 16 values that clips nothing."""
+    return _append("fp4", c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace, stream)
+
+
+def mla_cache_append_fp8_v41(c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace=None, stream=None):
+    """mla_cache_append_fp8 into the V4.1 rows [num_pages, 64, 528]: the first
+    448 latent values and the 64 RoPE values (c_kv[:, 448:] is ignored)."""
+    return _append("fp8_v41", c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace, stream)
+
+
+def mla_cache_append_fp4_v41(c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace=None, stream=None):
+    """mla_cache_append_fp4 into the V4.1 rows [num_pages, 64, 288]: the first
+    448 latent values and the 64 RoPE values (c_kv[:, 448:] is ignored)."""
+    return _append("fp4_v41", c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace, stream)
+
+
+def mla_cache_gather_bf16(kv_cache, block_table, seq_lens, cu_rows, n_rows, out=None, workspace=None, stream=None):
+    """Read packed rows back: out [n_rows, 576] bf16, sequence b's rows
+    [cu_rows[b], cu_rows[b+1]) being the last of its seq_lens[b] tokens (all of
+    them where the difference is seq_lens[b]).  Rows past cu_rows[B] of `out`
+    are left as they were."""
+    return _gather("bf16", kv_cache, block_table, seq_lens, cu_rows, n_rows, out, workspace, stream)
+
+
+def mla_cache_gather_fp8(kv_cache, block_table, seq_lens, cu_rows, n_rows, out=None, workspace=None, stream=None):
+    """mla_cache_gather_bf16 from an FP8 cache [num_pages, 64, 594] (dequantised)."""
+    return _gather("fp8", kv_cache, block_table, seq_lens, cu_rows, n_rows, out, workspace, stream)
+
+
+def mla_cache_gather_fp4(kv_cache, block_table, seq_lens, cu_rows, n_rows, out=None, workspace=None, stream=None):
+    """mla_cache_gather_bf16 from an FP4 cache [num_pages, 64, 324] (dequantised)."""
+    return _gather("fp4", kv_cache, block_table, seq_lens, cu_rows, n_rows, out, workspace, stream)
+
+
+def mla_cache_gather_fp8_v41(kv_cache, block_table, seq_lens, cu_rows, n_rows, out=None, workspace=None,
+                             stream=None):
+    """mla_cache_gather_bf16 from V4.1 rows [num_pages, 64, 528]; dims 448..511 are 0."""
+    return _gather("fp8_v41", kv_cache, block_table, seq_lens, cu_rows, n_rows, out, workspace, stream)
+
+
+def mla_cache_gather_fp4_v41(kv_cache, block_table, seq_lens, cu_rows, n_rows, out=None, workspace=None,
+                             stream=None):
+    """mla_cache_gather_bf16 from V4.1 rows [num_pages, 64, 288]; dims 448..511 are 0."""
+    return _gather("fp4_v41", kv_cache, block_table, seq_lens, cu_rows, n_rows, out, workspace, stream)
+
+
+def mla_expand_kv(latent, w_uk, w_uv, k_nope=None, v=None, workspace=None, stream=None):
+    """k_nope[t, h] = w_uk[h] @ latent[t], v[t, h] = w_uv[h] @ latent[t]:
+    latent [n, 512] bf16 (a view with a 16-byte row stride, such as gathered
+    rows' [:, :512]), w_uk, w_uv [128, 128, 512] bf16 -> two [n, 128, 128]."""
+    _check_rows(latent, "latent", (512,))
+    _check(w_uk, "w_uk", torch.bfloat16, (128, 128, 512))
+    _check(w_uv, "w_uv", torch.bfloat16, (128, 128, 512))
+    n = int(latent.shape[0])
+    if k_nope is None:
+        k_nope = torch.empty((n, 128, 128), dtype=torch.bfloat16, device=latent.device)
+    if v is None:
+        v = torch.empty((n, 128, 128), dtype=torch.bfloat16, device=latent.device)
+    _check(k_nope, "k_nope", torch.bfloat16, (n, 128, 128))
+    _check(v, "v", torch.bfloat16, (n, 128, 128))
+    if workspace is None:
+        workspace = _status_workspace(latent.device)
+    _check(workspace, "workspace", torch.uint8)
+    _same_device(dict(latent=latent, w_uk=w_uk, w_uv=w_uv, k_nope=k_nope, v=v, workspace=workspace),
+                 torch.cuda.current_device())
+    rc = load().mla_expand_kv(_ptr(latent), _stride(latent, 0, 512), _ptr(w_uk), _ptr(w_uv), n, 128, 128, _ptr(k_nope),
+                              _ptr(v), _ptr(workspace), ctypes.c_size_t(workspace.numel()), _stream(stream))
+    if rc != MLA_OK and n:
+        raise MLAError(rc, "mla_expand_kv")
+    return k_nope, v
+
+
+def mla_workspace_size_prefill(batch: int, num_q: int) -> int:
+    n = ctypes.c_size_t(0)
+    rc = load().mla_workspace_size_prefill(int(batch), int(num_q), ctypes.byref(n))
+    if rc != MLA_OK:
+        raise MLAError(rc, "mla_workspace_size_prefill")
+    return int(n.value)
+
+
+def alloc_workspace_prefill(batch: int, num_q: int, device=None) -> torch.Tensor:
+    """A zeroed workspace buffer (uint8) for the prefill of up to `batch`
+    sequences with `num_q` queries together."""
+    return torch.zeros(mla_workspace_size_prefill(batch, num_q), dtype=torch.uint8, device=device or "cuda")
+
+
+def mla_prefill_bf16(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
+                     workspace=None, stream=None):
+    """Expanded-form attention over ragged sequences: q_nope [nq, 128, 128],
+    q_rope [nq, 128, 64], k_nope [nk, 128, 128], k_rope [nk, 64], v [nk, 128,
+    128] bf16 (views with 16-byte strides and a contiguous last dimension
+    allowed), cu_q, cu_k int32 [B + 1].  causal: query i of a sequence's n_q
+    sees keys j <= i + n_k - n_q.  Returns (out [nq, 128, 128] bf16, lse
+    [nq, 128] fp32); rows past cu_q[B] are left as they were."""
+    _check_rows(q_nope, "q_nope", (128, 128))
+    nq = int(q_nope.shape[0])
+    _check_rows(q_rope, "q_rope", (128, 64), nq)
+    _check_rows(k_nope, "k_nope", (128, 128))
+    nk = int(k_nope.shape[0])
+    _check_rows(k_rope, "k_rope", (64,), nk)
+    _check_rows(v, "v", (128, 128), nk)
+    _check(cu_q, "cu_q", torch.int32)
+    if cu_q.dim() != 1 or cu_q.numel() < 1:
+        raise ValueError("cu_q must be [B + 1]")
+    B = int(cu_q.numel()) - 1
+    _check(cu_k, "cu_k", torch.int32, (B + 1,))
+    if out is None:
+        out = torch.empty((nq, 128, 128), dtype=torch.bfloat16, device=q_nope.device)
+    if lse is None:
+        lse = torch.empty((nq, 128), dtype=torch.float32, device=q_nope.device)
+    _check(out, "out", torch.bfloat16, (nq, 128, 128))
+    _check(lse, "lse", torch.float32, (nq, 128))
+    if workspace is None:
+        workspace = alloc_workspace_prefill(B, nq, q_nope.device)
+    _check(workspace, "workspace", torch.uint8)
+    _same_device(dict(q_nope=q_nope, q_rope=q_rope, k_nope=k_nope, k_rope=k_rope, v=v, cu_q=cu_q, cu_k=cu_k, out=out,
+                      lse=lse, workspace=workspace), torch.cuda.current_device())
+    if nq == 0:
+        return out, lse
+    strides = (ctypes.c_size_t * 9)(
+        _stride(q_nope, 0, 128 * 128), int(q_nope.stride(1)), _stride(q_rope, 0, 128 * 64), int(q_rope.stride(1)),
+        _stride(k_nope, 0, 128 * 128), int(k_nope.stride(1)), _stride(k_rope, 0, 64),
+        _stride(v, 0, 128 * 128), int(v.stride(1)))
+    rc = load().mla_prefill_bf16(
+        _ptr(q_nope), _ptr(q_rope), _ptr(k_nope), _ptr(k_rope), _ptr(v), strides, _ptr(cu_q), _ptr(cu_k), B, nq, nk,
+        128, 1 if causal else 0, ctypes.c_float(float(scale)), _ptr(out), _ptr(lse), _ptr(workspace),
+        ctypes.c_size_t(workspace.numel()), _stream(stream))
+    if rc != MLA_OK:
+        raise MLAError(rc, "mla_prefill_bf16")
+    return out, lse
 
 
 def mla_combine_splits(partial_out, partial_lse, split_indptr, out=None, lse=None, stream=None):

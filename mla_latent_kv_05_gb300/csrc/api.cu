@@ -11,6 +11,9 @@
 #include <mutex>
 
 #include "decode.cuh"
+#include "expand.cuh"
+#include "prefill.cuh"
+#include "rows.cuh"
 
 namespace {
 
@@ -189,6 +192,8 @@ int static_scratch(void** ptr) {
 }
 
 constexpr int kMaxTopk = 16384;
+constexpr int kMaxExpandRows = 1 << 24;    // tokens of one expansion (work items stay below 2^31)
+constexpr int kMaxPrefillRows = 1 << 24;   // packed queries or keys of one prefill
 
 // Sparse top-k decode: compact the slot lists, plan the B*Sq query rows as a
 // batch of rows with one query each, gather-attend, merge.
@@ -247,6 +252,57 @@ int run_sparse(const uint16_t* q_absorbed, const uint16_t* q_rope, const void* k
   return MLA_OK;
 }
 
+// Row strides (values) a 16-byte access or a TMA map takes.
+bool stride_ok(size_t s) { return s > 0 && s % 8 == 0 && s < (size_t{1} << 38); }
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+// Append (c_kv non-null) or gather (out non-null) of packed rows.
+int run_rows(RowFormat fmt, const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+             const void* cache, const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_rows, int batch,
+             int rows, int num_pages, int page_size, int max_pages, uint16_t* out, bool append, void* workspace,
+             size_t workspace_bytes, void* stream) {
+  if (!cache || !block_table || !seq_lens || !cu_rows || !workspace || (append ? !c_kv || !k_rope : !out))
+    return MLA_ERR_INVALID_ARG;
+  if (batch < 0 || rows < 0 || num_pages <= 0 || max_pages <= 0) return MLA_ERR_INVALID_ARG;
+  if (page_size != kPage || batch > kMaxRows) return MLA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_pages) * kPage >= INT_MAX / 2 ||
+      static_cast<long long>(max_pages) * kPage >= INT_MAX / 2 || rows >= INT_MAX / 2)
+    return MLA_ERR_UNSUPPORTED;
+  if (!aligned(cache, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_rows, 4) ||
+      !aligned(workspace, 256))
+    return MLA_ERR_INVALID_ARG;
+  if (append) {
+    if (!aligned(c_kv, 16) || !aligned(k_rope, 16) || !stride_ok(c_stride) || !stride_ok(r_stride))
+      return MLA_ERR_INVALID_ARG;
+  } else if (!aligned(out, 16)) {
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (workspace_bytes < sizeof(PlanHeader)) return MLA_ERR_WORKSPACE;
+  if (batch == 0 || rows == 0) return MLA_OK;
+  RowsParams p;
+  p.c_kv = reinterpret_cast<const __nv_bfloat16*>(c_kv);
+  p.k_rope = reinterpret_cast<const __nv_bfloat16*>(k_rope);
+  p.c_stride = static_cast<long long>(c_stride);
+  p.r_stride = static_cast<long long>(r_stride);
+  p.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu_rows = cu_rows;
+  p.batch = batch;
+  p.rows = rows;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.status = &static_cast<PlanHeader*>(workspace)->status;
+  return launch_rows(fmt, p, append, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
 }  // namespace
 
 // Only the C ABI below is exported (the library is built with hidden
@@ -271,6 +327,152 @@ int mla_up_project_wuv(const uint16_t* latent, const uint16_t* w_uv, int rows, i
       cudaSuccess)
     return MLA_ERR_CUDA;
   return launch_wuv(fn, latent, w_uv, rows, out, workspace, st) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_cache_append_bf16(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                          uint16_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return run_rows(RowFormat::kBf16, c_kv, c_stride, k_rope, r_stride, kv_cache, block_table, seq_lens, cu_rows, batch,
+                  rows, num_pages, page_size, max_pages, nullptr, true, workspace, workspace_bytes, stream);
+}
+
+int mla_cache_gather_bf16(const uint16_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          uint16_t* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_rows(RowFormat::kBf16, nullptr, 0, nullptr, 0, kv_cache, block_table, seq_lens, cu_rows, batch, rows,
+                  num_pages, page_size, max_pages, out, false, workspace, workspace_bytes, stream);
+}
+
+int mla_cache_append_fp8(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                          uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return run_rows(RowFormat::kFp8, c_kv, c_stride, k_rope, r_stride, kv_cache, block_table, seq_lens, cu_rows, batch,
+                  rows, num_pages, page_size, max_pages, nullptr, true, workspace, workspace_bytes, stream);
+}
+
+int mla_cache_gather_fp8(const uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          uint16_t* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_rows(RowFormat::kFp8, nullptr, 0, nullptr, 0, kv_cache, block_table, seq_lens, cu_rows, batch, rows,
+                  num_pages, page_size, max_pages, out, false, workspace, workspace_bytes, stream);
+}
+
+int mla_cache_append_fp4(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                          uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return run_rows(RowFormat::kFp4, c_kv, c_stride, k_rope, r_stride, kv_cache, block_table, seq_lens, cu_rows, batch,
+                  rows, num_pages, page_size, max_pages, nullptr, true, workspace, workspace_bytes, stream);
+}
+
+int mla_cache_gather_fp4(const uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          uint16_t* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_rows(RowFormat::kFp4, nullptr, 0, nullptr, 0, kv_cache, block_table, seq_lens, cu_rows, batch, rows,
+                  num_pages, page_size, max_pages, out, false, workspace, workspace_bytes, stream);
+}
+
+int mla_cache_append_fp8_v41(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                          uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return run_rows(RowFormat::kFp8V41, c_kv, c_stride, k_rope, r_stride, kv_cache, block_table, seq_lens, cu_rows, batch,
+                  rows, num_pages, page_size, max_pages, nullptr, true, workspace, workspace_bytes, stream);
+}
+
+int mla_cache_gather_fp8_v41(const uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          uint16_t* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_rows(RowFormat::kFp8V41, nullptr, 0, nullptr, 0, kv_cache, block_table, seq_lens, cu_rows, batch, rows,
+                  num_pages, page_size, max_pages, out, false, workspace, workspace_bytes, stream);
+}
+
+int mla_cache_append_fp4_v41(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                          uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return run_rows(RowFormat::kFp4V41, c_kv, c_stride, k_rope, r_stride, kv_cache, block_table, seq_lens, cu_rows, batch,
+                  rows, num_pages, page_size, max_pages, nullptr, true, workspace, workspace_bytes, stream);
+}
+
+int mla_cache_gather_fp4_v41(const uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
+                          uint16_t* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_rows(RowFormat::kFp4V41, nullptr, 0, nullptr, 0, kv_cache, block_table, seq_lens, cu_rows, batch, rows,
+                  num_pages, page_size, max_pages, out, false, workspace, workspace_bytes, stream);
+}
+
+int mla_expand_kv(const uint16_t* latent, size_t row_stride, const uint16_t* w_uk, const uint16_t* w_uv, int rows,
+                  int num_heads, int d_v, uint16_t* k_nope, uint16_t* v, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  if (!latent || !w_uk || !w_uv || !k_nope || !v || !workspace || rows < 0) return MLA_ERR_INVALID_ARG;
+  if (num_heads != kHeads || d_v != 128) return MLA_ERR_UNSUPPORTED;
+  if (rows > kMaxExpandRows) return MLA_ERR_UNSUPPORTED;
+  if (!stride_ok(row_stride) || row_stride < static_cast<size_t>(kDc)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(latent, 16) || !aligned(w_uk, 16) || !aligned(w_uv, 16) || !aligned(k_nope, 32) || !aligned(v, 32) ||
+      !aligned(workspace, 256))
+    return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < sizeof(PlanHeader)) return MLA_ERR_WORKSPACE;
+  if (rows == 0) return MLA_OK;
+  auto fn = encode_fn();
+  const int sms = sm_count();
+  if (!fn || sms <= 0) return MLA_ERR_CUDA;
+  return launch_expand(fn, latent, static_cast<long long>(row_stride), w_uk, w_uv, rows, k_nope, v, workspace, sms,
+                       static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+int mla_workspace_size_prefill(int batch, int num_q, size_t* bytes) {
+  if (!bytes || batch < 0 || num_q < 0) return MLA_ERR_INVALID_ARG;
+  if (batch > kMaxRows || num_q > kMaxPrefillRows) return MLA_ERR_UNSUPPORTED;
+  *bytes = prefill_ws(batch, num_q).total;
+  return MLA_OK;
+}
+
+int mla_prefill_bf16(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* k_nope, const uint16_t* k_rope,
+                     const uint16_t* v, const size_t* strides, const int32_t* cu_q, const int32_t* cu_k, int batch,
+                     int num_q, int num_k, int num_heads, int causal, float softmax_scale, uint16_t* out, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q_nope || !q_rope || !strides || !cu_q || !cu_k || !out || !lse || !workspace) return MLA_ERR_INVALID_ARG;
+  if (batch < 0 || num_q < 0 || num_k < 0 || !std::isfinite(softmax_scale) || !(softmax_scale > 0.f))
+    return MLA_ERR_INVALID_ARG;
+  if (num_k > 0 && (!k_nope || !k_rope || !v)) return MLA_ERR_INVALID_ARG;
+  if (num_heads != kHeads) return MLA_ERR_UNSUPPORTED;
+  if (batch > kMaxRows || num_q > kMaxPrefillRows || num_k > kMaxPrefillRows) return MLA_ERR_UNSUPPORTED;
+  for (int i = 0; i < 9; ++i)
+    if (!stride_ok(strides[i])) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q_nope, 16) || !aligned(q_rope, 16) || !aligned(k_nope, 16) || !aligned(k_rope, 16) || !aligned(v, 16) ||
+      !aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(out, 32) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < prefill_ws(batch, num_q).total) return MLA_ERR_WORKSPACE;
+  if (batch == 0 || num_q == 0) return MLA_OK;
+  auto fn = encode_fn();
+  const int sms = sm_count();
+  if (!fn || sms <= 0) return MLA_ERR_CUDA;
+  PrefillParams p;
+  // with no key nothing is read through the key pointers; the maps need valid addresses all the same
+  const uint16_t* any = q_nope;
+  p.q_nope = reinterpret_cast<const __nv_bfloat16*>(q_nope);
+  p.q_rope = reinterpret_cast<const __nv_bfloat16*>(q_rope);
+  p.k_nope = reinterpret_cast<const __nv_bfloat16*>(num_k > 0 ? k_nope : any);
+  p.k_rope = reinterpret_cast<const __nv_bfloat16*>(num_k > 0 ? k_rope : any);
+  p.v = reinterpret_cast<const __nv_bfloat16*>(num_k > 0 ? v : any);
+  long long* s[9] = {&p.qn_t, &p.qn_h, &p.qr_t, &p.qr_h, &p.kn_t, &p.kn_h, &p.kr_t, &p.v_t, &p.v_h};
+  for (int i = 0; i < 9; ++i) *s[i] = static_cast<long long>(strides[i]);
+  p.cu_q = cu_q;
+  p.cu_k = cu_k;
+  p.batch = batch;
+  p.nq = num_q;
+  p.nk = num_k;
+  p.causal = causal != 0;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.ws = static_cast<uint8_t*>(workspace);
+  return launch_prefill(fn, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 int mla_workspace_size_sparse(int batch, int sq, int topk, int num_heads, int page_size, size_t* bytes) {
@@ -394,7 +596,11 @@ int mla_get_status(void* workspace, void* stream) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return MLA_ERR_CUDA;
   int v = 0;
   if (cudaMemcpy(&v, workspace, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return MLA_ERR_CUDA;
-  if (v != 0 && cudaMemset(workspace, 0, sizeof(int)) != cudaSuccess) return MLA_ERR_CUDA;
+  // a reported timeout also leaves the abort flag set; both are cleared
+  if (v != 0 && (cudaMemset(workspace, 0, sizeof(int)) != cudaSuccess ||
+                 cudaMemset(static_cast<uint8_t*>(workspace) + offsetof(PlanHeader, abort_flag), 0, sizeof(int)) !=
+                     cudaSuccess))
+    return MLA_ERR_CUDA;
   return v;
 }
 

@@ -1,6 +1,7 @@
 // Shared constants, the workspace layout of the split-KV plan, and bounded
 // waits for the MLA decode kernels.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <utility>
@@ -95,6 +96,21 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   cfg.attrs = nullptr;
   cfg.numAttrs = 0;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// Raise a kernel's dynamic shared-memory limit once per device; `done` holds
+// one bit per device.  Safe from any thread (setting the limit twice is
+// harmless).
+template <typename Kern>
+cudaError_t allow_smem(Kern kern, uint32_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // Record the first problem seen (never overwrites an earlier one).

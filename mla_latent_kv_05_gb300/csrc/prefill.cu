@@ -1,0 +1,596 @@
+// Expanded-form MLA attention over ragged sequences (prefill).
+//
+// For query row i of a sequence with nq queries and nk keys, and head h:
+//     s_j = scale (q_nope_i . k_nope_j + q_rope_i . k_rope_j)
+//     out_i = sum_j softmax_j(s) v_j,   lse_i = ln sum_j exp(s_j)
+// over the keys j it sees: all nk, or with the causal mask j <= i + nk - nq
+// (the queries are the sequence's last nq tokens).  A row that sees no key
+// gets out = 0, lse = -inf.  The RoPE part of a key is shared by all heads
+// and read as it is, never copied into a per-head key.
+//
+// Bound: 2 * 128 * (192 + 128) operations per visible (query, key) pair
+// against 512 bytes of K and V per key and head, so with 256 query rows per
+// K/V read the tensor cores bound it.  One pass over the keys with a running
+// maximum and sum; S, P and O never leave the SM.
+//
+// One persistent CTA per SM, work items (head, 256 query rows) handed out by
+// a counter, head by head (a head's K and V are then in L2 while its tiles
+// run) and within a head the longest tiles first.  An item's rows are two
+// M = 128 tiles that share each K/V tile of 128 keys:
+//   tensor memory (512 columns): S0 | S1 | O0 | O1, 128 fp32 columns each; P
+//       (bf16, 64 columns) takes the place of the S it was made from;
+//   shared memory: Q0 | Q1 (48 KiB each), and a ring of eight 16-KiB chunks
+//       (128 keys x 64 values), three per K tile and two per V tile, so K
+//       and V are prefetched chunk by chunk as chunks are released;
+//   warp 0 issues the TMA loads, warp 1 the MMAs, warp 2 fetches the items,
+//   warps 4..7 and 8..11 are the softmax of tile 0 and tile 1 (thread = row).
+// The MMA warp alternates PV0(j) S0(j+1) PV1(j) S1(j+1), so while one tile's
+// softmax runs the tensor cores work on the other's.  S of the next item is
+// issued before the last PV of this one is waited for, so items overlap.
+//
+// The maximum is lazy: a row's reference moves only when a tile's maximum
+// exceeds it by more than 2^kLazy, so O is rescaled rarely; its softmax warps
+// do that themselves, after the previous PV of the tile has completed.
+//
+// Every wait is bounded: a timeout records MLA_STATUS_TIMEOUT and raises the
+// abort flag, all roles leave, and the kernel ends through its teardown.
+#include <climits>
+
+#include "prefill.cuh"
+
+namespace mla {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kKeys = 128;                         // keys per K/V tile
+constexpr uint32_t kChunk = 128u * 128u;           // 16 KiB: 128 rows x 64 values
+constexpr uint32_t kQTile = 3 * kChunk;            // 128 query rows x 192
+constexpr int kRing = 8;
+constexpr uint32_t kOffRing = 2 * kQTile;
+constexpr uint32_t kOffBar = kOffRing + kRing * kChunk;   // 224 KiB
+constexpr int kItemSlots = 2;
+enum Bar {
+  QFULL = 0, QEMPTY = QFULL + 2, FULL = QEMPTY + 2, EMPTY = FULL + kRing, SFULL = EMPTY + kRing, PREADY = SFULL + 2,
+  PVDONE = PREADY + 2, IFULL = PVDONE + 2, IEMPTY = IFULL + kItemSlots, DRAIN = IEMPTY + kItemSlots, NBAR
+};
+constexpr uint32_t kOffTmem = kOffBar + 8 * NBAR;
+constexpr uint32_t kOffItems = (kOffTmem + 16 + 15) & ~15u;     // kItemSlots x 32 bytes
+constexpr uint32_t kSmem = kOffItems + 32 * kItemSlots;
+static_assert(kSmem <= 232448, "shared memory budget");
+
+constexpr uint32_t kSCol = 0, kOCol = 256;         // + 128 t
+constexpr uint32_t kIdescS = ptx::idesc_bf16(128, 128, 0, 0);    // Q, K: K-major
+constexpr uint32_t kIdescPV = ptx::idesc_bf16(128, 128, 0, 1);   // P in tensor memory, V: MN-major
+constexpr uint32_t kIdescPVHalf = ptx::idesc_bf16(128, 64, 0, 1);
+// log2 units: P <= 2^12, exact in relative terms, and far from fp32 overflow in O and l
+constexpr float kLazy = 12.0f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Header fields this operator uses: n_tiles (tiles in the list) and chunk
+// (the next work item).
+struct Tile {
+  int q0, rows;   // first packed query row, query rows (1..256)
+  int k0, nk;     // first packed key, keys of the sequence
+  int lim;        // keys that row 0 sees before clamping to nk (row r: lim + r if causal)
+  int head;       // filled in for a fetched item; -1: no more items
+  int pad[2];
+};
+static_assert(sizeof(Tile) == 32, "tile record");
+
+__device__ __forceinline__ int visible(const Tile& t, int r, int causal) {
+  return max(0, min(t.nk, t.lim + (causal ? r : 0)));
+}
+// K/V tiles that query tile t of the item visits (the last of its rows sees the most)
+__device__ __forceinline__ int kv_tiles(const Tile& t, int half, int causal) {
+  if (t.rows <= 128 * half) return 0;
+  return (visible(t, min(t.rows, 128 * (half + 1)) - 1, causal) + kKeys - 1) / kKeys;
+}
+
+// ---------------------------------------------------------------- plan
+// One CTA: the list of 256-row tiles of all sequences, the ones with most K/V
+// tiles first (counting sort over the clipped tile count; the order within a
+// class does not matter, every item is computed on its own).
+constexpr int kClasses = 1024;
+
+__global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __restrict__ cu_q,
+                                                            const int32_t* __restrict__ cu_k, int batch, int nq, int nk,
+                                                            int causal, uint8_t* __restrict__ ws, PrefillWs L) {
+  __shared__ int s_count[kClasses];
+  __shared__ int s_warp[32];
+  PlanHeader* hdr = reinterpret_cast<PlanHeader*>(ws);
+  Tile* tiles = reinterpret_cast<Tile*>(ws + L.tiles);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  s_count[tid] = 0;
+  __syncthreads();
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int b = warp; b < batch; b += 32) {
+      const int q0 = __ldg(cu_q + b), q1 = __ldg(cu_q + b + 1), k0 = __ldg(cu_k + b), k1 = __ldg(cu_k + b + 1);
+      if (q0 < 0 || q1 < q0 || q1 > nq || k0 < 0 || k1 < k0 || k1 > nk) {
+        if (lane == 0 && pass == 0) set_status(&hdr->status, MLA_STATUS_BAD_SEQ_LEN);
+        continue;
+      }
+      const int n_q = q1 - q0, n_k = k1 - k0;
+      for (int i = lane; i * kPrefillTile < n_q; i += 32) {
+        Tile t;
+        t.q0 = q0 + i * kPrefillTile;
+        t.rows = min(kPrefillTile, n_q - i * kPrefillTile);
+        t.k0 = k0;
+        t.nk = n_k;
+        t.lim = causal ? i * kPrefillTile + 1 + (n_k - n_q) : n_k;
+        t.head = 0;
+        t.pad[0] = t.pad[1] = 0;
+        const int c = kClasses - 1 - min(kClasses - 1, max(kv_tiles(t, 0, causal), kv_tiles(t, 1, causal)));
+        const int pos = atomicAdd(&s_count[c], 1);
+        if (pass == 1) {
+          if (pos < L.max_tiles) tiles[pos] = t;
+          else set_status(&hdr->status, MLA_STATUS_BAD_SEQ_LEN);   // overlapping sequences: cu_q decreased somewhere
+        }
+      }
+    }
+    __syncthreads();
+    if (pass == 0) {
+      // exclusive scan: s_count[c] becomes the first position of class c
+      const int v = s_count[tid];
+      int x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) s_warp[warp] = x;
+      __syncthreads();
+      int before = 0;
+      for (int w = 0; w < warp; ++w) before += s_warp[w];
+      s_count[tid] = before + x - v;
+      if (tid == 1023) {
+        hdr->n_tiles = min(before + x, L.max_tiles);
+        hdr->chunk = 0;
+        hdr->abort_flag = 0;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---------------------------------------------------------------- attention
+struct Maps {
+  CUtensorMap qn, qr, kn, kr, v;
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const PrefillWs L) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = ptx::smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws);
+  auto BAR = [&](int i) { return sbase + kOffBar + 8u * static_cast<uint32_t>(i); };
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(BAR(QFULL + t), 1);
+      ptx::mbar_init(BAR(QEMPTY + t), 1);
+      ptx::mbar_init(BAR(SFULL + t), 1);
+      ptx::mbar_init(BAR(PREADY + t), 128);
+      ptx::mbar_init(BAR(PVDONE + t), 1);
+    }
+    for (int s = 0; s < kRing; ++s) { ptx::mbar_init(BAR(FULL + s), 1); ptx::mbar_init(BAR(EMPTY + s), 1); }
+    for (int s = 0; s < kItemSlots; ++s) {
+      ptx::mbar_init(BAR(IFULL + s), 1);
+      ptx::mbar_init(BAR(IEMPTY + s), 10);     // producer, MMA warp, eight softmax warps
+    }
+    ptx::mbar_init(BAR(DRAIN), 1);
+    ptx::fence_barrier_init();
+  }
+  if (warp == 2) {
+    ptx::tmem_alloc(sbase + kOffTmem, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem);
+  const bool smem_ok = (sbase & 1023u) == 0;
+  if (threadIdx.x == 0 && !smem_ok) set_status(&hdr->status, MLA_ERR_UNSUPPORTED);
+  const int causal = p.causal;
+
+  // The next item of this role's walk: false when there is none (or a wait
+  // gave up).  Each consumer reads the record and then releases its slot.
+  struct Walk { int slot = 0; uint32_t phase = 0; };
+  auto read_item = [&](Walk& w, Tile& t) {
+    const volatile int* src = reinterpret_cast<const volatile int*>(smem + kOffItems + 32 * w.slot);
+    t.q0 = src[0]; t.rows = src[1]; t.k0 = src[2]; t.nk = src[3]; t.lim = src[4]; t.head = src[5];
+  };
+  auto next_warp = [&](Walk& w, Tile& t) {
+    if (!wait_warp<false>(BAR(IFULL + w.slot), w.phase, hdr)) return false;
+    read_item(w, t);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(BAR(IEMPTY + w.slot));
+    if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
+    return t.head >= 0;
+  };
+
+  if (smem_ok && warp == 2) {
+    // ------------------------------------------------------------ items
+    if (lane == 0) {
+      const Tile* tiles = reinterpret_cast<const Tile*>(p.ws + L.tiles);
+      const int n = *reinterpret_cast<const volatile int*>(&hdr->n_tiles);
+      Walk w;
+      while (true) {
+        const int item = atomicAdd(&hdr->chunk, 1);
+        const bool more = item < n * kHeads;
+        Tile t;
+        t.q0 = t.rows = t.k0 = t.nk = t.lim = 0;
+        t.head = -1;
+        if (more) {
+          t = tiles[item % n];
+          t.head = item / n;
+        }
+        if (!wait_bounded<false>(BAR(IEMPTY + w.slot), w.phase ^ 1u, hdr)) break;
+        volatile int* dst = reinterpret_cast<volatile int*>(smem + kOffItems + 32 * w.slot);
+        dst[0] = t.q0; dst[1] = t.rows; dst[2] = t.k0; dst[3] = t.nk; dst[4] = t.lim; dst[5] = t.head;
+        ptx::mbar_arrive(BAR(IFULL + w.slot));
+        if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
+        if (!more) break;
+      }
+    }
+  } else if (smem_ok && warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t pol = ptx::policy_evict_normal();
+      Walk w;
+      uint32_t pos = 0;                        // chunks queued so far
+      uint32_t nq[2] = {0, 0};                 // Q tiles queued so far
+      bool ok = true;
+      auto chunk = [&](const CUtensorMap* map, int x, int y, int z) {
+        const uint32_t s = pos & (kRing - 1);
+        if (!wait_bounded<false>(BAR(EMPTY + s), ((pos >> 3) & 1u) ^ 1u, hdr)) { ok = false; return; }
+        ptx::mbar_arrive_expect_tx(BAR(FULL + s), kChunk);
+        ptx::tma_load_3d(sbase + kOffRing + s * kChunk, map, BAR(FULL + s), x, y, z, pol);
+        ++pos;
+      };
+      auto query = [&](int t, const Tile& it) {
+        if (!wait_bounded<false>(BAR(QEMPTY + t), (nq[t] & 1u) ^ 1u, hdr)) { ok = false; return; }
+        ptx::mbar_arrive_expect_tx(BAR(QFULL + t), kQTile);
+        const uint32_t dst = sbase + static_cast<uint32_t>(t) * kQTile;
+        const int row = it.q0 + 128 * t;
+        ptx::tma_load_3d(dst, &maps.qn, BAR(QFULL + t), 0, it.head, row, pol);
+        ptx::tma_load_3d(dst + kChunk, &maps.qn, BAR(QFULL + t), 64, it.head, row, pol);
+        ptx::tma_load_3d(dst + 2 * kChunk, &maps.qr, BAR(QFULL + t), 0, it.head, row, pol);
+        ++nq[t];
+      };
+      while (ok) {
+        if (!wait_bounded<false>(BAR(IFULL + w.slot), w.phase, hdr)) break;
+        Tile it;
+        read_item(w, it);
+        ptx::mbar_arrive(BAR(IEMPTY + w.slot));
+        if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
+        if (it.head < 0) break;
+        const int n0 = kv_tiles(it, 0, causal), n1 = kv_tiles(it, 1, causal), n = max(n0, n1);
+        if (n0 > 0) query(0, it);
+        for (int j = 0; j < n && ok; ++j) {
+          const int k = it.k0 + j * kKeys;
+          chunk(&maps.kn, 0, it.head, k);
+          if (ok) chunk(&maps.kn, 64, it.head, k);
+          if (ok) chunk(&maps.kr, 0, 0, k);
+          if (ok && j == 0 && n1 > 0) query(1, it);
+          if (ok) chunk(&maps.v, 0, it.head, k);
+          if (ok) chunk(&maps.v, 64, it.head, k);
+        }
+      }
+      // no copy may land after the CTA has left: wait for the last phase armed on each barrier
+      for (int t = 0; t < 2; ++t)
+        if (nq[t] > 0) wait_drain(BAR(QFULL + t), (nq[t] - 1) & 1u, hdr);
+      for (uint32_t s = 0; s < kRing; ++s) {
+        const uint32_t n = (pos + kRing - 1 - s) / kRing;
+        if (n > 0) wait_drain(BAR(FULL + s), (n - 1) & 1u, hdr);
+      }
+    }
+  } else if (smem_ok && warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    Walk w;
+    Tile it;
+    uint32_t kpos = 0;                       // ring position of the K tile to be scored next
+    uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
+    bool ok = true, issued = false;
+    // the next (item, K/V tile) step: ni = K/V tiles of each query tile, jn = the step
+    int jn = 0, ni[2] = {0, 0};
+    auto fetch = [&]() -> bool {             // the next item that has keys to visit
+      do {
+        if (!next_warp(w, it)) return false;
+        ni[0] = kv_tiles(it, 0, causal);
+        ni[1] = kv_tiles(it, 1, causal);
+      } while (max(ni[0], ni[1]) == 0);
+      jn = 0;
+      return true;
+    };
+    auto wait_chunks = [&](uint32_t pos, int n) {
+      for (int c = 0; c < n && ok; ++c)
+        ok = wait_warp<false>(BAR(FULL + ((pos + c) & (kRing - 1))), ((pos + c) >> 3) & 1u, hdr);
+    };
+    auto score = [&](int t, uint32_t pos, bool last_q, bool release) {
+      if (lane == 0) {
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          const uint64_t da = ptx::sdesc_sw128(sbase + static_cast<uint32_t>(t) * kQTile + c * kChunk, 16, 1024);
+          const uint32_t s = (pos + c) & (kRing - 1);
+          const uint64_t db = ptx::sdesc_sw128(sbase + kOffRing + s * kChunk, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            ptx::mma_ss(tmem + kSCol + 128u * t, da + static_cast<uint64_t>(2 * k), db + static_cast<uint64_t>(2 * k),
+                        kIdescS, (c > 0 || k > 0) ? 1u : 0u);
+          if (release) ptx::mma_commit(BAR(EMPTY + s));
+        }
+        ptx::mma_commit(BAR(SFULL + t));
+        if (last_q) ptx::mma_commit(BAR(QEMPTY + t));
+      }
+      __syncwarp();
+    };
+    bool more = fetch();
+    // step state: cur = the step whose P.V comes next (its S was issued)
+    int jc = -1, nc[2] = {0, 0}, nkc = 0;
+    uint32_t vpos = 0;
+    while (ok && (jc >= 0 || more)) {
+      bool have_v = false, have_k = false;
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (jc >= 0 && jc < nc[t]) {
+          if (!wait_warp<false>(BAR(PREADY + t), n_p[t] & 1u, hdr)) { ok = false; break; }
+          ++n_p[t];
+          if (!have_v) {
+            wait_chunks(vpos, 2);
+            if (!ok) break;
+            have_v = true;
+            const int valid = nkc - jc * kKeys;
+            if (valid < kKeys) {
+              // keys past the sequence's end have P = 0; make their V rows 0 too
+              // (they may be another sequence's, and hold NaN)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint4* dst = reinterpret_cast<uint4*>(smem + kOffRing + ((vpos + c) & (kRing - 1)) * kChunk);
+                for (int i = valid * 8 + lane; i < kKeys * 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+              }
+              ptx::fence_proxy_async_cta();
+              __syncwarp();
+            }
+          }
+          ptx::tc_fence_after();
+          const bool release = t == 1 || jc >= nc[1];
+          if (lane == 0) {
+            const uint32_t s0 = vpos & (kRing - 1), s1 = (vpos + 1) & (kRing - 1);
+            const uint32_t d = tmem + kOCol + 128u * t, a = tmem + kSCol + 128u * t;
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k) {
+              const uint32_t acc = (jc > 0 || k > 0) ? 1u : 0u;
+              const uint64_t db = ptx::sdesc_sw128(sbase + kOffRing + s0 * kChunk + 2048u * k, kChunk, 1024);
+              if (s1 > s0) {
+                ptx::mma_ts(d, a + 8u * k, db, kIdescPV, acc);
+              } else {
+                // the tile's second chunk wrapped to the ring's start: two halves
+                ptx::mma_ts(d, a + 8u * k, db, kIdescPVHalf, acc);
+                ptx::mma_ts(d + 64u, a + 8u * k, ptx::sdesc_sw128(sbase + kOffRing + s1 * kChunk + 2048u * k, kChunk, 1024),
+                            kIdescPVHalf, acc);
+              }
+            }
+            if (release) { ptx::mma_commit(BAR(EMPTY + s0)); ptx::mma_commit(BAR(EMPTY + s1)); }
+            ptx::mma_commit(BAR(PVDONE + t));
+          }
+          __syncwarp();
+        }
+        if (more && jn < ni[t]) {
+          if (jn == 0) {
+            if (!wait_warp<false>(BAR(QFULL + t), n_q[t] & 1u, hdr)) { ok = false; break; }
+            ++n_q[t];
+          }
+          if (!have_k) {
+            wait_chunks(kpos, 3);
+            if (!ok) break;
+            have_k = true;
+          }
+          ptx::tc_fence_after();
+          issued = true;
+          score(t, kpos, jn == ni[t] - 1, t == 1 || jn >= ni[1]);
+        }
+      }
+      if (!ok) break;
+      // advance: the step just scored becomes the one whose P.V comes next
+      if (more) {
+        jc = jn;
+        nc[0] = ni[0];
+        nc[1] = ni[1];
+        nkc = it.nk;
+        vpos = kpos + 3;
+        kpos += 5;
+        if (++jn >= max(ni[0], ni[1])) more = fetch();
+      } else {
+        jc = -1;
+      }
+    }
+    // every MMA this thread issued completes before the CTA may leave
+    if (issued && lane == 0) {
+      ptx::mma_commit(BAR(DRAIN));
+      wait_drain(BAR(DRAIN), 0u, hdr);
+    }
+    __syncwarp();
+  } else if (smem_ok && warp >= 4) {
+    // ------------------------------------------------------------ softmax and epilogue (thread = query row)
+    const int t = (warp - 4) >> 2;
+    const int r = 128 * t + (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lane_base + kSCol + 128u * t, o_addr = tmem + lane_base + kOCol + 128u * t;
+    const float c = p.scale_log2;
+    Walk w;
+    Tile it;
+    uint32_t steps = 0;                      // tiles turned into P so far (phase of SFULL, PVDONE)
+    bool ok = true;
+    while (ok && next_warp(w, it)) {
+      if (it.rows <= 128 * t) continue;
+      const int n = kv_tiles(it, t, causal);
+      const int vis = visible(it, r, causal);
+      float mc = 0.f;                        // reference maximum * c (0 while nothing was seen)
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        if (!wait_warp<false>(BAR(SFULL + t), steps & 1u, hdr)) { ok = false; break; }
+        ptx::tc_fence_after();
+        const int valid = vis - j * kKeys;
+        const bool full = __all_sync(0xffffffffu, valid >= kKeys);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t s[32];
+          ptx::tmem_ld32(s_addr + 32u * q, s);
+          ptx::tmem_wait_ld();
+          if (full) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * q + e < valid) mx = fmaxf(mx, __uint_as_float(s[e]));
+          }
+        }
+        float alpha = 1.f;
+        if (m_ref == -INFINITY) {
+          m_ref = mx;                        // nothing accumulated so far: l = 0, O = 0
+          mc = mx == -INFINITY ? 0.f : mx * c;
+        } else if ((mx - m_ref) * c > kLazy) {
+          m_ref = mx;
+          const float nmc = mx * c;
+          alpha = fast_exp2(mc - nmc);
+          mc = nmc;
+          l *= alpha;
+        }
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+          // O of the tiles so far is complete once the previous P.V is
+          if (!wait_warp<false>(BAR(PVDONE + t), (steps - 1) & 1u, hdr)) { ok = false; break; }
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[32];
+            ptx::tmem_ld32(o_addr + 32u * q, o);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            ptx::tmem_st32(o_addr + 32u * q, o);
+          }
+        }
+        float la = 0.f, lb = 0.f;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t s[64], pk[32];
+          ptx::tmem_ld32(s_addr + 64u * q, s);
+          ptx::tmem_ld32(s_addr + 64u * q + 32u, s + 32);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
+                                        make_float2(c, c), make_float2(-mc, -mc));
+            float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+            if (!full) {
+              if (64 * q + 2 * e >= valid) p0 = 0.f;
+              if (64 * q + 2 * e + 1 >= valid) p1 = 0.f;
+            }
+            const float2 sum = __fadd2_rn(make_float2(la, lb), make_float2(p0, p1));
+            la = sum.x;
+            lb = sum.y;
+            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+            pk[e] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          // P of keys 64q.. takes columns whose scores were read above
+          ptx::tmem_st32(s_addr + 32u * q, pk);
+        }
+        l += la + lb;
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(BAR(PREADY + t));
+        ++steps;
+      }
+      if (!ok) break;
+      if (n > 0) {
+        if (!wait_warp<false>(BAR(PVDONE + t), (steps - 1) & 1u, hdr)) { ok = false; break; }
+        ptx::tc_fence_after();
+      }
+      const bool live = r < it.rows;
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays NaN
+      const size_t orow = (static_cast<size_t>(it.q0) + r) * kHeads + it.head;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o[32], w16[16];
+        if (n > 0) {
+          ptx::tmem_ld32(o_addr + 32u * q, o);
+          ptx::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          w16[e] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        if (live) {
+          ptx::st_global_v8(p.out + orow * 128 + 32 * q, w16);
+          ptx::st_global_v8(p.out + orow * 128 + 32 * q + 16, w16 + 8);
+        }
+      }
+      if (live) p.lse[orow] = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
+      ptx::tc_fence_before();
+    }
+  }
+  // ------------------------------------------------------------ teardown
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// (64 values, heads, tokens) boxes of 64 x 1 x 128; strides in values.
+bool encode_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* base, int width, int heads,
+                int tokens, long long stride_t, long long stride_h) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride_h) * 2, static_cast<cuuint64_t>(stride_t) * 2};
+  cuuint32_t box[3] = {64, 1, 128};
+  cuuint32_t es[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(PFN_cuTensorMapEncodeTiled_v12000 encode, const PrefillParams& p, int sms,
+                           cudaStream_t stream) {
+  const PrefillWs L = prefill_ws(p.batch, p.nq);
+  if (L.max_tiles <= 0) return cudaSuccess;
+  Maps maps;
+  // with no key at all nothing is loaded; the maps still need one row
+  const int nk = p.nk > 0 ? p.nk : 1;
+  if (!encode_map(encode, &maps.qn, p.q_nope, 128, kHeads, p.nq, p.qn_t, p.qn_h) ||
+      !encode_map(encode, &maps.qr, p.q_rope, 64, kHeads, p.nq, p.qr_t, p.qr_h) ||
+      !encode_map(encode, &maps.kn, p.k_nope, 128, kHeads, nk, p.kn_t, p.kn_h) ||
+      !encode_map(encode, &maps.kr, p.k_rope, 64, 1, nk, p.kr_t, 64) ||
+      !encode_map(encode, &maps.v, p.v, 128, kHeads, nk, p.v_t, p.v_h))
+    return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = allow_smem(prefill_kernel, kSmem, configured);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(prefill_plan_kernel, dim3(1), dim3(1024), 0, stream, p.cu_q, p.cu_k, p.batch, p.nq, p.nk, p.causal,
+                    p.ws, L);
+  if (e != cudaSuccess) return e;
+  const long long items = static_cast<long long>(L.max_tiles) * kHeads;
+  return launch_kernel(prefill_kernel, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kThreads), kSmem,
+                       stream, maps, p, L);
+}
+
+}  // namespace mla

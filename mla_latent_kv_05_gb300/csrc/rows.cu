@@ -1,0 +1,249 @@
+// Cache rows: write new tokens' latent rows into a paged cache (append) and
+// read a sequence's rows back as bf16 (gather), in the five cache formats the
+// decode reads.
+//
+// Packed rows: sequence b owns rows [cu[b], cu[b+1]) of the packed tensors,
+// which are the LAST n_b = cu[b+1] - cu[b] of its seq_lens[b] tokens: packed
+// row i is token seq_lens[b] - cu[b+1] + i.
+//
+// Quantisation (the inverse of the decode's dequantisation): a group of G
+// values (G = 32 e4m3, 16 e2m1) with largest magnitude a takes the smallest
+// k with a <= M 2^k (M = 448, 6; k = 0 for an all-zero group), stored as the
+// e8m0 byte k + 127, and the codes round(v 2^-k) to nearest, ties to even.
+// With a = m 2^E, m in [1/2, 1): 448 = 0.875 2^9, 6 = 0.75 2^3, so k is E - 9
+// or E - 8 (E - 3 or E - 2), read from a's exponent and mantissa bits with no
+// rounding.  k is kept in [-127, 119] ([-127, 125]): at the top the codes
+// saturate instead of standing for values beyond bf16.  A group that holds
+// an infinity or a NaN takes scale byte 255 (the NaN scale) and zero codes.
+//
+// Both directions only move bytes, so they are bound by HBM when long and by
+// the launch and two dependent reads (the row's sequence, then its page) when
+// short.  One thread takes eight consecutive values (16 bytes of bf16), so
+// the bf16 side is one coalesced 16-byte access a thread and a group's
+// maximum needs one or two shuffles; a CTA takes four rows, whose slots four
+// warps look up while the values are already on their way.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "rows.cuh"
+
+namespace mla {
+
+namespace {
+
+constexpr int kRowsPerCta = 4;
+constexpr int kPiece = 8;   // values per thread
+
+template <RowFormat F> struct Fmt;
+template <> struct Fmt<RowFormat::kBf16> {
+  static constexpr int kValues = kRow, kBytes = kRow * 2;
+};
+template <> struct Fmt<RowFormat::kFp8> {
+  static constexpr int kValues = kRow, kBytes = kFp8Row, kGroup = 32, kScales = kRow, kTopK = 119;
+};
+template <> struct Fmt<RowFormat::kFp4> {
+  static constexpr int kValues = kRow, kBytes = kFp4Row, kGroup = 16, kScales = kFp4Codes, kTopK = 125;
+};
+template <> struct Fmt<RowFormat::kFp8V41> {
+  static constexpr int kValues = kV41Values, kBytes = kV41Row, kGroup = 32, kScales = kV41Values, kTopK = 119;
+};
+template <> struct Fmt<RowFormat::kFp4V41> {
+  static constexpr int kValues = kV41Values, kBytes = kV41Fp4Row, kGroup = 16, kScales = kV41Values / 2, kTopK = 125;
+};
+template <RowFormat F> constexpr bool kIsFp4 = F == RowFormat::kFp4 || F == RowFormat::kFp4V41;
+template <RowFormat F> constexpr bool kIsV41 = F == RowFormat::kFp8V41 || F == RowFormat::kFp4V41;
+
+// Cache slot (page * 64 + offset) of packed row i, by one warp: -1 for a row
+// past the last sequence (left alone), -2 for one whose token or page lies
+// outside the cache (recorded in the status word; never read or written).
+__device__ int row_slot(const RowsParams& p, int i, int lane) {
+  if (i >= p.rows) return -1;
+  // largest b with cu[b] <= i, 32 probes a round
+  int lo = 0, hi = p.batch;              // cu[lo] <= i is assumed, cu[hi + 1] is not probed
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const int probe = lo + (lane + 1) * step;
+    const bool le = probe <= hi && __ldg(p.cu_rows + probe) <= i;
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    const int n = __popc(m);             // cu is non-decreasing, so the probes that hold come first
+    const int nlo = lo + n * step;
+    hi = min(hi, nlo + step - 1);
+    lo = min(nlo, hi);
+  }
+  if (lo >= p.batch) return -1;          // cu[batch] <= i: behind the last sequence
+  const int c0 = __ldg(p.cu_rows + lo), c1 = __ldg(p.cu_rows + lo + 1);
+  int slot = -2, code = MLA_STATUS_BAD_SEQ_LEN;
+  if (i >= c0 && i < c1) {
+    const long long pos = static_cast<long long>(__ldg(p.seq_lens + lo)) - c1 + i;
+    if (pos >= 0 && pos < static_cast<long long>(p.max_pages) * kPage) {
+      const int page = __ldg(p.block_table + static_cast<size_t>(lo) * p.max_pages + (pos >> 6));
+      if (page >= 0 && page < p.num_pages) slot = page * kPage + static_cast<int>(pos & 63);
+      else code = MLA_STATUS_BAD_PAGE;
+    }
+  }
+  if (slot < 0 && lane == 0) set_status(p.status, code);
+  return slot;
+}
+
+// Scale exponent of a group whose largest magnitude has the bf16 bits `a`
+// (finite, sign cleared): see the top of the file.
+template <RowFormat F>
+__device__ __forceinline__ int scale_exponent(uint32_t a) {
+  if (a == 0) return 0;
+  const int e = static_cast<int>(a >> 7) - 126;     // a = m 2^e, m in [1/2, 1) (a subnormal lands below the clamp)
+  const uint32_t man = a & 0x7Fu;
+  const int k = kIsFp4<F> ? e - 3 + (man > 0x40u) : e - 9 + (man > 0x60u);
+  return min(max(k, -127), Fmt<F>::kTopK);
+}
+
+template <RowFormat F>
+__global__ void __launch_bounds__(kRowsPerCta * Fmt<F>::kValues / kPiece)
+append_kernel(const RowsParams p) {
+  using T = Fmt<F>;
+  constexpr int kPieces = T::kValues / kPiece;
+  __shared__ int s_slot[kRowsPerCta];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = threadIdx.x / kPieces, j = threadIdx.x - r * kPieces;
+  const int row = blockIdx.x * kRowsPerCta + r;
+  // V4.1 rows: values 0..447 are the latent's first 448, then the RoPE values
+  constexpr int kLatentPieces = (kIsV41<F> ? kV41Latent : kDc) / kPiece;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (row < p.rows)
+    v = __ldg(reinterpret_cast<const uint4*>(
+        j < kLatentPieces ? p.c_kv + static_cast<size_t>(row) * p.c_stride + j * kPiece
+                          : p.k_rope + static_cast<size_t>(row) * p.r_stride + (j - kLatentPieces) * kPiece));
+  if (warp < kRowsPerCta) {
+    const int slot = row_slot(p, blockIdx.x * kRowsPerCta + warp, lane);
+    if (lane == 0) s_slot[warp] = slot;
+  }
+  __syncthreads();
+  const int slot = s_slot[r];
+  uint8_t* dst = p.cache + static_cast<size_t>(slot < 0 ? 0 : slot) * T::kBytes;
+  if constexpr (F == RowFormat::kBf16) {
+    if (slot >= 0) *reinterpret_cast<uint4*>(dst + j * 16) = v;
+  } else {
+    // largest magnitude of the group as bf16 bits (their order as integers
+    // is the order of the magnitudes, infinities and NaNs at the top)
+    uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                           __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+#pragma unroll
+    for (int o = 1; o < T::kGroup / kPiece; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool finite = m < 0x7F80u;
+    const int k = finite ? scale_exponent<F>(m) : 0;
+    const float mul = finite ? __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : 0.f;   // 2^-k, normal: k <= 125
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t code[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // exact: a product that is not (below 2^-126) is far under the smallest code
+      const float lo = finite ? __uint_as_float(w[i] << 16) * mul : 0.f;
+      const float hi = finite ? __uint_as_float(w[i] & 0xFFFF0000u) * mul : 0.f;
+      if constexpr (kIsFp4<F>) {
+        asm("{\n .reg .b8 c;\n cvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n cvt.u32.u8 %0, c;\n}"
+            : "=r"(code[i]) : "f"(lo), "f"(hi));
+      } else {
+        unsigned short c;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(lo), "f"(hi));
+        code[i] = c;
+      }
+    }
+    if (slot < 0) return;
+    if constexpr (kIsFp4<F>) {
+      // rows start on 4-byte boundaries
+      *reinterpret_cast<uint32_t*>(dst + j * 4) = code[0] | (code[1] << 8) | (code[2] << 16) | (code[3] << 24);
+    } else if constexpr (F == RowFormat::kFp8V41) {
+      *reinterpret_cast<uint2*>(dst + j * 8) = make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+    } else {
+      // 594-byte rows: 2-byte boundaries
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint16_t*>(dst + j * 8 + 2 * i) = static_cast<uint16_t>(code[i]);
+    }
+    if (j % (T::kGroup / kPiece) == 0)
+      dst[T::kScales + j / (T::kGroup / kPiece)] = static_cast<uint8_t>(finite ? k + 127 : 255);
+  }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <RowFormat F>
+__global__ void __launch_bounds__(kRowsPerCta * kRow / kPiece) gather_kernel(const RowsParams p) {
+  using T = Fmt<F>;
+  constexpr int kPieces = kRow / kPiece;     // the output row has 576 values in every format
+  __shared__ int s_slot[kRowsPerCta];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = threadIdx.x / kPieces, j = threadIdx.x - r * kPieces;
+  const int row = blockIdx.x * kRowsPerCta + r;
+  if (warp < kRowsPerCta) {
+    const int slot = row_slot(p, blockIdx.x * kRowsPerCta + warp, lane);
+    if (lane == 0) s_slot[warp] = slot;
+  }
+  __syncthreads();
+  const int slot = s_slot[r];
+  if (slot == -1) return;                    // behind the last sequence: left as it was
+  uint4 o = make_uint4(0, 0, 0, 0);          // a row outside the cache reads as zeros
+  if (slot >= 0) {
+    const uint8_t* src = p.cache + static_cast<size_t>(slot) * T::kBytes;
+    if constexpr (F == RowFormat::kBf16) {
+      o = __ldg(reinterpret_cast<const uint4*>(src + j * 16));
+    } else {
+      // V4.1 rows: latent dims 448..511 are zero, the RoPE values are the row's last 64
+      constexpr int kPad0 = kIsV41<F> ? kV41Latent / kPiece : kPieces, kPad1 = kDc / kPiece;
+      const bool pad = j >= kPad0 && j < kPad1;
+      const int q = kIsV41<F> && j >= kPad1 ? j - (kPad1 - kPad0) : j;     // piece of the stored row
+      if (!pad) {
+        const uint32_t e = __ldg(src + T::kScales + q / (T::kGroup / kPiece));
+        const float sc = __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7FC00000u : e << 23));
+        uint32_t h[4];
+        if constexpr (kIsFp4<F>) {
+          const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(src + q * 4));
+          asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+              " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+              " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+              : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(c));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const unsigned short c = __ldg(reinterpret_cast<const unsigned short*>(src + q * 8 + 2 * i));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[i]) : "h"(c));
+          }
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+          w[i] = bf16_pair(f.x * sc, f.y * sc);   // exact in fp32, rounded once
+        }
+        o = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row) * kRow + j * kPiece) = o;
+}
+
+template <RowFormat F>
+cudaError_t launch(const RowsParams& p, bool append, cudaStream_t stream) {
+  const dim3 grid((p.rows + kRowsPerCta - 1) / kRowsPerCta);
+  if (append)
+    return launch_kernel(append_kernel<F>, grid, dim3(kRowsPerCta * Fmt<F>::kValues / kPiece), 0, stream, p);
+  return launch_kernel(gather_kernel<F>, grid, dim3(kRowsPerCta * kRow / kPiece), 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rows(RowFormat fmt, const RowsParams& p, bool append, cudaStream_t stream) {
+  if (p.rows <= 0) return cudaSuccess;
+  switch (fmt) {
+    case RowFormat::kBf16: return launch<RowFormat::kBf16>(p, append, stream);
+    case RowFormat::kFp8: return launch<RowFormat::kFp8>(p, append, stream);
+    case RowFormat::kFp4: return launch<RowFormat::kFp4>(p, append, stream);
+    case RowFormat::kFp8V41: return launch<RowFormat::kFp8V41>(p, append, stream);
+    case RowFormat::kFp4V41: return launch<RowFormat::kFp4V41>(p, append, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace mla
