@@ -239,6 +239,53 @@ int mla_decode_sparse_bf16(const uint16_t* q_absorbed, const uint16_t* q_rope,
                            uint16_t* out, float* lse, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/* Decode of a drafted tree: up to 64 candidate tokens per sequence, drafted
+ * as a tree (several continuations of one context), attend in one call.  The
+ * drafted tokens' rows are in the cache already: sequence b's nodes are the
+ * LAST n_nodes[b] of its seq_lens[b] tokens, node a being token ctx + a with
+ * ctx = seq_lens[b] - n_nodes[b].  parents [batch, nodes] int32: the node each
+ * node continues, in [-1, its own index), -1 for the context's end (several
+ * nodes may).  Node i sees the ctx context tokens, itself, and its ancestors;
+ * a chain (parents[i] = i - 1) is the causal rule of mla_decode_*.
+ * q_absorbed [batch, nodes, 128, 512], q_rope [batch, nodes, 128, 64], out
+ * and lse as for mla_decode_* with Sq = nodes (1 <= nodes <= 64); scores,
+ * cache formats and layouts are those of mla_decode_*, and q_absorbed, q_rope
+ * and out are 32-byte aligned.  n_nodes: [batch] int32, 0 <= n_nodes[b] <=
+ * nodes, or NULL when every sequence has `nodes`; a row past n_nodes[b] gets
+ * out = 0, lse = -inf.  A token that a node does not see takes no part in its
+ * result, whatever its row holds (including NaN).
+ * Device status: MLA_STATUS_BAD_SEQ_LEN for n_nodes[b] outside [0, nodes] or
+ * seq_lens[b] outside [n_nodes[b], max_pages*64] (its rows get out = 0, lse =
+ * -inf); MLA_STATUS_BAD_INDEX for a parent outside [-1, its index) (the path
+ * ends there); MLA_STATUS_BAD_PAGE as for the decode.
+ * workspace: mla_workspace_size_tree(...) bytes, as for the decode. */
+int mla_workspace_size_tree(int batch, int nodes, int num_heads, int page_size, size_t* bytes);
+int mla_decode_tree_bf16(const uint16_t* q_absorbed, const uint16_t* q_rope, const uint16_t* kv_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                         const int32_t* n_nodes, int batch, int nodes, int num_heads, int num_pages, int page_size,
+                         int max_pages, float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+int mla_decode_tree_fp8(const uint16_t* q_absorbed, const uint16_t* q_rope, const uint8_t* kv_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                         const int32_t* n_nodes, int batch, int nodes, int num_heads, int num_pages, int page_size,
+                         int max_pages, float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+int mla_decode_tree_fp4(const uint16_t* q_absorbed, const uint16_t* q_rope, const uint8_t* kv_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                         const int32_t* n_nodes, int batch, int nodes, int num_heads, int num_pages, int page_size,
+                         int max_pages, float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+int mla_decode_tree_fp8_v41(const uint16_t* q_absorbed, const uint16_t* q_rope, const uint8_t* kv_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                         const int32_t* n_nodes, int batch, int nodes, int num_heads, int num_pages, int page_size,
+                         int max_pages, float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+int mla_decode_tree_fp4_v41(const uint16_t* q_absorbed, const uint16_t* q_rope, const uint8_t* kv_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                         const int32_t* n_nodes, int batch, int nodes, int num_heads, int num_pages, int page_size,
+                         int max_pages, float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 /* Cache rows: write new tokens into a paged cache, and read tokens back.
  *
  * Packed rows.  cu_rows [batch+1] int32 (device, non-decreasing, cu_rows[0] =

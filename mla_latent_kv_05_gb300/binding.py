@@ -43,6 +43,10 @@ SIGNATURES = {
     "mla_decode_sparse_bf16": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P,
                                     ctypes.c_size_t, _P]),
     "mla_up_project_wuv": (_I, [_P, _P, _I, _I, _I, _P, _P, ctypes.c_size_t, _P]),
+    "mla_workspace_size_tree": (_I, [_I, _I, _I, _I, ctypes.POINTER(_Z)]),
+    **{"mla_decode_tree_" + f: (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P,
+                                     _Z, _P])
+       for f in ("bf16", "fp8", "fp4", "fp8_v41", "fp4_v41")},
     **{"mla_cache_append_" + f: (_I, [_P, _Z, _P, _Z, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _Z, _P])
        for f in ("bf16", "fp8", "fp4", "fp8_v41", "fp4_v41")},
     **{"mla_cache_gather_" + f: (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _Z, _P])
@@ -482,6 +486,96 @@ def mla_cache_gather_fp4_v41(kv_cache, block_table, seq_lens, cu_rows, n_rows, o
                              stream=None):
     """mla_cache_gather_bf16 from V4.1 rows [num_pages, 64, 288]; dims 448..511 are 0."""
     return _gather("fp4_v41", kv_cache, block_table, seq_lens, cu_rows, n_rows, out, workspace, stream)
+
+
+def mla_workspace_size_tree(batch: int, nodes: int, num_heads: int = 128, page_size: int = 64) -> int:
+    n = ctypes.c_size_t(0)
+    rc = load().mla_workspace_size_tree(int(batch), int(nodes), int(num_heads), int(page_size), ctypes.byref(n))
+    if rc != MLA_OK:
+        raise MLAError(rc, "mla_workspace_size_tree")
+    return int(n.value)
+
+
+def alloc_workspace_tree(batch: int, nodes: int, device=None) -> torch.Tensor:
+    """A zeroed workspace buffer (uint8) for the tree decode."""
+    return torch.zeros(mla_workspace_size_tree(batch, nodes), dtype=torch.uint8, device=device or "cuda")
+
+
+def _tree(fmt, q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, scale, n_nodes, out, lse, workspace,
+          stream):
+    name = "mla_decode_tree_" + fmt
+    B, T, H, _ = q_absorbed.shape
+    _check(q_absorbed, "q_absorbed", torch.bfloat16, (B, T, H, 512))
+    _check(q_rope, "q_rope", torch.bfloat16, (B, T, H, 64))
+    _check(kv_cache, "kv_cache", torch.bfloat16 if fmt == "bf16" else torch.uint8)
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != _ROW_WIDTH[fmt]:
+        raise ValueError(f"kv_cache must be [num_pages, page_size, {_ROW_WIDTH[fmt]}], got {tuple(kv_cache.shape)}")
+    _check(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    _check(seq_lens, "seq_lens", torch.int32, (B,))
+    _check(parents, "parents", torch.int32, (B, T))
+    if n_nodes is not None:
+        _check(n_nodes, "n_nodes", torch.int32, (B,))
+    if out is None:
+        out = torch.empty((B, T, H, 512), dtype=torch.bfloat16, device=q_absorbed.device)
+    if lse is None:
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=q_absorbed.device)
+    _check(out, "out", torch.bfloat16, (B, T, H, 512))
+    _check(lse, "lse", torch.float32, (B, T, H))
+    if workspace is None:
+        workspace = alloc_workspace_tree(B, T, q_absorbed.device)
+    _check(workspace, "workspace", torch.uint8)
+    _same_device(dict(q_absorbed=q_absorbed, q_rope=q_rope, kv_cache=kv_cache, block_table=block_table,
+                      seq_lens=seq_lens, parents=parents, n_nodes=n_nodes, out=out, lse=lse, workspace=workspace),
+                 torch.cuda.current_device())
+    rc = getattr(load(), name)(
+        _ptr(q_absorbed), _ptr(q_rope), _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens), _ptr(parents),
+        _ptr(n_nodes), int(B), int(T), int(H), int(kv_cache.shape[0]), int(kv_cache.shape[1]),
+        int(block_table.shape[1]), ctypes.c_float(float(scale)), _ptr(out), _ptr(lse), _ptr(workspace),
+        ctypes.c_size_t(workspace.numel()), _stream(stream))
+    if rc != MLA_OK:
+        raise MLAError(rc, name)
+    return out, lse
+
+
+def mla_decode_tree_bf16(q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, scale, n_nodes=None, out=None,
+                         lse=None, workspace=None, stream=None):
+    """Decode of a drafted tree over a bf16 latent cache [num_pages, 64, 576]:
+    q_absorbed [B, T, 128, 512], q_rope [B, T, 128, 64]; sequence b's nodes are
+    the last n_nodes[b] (None: T) of its seq_lens[b] cached tokens, parents
+    [B, T] int32 names the node each node continues (-1: the context).  Node i
+    sees the context, itself and its ancestors.  Returns (out, lse)."""
+    return _tree("bf16", q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, scale, n_nodes, out, lse,
+                 workspace, stream)
+
+
+def mla_decode_tree_fp8(q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, scale, n_nodes=None, out=None,
+                        lse=None, workspace=None, stream=None):
+    """mla_decode_tree_bf16 over the cache mla_decode_fp8 reads, [num_pages, 64, 594]."""
+    return _tree("fp8", q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, scale, n_nodes, out, lse,
+                 workspace, stream)
+
+
+def mla_decode_tree_fp4(q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, scale, n_nodes=None, out=None,
+                        lse=None, workspace=None, stream=None):
+    """mla_decode_tree_bf16 over the cache mla_decode_fp4 reads, [num_pages, 64, 324]."""
+    return _tree("fp4", q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, scale, n_nodes, out, lse,
+                 workspace, stream)
+
+
+def mla_decode_tree_fp8_v41(q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, scale, n_nodes=None, out=None,
+                        lse=None, workspace=None, stream=None):
+    """mla_decode_tree_bf16 over the cache mla_decode_fp8_v41 reads, [num_pages, 64, 528]."""
+    return _tree("fp8_v41", q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, scale, n_nodes, out, lse,
+                 workspace, stream)
+
+
+def mla_decode_tree_fp4_v41(q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, scale, n_nodes=None, out=None,
+                        lse=None, workspace=None, stream=None):
+    """mla_decode_tree_bf16 over the cache mla_decode_fp4_v41 reads, [num_pages, 64, 288]."""
+    return _tree("fp4_v41", q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, scale, n_nodes, out, lse,
+                 workspace, stream)
 
 
 def mla_expand_kv(latent, w_uk, w_uv, k_nope=None, v=None, workspace=None, stream=None):

@@ -125,6 +125,7 @@ int run_decode(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rop
   p.kv_bf16 = quant ? nullptr : static_cast<const uint8_t*>(kv_cache);
   p.sp_slots = nullptr;
   p.topk = 0;
+  p.tree_nodes = 0;
   p.block_table = block_table;
   p.batch = batch;
   p.sq = sq;
@@ -249,6 +250,81 @@ int run_sparse(const uint16_t* q_absorbed, const uint16_t* q_rope, const void* k
   if (launch_decode_sparse(p, ppg, pdl, stream) != cudaSuccess) return MLA_ERR_CUDA;
   if (ev1 && cudaEventRecord(ev1, stream) != cudaSuccess) return MLA_ERR_CUDA;
   if (launch_combine_plan(workspace, L, rows, 1, p.out, lse, pdl, stream) != cudaSuccess) return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+// Tree decode: the drafted nodes' masks and lengths, then the split planner
+// over the batch * nodes rows with one query each, the attention, the merge.
+int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope, const void* kv_cache,
+             const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents, const int32_t* n_nodes,
+             int batch, int nodes, int num_heads, int num_pages, int page_size, int max_pages, float softmax_scale,
+             uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream_ptr) {
+  if (!parents || nodes <= 0) return MLA_ERR_INVALID_ARG;
+  int st = validate_common(q_absorbed, q_rope, kv_cache, block_table, seq_lens, batch, 1, num_heads, num_pages,
+                           page_size, max_pages, softmax_scale, out, lse, workspace);
+  if (st != MLA_OK) return st;
+  if (nodes > kMaxNodes || static_cast<long long>(batch) * nodes > kMaxRows) return MLA_ERR_UNSUPPORTED;
+  // the planner's page totals over the rows are 32-bit
+  if (static_cast<long long>(batch) * nodes * max_pages >= (1ll << 30)) return MLA_ERR_UNSUPPORTED;
+  // query rows are read and output rows written 32 bytes at a time
+  if (!aligned(q_absorbed, 32) || !aligned(q_rope, 32) || !aligned(out, 32) || !aligned(parents, 4) ||
+      !aligned(n_nodes, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (batch == 0) return MLA_OK;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  const int pairs = decode_max_pairs();
+  if (pairs <= 0) return MLA_ERR_CUDA;
+  const int rows = batch * nodes;
+  const WsLayout L = ws_layout(rows, 1, pairs, 0, true);
+  if (workspace_bytes < L.total) return MLA_ERR_WORKSPACE;
+  const int ppg = pairs_for(pairs, static_cast<long long>(rows) * max_pages);
+  CacheMaps maps;
+  const bool quant = kind != CacheKind::kBf16;
+  if (!quant) {
+    st = make_cache_tmap(&maps.k, kv_cache, num_pages, 5);
+    if (st == MLA_OK) st = make_cache_tmap(&maps.k8, kv_cache, num_pages, 5, 8);
+    if (st == MLA_OK) st = make_cache_tmap(&maps.kb, kv_cache, num_pages, 4);
+    if (st == MLA_OK) st = make_cache_tmap(&maps.kb8, kv_cache, num_pages, 4, 8);
+    if (st == MLA_OK) st = make_cache_tmap(&maps.v, kv_cache, num_pages, 8);
+    if (st != MLA_OK) return st;
+  }
+  __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out);
+  if (launch_tree_prep(parents, n_nodes, seq_lens, batch, nodes, max_pages, workspace, L, o, lse, stream) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  const int32_t* row_lens = reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(workspace) + L.sp_lens);
+  if (launch_plan(row_lens, rows, 1, max_pages, ppg, workspace, L, nullptr, nullptr, stream) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  DecodeParams p;
+  memset(&p, 0, sizeof(p));
+  p.q_abs = reinterpret_cast<const __nv_bfloat16*>(q_absorbed);
+  p.q_rope = reinterpret_cast<const __nv_bfloat16*>(q_rope);
+  p.kv_quant = quant ? static_cast<const uint8_t*>(kv_cache) : nullptr;
+  p.kv_bf16 = quant ? nullptr : static_cast<const uint8_t*>(kv_cache);
+  p.block_table = block_table;
+  p.batch = rows;
+  p.sq = 1;
+  p.pairs_per_group = ppg;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.tree_nodes = nodes;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.out = o;
+  p.lse = lse;
+  p.ws = static_cast<uint8_t*>(workspace);
+  p.L = L;
+  cudaEvent_t ev0 = g_prof_before, ev1 = g_prof_after;
+  g_prof_before = g_prof_after = nullptr;
+  const bool pdl = ev0 == nullptr;
+  if (ev0 && cudaEventRecord(ev0, stream) != cudaSuccess) return MLA_ERR_CUDA;
+  cudaError_t le;
+  if (kind == CacheKind::kFp8) le = launch_tree_fp8(p, ppg, pdl, stream);
+  else if (kind == CacheKind::kFp4) le = launch_tree_fp4(p, ppg, pdl, stream);
+  else if (kind == CacheKind::kFp8V41) le = launch_tree_fp8_v41(p, ppg, pdl, stream);
+  else if (kind == CacheKind::kFp4V41) le = launch_tree_fp4_v41(p, ppg, pdl, stream);
+  else le = launch_tree_bf16(maps, p, ppg, pdl, stream);
+  if (le != cudaSuccess) return MLA_ERR_CUDA;
+  if (ev1 && cudaEventRecord(ev1, stream) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_combine_plan(workspace, L, rows, 1, o, lse, pdl, stream, true) != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }
 
@@ -568,6 +644,66 @@ int mla_decode_fp4_v41(const uint16_t* q_absorbed, const uint16_t* q_rope, const
                        void* workspace, size_t workspace_bytes, void* stream) {
   return run_decode(CacheKind::kFp4V41, q_absorbed, q_rope, kv_cache, block_table, seq_lens, batch, sq, num_heads,
                     num_pages, page_size, max_pages, softmax_scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+int mla_workspace_size_tree(int batch, int nodes, int num_heads, int page_size, size_t* bytes) {
+  if (!bytes || batch < 0 || nodes <= 0) return MLA_ERR_INVALID_ARG;
+  if (num_heads != kHeads || page_size != kPage || nodes > kMaxNodes) return MLA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(batch) * nodes > kMaxRows) return MLA_ERR_UNSUPPORTED;
+  const int pairs = decode_max_pairs();
+  if (pairs <= 0) return MLA_ERR_CUDA;
+  *bytes = ws_layout(batch > 0 ? batch * nodes : 1, 1, pairs, 0, true).total;
+  return MLA_OK;
+}
+
+int mla_decode_tree_bf16(const uint16_t* q_absorbed, const uint16_t* q_rope, const uint16_t* kv_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                         const int32_t* n_nodes, int batch, int nodes, int num_heads, int num_pages, int page_size,
+                         int max_pages, float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  return run_tree(CacheKind::kBf16, q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, n_nodes, batch, nodes,
+                  num_heads, num_pages, page_size, max_pages, softmax_scale, out, lse, workspace, workspace_bytes,
+                  stream);
+}
+
+int mla_decode_tree_fp8(const uint16_t* q_absorbed, const uint16_t* q_rope, const uint8_t* kv_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                         const int32_t* n_nodes, int batch, int nodes, int num_heads, int num_pages, int page_size,
+                         int max_pages, float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  return run_tree(CacheKind::kFp8, q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, n_nodes, batch, nodes,
+                  num_heads, num_pages, page_size, max_pages, softmax_scale, out, lse, workspace, workspace_bytes,
+                  stream);
+}
+
+int mla_decode_tree_fp4(const uint16_t* q_absorbed, const uint16_t* q_rope, const uint8_t* kv_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                         const int32_t* n_nodes, int batch, int nodes, int num_heads, int num_pages, int page_size,
+                         int max_pages, float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  return run_tree(CacheKind::kFp4, q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, n_nodes, batch, nodes,
+                  num_heads, num_pages, page_size, max_pages, softmax_scale, out, lse, workspace, workspace_bytes,
+                  stream);
+}
+
+int mla_decode_tree_fp8_v41(const uint16_t* q_absorbed, const uint16_t* q_rope, const uint8_t* kv_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                         const int32_t* n_nodes, int batch, int nodes, int num_heads, int num_pages, int page_size,
+                         int max_pages, float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  return run_tree(CacheKind::kFp8V41, q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, n_nodes, batch, nodes,
+                  num_heads, num_pages, page_size, max_pages, softmax_scale, out, lse, workspace, workspace_bytes,
+                  stream);
+}
+
+int mla_decode_tree_fp4_v41(const uint16_t* q_absorbed, const uint16_t* q_rope, const uint8_t* kv_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                         const int32_t* n_nodes, int batch, int nodes, int num_heads, int num_pages, int page_size,
+                         int max_pages, float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  return run_tree(CacheKind::kFp4V41, q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, n_nodes, batch, nodes,
+                  num_heads, num_pages, page_size, max_pages, softmax_scale, out, lse, workspace, workspace_bytes,
+                  stream);
 }
 
 int mla_combine_splits(const float* partial_out, const float* partial_lse, const int32_t* split_indptr, int rows,

@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 // (n_parts[b] > 1); other rows were written by the attention kernel (one
 // part) or the planner (no token).  Four parts' loads are in flight at a
 // time; the parts are summed in slot order.
+template <bool kF32>
 __global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __restrict__ ws, WsLayout Lw, int sq,
                                                            __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
   // The plan (part counts and slot bases) was written by the planner, which
@@ -113,7 +114,19 @@ __global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __rest
   if (parts <= 1) return;
   const int start = i * spq + base;
   const float* part_lse = reinterpret_cast<const float*>(ws + Lw.part_lse);
-  const __nv_bfloat16* part_out = reinterpret_cast<const __nv_bfloat16*>(ws + Lw.part_out);
+  // fp32 partials (tree decode): the same 16 values a lane, in two 32-byte loads
+  constexpr int kWords = kF32 ? 16 : 8;
+  auto load = [&](int part, uint32_t* x) {
+    const size_t e = (static_cast<size_t>(start + part) * kHeads + (blockIdx.y * 8 + (threadIdx.x >> 5))) * kDc +
+                     16 * (threadIdx.x & 31);
+    if constexpr (kF32) {
+      const float* src = reinterpret_cast<const float*>(ws + Lw.part_out) + e;
+      ptx::ld_global_cg_v8(src, x);
+      ptx::ld_global_cg_v8(src + 8, x + 8);
+    } else {
+      ptx::ld_global_cg_v8(reinterpret_cast<const __nv_bfloat16*>(ws + Lw.part_out) + e, x);
+    }
+  };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y * 8 + warp;
   float acc[16];
@@ -128,10 +141,10 @@ __global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __rest
     const int n = min(32, parts - s0);
     const int sl = s0 + lane;
     const float v = sl < parts ? __ldcg(part_lse + static_cast<size_t>(start + sl) * kHeads + h) : -INFINITY;
-    uint32_t x[4][8];
+    uint32_t x[4][kWords];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (u < n) ptx::ld_global_cg_v8(part_out + (static_cast<size_t>(start + s0 + u) * kHeads + h) * kDc + 16 * lane, x[u]);
+      if (u < n) load(s0 + u, x[u]);
     float gm = v;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
@@ -148,8 +161,7 @@ __global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __rest
       if (j0 > 0) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (j0 + u < n)
-            ptx::ld_global_cg_v8(part_out + (static_cast<size_t>(start + s0 + j0 + u) * kHeads + h) * kDc + 16 * lane, x[u]);
+          if (j0 + u < n) load(s0 + j0 + u, x[u]);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -158,7 +170,9 @@ __global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __rest
           sum += wg;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[u][e]));
+            const float2 f = kF32 ? make_float2(__uint_as_float(x[u][(2 * e) % kWords]),
+                                                __uint_as_float(x[u][(2 * e + 1) % kWords]))
+                                  : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[u][e]));
             acc[2 * e] = fmaf(wg, f.x, acc[2 * e]);
             acc[2 * e + 1] = fmaf(wg, f.y, acc[2 * e + 1]);
           }
@@ -180,7 +194,7 @@ __global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __rest
 }  // namespace
 
 cudaError_t launch_combine_plan(const void* ws, const WsLayout& Lw, int batch, int sq, __nv_bfloat16* out, float* lse,
-                                bool pdl, cudaStream_t stream) {
+                                bool pdl, cudaStream_t stream, bool f32) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(batch * sq, kHeads / 8, 1);
   cfg.blockDim = dim3(256, 1, 1);
@@ -190,7 +204,8 @@ cudaError_t launch_combine_plan(const void* ws, const WsLayout& Lw, int batch, i
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_plan_kernel, static_cast<const uint8_t*>(ws), Lw, sq, out, lse);
+  return cudaLaunchKernelEx(&cfg, f32 ? combine_plan_kernel<true> : combine_plan_kernel<false>,
+                            static_cast<const uint8_t*>(ws), Lw, sq, out, lse);
 }
 
 // Public merge: parts of row r are [indptr[r], indptr[r+1]).

@@ -30,6 +30,7 @@ constexpr int kV41Row = kV41Values + kV41Values / 32;   // 528 bytes
 // 16 values): 288 bytes, the same value order.
 constexpr int kV41Fp4Row = kV41Values / 2 + kV41Values / 16;   // 288 bytes
 constexpr int kMaxSq = 4;
+constexpr int kMaxNodes = 64;       // drafted nodes of a sequence (one bit each)
 constexpr int kMaxRows = 1 << 16;   // batch * Sq handled by the planner
 
 // Plan header at workspace offset 0.
@@ -50,6 +51,7 @@ struct WsLayout {
   size_t lens, tile_start, row_cost, pair_lo, pair_rank, pair_b0, first_pair, slot_base, n_parts, empty_rows;
   size_t part_lse, part_out;
   size_t sp_lens, sp_slots;   // sparse decode: listed tokens per row, compacted slot lists [rows, topk]
+  size_t tree_seen;           // tree decode: per row, bit a = draft node a is the row's node or an ancestor
   size_t total;
   int max_slots;
 };
@@ -57,8 +59,10 @@ struct WsLayout {
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // topk > 0: the sparse decode's extra arrays (its rows are batch * sq query
-// rows, planned as a batch of that many rows with one query each)
-__host__ __device__ inline WsLayout ws_layout(int batch, int sq, int pairs, int topk = 0) {
+// rows, planned as a batch of that many rows with one query each).  tree:
+// the tree decode's (its rows are batch * nodes, planned the same way; its
+// partials are fp32).
+__host__ __device__ inline WsLayout ws_layout(int batch, int sq, int pairs, int topk = 0, bool tree = false) {
   WsLayout L;
   const int pg = pairs / sq > 0 ? pairs / sq : 1;
   // every pair boundary splits at most one row: slots per query <= 2*(pg-1)
@@ -75,9 +79,10 @@ __host__ __device__ inline WsLayout ws_layout(int batch, int sq, int pairs, int 
   L.n_parts = o;     o = align256(o + sizeof(int) * batch);
   L.empty_rows = o;  o = align256(o + sizeof(int) * batch);
   L.part_lse = o;    o = align256(o + sizeof(float) * static_cast<size_t>(L.max_slots) * kHeads);
-  L.part_out = o;    o = align256(o + 2 * static_cast<size_t>(L.max_slots) * kHeads * kDc);   // bf16 partials
-  L.sp_lens = o;     o = align256(o + (topk > 0 ? sizeof(int) * batch : 0));
+  L.part_out = o;    o = align256(o + (tree ? 4 : 2) * static_cast<size_t>(L.max_slots) * kHeads * kDc);   // bf16 partials
+  L.sp_lens = o;     o = align256(o + (topk > 0 || tree ? sizeof(int) * batch : 0));
   L.sp_slots = o;    o = align256(o + (topk > 0 ? sizeof(int) * static_cast<size_t>(batch) * topk : 0));
+  L.tree_seen = o;   o = align256(o + (tree ? sizeof(uint64_t) * static_cast<size_t>(batch) : 0));
   L.total = o;
   return L;
 }

@@ -526,6 +526,18 @@ __device__ __forceinline__ void load_q_rolled(const uint8_t* qa, const uint8_t* 
   }
 }
 
+// Tree decode: bits of the columns starting at some token that a node sees,
+// `ctx` of them context (may be negative or large), `valid` of them at most;
+// draft token a is column ctx + a and seen when bit a of `seen` is set.
+__device__ __forceinline__ uint64_t tree_bits(uint64_t seen, int ctx, int valid) {
+  uint64_t m;
+  if (ctx >= 64) m = ~uint64_t{0};
+  else if (ctx > 0) m = (seen << ctx) | ((uint64_t{1} << ctx) - 1);
+  else m = ctx > -64 ? seen >> -ctx : 0;
+  if (valid <= 0) return 0;
+  return valid >= 64 ? m : m & ((uint64_t{1} << valid) - 1);
+}
+
 }  // namespace dk
 
 // kMode 0: bf16 cache via TMA; 1: FP8 cache via bulk copies + dequant to
@@ -534,7 +546,17 @@ __device__ __forceinline__ void load_q_rolled(const uint8_t* qa, const uint8_t* 
 // over the bf16 cache (rows gathered by listed slot with 16-byte cp.async);
 // 4 / 5: the FP4 cache as 1 / 2; 6 / 7: the 528-byte V4.1 FP8 rows as 1 / 2;
 // 8 / 9: the 288-byte V4.1 FP4 rows as 1 / 2
-template <int kMode>
+//
+// kTree: each row is a drafted node (row = sequence * p.tree_nodes + node)
+// that sees its sequence's context and, of the drafted tokens behind it,
+// those whose bit is set in its mask (itself and its ancestors).  The rows
+// are planned like single queries of length context + node + 1; full tiles
+// of context take the same path as without a tree, and only the tiles that
+// reach the drafted tokens test bits.  Split rows keep fp32 partials: a row
+// is cut into two parts or three here, so a bf16 rounding of each would be
+// as large as the result's own, where a long decode row averages it over
+// many parts.
+template <int kMode, bool kTree = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dk::Cfg<kMode>::kThreads, 1)
 mla_decode_pair_kernel(const __grid_constant__ CacheMaps maps, const DecodeParams p) {
   using namespace dk;
@@ -576,9 +598,11 @@ mla_decode_pair_kernel(const __grid_constant__ CacheMaps maps, const DecodeParam
   float* part_lse = reinterpret_cast<float*>(p.ws + p.L.part_lse);
   __nv_bfloat16* part_out = reinterpret_cast<__nv_bfloat16*>(p.ws + p.L.part_out);
   const int* n_parts = reinterpret_cast<const int*>(p.ws + p.L.n_parts);
+  const uint64_t* tree_seen = reinterpret_cast<const uint64_t*>(p.ws + p.L.tree_seen);
   auto BAR = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * static_cast<uint32_t>(i); };
   // physical page of row-local half page hp of batch row b (or -1 if out of range)
   auto half_page = [&](int b, int hp) -> int {
+    if constexpr (kTree) b /= p.tree_nodes;   // rows of one sequence share its pages
     const int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + (hp >> 1));
     return (page < 0 || page >= p.num_pages) ? -1 : page;
   };
@@ -1080,6 +1104,8 @@ mla_decode_pair_kernel(const __grid_constant__ CacheMaps maps, const DecodeParam
     while (ok && w.next(sg)) {
       issued = true;
       const int len_i = lens[sg.b] - (sq - 1 - group);
+      const int ctx_i = kTree ? len_i - 1 - sg.b % p.tree_nodes : 0;   // tree: tokens of the context
+      const uint64_t seen_i = kTree ? tree_seen[sg.b] : 0;
       const int hp_end = 2 * sg.t1;
       for (int h0 = 2 * sg.t0; h0 < hp_end && ok; h0 += TH) {
         const int nh = min(TH, hp_end - h0);
@@ -1109,7 +1135,21 @@ mla_decode_pair_kernel(const __grid_constant__ CacheMaps maps, const DecodeParam
           if (!wait_warp<false>(BAR(VFULL + vs), vphase, hdr)) { ok = false; break; }
           if constexpr (kMode == 3) ptx::fence_proxy_async_cta();   // rows written by cp.async
           const int valid = len_i - (h0 + j) * kHalf;   // tokens of this half page visible to the query
-          if (valid < kHalf) {
+          if constexpr (kTree) {
+            // drafted tokens off the node's path, and those past it: V = 0
+            const uint32_t seen = static_cast<uint32_t>(tree_bits(seen_i, ctx_i - (h0 + j) * kHalf, valid));
+            if (seen != 0xFFFFFFFFu) {
+              uint8_t* slot = smem + static_cast<uint32_t>(vs) * kVSlot;
+              for (int i = lane; i < kHalf * 8 * 8; i += 32) {
+                const int r = i / 64, c = (i / 8) & 7, q = i & 7;
+                if (!((seen >> r) & 1u))
+                  *reinterpret_cast<uint4*>(slot + (r >> 3) * kVGroup + c * kAtom + (r & 7) * 128 + q * 16) =
+                      make_uint4(0, 0, 0, 0);
+              }
+              ptx::fence_proxy_async_cta();
+              __syncwarp();
+            }
+          } else if (valid < kHalf) {
             // rows past the visible length get P = 0; make their V finite too
             const int v0 = valid > 0 ? valid : 0;
             uint8_t* slot = smem + static_cast<uint32_t>(vs) * kVSlot;
@@ -1179,6 +1219,8 @@ mla_decode_pair_kernel(const __grid_constant__ CacheMaps maps, const DecodeParam
     while (ok && w.next(sg)) {
       const int row = sg.b * sq + group;
       const int len_i = lens[sg.b] - (sq - 1 - group);
+      const int ctx_i = kTree ? len_i - 1 - sg.b % p.tree_nodes : 0;   // tree: tokens of the context
+      const uint64_t seen_i = kTree ? tree_seen[sg.b] : 0;
       {
         // Q row h -> TMEM lane h, columns [0, 288): two bf16 per column, K
         // order, 32 columns (128 B of the row) per chunk.  With two groups,
@@ -1219,7 +1261,16 @@ mla_decode_pair_kernel(const __grid_constant__ CacheMaps maps, const DecodeParam
         // row max of the masked raw scores.  m_ref stays in raw score units and
         // P = exp2((s - m_ref) * c), so the max element gets exactly exp2(0) = 1
         // whatever the magnitude of the scores (scale c > 0).
-        const bool full = valid >= kN;                 // the same for every head of the tile
+        const bool full = valid >= kN && (!kTree || ctx_i - h0 * kHalf >= kN);   // the same for every head of the tile
+        // tree: bits of the tile's columns that the node sees, this group's and the other's
+        uint64_t see_mine = 0, see_other = 0;
+        if (kTree && !full) {
+          const int tc = ctx_i - h0 * kHalf;
+          see_mine = tree_bits(seen_i, tc - c_mine, valid - c_mine);
+          if constexpr (kSG == 2) see_other = tree_bits(seen_i, tc - c_other, valid - c_other);
+        }
+        auto sees = [&](int e) { return kTree ? ((see_mine >> e) & 1u) != 0 : c_mine + e < valid; };
+        auto sees_other = [&](int e) { return kTree ? ((see_other >> e) & 1u) != 0 : c_other + e < valid; };
         float mx = -INFINITY;
         if (full) {
           if constexpr (kSG == 2) {
@@ -1232,9 +1283,9 @@ mla_decode_pair_kernel(const __grid_constant__ CacheMaps maps, const DecodeParam
         } else {
 #pragma unroll
           for (int e = 0; e < kHC; ++e) {
-            if (c_mine + e < valid) mx = fmaxf(mx, __uint_as_float(mine[e]));
+            if (sees(e)) mx = fmaxf(mx, __uint_as_float(mine[e]));
             if constexpr (kSG == 2)
-              if (c_other + e < valid) mx = fmaxf(mx, __uint_as_float(other[e]));
+              if (sees_other(e)) mx = fmaxf(mx, __uint_as_float(other[e]));
           }
         }
         float alpha = 1.f;
@@ -1259,9 +1310,8 @@ mla_decode_pair_kernel(const __grid_constant__ CacheMaps maps, const DecodeParam
         } else {
 #pragma unroll
           for (int e = 0; e < kHC / 2; ++e) {
-            const int col = c_mine + 2 * e;
-            const float p0 = col < valid ? fast_exp2((__uint_as_float(mine[2 * e]) - m_ref) * c) : 0.f;
-            const float p1 = col + 1 < valid ? fast_exp2((__uint_as_float(mine[2 * e + 1]) - m_ref) * c) : 0.f;
+            const float p0 = sees(2 * e) ? fast_exp2((__uint_as_float(mine[2 * e]) - m_ref) * c) : 0.f;
+            const float p1 = sees(2 * e + 1) ? fast_exp2((__uint_as_float(mine[2 * e + 1]) - m_ref) * c) : 0.f;
             pk[e] = kF16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
             la += p0;
             lb += p1;
@@ -1419,6 +1469,17 @@ mla_decode_pair_kernel(const __grid_constant__ CacheMaps maps, const DecodeParam
           ptx::tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < kEpBatch; ++k) {
+            if constexpr (kTree) {
+              if (parts > 1) {   // fp32 partial
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[k][e] = __float_as_uint(__uint_as_float(r[k][e]) * inv_l);
+                float* part = reinterpret_cast<float*>(part_out) +
+                              (static_cast<size_t>(slot0 + mine) * kHeads + h) * kDc + (cc + k) * 32;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) ptx::st_global_v8(part + e, r[k] + e);
+                continue;
+              }
+            }
             uint32_t o[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -1462,10 +1523,10 @@ namespace {
 // unnamed namespace so that its per-device static is this library's own:
 // a function-local static of a template with external linkage is one
 // object per process, shared by every loaded copy of the library.
-template <int kMode>
+template <int kMode, bool kTree = false>
 cudaError_t launch_decode_mode(const CacheMaps& maps, const DecodeParams& p, int n_pairs, bool pdl,
                                cudaStream_t stream) {
-  auto kern = mla_decode_pair_kernel<kMode>;
+  auto kern = mla_decode_pair_kernel<kMode, kTree>;
   static int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1548,6 +1609,45 @@ cudaError_t launch_decode_sparse(const DecodeParams& p, int n_pairs, bool pdl, c
   CacheMaps unused;
   memset(&unused, 0, sizeof(unused));
   return launch_decode_mode<3>(unused, p, n_pairs, pdl, stream);
+}
+
+cudaError_t launch_tree_bf16(const CacheMaps& maps, const DecodeParams& p, int n_pairs, bool pdl,
+                             cudaStream_t stream) {
+  return launch_decode_mode<0, true>(maps, p, n_pairs, pdl, stream);
+}
+
+namespace {
+
+// as the decode's: the f16-operand pass, then the exact bf16-operand pass,
+// which returns at once unless the first pass flagged an input
+template <int kF16Mode, int kExactMode>
+cudaError_t launch_tree_quant(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream) {
+  CacheMaps unused;
+  memset(&unused, 0, sizeof(unused));
+  DecodeParams q = p;
+  q.fp8_fallback = 0;
+  cudaError_t e = launch_decode_mode<kF16Mode, true>(unused, q, n_pairs, pdl, stream);
+  if (e != cudaSuccess) return e;
+  q.fp8_fallback = 1;
+  return launch_decode_mode<kExactMode, true>(unused, q, n_pairs, pdl, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_fp8(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream) {
+  return launch_tree_quant<2, 1>(p, n_pairs, pdl, stream);
+}
+
+cudaError_t launch_tree_fp4(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream) {
+  return launch_tree_quant<5, 4>(p, n_pairs, pdl, stream);
+}
+
+cudaError_t launch_tree_fp8_v41(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream) {
+  return launch_tree_quant<7, 6>(p, n_pairs, pdl, stream);
+}
+
+cudaError_t launch_tree_fp4_v41(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream) {
+  return launch_tree_quant<9, 8>(p, n_pairs, pdl, stream);
 }
 
 int decode_max_pairs() {

@@ -20,18 +20,26 @@ struct DecodeParams {
   int fp8_fallback;              // FP8/FP4 exact pass: run only if the f16 pass flagged its inputs
   const int32_t* sp_slots;       // sparse decode: compacted slot lists [rows, topk] (workspace)
   int topk;
+  int tree_nodes;                // tree decode: rows are (sequence, node) pairs, this many per sequence
   __nv_bfloat16* out;            // [B, Sq, 128, 512]
   float* lse;                    // [B, Sq, 128]
   uint8_t* ws;
   WsLayout L;
 };
 
-// out / lse: the rows with no token are written here (out = 0, lse = -inf).
+// out / lse: the rows with no token are written here (out = 0, lse = -inf),
+// unless out is null.
 cudaError_t launch_plan(const int32_t* seq_lens, int batch, int sq, int max_pages, int pairs_per_group,
                         void* ws, const WsLayout& L, __nv_bfloat16* out, float* lse, cudaStream_t stream);
 // Sparse decode: compact each query row's listed slots into the workspace.
 cudaError_t launch_sparse_prep(const int32_t* token_slots, int rows, int topk, int num_slots, void* ws,
                                const WsLayout& L, cudaStream_t stream);
+// Tree decode: per (sequence, node) row its visible length and the bits of
+// the draft nodes it sees, into the workspace; rows with nothing to see are
+// written here (out = 0, lse = -inf).
+cudaError_t launch_tree_prep(const int32_t* parents, const int32_t* n_nodes, const int32_t* seq_lens, int batch,
+                             int nodes, int max_pages, void* ws, const WsLayout& L, __nv_bfloat16* out, float* lse,
+                             cudaStream_t stream);
 // TMA descriptors of the bf16 cache (4-D: 64 columns, 8 rows, 9 chunks, row
 // groups).  The score SM loads chunks 0..4 (k) and 5..8 (kb) of a half page,
 // or of a whole page when a tile's two adjacent slots are the two halves of
@@ -52,12 +60,20 @@ cudaError_t launch_decode_fp4_v41(const DecodeParams& p, int n_pairs, bool pdl, 
 // Sparse decode over the bf16 cache (p.kv_bf16, p.sp_slots; rows planned
 // with one query each).
 cudaError_t launch_decode_sparse(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream);
+// Tree decode over each cache format (p.tree_nodes set; rows planned with one
+// query each).
+cudaError_t launch_tree_bf16(const CacheMaps& maps, const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream);
+cudaError_t launch_tree_fp8(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream);
+cudaError_t launch_tree_fp4(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream);
+cudaError_t launch_tree_fp8_v41(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream);
+cudaError_t launch_tree_fp4_v41(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream);
 int decode_max_pairs();
 // W^UV up-projection of latent outputs (see wuv.cu).
 cudaError_t launch_wuv(PFN_cuTensorMapEncodeTiled_v12000 encode, const void* o, const void* w, int rows, void* out,
                        void* hdr, cudaStream_t stream);
+// f32: the partials are fp32 (tree decode) instead of bf16.
 cudaError_t launch_combine_plan(const void* ws, const WsLayout& Lw, int batch, int sq, __nv_bfloat16* out, float* lse,
-                                bool pdl, cudaStream_t stream);
+                                bool pdl, cudaStream_t stream, bool f32 = false);
 cudaError_t launch_combine_indptr(const float* part_out, const float* part_lse, const int32_t* indptr, int rows,
                                   __nv_bfloat16* out, float* lse, cudaStream_t stream);
 
