@@ -50,8 +50,9 @@ constexpr int kRing = 8;
 constexpr uint32_t kOffRing = 2 * kQTile;
 constexpr uint32_t kOffBar = kOffRing + kRing * kChunk;   // 224 KiB
 constexpr int kItemSlots = 2;
+constexpr int kTiles = 4;                          // K or V tiles in flight at most (barriers)
 enum Bar {
-  QFULL = 0, QEMPTY = QFULL + 2, FULL = QEMPTY + 2, EMPTY = FULL + kRing, SFULL = EMPTY + kRing, PREADY = SFULL + 2,
+  QFULL = 0, QEMPTY = QFULL + 2, FULL = QEMPTY + 2, EMPTY = FULL + kTiles, SFULL = EMPTY + kTiles, PREADY = SFULL + 2,
   PVDONE = PREADY + 2, IFULL = PVDONE + 2, IEMPTY = IFULL + kItemSlots, DRAIN = IEMPTY + kItemSlots, NBAR
 };
 constexpr uint32_t kOffTmem = kOffBar + 8 * NBAR;
@@ -158,6 +159,26 @@ struct Maps {
   CUtensorMap qn, qr, kn, kr, v;
 };
 
+// tcgen05.mma and its commit, issued by the lanes where `on` holds (one of a
+// converged warp).
+__device__ __forceinline__ void mma_ss_if(bool on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(static_cast<uint32_t>(on))
+               : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(bool on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+               :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(static_cast<uint32_t>(on))
+               : "memory");
+}
+__device__ __forceinline__ void commit_if(bool on, uint32_t bar) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+               "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+               :: "r"(bar), "r"(static_cast<uint32_t>(on)) : "memory");
+}
+
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -184,7 +205,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       ptx::mbar_init(BAR(PREADY + t), 128);
       ptx::mbar_init(BAR(PVDONE + t), 1);
     }
-    for (int s = 0; s < kRing; ++s) { ptx::mbar_init(BAR(FULL + s), 1); ptx::mbar_init(BAR(EMPTY + s), 1); }
+    for (int s = 0; s < kTiles; ++s) { ptx::mbar_init(BAR(FULL + s), 1); ptx::mbar_init(BAR(EMPTY + s), 1); }
     for (int s = 0; s < kItemSlots; ++s) {
       ptx::mbar_init(BAR(IFULL + s), 1);
       ptx::mbar_init(BAR(IEMPTY + s), 10);     // producer, MMA warp, eight softmax warps
@@ -249,14 +270,19 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     if (lane == 0) {
       const uint64_t pol = ptx::policy_evict_normal();
       Walk w;
-      uint32_t pos = 0;                        // chunks queued so far
+      uint32_t pos = 0, seq = 0;               // chunks and tiles queued so far
       uint32_t nq[2] = {0, 0};                 // Q tiles queued so far
       bool ok = true;
+      // The ring holds eight chunks, so a tile's slots were last used by the
+      // third and fourth tiles before it (K 3 + V 2 + K 3, or V 2 + K 3 + V 2
+      // and one chunk of a K).
+      auto slot_free = [&]() {
+        if (seq >= 4) ok = wait_bounded<false>(BAR(EMPTY + (seq & 3u)), ((seq - 4) >> 2) & 1u, hdr);
+        if (ok && seq >= 3) ok = wait_bounded<false>(BAR(EMPTY + ((seq - 3) & 3u)), ((seq - 3) >> 2) & 1u, hdr);
+        return ok;
+      };
       auto chunk = [&](const CUtensorMap* map, int x, int y, int z) {
-        const uint32_t s = pos & (kRing - 1);
-        if (!wait_bounded<false>(BAR(EMPTY + s), ((pos >> 3) & 1u) ^ 1u, hdr)) { ok = false; return; }
-        ptx::mbar_arrive_expect_tx(BAR(FULL + s), kChunk);
-        ptx::tma_load_3d(sbase + kOffRing + s * kChunk, map, BAR(FULL + s), x, y, z, pol);
+        ptx::tma_load_3d(sbase + kOffRing + (pos & (kRing - 1)) * kChunk, map, BAR(FULL + (seq & 3u)), x, y, z, pol);
         ++pos;
       };
       auto query = [&](int t, const Tile& it) {
@@ -280,81 +306,77 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         if (n0 > 0) query(0, it);
         for (int j = 0; j < n && ok; ++j) {
           const int k = it.k0 + j * kKeys;
+          if (!slot_free()) break;
+          ptx::mbar_arrive_expect_tx(BAR(FULL + (seq & 3u)), 3 * kChunk);
           chunk(&maps.kn, 0, it.head, k);
-          if (ok) chunk(&maps.kn, 64, it.head, k);
-          if (ok) chunk(&maps.kr, 0, 0, k);
-          if (ok && j == 0 && n1 > 0) query(1, it);
-          if (ok) chunk(&maps.v, 0, it.head, k);
-          if (ok) chunk(&maps.v, 64, it.head, k);
+          chunk(&maps.kn, 64, it.head, k);
+          chunk(&maps.kr, 0, 0, k);
+          ++seq;
+          if (j == 0 && n1 > 0) query(1, it);
+          if (!ok || !slot_free()) break;
+          ptx::mbar_arrive_expect_tx(BAR(FULL + (seq & 3u)), 2 * kChunk);
+          chunk(&maps.v, 0, it.head, k);
+          chunk(&maps.v, 64, it.head, k);
+          ++seq;
         }
       }
       // no copy may land after the CTA has left: wait for the last phase armed on each barrier
       for (int t = 0; t < 2; ++t)
         if (nq[t] > 0) wait_drain(BAR(QFULL + t), (nq[t] - 1) & 1u, hdr);
-      for (uint32_t s = 0; s < kRing; ++s) {
-        const uint32_t n = (pos + kRing - 1 - s) / kRing;
+      for (uint32_t s = 0; s < kTiles; ++s) {
+        const uint32_t n = (seq + kTiles - 1 - s) / kTiles;
         if (n > 0) wait_drain(BAR(FULL + s), (n - 1) & 1u, hdr);
       }
     }
   } else if (smem_ok && warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    // The whole warp walks the steps together and one lane issues (a
+    // predicate on the instruction, not a branch), so that descriptors and
+    // addresses stay warp-uniform values: with a one-lane branch around the
+    // issue each MMA took about twice its 64 cycles to get out.
     Walk w;
     Tile it;
-    uint32_t kpos = 0;                       // ring position of the K tile to be scored next
+    const bool lead = lane == 0;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t sb = __shfl_sync(0xffffffffu, sbase, 0);
+    const uint64_t desc_q = ptx::sdesc_sw128(sb, 16, 1024);                     // + chunks, K-steps
+    const uint64_t desc_k = ptx::sdesc_sw128(sb + kOffRing, 16, 1024);
+    const uint64_t desc_v = ptx::sdesc_sw128(sb + kOffRing, kChunk, 1024);
+    constexpr uint64_t kChunkD = kChunk >> 4;                                    // a chunk in descriptor units
+    uint32_t kpos = 0, kseq = 0;             // ring position and tile number of the K tile to be scored next
     uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
     bool ok = true, issued = false;
     // the next (item, K/V tile) step: ni = K/V tiles of each query tile, jn = the step
     int jn = 0, ni[2] = {0, 0};
-    auto fetch = [&]() -> bool {             // the next item that has keys to visit
-      do {
-        if (!next_warp(w, it)) return false;
-        ni[0] = kv_tiles(it, 0, causal);
-        ni[1] = kv_tiles(it, 1, causal);
-      } while (max(ni[0], ni[1]) == 0);
+    // One item at a time, even one without keys: the softmax warps read an item
+    // only after this one's last P.V, so waiting for more than the next item
+    // before that P.V would wait for ever.
+    auto fetch = [&]() -> bool {
+      if (!next_warp(w, it)) return false;
+      ni[0] = __shfl_sync(0xffffffffu, kv_tiles(it, 0, causal), 0);
+      ni[1] = __shfl_sync(0xffffffffu, kv_tiles(it, 1, causal), 0);
       jn = 0;
       return true;
     };
-    auto wait_chunks = [&](uint32_t pos, int n) {
-      for (int c = 0; c < n && ok; ++c)
-        ok = wait_warp<false>(BAR(FULL + ((pos + c) & (kRing - 1))), ((pos + c) >> 3) & 1u, hdr);
-    };
-    auto score = [&](int t, uint32_t pos, bool last_q, bool release) {
-      if (lane == 0) {
-#pragma unroll
-        for (int c = 0; c < 3; ++c) {
-          const uint64_t da = ptx::sdesc_sw128(sbase + static_cast<uint32_t>(t) * kQTile + c * kChunk, 16, 1024);
-          const uint32_t s = (pos + c) & (kRing - 1);
-          const uint64_t db = ptx::sdesc_sw128(sbase + kOffRing + s * kChunk, 16, 1024);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            ptx::mma_ss(tmem + kSCol + 128u * t, da + static_cast<uint64_t>(2 * k), db + static_cast<uint64_t>(2 * k),
-                        kIdescS, (c > 0 || k > 0) ? 1u : 0u);
-          if (release) ptx::mma_commit(BAR(EMPTY + s));
-        }
-        ptx::mma_commit(BAR(SFULL + t));
-        if (last_q) ptx::mma_commit(BAR(QEMPTY + t));
-      }
-      __syncwarp();
-    };
     bool more = fetch();
-    // step state: cur = the step whose P.V comes next (its S was issued)
+    // step state: the step whose P.V comes next (its S was issued); jc < 0: none
     int jc = -1, nc[2] = {0, 0}, nkc = 0;
-    uint32_t vpos = 0;
+    uint32_t vpos = 0, vseq = 0;
     while (ok && (jc >= 0 || more)) {
       bool have_v = false, have_k = false;
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (jc >= 0 && jc < nc[t]) {
-          if (!wait_warp<false>(BAR(PREADY + t), n_p[t] & 1u, hdr)) { ok = false; break; }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (ok && jc >= 0 && jc < nc[t]) {
+          ok = wait_warp<false>(BAR(PREADY + t), n_p[t] & 1u, hdr);
           ++n_p[t];
-          if (!have_v) {
-            wait_chunks(vpos, 2);
-            if (!ok) break;
+          if (ok && !have_v) {
+            ok = wait_warp<false>(BAR(FULL + (vseq & 3u)), (vseq >> 2) & 1u, hdr);
             have_v = true;
             const int valid = nkc - jc * kKeys;
-            if (valid < kKeys) {
+            if (ok && valid < kKeys) {
               // keys past the sequence's end have P = 0; make their V rows 0 too
               // (they may be another sequence's, and hold NaN)
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < 2; ++c) {
                 uint4* dst = reinterpret_cast<uint4*>(smem + kOffRing + ((vpos + c) & (kRing - 1)) * kChunk);
                 for (int i = valid * 8 + lane; i < kKeys * 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
@@ -363,53 +385,65 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
               __syncwarp();
             }
           }
+          if (!ok) break;
           ptx::tc_fence_after();
-          const bool release = t == 1 || jc >= nc[1];
-          if (lane == 0) {
-            const uint32_t s0 = vpos & (kRing - 1), s1 = (vpos + 1) & (kRing - 1);
-            const uint32_t d = tmem + kOCol + 128u * t, a = tmem + kSCol + 128u * t;
+          const uint32_t s0 = vpos & (kRing - 1);
+          const uint32_t d = tm + kOCol + 128u * t, a = tm + kSCol + 128u * t;
+          const uint64_t db = desc_v + s0 * kChunkD;
+          if (s0 != kRing - 1) {
 #pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ts_if(lead, d, a + 8u * k, db + 128u * k, kIdescPV, jc > 0 || k > 0);
+          } else {
+            // the tile's second chunk wrapped to the ring's start: two halves
+#pragma unroll 1
             for (int k = 0; k < kKeys / 16; ++k) {
-              const uint32_t acc = (jc > 0 || k > 0) ? 1u : 0u;
-              const uint64_t db = ptx::sdesc_sw128(sbase + kOffRing + s0 * kChunk + 2048u * k, kChunk, 1024);
-              if (s1 > s0) {
-                ptx::mma_ts(d, a + 8u * k, db, kIdescPV, acc);
-              } else {
-                // the tile's second chunk wrapped to the ring's start: two halves
-                ptx::mma_ts(d, a + 8u * k, db, kIdescPVHalf, acc);
-                ptx::mma_ts(d + 64u, a + 8u * k, ptx::sdesc_sw128(sbase + kOffRing + s1 * kChunk + 2048u * k, kChunk, 1024),
-                            kIdescPVHalf, acc);
-              }
+              mma_ts_if(lead, d, a + 8u * k, db + 128u * k, kIdescPVHalf, jc > 0 || k > 0);
+              mma_ts_if(lead, d + 64u, a + 8u * k, desc_v + 128u * k, kIdescPVHalf, jc > 0 || k > 0);
             }
-            if (release) { ptx::mma_commit(BAR(EMPTY + s0)); ptx::mma_commit(BAR(EMPTY + s1)); }
-            ptx::mma_commit(BAR(PVDONE + t));
           }
-          __syncwarp();
+          commit_if(lead && (t == 1 || jc >= nc[1]), BAR(EMPTY + (vseq & 3u)));
+          commit_if(lead, BAR(PVDONE + t));
         }
-        if (more && jn < ni[t]) {
+        if (ok && more && jn < ni[t]) {
           if (jn == 0) {
-            if (!wait_warp<false>(BAR(QFULL + t), n_q[t] & 1u, hdr)) { ok = false; break; }
+            ok = wait_warp<false>(BAR(QFULL + t), n_q[t] & 1u, hdr);
             ++n_q[t];
           }
-          if (!have_k) {
-            wait_chunks(kpos, 3);
-            if (!ok) break;
+          if (ok && !have_k) {
+            ok = wait_warp<false>(BAR(FULL + (kseq & 3u)), (kseq >> 2) & 1u, hdr);
             have_k = true;
           }
+          if (!ok) break;
           ptx::tc_fence_after();
           issued = true;
-          score(t, kpos, jn == ni[t] - 1, t == 1 || jn >= ni[1]);
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            const uint64_t da = desc_q + (3u * t + c) * kChunkD;
+            const uint64_t db = desc_k + ((kpos + c) & (kRing - 1)) * kChunkD;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ss_if(lead, tm + kSCol + 128u * t, da + 2u * k, db + 2u * k, kIdescS, c > 0 || k > 0);
+          }
+          commit_if(lead && (t == 1 || jn >= ni[1]), BAR(EMPTY + (kseq & 3u)));
+          commit_if(lead, BAR(SFULL + t));
+          commit_if(lead && jn == ni[t] - 1, BAR(QEMPTY + t));
         }
       }
       if (!ok) break;
       // advance: the step just scored becomes the one whose P.V comes next
-      if (more) {
+      if (more && max(ni[0], ni[1]) == 0) {
+        jc = -1;                             // an item without keys has no step
+        more = fetch();
+      } else if (more) {
         jc = jn;
         nc[0] = ni[0];
         nc[1] = ni[1];
         nkc = it.nk;
         vpos = kpos + 3;
+        vseq = kseq + 1;
         kpos += 5;
+        kseq += 2;
         if (++jn >= max(ni[0], ni[1])) more = fetch();
       } else {
         jc = -1;

@@ -169,6 +169,14 @@ def test_many_short_sequences(cuda_device):
     check(out, lse, d, True, heads=[5, 100])
 
 
+@pytest.mark.parametrize("nq,nk", [([300] * 12 + [700, 5], [0] * 12 + [10, 9]), ([900, 260, 900], [100, 600, 3])])
+def test_runs_of_tiles_without_keys(cuda_device, nq, nk):
+    # many tiles whose queries see nothing, between tiles that have work
+    d = make(nq, nk, 13)
+    out, lse = status_run(cuda(d))
+    check(out, lse, d, True, heads=[0, 77])
+
+
 def test_captured_graph_two_streams_and_repeatability(cuda_device):
     d = make([300, 45], [420, 45], 9)
     c = cuda(d)
