@@ -37,6 +37,7 @@
 #include <climits>
 
 #include "prefill.cuh"
+#include "waits.cuh"
 
 namespace mla {
 
@@ -159,6 +160,15 @@ struct Maps {
   CUtensorMap qn, qr, kn, kr, v;
 };
 
+// 32 lanes x 16 columns to tensor memory.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32"
+               " [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                  "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+               : "memory");
+}
+
 // tcgen05.mma and its commit, issued by the lanes where `on` holds (one of a
 // converged warp).
 __device__ __forceinline__ void mma_ss_if(bool on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
@@ -233,7 +243,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     t.q0 = src[0]; t.rows = src[1]; t.k0 = src[2]; t.nk = src[3]; t.lim = src[4]; t.head = src[5];
   };
   auto next_warp = [&](Walk& w, Tile& t) {
-    if (!wait_warp<false>(BAR(IFULL + w.slot), w.phase, hdr)) return false;
+    if (!wait_short_warp(BAR(IFULL + w.slot), w.phase, hdr)) return false;
     read_item(w, t);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(BAR(IEMPTY + w.slot));
@@ -257,7 +267,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           t = tiles[item % n];
           t.head = item / n;
         }
-        if (!wait_bounded<false>(BAR(IEMPTY + w.slot), w.phase ^ 1u, hdr)) break;
+        if (!wait_short(BAR(IEMPTY + w.slot), w.phase ^ 1u, hdr)) break;
         volatile int* dst = reinterpret_cast<volatile int*>(smem + kOffItems + 32 * w.slot);
         dst[0] = t.q0; dst[1] = t.rows; dst[2] = t.k0; dst[3] = t.nk; dst[4] = t.lim; dst[5] = t.head;
         ptx::mbar_arrive(BAR(IFULL + w.slot));
@@ -271,39 +281,42 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       const uint64_t pol = ptx::policy_evict_normal();
       Walk w;
       uint32_t pos = 0, seq = 0;               // chunks and tiles queued so far
-      uint32_t nq[2] = {0, 0};                 // Q tiles queued so far
+      uint32_t nq0 = 0, nq1 = 0;               // Q tiles queued so far
       bool ok = true;
       // The ring holds eight chunks, so a tile's slots were last used by the
       // third and fourth tiles before it (K 3 + V 2 + K 3, or V 2 + K 3 + V 2
       // and one chunk of a K).
       auto slot_free = [&]() {
-        if (seq >= 4) ok = wait_bounded<false>(BAR(EMPTY + (seq & 3u)), ((seq - 4) >> 2) & 1u, hdr);
-        if (ok && seq >= 3) ok = wait_bounded<false>(BAR(EMPTY + ((seq - 3) & 3u)), ((seq - 3) >> 2) & 1u, hdr);
+        if (seq >= 4) ok = wait_short(BAR(EMPTY + (seq & 3u)), ((seq - 4) >> 2) & 1u, hdr);
+        if (ok && seq >= 3) ok = wait_short(BAR(EMPTY + ((seq - 3) & 3u)), ((seq - 3) >> 2) & 1u, hdr);
         return ok;
       };
       auto chunk = [&](const CUtensorMap* map, int x, int y, int z) {
         ptx::tma_load_3d(sbase + kOffRing + (pos & (kRing - 1)) * kChunk, map, BAR(FULL + (seq & 3u)), x, y, z, pol);
         ++pos;
       };
-      auto query = [&](int t, const Tile& it) {
-        if (!wait_bounded<false>(BAR(QEMPTY + t), (nq[t] & 1u) ^ 1u, hdr)) { ok = false; return; }
+      auto query = [&](int t, uint32_t n, const Tile& it) {
+        ok = wait_short(BAR(QEMPTY + t), (n & 1u) ^ 1u, hdr);
+        if (!ok) return;
         ptx::mbar_arrive_expect_tx(BAR(QFULL + t), kQTile);
         const uint32_t dst = sbase + static_cast<uint32_t>(t) * kQTile;
         const int row = it.q0 + 128 * t;
         ptx::tma_load_3d(dst, &maps.qn, BAR(QFULL + t), 0, it.head, row, pol);
         ptx::tma_load_3d(dst + kChunk, &maps.qn, BAR(QFULL + t), 64, it.head, row, pol);
         ptx::tma_load_3d(dst + 2 * kChunk, &maps.qr, BAR(QFULL + t), 0, it.head, row, pol);
-        ++nq[t];
       };
       while (ok) {
-        if (!wait_bounded<false>(BAR(IFULL + w.slot), w.phase, hdr)) break;
+        if (!wait_short(BAR(IFULL + w.slot), w.phase, hdr)) break;
         Tile it;
         read_item(w, it);
         ptx::mbar_arrive(BAR(IEMPTY + w.slot));
         if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
         if (it.head < 0) break;
         const int n0 = kv_tiles(it, 0, causal), n1 = kv_tiles(it, 1, causal), n = max(n0, n1);
-        if (n0 > 0) query(0, it);
+        if (n0 > 0) {
+          query(0, nq0, it);
+          if (ok) ++nq0;
+        }
         for (int j = 0; j < n && ok; ++j) {
           const int k = it.k0 + j * kKeys;
           if (!slot_free()) break;
@@ -312,7 +325,10 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           chunk(&maps.kn, 64, it.head, k);
           chunk(&maps.kr, 0, 0, k);
           ++seq;
-          if (j == 0 && n1 > 0) query(1, it);
+          if (j == 0 && n1 > 0) {
+            query(1, nq1, it);
+            if (ok) ++nq1;
+          }
           if (!ok || !slot_free()) break;
           ptx::mbar_arrive_expect_tx(BAR(FULL + (seq & 3u)), 2 * kChunk);
           chunk(&maps.v, 0, it.head, k);
@@ -321,8 +337,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         }
       }
       // no copy may land after the CTA has left: wait for the last phase armed on each barrier
-      for (int t = 0; t < 2; ++t)
-        if (nq[t] > 0) wait_drain(BAR(QFULL + t), (nq[t] - 1) & 1u, hdr);
+      if (nq0 > 0) wait_drain(BAR(QFULL), (nq0 - 1) & 1u, hdr);
+      if (nq1 > 0) wait_drain(BAR(QFULL + 1), (nq1 - 1) & 1u, hdr);
       for (uint32_t s = 0; s < kTiles; ++s) {
         const uint32_t n = (seq + kTiles - 1 - s) / kTiles;
         if (n > 0) wait_drain(BAR(FULL + s), (n - 1) & 1u, hdr);
@@ -344,33 +360,33 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     const uint64_t desc_v = ptx::sdesc_sw128(sb + kOffRing, kChunk, 1024);
     constexpr uint64_t kChunkD = kChunk >> 4;                                    // a chunk in descriptor units
     uint32_t kpos = 0, kseq = 0;             // ring position and tile number of the K tile to be scored next
-    uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
+    uint32_t q_phase = 0, p_phase = 0;       // bit t: parity of QFULL[t], PREADY[t]
     bool ok = true, issued = false;
-    // the next (item, K/V tile) step: ni = K/V tiles of each query tile, jn = the step
-    int jn = 0, ni[2] = {0, 0};
+    // the next (item, K/V tile) step: n0, n1 = K/V tiles of each query tile, jn = the step
+    int jn = 0, n0 = 0, n1 = 0;
     // One item at a time, even one without keys: the softmax warps read an item
     // only after this one's last P.V, so waiting for more than the next item
     // before that P.V would wait for ever.
     auto fetch = [&]() -> bool {
       if (!next_warp(w, it)) return false;
-      ni[0] = __shfl_sync(0xffffffffu, kv_tiles(it, 0, causal), 0);
-      ni[1] = __shfl_sync(0xffffffffu, kv_tiles(it, 1, causal), 0);
+      n0 = __shfl_sync(0xffffffffu, kv_tiles(it, 0, causal), 0);
+      n1 = __shfl_sync(0xffffffffu, kv_tiles(it, 1, causal), 0);
       jn = 0;
       return true;
     };
     bool more = fetch();
     // step state: the step whose P.V comes next (its S was issued); jc < 0: none
-    int jc = -1, nc[2] = {0, 0}, nkc = 0;
+    int jc = -1, c0 = 0, c1 = 0, nkc = 0;
     uint32_t vpos = 0, vseq = 0;
     while (ok && (jc >= 0 || more)) {
       bool have_v = false, have_k = false;
-#pragma unroll
+#pragma unroll 1
       for (int t = 0; t < 2; ++t) {
-        if (ok && jc >= 0 && jc < nc[t]) {
-          ok = wait_warp<false>(BAR(PREADY + t), n_p[t] & 1u, hdr);
-          ++n_p[t];
+        if (ok && jc >= 0 && jc < (t ? c1 : c0)) {
+          ok = wait_short_warp(BAR(PREADY + t), (p_phase >> t) & 1u, hdr);
+          p_phase ^= 1u << t;
           if (ok && !have_v) {
-            ok = wait_warp<false>(BAR(FULL + (vseq & 3u)), (vseq >> 2) & 1u, hdr);
+            ok = wait_short_warp(BAR(FULL + (vseq & 3u)), (vseq >> 2) & 1u, hdr);
             have_v = true;
             const int valid = nkc - jc * kKeys;
             if (ok && valid < kKeys) {
@@ -402,16 +418,17 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
               mma_ts_if(lead, d + 64u, a + 8u * k, desc_v + 128u * k, kIdescPVHalf, jc > 0 || k > 0);
             }
           }
-          commit_if(lead && (t == 1 || jc >= nc[1]), BAR(EMPTY + (vseq & 3u)));
+          commit_if(lead && (t == 1 || jc >= c1), BAR(EMPTY + (vseq & 3u)));
           commit_if(lead, BAR(PVDONE + t));
         }
-        if (ok && more && jn < ni[t]) {
+        const int nt = t ? n1 : n0;
+        if (ok && more && jn < nt) {
           if (jn == 0) {
-            ok = wait_warp<false>(BAR(QFULL + t), n_q[t] & 1u, hdr);
-            ++n_q[t];
+            ok = wait_short_warp(BAR(QFULL + t), (q_phase >> t) & 1u, hdr);
+            q_phase ^= 1u << t;
           }
           if (ok && !have_k) {
-            ok = wait_warp<false>(BAR(FULL + (kseq & 3u)), (kseq >> 2) & 1u, hdr);
+            ok = wait_short_warp(BAR(FULL + (kseq & 3u)), (kseq >> 2) & 1u, hdr);
             have_k = true;
           }
           if (!ok) break;
@@ -425,26 +442,26 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
             for (int k = 0; k < 4; ++k)
               mma_ss_if(lead, tm + kSCol + 128u * t, da + 2u * k, db + 2u * k, kIdescS, c > 0 || k > 0);
           }
-          commit_if(lead && (t == 1 || jn >= ni[1]), BAR(EMPTY + (kseq & 3u)));
+          commit_if(lead && (t == 1 || jn >= n1), BAR(EMPTY + (kseq & 3u)));
           commit_if(lead, BAR(SFULL + t));
-          commit_if(lead && jn == ni[t] - 1, BAR(QEMPTY + t));
+          commit_if(lead && jn == nt - 1, BAR(QEMPTY + t));
         }
       }
       if (!ok) break;
       // advance: the step just scored becomes the one whose P.V comes next
-      if (more && max(ni[0], ni[1]) == 0) {
+      if (more && max(n0, n1) == 0) {
         jc = -1;                             // an item without keys has no step
         more = fetch();
       } else if (more) {
         jc = jn;
-        nc[0] = ni[0];
-        nc[1] = ni[1];
+        c0 = n0;
+        c1 = n1;
         nkc = it.nk;
         vpos = kpos + 3;
         vseq = kseq + 1;
         kpos += 5;
         kseq += 2;
-        if (++jn >= max(ni[0], ni[1])) more = fetch();
+        if (++jn >= max(n0, n1)) more = fetch();
       } else {
         jc = -1;
       }
@@ -473,24 +490,29 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       float mc = 0.f;                        // reference maximum * c (0 while nothing was seen)
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
-        if (!wait_warp<false>(BAR(SFULL + t), steps & 1u, hdr)) { ok = false; break; }
+        if (!wait_short_warp(BAR(SFULL + t), steps & 1u, hdr)) { ok = false; break; }
         ptx::tc_fence_after();
         const int valid = vis - j * kKeys;
         const bool full = __all_sync(0xffffffffu, valid >= kKeys);
         float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           uint32_t s[32];
           ptx::tmem_ld32(s_addr + 32u * q, s);
           ptx::tmem_wait_ld();
-          if (full) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-          } else {
+          const int left = full ? 32 : valid - 32 * q;
+          if (left < 32) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (32 * q + e < valid) mx = fmaxf(mx, __uint_as_float(s[e]));
+              if (e >= left) s[e] = 0xFF800000u;   // -inf
           }
+          float m0 = mx, m1 = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            m0 = max3(m0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+            m1 = max3(m1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+          }
+          mx = fmaxf(m0, m1);
         }
         float alpha = 1.f;
         if (m_ref == -INFINITY) {
@@ -505,7 +527,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         }
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
           // O of the tiles so far is complete once the previous P.V is
-          if (!wait_warp<false>(BAR(PVDONE + t), (steps - 1) & 1u, hdr)) { ok = false; break; }
+          if (!wait_short_warp(BAR(PVDONE + t), (steps - 1) & 1u, hdr)) { ok = false; break; }
           ptx::tc_fence_after();
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
@@ -518,29 +540,27 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           }
         }
         float la = 0.f, lb = 0.f;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t s[64], pk[32];
-          ptx::tmem_ld32(s_addr + 64u * q, s);
-          ptx::tmem_ld32(s_addr + 64u * q + 32u, s + 32);
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t s[32], pk[16];
+          ptx::tmem_ld32(s_addr + 32u * q, s);
           ptx::tmem_wait_ld();
+          const int left = full ? 32 : valid - 32 * q;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
+          for (int e = 0; e < 16; ++e) {
             const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
                                         make_float2(c, c), make_float2(-mc, -mc));
             float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-            if (!full) {
-              if (64 * q + 2 * e >= valid) p0 = 0.f;
-              if (64 * q + 2 * e + 1 >= valid) p1 = 0.f;
-            }
+            if (2 * e >= left) p0 = 0.f;
+            if (2 * e + 1 >= left) p1 = 0.f;
             const float2 sum = __fadd2_rn(make_float2(la, lb), make_float2(p0, p1));
             la = sum.x;
             lb = sum.y;
             const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
             pk[e] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          // P of keys 64q.. takes columns whose scores were read above
-          ptx::tmem_st32(s_addr + 32u * q, pk);
+          // P of keys 32q.. takes columns whose scores were read above
+          tmem_st16(s_addr + 16u * q, pk);
         }
         l += la + lb;
         ptx::tmem_wait_st();
@@ -550,7 +570,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       }
       if (!ok) break;
       if (n > 0) {
-        if (!wait_warp<false>(BAR(PVDONE + t), (steps - 1) & 1u, hdr)) { ok = false; break; }
+        if (!wait_short_warp(BAR(PVDONE + t), (steps - 1) & 1u, hdr)) { ok = false; break; }
         ptx::tc_fence_after();
       }
       const bool live = r < it.rows;
