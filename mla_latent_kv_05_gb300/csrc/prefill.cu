@@ -169,24 +169,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 
-// tcgen05.mma and its commit, issued by the lanes where `on` holds (one of a
-// converged warp).
-__device__ __forceinline__ void mma_ss_if(bool on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(static_cast<uint32_t>(on))
-               : "memory");
-}
-__device__ __forceinline__ void mma_ts_if(bool on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-               :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(static_cast<uint32_t>(on))
-               : "memory");
-}
-__device__ __forceinline__ void commit_if(bool on, uint32_t bar) {
-  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-               "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
-               :: "r"(bar), "r"(static_cast<uint32_t>(on)) : "memory");
+// One lane of a converged warp.  The compiler knows that a branch on it is
+// taken by a single thread and keeps what it issues in uniform registers: a
+// commit costs about 2 cycles to issue in such a branch, 46 under lane == 0 and
+// 60 as a predicated instruction, and an MMA's descriptors no moves.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -346,13 +336,12 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     }
   } else if (smem_ok && warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    // The whole warp walks the steps together and one lane issues (a
-    // predicate on the instruction, not a branch), so that descriptors and
-    // addresses stay warp-uniform values: with a one-lane branch around the
-    // issue each MMA took about twice its 64 cycles to get out.
+    // The whole warp walks the steps together, so that positions, descriptors
+    // and addresses stay warp-uniform values, and an elected lane issues.  A
+    // wait costs about 100 cycles even when its phase is complete, so K and V
+    // are waited for before P, while the other tile's MMAs run.
     Walk w;
     Tile it;
-    const bool lead = lane == 0;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t sb = __shfl_sync(0xffffffffu, sbase, 0);
     const uint64_t desc_q = ptx::sdesc_sw128(sb, 16, 1024);                     // + chunks, K-steps
@@ -379,73 +368,74 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     int jc = -1, c0 = 0, c1 = 0, nkc = 0;
     uint32_t vpos = 0, vseq = 0;
     while (ok && (jc >= 0 || more)) {
-      bool have_v = false, have_k = false;
+      const bool pv = jc >= 0;
+      if (pv) {
+        ok = wait_short_warp(BAR(FULL + (vseq & 3u)), (vseq >> 2) & 1u, hdr);
+        const int valid = nkc - jc * kKeys;
+        if (ok && valid < kKeys) {
+          // keys past the sequence's end have P = 0; make their V rows 0 too
+          // (they may be another sequence's, and hold NaN)
 #pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
-        if (ok && jc >= 0 && jc < (t ? c1 : c0)) {
+          for (int c = 0; c < 2; ++c) {
+            uint4* dst = reinterpret_cast<uint4*>(smem + kOffRing + ((vpos + c) & (kRing - 1)) * kChunk);
+            for (int i = valid * 8 + lane; i < kKeys * 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+          }
+          ptx::fence_proxy_async_cta();
+          __syncwarp();
+        }
+      }
+      const bool sc = more && max(n0, n1) > 0;
+      if (ok && sc) ok = wait_short_warp(BAR(FULL + (kseq & 3u)), (kseq >> 2) & 1u, hdr);
+#pragma unroll 1
+      for (int t = 0; t < 2 && ok; ++t) {
+        const bool pv_t = pv && jc < (t ? c1 : c0);
+        const int nt = t ? n1 : n0;
+        const bool sc_t = sc && jn < nt;
+        if (sc_t && jn == 0) {
+          ok = wait_short_warp(BAR(QFULL + t), (q_phase >> t) & 1u, hdr);
+          q_phase ^= 1u << t;
+        }
+        if (ok && pv_t) {
           ok = wait_short_warp(BAR(PREADY + t), (p_phase >> t) & 1u, hdr);
           p_phase ^= 1u << t;
-          if (ok && !have_v) {
-            ok = wait_short_warp(BAR(FULL + (vseq & 3u)), (vseq >> 2) & 1u, hdr);
-            have_v = true;
-            const int valid = nkc - jc * kKeys;
-            if (ok && valid < kKeys) {
-              // keys past the sequence's end have P = 0; make their V rows 0 too
-              // (they may be another sequence's, and hold NaN)
+        }
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t s0 = vpos & (kRing - 1);
+        const uint32_t d = tm + kOCol + 128u * t, a = tm + kSCol + 128u * t;
+        if (elect_one()) {
+          if (pv_t) {
+            const uint64_t db = desc_v + s0 * kChunkD;
+            if (s0 != kRing - 1) {
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                ptx::mma_ts(d, a + 8u * k, db + 128u * k, kIdescPV, (jc > 0 || k > 0) ? 1u : 0u);
+            } else {
+              // the tile's second chunk wrapped to the ring's start: two halves
 #pragma unroll 1
-              for (int c = 0; c < 2; ++c) {
-                uint4* dst = reinterpret_cast<uint4*>(smem + kOffRing + ((vpos + c) & (kRing - 1)) * kChunk);
-                for (int i = valid * 8 + lane; i < kKeys * 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+              for (int k = 0; k < kKeys / 16; ++k) {
+                ptx::mma_ts(d, a + 8u * k, db + 128u * k, kIdescPVHalf, (jc > 0 || k > 0) ? 1u : 0u);
+                ptx::mma_ts(d + 64u, a + 8u * k, desc_v + 128u * k, kIdescPVHalf, (jc > 0 || k > 0) ? 1u : 0u);
               }
-              ptx::fence_proxy_async_cta();
-              __syncwarp();
             }
+            if (t == 1 || jc >= c1) ptx::mma_commit(BAR(EMPTY + (vseq & 3u)));
+            ptx::mma_commit(BAR(PVDONE + t));
           }
-          if (!ok) break;
-          ptx::tc_fence_after();
-          const uint32_t s0 = vpos & (kRing - 1);
-          const uint32_t d = tm + kOCol + 128u * t, a = tm + kSCol + 128u * t;
-          const uint64_t db = desc_v + s0 * kChunkD;
-          if (s0 != kRing - 1) {
+          if (sc_t) {
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts_if(lead, d, a + 8u * k, db + 128u * k, kIdescPV, jc > 0 || k > 0);
-          } else {
-            // the tile's second chunk wrapped to the ring's start: two halves
-#pragma unroll 1
-            for (int k = 0; k < kKeys / 16; ++k) {
-              mma_ts_if(lead, d, a + 8u * k, db + 128u * k, kIdescPVHalf, jc > 0 || k > 0);
-              mma_ts_if(lead, d + 64u, a + 8u * k, desc_v + 128u * k, kIdescPVHalf, jc > 0 || k > 0);
+            for (int c = 0; c < 3; ++c) {
+              const uint64_t da = desc_q + (3u * t + c) * kChunkD;
+              const uint64_t db = desc_k + ((kpos + c) & (kRing - 1)) * kChunkD;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) ptx::mma_ss(a, da + 2u * k, db + 2u * k, kIdescS, (c > 0 || k > 0) ? 1u : 0u);
             }
+            ptx::mma_commit(BAR(SFULL + t));
+            if (t == 1 || jn >= n1) ptx::mma_commit(BAR(EMPTY + (kseq & 3u)));
+            if (jn == nt - 1) ptx::mma_commit(BAR(QEMPTY + t));
           }
-          commit_if(lead && (t == 1 || jc >= c1), BAR(EMPTY + (vseq & 3u)));
-          commit_if(lead, BAR(PVDONE + t));
         }
-        const int nt = t ? n1 : n0;
-        if (ok && more && jn < nt) {
-          if (jn == 0) {
-            ok = wait_short_warp(BAR(QFULL + t), (q_phase >> t) & 1u, hdr);
-            q_phase ^= 1u << t;
-          }
-          if (ok && !have_k) {
-            ok = wait_short_warp(BAR(FULL + (kseq & 3u)), (kseq >> 2) & 1u, hdr);
-            have_k = true;
-          }
-          if (!ok) break;
-          ptx::tc_fence_after();
-          issued = true;
-#pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            const uint64_t da = desc_q + (3u * t + c) * kChunkD;
-            const uint64_t db = desc_k + ((kpos + c) & (kRing - 1)) * kChunkD;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ss_if(lead, tm + kSCol + 128u * t, da + 2u * k, db + 2u * k, kIdescS, c > 0 || k > 0);
-          }
-          commit_if(lead && (t == 1 || jn >= n1), BAR(EMPTY + (kseq & 3u)));
-          commit_if(lead, BAR(SFULL + t));
-          commit_if(lead && jn == nt - 1, BAR(QEMPTY + t));
-        }
+        __syncwarp();
+        issued |= sc_t;
       }
       if (!ok) break;
       // advance: the step just scored becomes the one whose P.V comes next
@@ -467,7 +457,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       }
     }
     // every MMA this thread issued completes before the CTA may leave
-    if (issued && lane == 0) {
+    if (issued && elect_one()) {   // the lane that issued them
       ptx::mma_commit(BAR(DRAIN));
       wait_drain(BAR(DRAIN), 0u, hdr);
     }
