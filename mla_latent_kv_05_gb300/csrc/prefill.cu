@@ -54,7 +54,7 @@ constexpr int kItemSlots = 2;
 constexpr int kTiles = 4;                          // K or V tiles in flight at most (barriers)
 enum Bar {
   QFULL = 0, QEMPTY = QFULL + 2, FULL = QEMPTY + 2, EMPTY = FULL + kTiles, SFULL = EMPTY + kTiles, PREADY = SFULL + 2,
-  PVDONE = PREADY + 2, IFULL = PVDONE + 2, IEMPTY = IFULL + kItemSlots, DRAIN = IEMPTY + kItemSlots, NBAR
+  PVDONE = PREADY + 4, IFULL = PVDONE + 2, IEMPTY = IFULL + kItemSlots, DRAIN = IEMPTY + kItemSlots, NBAR
 };
 constexpr uint32_t kOffTmem = kOffBar + 8 * NBAR;
 constexpr uint32_t kOffItems = (kOffTmem + 16 + 15) & ~15u;     // kItemSlots x 32 bytes
@@ -179,6 +179,9 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
+
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -188,6 +191,40 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// Maximum of a row's 128 scores.
+__device__ __forceinline__ float row_max(const uint32_t* s) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < 128; e += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = max3(m[i], __uint_as_float(s[e + 2 * i]), __uint_as_float(s[e + 2 * i + 1]));
+  return max3(fmaxf(m[0], m[1]), m[2], m[3]);
+}
+
+// P = exp2(s c - mc) of 64 scores, as bf16 into 32 columns of tensor memory;
+// the unrounded sum is added to `sum`.
+__device__ __forceinline__ void p_half(const uint32_t* s, float c, float mc, float& sum, uint32_t addr) {
+  float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint32_t* v = s + 32 * q + 2 * e;
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), make_float2(c, c),
+                                  make_float2(-mc, -mc));
+      const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+      if (e & 1) acc1 = __fadd2_rn(acc1, p);
+      else acc0 = __fadd2_rn(acc0, p);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
+      pk[e] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    tmem_st16(addr + 16u * q, pk);
+  }
+  acc0 = __fadd2_rn(acc0, acc1);
+  sum += acc0.x + acc0.y;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -202,7 +239,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       ptx::mbar_init(BAR(QFULL + t), 1);
       ptx::mbar_init(BAR(QEMPTY + t), 1);
       ptx::mbar_init(BAR(SFULL + t), 1);
-      ptx::mbar_init(BAR(PREADY + t), 128);
+      ptx::mbar_init(BAR(PREADY + t), 128);         // P of the tile's first 64 keys
+      ptx::mbar_init(BAR(PREADY + 2 + t), 128);     // and of its last 64
       ptx::mbar_init(BAR(PVDONE + t), 1);
     }
     for (int s = 0; s < kTiles; ++s) { ptx::mbar_init(BAR(FULL + s), 1); ptx::mbar_init(BAR(EMPTY + s), 1); }
@@ -241,8 +279,12 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     return t.head >= 0;
   };
 
+  // The softmax warps hold a row's 128 scores in registers: the registers
+  // (168 a thread at launch) are split 72 to warps 0..3, 216 to warps 4..11
+  // (4 * 72 + 8 * 216 = 12 * 168), each role's branch setting its own.
   if (smem_ok && warp == 2) {
     // ------------------------------------------------------------ items
+    reg_dec();
     if (lane == 0) {
       const Tile* tiles = reinterpret_cast<const Tile*>(p.ws + L.tiles);
       const int n = *reinterpret_cast<const volatile int*>(&hdr->n_tiles);
@@ -267,6 +309,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     }
   } else if (smem_ok && warp == 0) {
     // ------------------------------------------------------------ TMA producer
+    reg_dec();
     if (lane == 0) {
       const uint64_t pol = ptx::policy_evict_normal();
       Walk w;
@@ -336,6 +379,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     }
   } else if (smem_ok && warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    reg_dec();
     // The whole warp walks the steps together, so that positions, descriptors
     // and addresses stay warp-uniform values, and an elected lane issues.  A
     // wait costs about 100 cycles even when its phase is complete, so K and V
@@ -395,33 +439,44 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           ok = wait_short_warp(BAR(QFULL + t), (q_phase >> t) & 1u, hdr);
           q_phase ^= 1u << t;
         }
+        const uint32_t d = tm + kOCol + 128u * t, a = tm + kSCol + 128u * t;
         if (ok && pv_t) {
-          ok = wait_short_warp(BAR(PREADY + t), (p_phase >> t) & 1u, hdr);
+          const uint32_t s0 = vpos & (kRing - 1);
+          const uint64_t db = desc_v + s0 * kChunkD;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            ok = wait_short_warp(BAR(PREADY + 2 * half + t), (p_phase >> t) & 1u, hdr);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t ah = a + 32u * half;
+            const uint64_t dh = db + 512u * half;
+            if (elect_one()) {
+              if (s0 != kRing - 1) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  ptx::mma_ts(d, ah + 8u * k, dh + 128u * k, kIdescPV, (jc > 0 || half > 0 || k > 0) ? 1u : 0u);
+              } else {
+                // the tile's second chunk wrapped to the ring's start: two halves
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t acc = (jc > 0 || half > 0 || k > 0) ? 1u : 0u;
+                  ptx::mma_ts(d, ah + 8u * k, dh + 128u * k, kIdescPVHalf, acc);
+                  ptx::mma_ts(d + 64u, ah + 8u * k, desc_v + 512u * half + 128u * k, kIdescPVHalf, acc);
+                }
+              }
+              if (half == 1) {
+                if (t == 1 || jc >= c1) ptx::mma_commit(BAR(EMPTY + (vseq & 3u)));
+                ptx::mma_commit(BAR(PVDONE + t));
+              }
+            }
+            __syncwarp();
+          }
           p_phase ^= 1u << t;
         }
         if (!ok) break;
-        ptx::tc_fence_after();
-        const uint32_t s0 = vpos & (kRing - 1);
-        const uint32_t d = tm + kOCol + 128u * t, a = tm + kSCol + 128u * t;
-        if (elect_one()) {
-          if (pv_t) {
-            const uint64_t db = desc_v + s0 * kChunkD;
-            if (s0 != kRing - 1) {
-#pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
-                ptx::mma_ts(d, a + 8u * k, db + 128u * k, kIdescPV, (jc > 0 || k > 0) ? 1u : 0u);
-            } else {
-              // the tile's second chunk wrapped to the ring's start: two halves
-#pragma unroll 1
-              for (int k = 0; k < kKeys / 16; ++k) {
-                ptx::mma_ts(d, a + 8u * k, db + 128u * k, kIdescPVHalf, (jc > 0 || k > 0) ? 1u : 0u);
-                ptx::mma_ts(d + 64u, a + 8u * k, desc_v + 128u * k, kIdescPVHalf, (jc > 0 || k > 0) ? 1u : 0u);
-              }
-            }
-            if (t == 1 || jc >= c1) ptx::mma_commit(BAR(EMPTY + (vseq & 3u)));
-            ptx::mma_commit(BAR(PVDONE + t));
-          }
-          if (sc_t) {
+        if (sc_t) {
+          ptx::tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
               const uint64_t da = desc_q + (3u * t + c) * kChunkD;
@@ -464,6 +519,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     __syncwarp();
   } else if (smem_ok && warp >= 4) {
     // ------------------------------------------------------------ softmax and epilogue (thread = query row)
+    reg_inc();
     const int t = (warp - 4) >> 2;
     const int r = 128 * t + (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -482,80 +538,61 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       for (int j = 0; j < n; ++j) {
         if (!wait_short_warp(BAR(SFULL + t), steps & 1u, hdr)) { ok = false; break; }
         ptx::tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ptx::tmem_ld32(s_addr + 32u * q, s + 32 * q);
+        ptx::tmem_wait_ld();
         const int valid = vis - j * kKeys;
-        const bool full = __all_sync(0xffffffffu, valid >= kKeys);
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t s[32];
-          ptx::tmem_ld32(s_addr + 32u * q, s);
-          ptx::tmem_wait_ld();
-          const int left = full ? 32 : valid - 32 * q;
-          if (left < 32) {
+        if (!__all_sync(0xffffffffu, valid >= kKeys)) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e >= left) s[e] = 0xFF800000u;   // -inf
-          }
-          float m0 = mx, m1 = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            m0 = max3(m0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-            m1 = max3(m1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
-          }
-          mx = fmaxf(m0, m1);
+          for (int e = 0; e < 128; ++e)
+            if (e >= valid) s[e] = 0xFF800000u;   // -inf
         }
-        float alpha = 1.f;
-        if (m_ref == -INFINITY) {
-          m_ref = mx;                        // nothing accumulated so far: l = 0, O = 0
-          mc = mx == -INFINITY ? 0.f : mx * c;
-        } else if ((mx - m_ref) * c > kLazy) {
-          m_ref = mx;
-          const float nmc = mx * c;
-          alpha = fast_exp2(mc - nmc);
-          mc = nmc;
-          l *= alpha;
+        if (j == 0) {
+          m_ref = row_max(s);
+          mc = m_ref == -INFINITY ? 0.f : m_ref * c;
         }
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+        // The first half's P is computed against the reference so far while
+        // the row's maximum is still being found; if that then exceeds the
+        // reference by too much for any row, O is rescaled and the half redone.
+        float ls, mx;
+        while (true) {
+          ls = 0.f;
+          p_half(s, c, mc, ls, s_addr);
+          if (j == 0) break;
+          mx = row_max(s);
+          const bool up = m_ref == -INFINITY ? mx != -INFINITY : (mx - m_ref) * c > kLazy;
+          if (!__any_sync(0xffffffffu, up)) break;
+          float alpha = 1.f;
+          if (up) {
+            const float nmc = mx * c;
+            alpha = m_ref == -INFINITY ? 1.f : fast_exp2(mc - nmc);   // -inf: l = 0 and O = 0 so far
+            m_ref = mx;
+            mc = nmc;
+            l *= alpha;
+          }
           // O of the tiles so far is complete once the previous P.V is
           if (!wait_short_warp(BAR(PVDONE + t), (steps - 1) & 1u, hdr)) { ok = false; break; }
           ptx::tc_fence_after();
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t o[32];
-            ptx::tmem_ld32(o_addr + 32u * q, o);
+          for (int q = 0; q < 8; ++q) {
+            uint32_t o[16];
+            ptx::tmem_ld16(o_addr + 16u * q, o);
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            ptx::tmem_st32(o_addr + 32u * q, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(o_addr + 16u * q, o);
           }
         }
-        float la = 0.f, lb = 0.f;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t s[32], pk[16];
-          ptx::tmem_ld32(s_addr + 32u * q, s);
-          ptx::tmem_wait_ld();
-          const int left = full ? 32 : valid - 32 * q;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
-                                        make_float2(c, c), make_float2(-mc, -mc));
-            float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-            if (2 * e >= left) p0 = 0.f;
-            if (2 * e + 1 >= left) p1 = 0.f;
-            const float2 sum = __fadd2_rn(make_float2(la, lb), make_float2(p0, p1));
-            la = sum.x;
-            lb = sum.y;
-            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-            pk[e] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-          // P of keys 32q.. takes columns whose scores were read above
-          tmem_st16(s_addr + 16u * q, pk);
-        }
-        l += la + lb;
+        if (!ok) break;
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         ptx::mbar_arrive(BAR(PREADY + t));
+        p_half(s + 64, c, mc, ls, s_addr + 32u);
+        l += ls;
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(BAR(PREADY + 2 + t));
         ++steps;
       }
       if (!ok) break;
@@ -589,6 +626,9 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       if (live) p.lse[orow] = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
       ptx::tc_fence_before();
     }
+  }
+  else if (smem_ok) {
+    reg_dec();   // warp 3 has no role
   }
   // ------------------------------------------------------------ teardown
   ptx::tc_fence_before();
