@@ -22,11 +22,13 @@
 //   shared memory: Q0 | Q1 (48 KiB each), and a ring of eight 16-KiB chunks
 //       (128 keys x 64 values), three per K tile and two per V tile, so K
 //       and V are prefetched chunk by chunk as chunks are released;
-//   warp 0 issues the TMA loads, warp 1 the MMAs, warp 2 fetches the items,
-//   warps 4..7 and 8..11 are the softmax of tile 0 and tile 1 (thread = row).
-// The MMA warp alternates PV0(j) S0(j+1) PV1(j) S1(j+1), so while one tile's
-// softmax runs the tensor cores work on the other's.  S of the next item is
-// issued before the last PV of this one is waited for, so items overlap.
+//   warp 0 issues the TMA loads, warps 1 and 3 the MMAs of tile 0 and tile 1,
+//   warp 2 fetches the items, warps 4..7 and 8..11 are the softmax of tile 0
+//   and tile 1 (thread = row).
+// An MMA warp issues P.V of step j and then S of step j + 1 (which overwrites
+// that P: the tensor pipe runs in order), so while one tile's softmax runs the
+// tensor cores work on the other's.  The step after an item's last is the next
+// item's first, so items overlap.
 //
 // The maximum is lazy: a row's reference moves only when a tile's maximum
 // exceeds it by more than 2^kLazy, so O is rescaled rarely; its softmax warps
@@ -43,7 +45,7 @@ namespace mla {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kKeys = 128;                         // keys per K/V tile
 constexpr uint32_t kChunk = 128u * 128u;           // 16 KiB: 128 rows x 64 values
 constexpr uint32_t kQTile = 3 * kChunk;            // 128 query rows x 192
@@ -54,11 +56,13 @@ constexpr int kItemSlots = 2;
 constexpr int kTiles = 4;                          // K or V tiles in flight at most (barriers)
 enum Bar {
   QFULL = 0, QEMPTY = QFULL + 2, FULL = QEMPTY + 2, EMPTY = FULL + kTiles, SFULL = EMPTY + kTiles, PREADY = SFULL + 2,
-  PVDONE = PREADY + 4, IFULL = PVDONE + 2, IEMPTY = IFULL + kItemSlots, DRAIN = IEMPTY + kItemSlots, NBAR
+  PVDONE = PREADY + 2, IFULL = PVDONE + 2, IEMPTY = IFULL + kItemSlots, DRAIN = IEMPTY + kItemSlots,
+  NBAR = DRAIN + 2
 };
 constexpr uint32_t kOffTmem = kOffBar + 8 * NBAR;
 constexpr uint32_t kOffItems = (kOffTmem + 16 + 15) & ~15u;     // kItemSlots x 32 bytes
-constexpr uint32_t kSmem = kOffItems + 32 * kItemSlots;
+constexpr uint32_t kOffPair = kOffItems + 32 * kItemSlots;      // fp32 [2 tiles][2 halves][128 rows]
+constexpr uint32_t kSmem = kOffPair + 2 * 2 * 128 * 4;
 static_assert(kSmem <= 232448, "shared memory budget");
 
 constexpr uint32_t kSCol = 0, kOCol = 256;         // + 128 t
@@ -179,8 +183,8 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
-__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 104;"); }
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
@@ -193,14 +197,25 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Maximum of a row's 128 scores.
+// Maximum of 64 scores.
 __device__ __forceinline__ float row_max(const uint32_t* s) {
-  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  float m[8];
 #pragma unroll
-  for (int e = 0; e < 128; e += 8)
+  for (int i = 0; i < 8; ++i) m[i] = fmaxf(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = max3(m[i], __uint_as_float(s[e + 2 * i]), __uint_as_float(s[e + 2 * i + 1]));
-  return max3(fmaxf(m[0], m[1]), m[2], m[3]);
+  for (int e = 16; e < 64; e += 16)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = max3(m[i], __uint_as_float(s[e + 2 * i]), __uint_as_float(s[e + 2 * i + 1]));
+  return fmaxf(max3(max3(m[0], m[1], m[2]), m[3], m[4]), max3(m[5], m[6], m[7]));
+}
+
+// Named barrier of two warps, and the same with an OR over their 64 threads.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" :: "r"(id) : "memory"); }
+__device__ __forceinline__ bool any_of_pair(int id, bool v) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %2, 0;\n\tbar.red.or.pred p, %1, 64, q;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(r) : "r"(id), "r"(static_cast<uint32_t>(v)) : "memory");
+  return r != 0;
 }
 
 // P = exp2(s c - mc) of 64 scores, as bf16 into 32 columns of tensor memory;
@@ -239,16 +254,16 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       ptx::mbar_init(BAR(QFULL + t), 1);
       ptx::mbar_init(BAR(QEMPTY + t), 1);
       ptx::mbar_init(BAR(SFULL + t), 1);
-      ptx::mbar_init(BAR(PREADY + t), 128);         // P of the tile's first 64 keys
-      ptx::mbar_init(BAR(PREADY + 2 + t), 128);     // and of its last 64
+      ptx::mbar_init(BAR(PREADY + t), 8);           // one arrival a softmax warp
       ptx::mbar_init(BAR(PVDONE + t), 1);
     }
-    for (int s = 0; s < kTiles; ++s) { ptx::mbar_init(BAR(FULL + s), 1); ptx::mbar_init(BAR(EMPTY + s), 1); }
+    for (int s = 0; s < kTiles; ++s) { ptx::mbar_init(BAR(FULL + s), 1); ptx::mbar_init(BAR(EMPTY + s), 2); }
     for (int s = 0; s < kItemSlots; ++s) {
       ptx::mbar_init(BAR(IFULL + s), 1);
-      ptx::mbar_init(BAR(IEMPTY + s), 10);     // producer, MMA warp, eight softmax warps
+      ptx::mbar_init(BAR(IEMPTY + s), 19);     // producer, two MMA warps, sixteen softmax warps
     }
     ptx::mbar_init(BAR(DRAIN), 1);
+    ptx::mbar_init(BAR(DRAIN + 1), 1);
     ptx::fence_barrier_init();
   }
   if (warp == 2) {
@@ -271,7 +286,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     t.q0 = src[0]; t.rows = src[1]; t.k0 = src[2]; t.nk = src[3]; t.lim = src[4]; t.head = src[5];
   };
   auto next_warp = [&](Walk& w, Tile& t) {
-    if (!wait_short_warp(BAR(IFULL + w.slot), w.phase, hdr)) return false;
+    if (!wait_short_warp(BAR(IFULL + w.slot), w.phase, hdr)) { t.head = -1; t.nk = 0; return false; }
     read_item(w, t);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(BAR(IEMPTY + w.slot));
@@ -279,9 +294,9 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     return t.head >= 0;
   };
 
-  // The softmax warps hold a row's 128 scores in registers: the registers
-  // (168 a thread at launch) are split 72 to warps 0..3, 216 to warps 4..11
-  // (4 * 72 + 8 * 216 = 12 * 168), each role's branch setting its own.
+  // Registers (96 a thread at launch) are split 64 to warps 0..3, 104 to the
+  // softmax warps (4 * 64 + 16 * 104 = 20 * 96), each role's branch setting
+  // its own.
   if (smem_ok && warp == 2) {
     // ------------------------------------------------------------ items
     reg_dec();
@@ -377,48 +392,56 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         if (n > 0) wait_drain(BAR(FULL + s), (n - 1) & 1u, hdr);
       }
     }
-  } else if (smem_ok && warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (smem_ok && warp < 4) {
+    // ------------------------------------------------------------ MMA issuers: warp 1 tile 0, warp 3 tile 1
+    // The warp walks the steps together and an elected lane issues.  A wait
+    // costs about 100 cycles even when its phase is complete, and the tensor
+    // pipe queues only a few MMAs, so each query tile has a warp of its own:
+    // one's waits pass while the other's MMAs run.  K and V are waited for
+    // before P.  Everything that steers the loop comes through a shuffle or a
+    // vote, so positions and descriptors stay warp-uniform.  On a step that
+    // its tile does not take part in, a warp releases K and V at once.
     reg_dec();
-    // The whole warp walks the steps together, so that positions, descriptors
-    // and addresses stay warp-uniform values, and an elected lane issues.  A
-    // wait costs about 100 cycles even when its phase is complete, so K and V
-    // are waited for before P, while the other tile's MMAs run.
+    const int t = warp >> 1;
     Walk w;
     Tile it;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t sb = __shfl_sync(0xffffffffu, sbase, 0);
-    const uint64_t desc_q = ptx::sdesc_sw128(sb, 16, 1024);                     // + chunks, K-steps
+    const uint32_t d = tm + kOCol + 128u * t, a = tm + kSCol + 128u * t;
+    const uint64_t desc_q = ptx::sdesc_sw128(sb + static_cast<uint32_t>(t) * kQTile, 16, 1024);   // + chunks, K-steps
     const uint64_t desc_k = ptx::sdesc_sw128(sb + kOffRing, 16, 1024);
     const uint64_t desc_v = ptx::sdesc_sw128(sb + kOffRing, kChunk, 1024);
     constexpr uint64_t kChunkD = kChunk >> 4;                                    // a chunk in descriptor units
     uint32_t kpos = 0, kseq = 0;             // ring position and tile number of the K tile to be scored next
-    uint32_t q_phase = 0, p_phase = 0;       // bit t: parity of QFULL[t], PREADY[t]
+    uint32_t q_phase = 0, p_phase = 0;
     bool ok = true, issued = false;
-    // the next (item, K/V tile) step: n0, n1 = K/V tiles of each query tile, jn = the step
-    int jn = 0, n0 = 0, n1 = 0;
+    // the next (item, K/V tile) step jn: the item's steps, this tile's share of them, the sequence's keys
+    int jn = 0, n_all = 0, n_mine = 0, nkn = 0;
     // One item at a time, even one without keys: the softmax warps read an item
     // only after this one's last P.V, so waiting for more than the next item
     // before that P.V would wait for ever.
     auto fetch = [&]() -> bool {
-      if (!next_warp(w, it)) return false;
-      n0 = __shfl_sync(0xffffffffu, kv_tiles(it, 0, causal), 0);
-      n1 = __shfl_sync(0xffffffffu, kv_tiles(it, 1, causal), 0);
+      const bool have = next_warp(w, it);
+      const int n0 = have ? kv_tiles(it, 0, causal) : 0, n1 = have ? kv_tiles(it, 1, causal) : 0;
+      n_all = __shfl_sync(0xffffffffu, max(n0, n1), 0);
+      n_mine = __shfl_sync(0xffffffffu, t ? n1 : n0, 0);
+      nkn = __shfl_sync(0xffffffffu, it.nk, 0);
       jn = 0;
-      return true;
+      return __shfl_sync(0xffffffffu, have ? 1 : 0, 0) != 0;
     };
     bool more = fetch();
     // step state: the step whose P.V comes next (its S was issued); jc < 0: none
-    int jc = -1, c0 = 0, c1 = 0, nkc = 0;
+    int jc = -1, n_cur = 0, nkc = 0;
     uint32_t vpos = 0, vseq = 0;
     while (ok && (jc >= 0 || more)) {
-      const bool pv = jc >= 0;
-      if (pv) {
+      const bool pv = jc >= 0 && jc < n_cur;
+      if (jc >= 0) {
         ok = wait_short_warp(BAR(FULL + (vseq & 3u)), (vseq >> 2) & 1u, hdr);
         const int valid = nkc - jc * kKeys;
-        if (ok && valid < kKeys) {
+        if (ok && pv && valid < kKeys) {
           // keys past the sequence's end have P = 0; make their V rows 0 too
-          // (they may be another sequence's, and hold NaN)
+          // (they may be another sequence's, and hold NaN); both tiles' warps
+          // write the same zeros before their own MMAs
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             uint4* dst = reinterpret_cast<uint4*>(smem + kOffRing + ((vpos + c) & (kRing - 1)) * kChunk);
@@ -427,184 +450,179 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           ptx::fence_proxy_async_cta();
           __syncwarp();
         }
+        if (ok && !pv && elect_one()) ptx::mbar_arrive(BAR(EMPTY + (vseq & 3u)));
       }
-      const bool sc = more && max(n0, n1) > 0;
-      if (ok && sc) ok = wait_short_warp(BAR(FULL + (kseq & 3u)), (kseq >> 2) & 1u, hdr);
-#pragma unroll 1
-      for (int t = 0; t < 2 && ok; ++t) {
-        const bool pv_t = pv && jc < (t ? c1 : c0);
-        const int nt = t ? n1 : n0;
-        const bool sc_t = sc && jn < nt;
-        if (sc_t && jn == 0) {
-          ok = wait_short_warp(BAR(QFULL + t), (q_phase >> t) & 1u, hdr);
-          q_phase ^= 1u << t;
-        }
-        const uint32_t d = tm + kOCol + 128u * t, a = tm + kSCol + 128u * t;
-        if (ok && pv_t) {
-          const uint32_t s0 = vpos & (kRing - 1);
-          const uint64_t db = desc_v + s0 * kChunkD;
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            ok = wait_short_warp(BAR(PREADY + 2 * half + t), (p_phase >> t) & 1u, hdr);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            const uint32_t ah = a + 32u * half;
-            const uint64_t dh = db + 512u * half;
-            if (elect_one()) {
-              if (s0 != kRing - 1) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  ptx::mma_ts(d, ah + 8u * k, dh + 128u * k, kIdescPV, (jc > 0 || half > 0 || k > 0) ? 1u : 0u);
-              } else {
-                // the tile's second chunk wrapped to the ring's start: two halves
-#pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t acc = (jc > 0 || half > 0 || k > 0) ? 1u : 0u;
-                  ptx::mma_ts(d, ah + 8u * k, dh + 128u * k, kIdescPVHalf, acc);
-                  ptx::mma_ts(d + 64u, ah + 8u * k, desc_v + 512u * half + 128u * k, kIdescPVHalf, acc);
-                }
-              }
-              if (half == 1) {
-                if (t == 1 || jc >= c1) ptx::mma_commit(BAR(EMPTY + (vseq & 3u)));
-                ptx::mma_commit(BAR(PVDONE + t));
-              }
-            }
-            __syncwarp();
-          }
-          p_phase ^= 1u << t;
-        }
-        if (!ok) break;
-        if (sc_t) {
-          ptx::tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int c = 0; c < 3; ++c) {
-              const uint64_t da = desc_q + (3u * t + c) * kChunkD;
-              const uint64_t db = desc_k + ((kpos + c) & (kRing - 1)) * kChunkD;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) ptx::mma_ss(a, da + 2u * k, db + 2u * k, kIdescS, (c > 0 || k > 0) ? 1u : 0u);
-            }
-            ptx::mma_commit(BAR(SFULL + t));
-            if (t == 1 || jn >= n1) ptx::mma_commit(BAR(EMPTY + (kseq & 3u)));
-            if (jn == nt - 1) ptx::mma_commit(BAR(QEMPTY + t));
-          }
-        }
-        __syncwarp();
-        issued |= sc_t;
+      const bool step = more && n_all > 0, sc = step && jn < n_mine;
+      if (ok && step) {
+        ok = wait_short_warp(BAR(FULL + (kseq & 3u)), (kseq >> 2) & 1u, hdr);
+        if (ok && !sc && elect_one()) ptx::mbar_arrive(BAR(EMPTY + (kseq & 3u)));
+      }
+      if (ok && sc && jn == 0) {
+        ok = wait_short_warp(BAR(QFULL + t), q_phase, hdr);
+        q_phase ^= 1u;
+      }
+      if (ok && pv) {
+        ok = wait_short_warp(BAR(PREADY + t), p_phase, hdr);
+        p_phase ^= 1u;
       }
       if (!ok) break;
+      ptx::tc_fence_after();
+      if (pv) {
+        const uint32_t s0 = vpos & (kRing - 1);
+        const uint64_t db = desc_v + s0 * kChunkD;
+        if (elect_one()) {
+          if (s0 != kRing - 1) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              ptx::mma_ts(d, a + 64u * (k >> 2) + 8u * (k & 3), db + 128u * k, kIdescPV, (jc > 0 || k > 0) ? 1u : 0u);
+          } else {
+            // the tile's second chunk wrapped to the ring's start: two halves
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t acc = (jc > 0 || k > 0) ? 1u : 0u, ak = a + 64u * (k >> 2) + 8u * (k & 3);
+              ptx::mma_ts(d, ak, db + 128u * k, kIdescPVHalf, acc);
+              ptx::mma_ts(d + 64u, ak, desc_v + 128u * k, kIdescPVHalf, acc);
+            }
+          }
+          ptx::mma_commit(BAR(EMPTY + (vseq & 3u)));
+          ptx::mma_commit(BAR(PVDONE + t));
+        }
+        __syncwarp();
+      }
+      if (sc) {
+        if (elect_one()) {
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            const uint64_t da = desc_q + c * kChunkD;
+            const uint64_t db = desc_k + ((kpos + c) & (kRing - 1)) * kChunkD;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ptx::mma_ss(a, da + 2u * k, db + 2u * k, kIdescS, (c > 0 || k > 0) ? 1u : 0u);
+          }
+          ptx::mma_commit(BAR(SFULL + t));
+          ptx::mma_commit(BAR(EMPTY + (kseq & 3u)));
+          if (jn == n_mine - 1) ptx::mma_commit(BAR(QEMPTY + t));
+        }
+        __syncwarp();
+        issued = true;
+      }
       // advance: the step just scored becomes the one whose P.V comes next
-      if (more && max(n0, n1) == 0) {
-        jc = -1;                             // an item without keys has no step
-        more = fetch();
-      } else if (more) {
+      jc = -1;
+      if (step) {
         jc = jn;
-        c0 = n0;
-        c1 = n1;
-        nkc = it.nk;
+        n_cur = n_mine;
+        nkc = nkn;
         vpos = kpos + 3;
         vseq = kseq + 1;
         kpos += 5;
         kseq += 2;
-        if (++jn >= max(n0, n1)) more = fetch();
-      } else {
-        jc = -1;
+        ++jn;
       }
+      if (more && jn >= n_all) more = fetch();   // (an item without keys has no step)
     }
-    // every MMA this thread issued completes before the CTA may leave
+    // every MMA this warp issued completes before the CTA may leave
     if (issued && elect_one()) {   // the lane that issued them
-      ptx::mma_commit(BAR(DRAIN));
-      wait_drain(BAR(DRAIN), 0u, hdr);
+      ptx::mma_commit(BAR(DRAIN + t));
+      wait_drain(BAR(DRAIN + t), 0u, hdr);
     }
     __syncwarp();
   } else if (smem_ok && warp >= 4) {
-    // ------------------------------------------------------------ softmax and epilogue (thread = query row)
+    // ------------------------------------------------------------ softmax and epilogue
+    // Eight warps a tile: two threads share a row, each with 64 of a tile's
+    // keys (and 64 of the output's columns).  Their warps meet at a named
+    // barrier once a tile, which also tells whether any row's maximum passed
+    // its reference by too much; only then (and on an item's first tile) do
+    // they exchange maxima, so both always hold the same reference.
     reg_inc();
-    const int t = (warp - 4) >> 2;
-    const int r = 128 * t + (warp & 3) * 32 + lane;
+    const int t = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1;
+    const int rt = (warp & 3) * 32 + lane;                 // row of the tile
+    const int r = 128 * t + rt;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + lane_base + kSCol + 128u * t, o_addr = tmem + lane_base + kOCol + 128u * t;
+    // S of keys 64 hf.. is in columns 64 hf.. of the tile's S; their P replaces its first 32 columns
+    const uint32_t s_addr = tmem + lane_base + kSCol + 128u * t + 64u * hf;
+    const uint32_t o_addr = tmem + lane_base + kOCol + 128u * t + 64u * hf;
+    const int pair = 1 + 4 * t + (warp & 3);               // named barrier of the two warps that share rows
+    volatile float* own = reinterpret_cast<volatile float*>(smem + kOffPair) + (2 * t + hf) * 128 + rt;
+    const volatile float* other = reinterpret_cast<const volatile float*>(smem + kOffPair) + (2 * t + (hf ^ 1)) * 128 + rt;
     const float c = p.scale_log2;
     Walk w;
     Tile it;
     uint32_t steps = 0;                      // tiles turned into P so far (phase of SFULL, PVDONE)
     bool ok = true;
-    while (ok && next_warp(w, it)) {
+    // Both warps of a pair leave at the same place: what one of them knows alone
+    // (a wait that gave up) takes effect only once the other has heard of it.
+    while (true) {
+      const bool have = next_warp(w, it);
+      if (any_of_pair(pair, !have)) break;
       if (it.rows <= 128 * t) continue;
       const int n = kv_tiles(it, t, causal);
-      const int vis = visible(it, r, causal);
+      const int vis = visible(it, r, causal) - 64 * hf;    // of this thread's keys
       float mc = 0.f;                        // reference maximum * c (0 while nothing was seen)
-      float m_ref = -INFINITY, l = 0.f;
+      float m_ref = -INFINITY, l = 0.f;      // l: this thread's keys
+      bool quit = false;
       for (int j = 0; j < n; ++j) {
-        if (!wait_short_warp(BAR(SFULL + t), steps & 1u, hdr)) { ok = false; break; }
+        if (!wait_short_warp(BAR(SFULL + t), steps & 1u, hdr)) ok = false;
         ptx::tc_fence_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ptx::tmem_ld32(s_addr + 32u * q, s + 32 * q);
+        uint32_t s[64];
+        ptx::tmem_ld32(s_addr, s);
+        ptx::tmem_ld32(s_addr + 32u, s + 32);
         ptx::tmem_wait_ld();
         const int valid = vis - j * kKeys;
-        if (!__all_sync(0xffffffffu, valid >= kKeys)) {
+        if (!__all_sync(0xffffffffu, valid >= 64)) {
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
+          for (int e = 0; e < 64; ++e)
             if (e >= valid) s[e] = 0xFF800000u;   // -inf
         }
-        if (j == 0) {
-          m_ref = row_max(s);
-          mc = m_ref == -INFINITY ? 0.f : m_ref * c;
-        }
-        // The first half's P is computed against the reference so far while
-        // the row's maximum is still being found; if that then exceeds the
-        // reference by too much for any row, O is rescaled and the half redone.
-        float ls, mx;
-        while (true) {
-          ls = 0.f;
-          p_half(s, c, mc, ls, s_addr);
-          if (j == 0) break;
-          mx = row_max(s);
-          const bool up = m_ref == -INFINITY ? mx != -INFINITY : (mx - m_ref) * c > kLazy;
-          if (!__any_sync(0xffffffffu, up)) break;
+        float mx = row_max(s);
+        const bool up = !ok || j == 0 || (m_ref == -INFINITY ? mx != -INFINITY : (mx - m_ref) * c > kLazy);
+        if (any_of_pair(pair, up)) {
+          // rare: agree on the rows' maxima and move the references that need it
+          *own = mx;
+          quit = any_of_pair(pair, !ok);
+          mx = fmaxf(mx, *other);
           float alpha = 1.f;
-          if (up) {
+          if (m_ref == -INFINITY ? mx != -INFINITY : (mx - m_ref) * c > kLazy) {
             const float nmc = mx * c;
             alpha = m_ref == -INFINITY ? 1.f : fast_exp2(mc - nmc);   // -inf: l = 0 and O = 0 so far
             m_ref = mx;
             mc = nmc;
             l *= alpha;
           }
-          // O of the tiles so far is complete once the previous P.V is
-          if (!wait_short_warp(BAR(PVDONE + t), (steps - 1) & 1u, hdr)) { ok = false; break; }
-          ptx::tc_fence_after();
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+            // O of the tiles so far is complete once the previous P.V is
+            if (!wait_short_warp(BAR(PVDONE + t), (steps - 1) & 1u, hdr)) ok = false;
+            ptx::tc_fence_after();
 #pragma unroll 1
-          for (int q = 0; q < 8; ++q) {
-            uint32_t o[16];
-            ptx::tmem_ld16(o_addr + 16u * q, o);
-            ptx::tmem_wait_ld();
+            for (int q = 0; q < 4; ++q) {
+              uint32_t o[16];
+              ptx::tmem_ld16(o_addr + 16u * q, o);
+              ptx::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st16(o_addr + 16u * q, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(o_addr + 16u * q, o);
+            }
           }
         }
-        if (!ok) break;
+        p_half(s, c, mc, l, s_addr);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(BAR(PREADY + t));
-        p_half(s + 64, c, mc, ls, s_addr + 32u);
-        l += ls;
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(BAR(PREADY + 2 + t));
+        __syncwarp();
+        if (elect_one()) ptx::mbar_arrive(BAR(PREADY + t));
         ++steps;
+        if (quit) break;
       }
-      if (!ok) break;
-      if (n > 0) {
-        if (!wait_short_warp(BAR(PVDONE + t), (steps - 1) & 1u, hdr)) { ok = false; break; }
+      if (!quit && n > 0) {
+        if (!wait_short_warp(BAR(PVDONE + t), (steps - 1) & 1u, hdr)) ok = false;
         ptx::tc_fence_after();
       }
+      pair_sync(pair);                       // the partner has read what an exchange left here
+      *own = l;
+      if (any_of_pair(pair, !ok)) break;
+      l += *other;
       const bool live = r < it.rows;
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays NaN
       const size_t orow = (static_cast<size_t>(it.q0) + r) * kHeads + it.head;
 #pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 2; ++q) {
         uint32_t o[32], w16[16];
         if (n > 0) {
           ptx::tmem_ld32(o_addr + 32u * q, o);
@@ -619,16 +637,13 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           w16[e] = *reinterpret_cast<const uint32_t*>(&b);
         }
         if (live) {
-          ptx::st_global_v8(p.out + orow * 128 + 32 * q, w16);
-          ptx::st_global_v8(p.out + orow * 128 + 32 * q + 16, w16 + 8);
+          ptx::st_global_v8(p.out + orow * 128 + 64 * hf + 32 * q, w16);
+          ptx::st_global_v8(p.out + orow * 128 + 64 * hf + 32 * q + 16, w16 + 8);
         }
       }
-      if (live) p.lse[orow] = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
+      if (live && hf == 0) p.lse[orow] = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
       ptx::tc_fence_before();
     }
-  }
-  else if (smem_ok) {
-    reg_dec();   // warp 3 has no role
   }
   // ------------------------------------------------------------ teardown
   ptx::tc_fence_before();
