@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
   Tile* tiles = reinterpret_cast<Tile*>(ws + L.tiles);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   s_count[tid] = 0;
+  ptx::grid_dep_launch();   // the attention kernel may set itself up; it waits for this grid before it reads the list
   __syncthreads();
   for (int pass = 0; pass < 2; ++pass) {
     for (int b = warp; b < batch; b += 32) {
@@ -273,6 +274,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem), 0);
+  // everything above overlaps the plan kernel, whose list is read from here on
+  ptx::grid_dep_wait();
   const bool smem_ok = (sbase & 1023u) == 0;
   if (threadIdx.x == 0 && !smem_ok) set_status(&hdr->status, MLA_ERR_UNSUPPORTED);
   const int causal = p.causal;
@@ -711,8 +714,17 @@ cudaError_t launch_prefill(PFN_cuTensorMapEncodeTiled_v12000 encode, const Prefi
                     p.ws, L);
   if (e != cudaSuccess) return e;
   const long long items = static_cast<long long>(L.max_tiles) * kHeads;
-  return launch_kernel(prefill_kernel, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kThreads), kSmem,
-                       stream, maps, p, L);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items < sms ? items : sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefill_kernel, maps, p, L);
 }
 
 }  // namespace mla
