@@ -5,24 +5,36 @@
 // this is one product of M = n, K = 512, N = 128 heads x 256.
 //
 // Bound: 2 n 512 32768 operations against 64 KiB of bf16 written per token,
-// so at 8192 tokens the tensor cores need about twice HBM's time.  The
-// latent tile (128 tokens x 512, 128 KiB) therefore stays in shared memory
-// while the heads' weights stream past it from L2 (33.5 MB, resident there),
-// and the fp32 accumulators are double-buffered in tensor memory so that
-// writing a tile overlaps the next one's products.
+// so at 8192 tokens the tensor cores need about as long as HBM does for the
+// output, and what has to be kept off their path is traffic through L2.
 //
-// One persistent CTA per SM.  A work item is (token tile m, head h); a CTA
-// takes a contiguous run of items in m-major order, so it loads a latent tile
-// once per m it touches.  Per item: D[128 x 256] = C[128 x 512] . [W^UK_h;
-// W^UV_h]^T, 32 K-steps of tcgen05.mma M = 128, N = 256, K = 16, both
-// operands K-major with 128-byte swizzle.  Warp 0 issues the TMA loads, warp
-// 1 the MMAs, warps 4..11 write (4..7 the keys, 8..11 the values; thread =
-// token).  Rows past n are read as zeros and not written.
+// A pair of CTAs computes 256 tokens x 256 columns with cta_group::2 MMAs (M =
+// 256, N = 256): each CTA holds half of the weights' rows (rank 0 W^UK, rank 1
+// W^UV) and half of the tokens, so an operand crosses L2 once for the pair.
+// One head's weights stay in shared memory (128 KiB a CTA) while latent tiles
+// stream past them, not the other way round: streaming the 33.5 MB of weights
+// past a resident latent tile moves as many bytes, but with the output
+// streaming out beside it the two did not overlap in L2 (8192 tokens: 203 us;
+// with every pair reading one head's weights, for timing only, 154 us), while
+// the latent rows in use are few enough (8 MB) to be served beside it.  The
+// output leaves as TMA stores of whole 128-byte lines from a staging buffer,
+// and the fp32 accumulators (256 columns of each SM's tensor memory) are
+// double-buffered, so writing an item overlaps the next one's products.
+//
+// Persistent pairs; a work item is (head h, token tile m), and a pair takes a
+// contiguous run of items ordered by (block of 32 token tiles, head, tile).
+// Per item: 32 K-steps of tcgen05.mma, both operands K-major with 128-byte
+// swizzle, in K blocks of 64: the latent through a four-block ring, the
+// weights' eight blocks each reloaded as soon as their last use is over.  Warp
+// 0 of each rank issues its loads (all counted on rank 0's barriers), warp 1
+// of rank 0 the MMAs, warps 4..11 of each rank write (4..7 the keys, 8..11 the
+// values; thread = token).  Rows past n are read as zeros and not written.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include "expand.cuh"
+#include "waits.cuh"
 
 namespace mla {
 
@@ -31,122 +43,191 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kKBlock = 64;                             // K values per block (128-byte rows)
 constexpr int kKBlocks = kDc / kKBlock;                 // 8
-constexpr uint32_t kABlock = 128u * 128u;               // 16 KiB: 128 tokens x 64 values
-constexpr uint32_t kBBlock = 2 * kABlock;               // 32 KiB: 128 key rows, then 128 value rows
-constexpr int kStages = 3;
-constexpr uint32_t kOffB = kKBlocks * kABlock;          // after the latent tile
-constexpr uint32_t kOffBar = kOffB + kStages * kBBlock; // 224 KiB
-constexpr uint32_t kSmem = kOffBar + 256;
-constexpr uint32_t kIdesc = ptx::idesc_bf16(128, 256, 0, 0);
+constexpr uint32_t kBlock = 128u * 128u;                // 16 KiB: 128 tokens, or weight rows, x 64 values
+constexpr int kStages = 4;
+constexpr uint32_t kStageOut = 32u * 128u;              // 4 KiB per writer warp: 32 tokens x 64 values
+constexpr uint32_t kOffRing = kKBlocks * kBlock;        // after the weights
+constexpr uint32_t kOffOut = kOffRing + kStages * kBlock;
+constexpr uint32_t kOffBar = kOffOut + 8 * kStageOut;   // 224 KiB
+constexpr uint32_t kSmem = kOffBar + 512;
+constexpr uint32_t kIdesc = ptx::idesc_bf16(256, 256, 0, 0);
 
 enum Bar {
-  AFULL = 0, AEMPTY, BFULL, BEMPTY = BFULL + kStages, DFULL = BEMPTY + kStages, DEMPTY = DFULL + 2, DRAIN = DEMPTY + 2,
-  NBAR
+  WFULL = 0, WEMPTY = WFULL + kKBlocks, CFULL = WEMPTY + kKBlocks, CEMPTY = CFULL + kStages, DFULL = CEMPTY + kStages,
+  DEMPTY = DFULL + 2, DRAIN = DEMPTY + 2, NBAR
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
-expand_kernel(const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_uk,
-              const __grid_constant__ CUtensorMap tmap_uv, int rows, int items, __nv_bfloat16* __restrict__ k_out,
-              __nv_bfloat16* __restrict__ v_out, PlanHeader* hdr) {
+// ------------------------------------------------------------ cta_group::2 pieces
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(dst_smem), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_tmem_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(ncols) : "memory");
+}
+// D (+)= A B^T over the pair: A and D rows 128 of each CTA, B rows half from each
+__device__ __forceinline__ void pair_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// arrive on the barrier at this offset in both CTAs once this thread's MMAs are done
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               :: "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+// tiled loads whose bytes are counted on a barrier of either CTA of the pair (a cluster address)
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, uint64_t policy) {
+  asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+               " [%0], [%1, {%3, %4}], [%2], %5;"
+               :: "r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(y), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z,
+                                             uint64_t policy) {
+  asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+               " [%0], [%1, {%3, %4, %5}], [%2], %6;"
+               :: "r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy) : "memory");
+}
+// tiled store from shared memory, in this thread's bulk group
+__device__ __forceinline__ void store_3d(const void* tmap, uint32_t src, int x, int y, int z, uint64_t policy) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;"
+               :: "l"(tmap), "r"(src), "r"(x), "r"(y), "r"(z), "l"(policy) : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+constexpr int kTileBlock = 32;   // token tiles of a block
+
+// Item i of all: the blocks of kTileBlock token tiles in turn, in each the
+// heads, in each head the block's tiles.
+__device__ __forceinline__ void item_of(int i, int tiles, int& m, int& h) {
+  const int block = i / (kTileBlock * kHeads), left = i - block * (kTileBlock * kHeads);
+  const int size = min(kTileBlock, tiles - block * kTileBlock);
+  h = left / size;
+  m = block * kTileBlock + left - h * size;
+}
+
+struct ExpandMaps {
+  CUtensorMap c, w[2], out[2];   // latent; W^UK, W^UV; keys, values
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, PlanHeader* hdr) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = ptx::smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   auto BAR = [&](int i) { return sbase + kOffBar + 8u * static_cast<uint32_t>(i); };
   const uint32_t tmem_slot = sbase + kOffBar + 8u * NBAR;
   if (threadIdx.x == 0) {
-    ptx::mbar_init(BAR(AFULL), 1);
-    ptx::mbar_init(BAR(AEMPTY), 1);
-    for (int s = 0; s < kStages; ++s) { ptx::mbar_init(BAR(BFULL + s), 1); ptx::mbar_init(BAR(BEMPTY + s), 1); }
-    for (int s = 0; s < 2; ++s) { ptx::mbar_init(BAR(DFULL + s), 1); ptx::mbar_init(BAR(DEMPTY + s), 256); }
+    for (int b = 0; b < kKBlocks; ++b) { ptx::mbar_init(BAR(WFULL + b), 1); ptx::mbar_init(BAR(WEMPTY + b), 1); }
+    for (int s = 0; s < kStages; ++s) { ptx::mbar_init(BAR(CFULL + s), 1); ptx::mbar_init(BAR(CEMPTY + s), 1); }
+    for (int s = 0; s < 2; ++s) { ptx::mbar_init(BAR(DFULL + s), 1); ptx::mbar_init(BAR(DEMPTY + s), 16); }   // both ranks' writer warps
     ptx::mbar_init(BAR(DRAIN), 1);
     ptx::fence_barrier_init();
   }
   if (warp == 2) {
-    ptx::tmem_alloc(tmem_slot, 512);
-    ptx::tmem_relinquish();
+    pair_tmem_alloc(tmem_slot, 512);
+    pair_tmem_relinquish();
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 8u * NBAR);
-  const bool smem_ok = (sbase & 1023u) == 0;
+  ptx::cluster_sync();   // both ranks' barriers are initialised before any load or commit of the pair
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 8u * NBAR), 0);
+  const bool smem_ok = (sbase & 1023u) == 0;   // the same in both ranks
   if (threadIdx.x == 0 && !smem_ok) set_status(&hdr->status, MLA_ERR_UNSUPPORTED);
-  // this CTA's items [lo, hi): item = m * 128 + h
-  const int lo = static_cast<int>(static_cast<long long>(items) * blockIdx.x / gridDim.x);
-  const int hi = smem_ok ? static_cast<int>(static_cast<long long>(items) * (blockIdx.x + 1) / gridDim.x) : lo;
+  // this pair's items [lo, hi)
+  const long long items = static_cast<long long>(tiles) * kHeads;
+  const uint32_t pair = ptx::cluster_id_x(), pairs = gridDim.x >> 1;
+  const int lo = static_cast<int>(items * pair / pairs);
+  const int hi = smem_ok ? static_cast<int>(items * (pair + 1) / pairs) : lo;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
+    // ------------------------------------------------------------ loads (each rank its own halves)
     if (lane == 0) {
       const uint64_t pol = ptx::policy_evict_normal();
-      int s = 0, na = 0, nb = 0;
-      uint32_t ph = 0, aph = 0;
+      int s = 0, nw = 0, nc = 0;             // ring stage; heads' weights and latent blocks loaded so far
+      uint32_t ph = 0;
       bool ok = true;
-      for (int it = lo; it < hi && ok; ++it) {
-        const int m = it / kHeads, h = it - m * kHeads;
-        if (it == lo || h == 0) {
-          if (!wait_bounded<false>(BAR(AEMPTY), aph ^ 1u, hdr)) { ok = false; break; }
-          ptx::mbar_arrive_expect_tx(BAR(AFULL), kKBlocks * kABlock);
-          for (int kb = 0; kb < kKBlocks; ++kb)
-            ptx::tma_load_2d(sbase + kb * kABlock, &tmap_c, BAR(AFULL), kb * kKBlock, m * 128, pol);
-          aph ^= 1u;
-          ++na;
-        }
+      int h_last = -1;
+      for (int i = lo; i < hi && ok; ++i) {
+        int m, h;
+        item_of(i, tiles, m, h);
+        const bool weights = h != h_last || i == lo;
+        h_last = h;
         for (int kb = 0; kb < kKBlocks; ++kb) {
-          if (!wait_bounded<false>(BAR(BEMPTY + s), ph ^ 1u, hdr)) { ok = false; break; }
-          ptx::mbar_arrive_expect_tx(BAR(BFULL + s), kBBlock);
-          const uint32_t dst = sbase + kOffB + static_cast<uint32_t>(s) * kBBlock;
-          ptx::tma_load_3d(dst, &tmap_uk, BAR(BFULL + s), kb * kKBlock, 0, h, pol);
-          ptx::tma_load_3d(dst + kABlock, &tmap_uv, BAR(BFULL + s), kb * kKBlock, 0, h, pol);
-          ++nb;
+          if (weights) {
+            ok = wait_short<true>(BAR(WEMPTY + kb), (nw & 1u) ^ 1u, hdr);
+            if (!ok) break;
+            if (rank == 0) ptx::mbar_arrive_expect_tx(BAR(WFULL + kb), 2 * kBlock);
+            pair_load_3d(sbase + kb * kBlock, &maps.w[rank], ptx::mapa(BAR(WFULL + kb), 0), kb * kKBlock, 0, h, pol);
+          }
+          ok = wait_short<true>(BAR(CEMPTY + s), ph ^ 1u, hdr);
+          if (!ok) break;
+          if (rank == 0) ptx::mbar_arrive_expect_tx(BAR(CFULL + s), 2 * kBlock);
+          pair_load_2d(sbase + kOffRing + static_cast<uint32_t>(s) * kBlock, &maps.c, ptx::mapa(BAR(CFULL + s), 0),
+                       kb * kKBlock, m * 256 + static_cast<int>(rank) * 128, pol);
+          ++nc;
           if (++s == kStages) { s = 0; ph ^= 1u; }
         }
+        if (weights) ++nw;
       }
-      // no copy may land after the CTA has left: wait for the last phases armed
-      if (na > 0) wait_drain(BAR(AFULL), (na - 1) & 1, hdr);
-      for (int i = 0; i < kStages; ++i) {
-        const int n = (nb + kStages - 1 - i) / kStages;     // times stage i was armed
-        if (n > 0) wait_drain(BAR(BFULL + i), (n - 1) & 1, hdr);
+      // no copy may land after the CTA has left: rank 0's barriers count both
+      // ranks' bytes (after a wait that gave up, the pause at the end covers
+      // what was not waited for here)
+      if (rank == 0 && ok) {
+#pragma unroll 1
+        for (int b = 0; b < kKBlocks; ++b)
+          if (nw > 0) wait_drain(BAR(WFULL + b), (nw - 1) & 1, hdr);
+#pragma unroll 1
+        for (int b = 0; b < kStages; ++b) {
+          const int n = (nc + kStages - 1 - b) / kStages;     // times stage b was armed
+          if (n > 0) wait_drain(BAR(CFULL + b), (n - 1) & 1, hdr);
+        }
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------ MMA issuer
     int s = 0, d = 0;
-    uint32_t ph = 0, aph = 0, dph = 0;
+    uint32_t ph = 0, wph = 0, dph = 0;
     bool ok = true;
-    for (int it = lo; it < hi && ok; ++it) {
-      const int h = it % kHeads;
-      if (it == lo || h == 0) {
-        if (!wait_warp<false>(BAR(AFULL), aph, hdr)) { ok = false; break; }
-        aph ^= 1u;
-      }
-      if (!wait_warp<false>(BAR(DEMPTY + d), dph ^ 1u, hdr)) { ok = false; break; }
-      ptx::tc_fence_after();
-      for (int kb = 0; kb < kKBlocks; ++kb) {
-        if (!wait_warp<false>(BAR(BFULL + s), ph, hdr)) { ok = false; break; }
+    const uint64_t desc_w = ptx::sdesc_sw128(sbase, 16, 1024), desc_c = ptx::sdesc_sw128(sbase + kOffRing, 16, 1024);
+    int m, h = -1, h_next = -1, h_last = -1;
+    if (lo < hi) item_of(lo, tiles, m, h_next);
+    for (int i = lo; i < hi && ok; ++i) {
+      h = h_next;
+      h_next = -1;
+      if (i + 1 < hi) item_of(i + 1, tiles, m, h_next);
+      const bool first = h != h_last, last = h_next != h;     // of this head's weights
+      h_last = h;
+      ok = wait_short_warp<true>(BAR(DEMPTY + d), dph ^ 1u, hdr);
+      for (int kb = 0; kb < kKBlocks && ok; ++kb) {
+        if (first) ok = wait_short_warp<true>(BAR(WFULL + kb), wph, hdr);
+        if (ok) ok = wait_short_warp<true>(BAR(CFULL + s), ph, hdr);
+        if (!ok) break;
         ptx::tc_fence_after();
-        if (lane == 0) {
-          const uint64_t da = ptx::sdesc_sw128(sbase + kb * kABlock, 16, 1024);
-          const uint64_t db = ptx::sdesc_sw128(sbase + kOffB + static_cast<uint32_t>(s) * kBBlock, 16, 1024);
+        if (elect_one()) {
+          const uint64_t da = desc_c + static_cast<uint64_t>(s) * (kBlock >> 4);
+          const uint64_t db = desc_w + static_cast<uint64_t>(kb) * (kBlock >> 4);
 #pragma unroll
           for (int k = 0; k < kKBlock / 16; ++k)
-            ptx::mma_ss(tmem + 256u * d, da + static_cast<uint64_t>((k * 32) >> 4),
-                        db + static_cast<uint64_t>((k * 32) >> 4), kIdesc, (kb > 0 || k > 0) ? 1u : 0u);
-          ptx::mma_commit(BAR(BEMPTY + s));
-          if (kb == kKBlocks - 1) {
-            ptx::mma_commit(BAR(DFULL + d));
-            if (h == kHeads - 1) ptx::mma_commit(BAR(AEMPTY));   // the latent tile is done with
-          }
+            pair_mma_ss(tmem + 256u * d, da + 2u * k, db + 2u * k, kIdesc, (kb > 0 || k > 0) ? 1u : 0u);
+          pair_commit(BAR(CEMPTY + s));
+          if (last) pair_commit(BAR(WEMPTY + kb));
+          if (kb == kKBlocks - 1) pair_commit(BAR(DFULL + d));
         }
         __syncwarp();
         if (++s == kStages) { s = 0; ph ^= 1u; }
       }
+      if (first) wph ^= 1u;
       d ^= 1;
       if (d == 0) dph ^= 1u;
     }
-    // every MMA this thread issued completes before the CTA may leave
-    if (lo < hi && lane == 0) {
-      ptx::mma_commit(BAR(DRAIN));
+    // every MMA (and commit to the other rank) completes before the pair may leave
+    if (lo < hi && elect_one()) {   // the lane that issued them
+      pair_commit(BAR(DRAIN));
       wait_drain(BAR(DRAIN), 0u, hdr);
     }
     __syncwarp();
@@ -154,43 +235,65 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_c, const __grid_constant_
     // ------------------------------------------------------------ writers
     const int half = (warp - 4) >> 2;                    // 0: keys, 1: values
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int tr = (warp & 3) * 32 + lane;               // token of the tile
-    __nv_bfloat16* base = half == 0 ? k_out : v_out;
+    const uint32_t stage = sbase + kOffOut + static_cast<uint32_t>(warp - 4) * kStageOut;
+    uint8_t* stage_row = smem + kOffOut + static_cast<uint32_t>(warp - 4) * kStageOut + lane * 128;
+    const uint64_t pol = ptx::policy_evict_first();      // the output leaves L2 first
     int d = 0;
     uint32_t dph = 0;
-    for (int it = lo; it < hi; ++it) {
-      const int m = it / kHeads, h = it - m * kHeads;
-      if (!wait_warp<false>(BAR(DFULL + d), dph, hdr)) break;
+    for (int i = lo; i < hi; ++i) {
+      int m, h;
+      item_of(i, tiles, m, h);
+      const int row0 = m * 256 + static_cast<int>(rank) * 128 + (warp & 3) * 32;     // the warp's first token
+      if (!wait_short_warp<true>(BAR(DFULL + d), dph, hdr)) break;
       ptx::tc_fence_after();
-      const int row = m * 128 + tr;
-      __nv_bfloat16* dst = base + (static_cast<size_t>(row) * kHeads + h) * 128;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        ptx::tmem_ld32(tmem + lane_base + 256u * d + 128u * half + 32u * c, r);
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {                      // 64 columns at a time
+        uint32_t r[64];
+        ptx::tmem_ld32(tmem + lane_base + 256u * d + 128u * half + 64u * c, r);
+        ptx::tmem_ld32(tmem + lane_base + 256u * d + 128u * half + 64u * c + 32u, r + 32);
         ptx::tmem_wait_ld();
-        if (row < rows) {
-          uint32_t o[16];
+        if (c == 1) {
+          // this warp has read its part of D
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (elect_one()) ptx::mbar_arrive_remote(ptx::mapa(BAR(DEMPTY + d), 0));
+        }
+        if (row0 < rows) {
+          // the last store must have read the staging rows
+          if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-            o[e] = *reinterpret_cast<const uint32_t*>(&b);
+          for (int q = 0; q < 8; ++q) {                  // 16-byte pieces, 128-byte swizzle
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 b =
+                  __floats2bfloat162_rn(__uint_as_float(r[8 * q + 2 * e]), __uint_as_float(r[8 * q + 2 * e + 1]));
+              o[e] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            *reinterpret_cast<uint4*>(stage_row + ((q ^ (lane & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          ptx::st_global_v8(dst + 32 * c, o);
-          ptx::st_global_v8(dst + 32 * c + 16, o + 8);
+          ptx::fence_proxy_async_cta();
+          __syncwarp();
+          if (elect_one()) store_3d(&maps.out[half], stage, 64 * c, h, row0, pol);   // rows past n are clipped
+          __syncwarp();
         }
       }
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(BAR(DEMPTY + d));
       d ^= 1;
       if (d == 0) dph ^= 1u;
     }
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
+  // after a wait gave up, loads that rank 1 issued may be in flight uncounted:
+  // give them time to land before either CTA leaves
+  if (read_status(&hdr->abort_flag) != 0) spin_ns(20000);
   ptx::tc_fence_before();
   __syncthreads();
+  ptx::cluster_sync();
   if (warp == 2) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    pair_tmem_dealloc(tmem, 512);
   }
 }
 
@@ -200,36 +303,38 @@ cudaError_t launch_expand(PFN_cuTensorMapEncodeTiled_v12000 encode, const void* 
                           const void* w_uk, const void* w_uv, int rows, void* k_nope, void* v, void* hdr, int sms,
                           cudaStream_t stream) {
   if (rows <= 0) return cudaSuccess;
-  CUtensorMap tm_c, tm_uk, tm_uv;
+  ExpandMaps maps;
+  auto map = [&](CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                 const cuuint32_t* box) {
+    const cuuint32_t es[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t n = static_cast<cuuint64_t>(rows);
   {
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(kDc), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_stride) * 2};
-    cuuint32_t box[2] = {kKBlock, 128};
-    cuuint32_t es[2] = {1, 1};
-    if (encode(&tm_c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(latent), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    const cuuint64_t dims[2] = {kDc, n}, strides[1] = {static_cast<cuuint64_t>(row_stride) * 2};
+    const cuuint32_t box[2] = {kKBlock, 128};
+    if (!map(&maps.c, latent, 2, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t dims[3] = {kDc, 128, kHeads}, strides[2] = {kDc * 2, 128 * kDc * 2};
+    const cuuint32_t box[3] = {kKBlock, 128, 1};
+    if (!map(&maps.w[0], w_uk, 3, dims, strides, box) || !map(&maps.w[1], w_uv, 3, dims, strides, box))
       return cudaErrorInvalidValue;
   }
-  const void* w[2] = {w_uk, w_uv};
-  CUtensorMap* tw[2] = {&tm_uk, &tm_uv};
-  for (int i = 0; i < 2; ++i) {
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(kDc), 128, static_cast<cuuint64_t>(kHeads)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(kDc) * 2, static_cast<cuuint64_t>(128) * kDc * 2};
-    cuuint32_t box[3] = {kKBlock, 128, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    if (encode(tw[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(w[i]), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+  {
+    const cuuint64_t dims[3] = {128, kHeads, n}, strides[2] = {256, kHeads * 256};
+    const cuuint32_t box[3] = {64, 1, 32};
+    if (!map(&maps.out[0], k_nope, 3, dims, strides, box) || !map(&maps.out[1], v, 3, dims, strides, box))
       return cudaErrorInvalidValue;
   }
   static std::atomic<uint64_t> configured{0};
   const cudaError_t e = allow_smem(expand_kernel, kSmem, configured);
   if (e != cudaSuccess) return e;
-  const int items = (rows + 127) / 128 * kHeads;
-  return launch_kernel(expand_kernel, dim3(items < sms ? items : sms), dim3(kThreads), kSmem, stream, tm_c, tm_uk,
-                       tm_uv, rows, items, static_cast<__nv_bfloat16*>(k_nope), static_cast<__nv_bfloat16*>(v),
-                       static_cast<PlanHeader*>(hdr));
+  const int tiles = (rows + 255) / 256, pairs = sms / 2 > 0 ? sms / 2 : 1;
+  return launch_kernel(expand_kernel, dim3(2 * (pairs < kHeads ? pairs : kHeads)), dim3(kThreads), kSmem, stream, maps,
+                       rows, tiles, static_cast<PlanHeader*>(hdr));
 }
 
 }  // namespace mla

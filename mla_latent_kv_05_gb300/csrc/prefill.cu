@@ -189,16 +189,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 
-// One lane of a converged warp.  The compiler knows that a branch on it is
-// taken by a single thread and keeps what it issues in uniform registers: a
-// commit costs about 2 cycles to issue in such a branch, 46 under lane == 0 and
-// 60 as a predicated instruction, and an MMA's descriptors no moves.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
 // Registers (128 a thread at launch): 80 for warps 0..3, 96 for the output
 // warps, 168 for the softmax warps (4 * 80 + 4 * 96 + 8 * 168 = 16 * 128),
 // each role's branch setting its own.

@@ -1,6 +1,7 @@
-// Bounded mbarrier waits with little code: kernels whose warps play different
-// roles share the instruction caches, and an unrolled wait in every place
-// costs the other roles their lines.
+// Small pieces that warp-specialised tcgen05 kernels share: bounded mbarrier
+// waits with little code (the roles share the instruction caches, and an
+// unrolled wait in every place costs the other roles their lines) and the
+// election of an issuing lane.
 #pragma once
 #include "common.cuh"
 
@@ -8,11 +9,13 @@ namespace mla {
 
 // As wait_bounded<false> (common.cuh): false, with MLA_STATUS_TIMEOUT recorded
 // and the abort flag raised, when the phase did not complete in time; false
-// too once another thread of the grid gave up.
+// too once another thread of the grid gave up.  kCluster: acquire at cluster
+// scope, for phases that another CTA's arrivals complete.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity, PlanHeader* hdr) {
   uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t n = 1; !ptx::mbar_try_wait(bar, parity); ++n) {
+  for (uint32_t n = 1; !(kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity)); ++n) {
     if ((n & 1023u) != 0) continue;
     const uint64_t now = ptx::globaltimer();
     if (t0 == 0) t0 = now;
@@ -27,8 +30,19 @@ __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity, PlanHe
 }
 
 // The same for a converged warp, which leaves together.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_short_warp(uint32_t bar, uint32_t parity, PlanHeader* hdr) {
-  return __all_sync(0xffffffffu, wait_short(bar, parity, hdr));
+  return __all_sync(0xffffffffu, wait_short<kCluster>(bar, parity, hdr));
+}
+
+// One lane of a converged warp.  The compiler knows that a branch on it is
+// taken by a single thread and keeps what it issues in uniform registers: a
+// commit costs about 2 cycles to issue in such a branch, 46 under lane == 0 and
+// 60 as a predicated instruction, and an MMA's descriptors no moves.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 }  // namespace mla

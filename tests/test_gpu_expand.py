@@ -35,6 +35,15 @@ def test_matches_float64(cuda_device, n):
     check(v, rows, w_uv)
 
 
+@pytest.mark.parametrize("n", [8192 + 257, 16900])
+def test_more_tokens_than_a_block_of_tiles_on_sampled_rows(cuda_device, n):
+    rows, w_uk, w_uv = make(n, n)
+    k, v = binding.mla_expand_kv(rows, w_uk, w_uv)
+    at = torch.cat([torch.arange(0, n, 509), torch.tensor([8191, 8192, 8193, n - 257, n - 1])]).cuda()
+    check(k[at], rows[at], w_uk)
+    check(v[at], rows[at], w_uv)
+
+
 def test_strided_rows_outputs_given_and_neighbours_kept(cuda_device):
     rows, w_uk, w_uv = make(200, 3, 576)
     k = torch.full((202, 128, 128), 5.0, dtype=torch.bfloat16, device="cuda")
