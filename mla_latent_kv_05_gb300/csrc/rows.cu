@@ -20,8 +20,10 @@
 // the launch and two dependent reads (the row's sequence, then its page) when
 // short.  One thread takes eight consecutive values (16 bytes of bf16), so
 // the bf16 side is one coalesced 16-byte access a thread and a group's
-// maximum needs one or two shuffles; a CTA takes four rows, whose slots four
-// warps look up while the values are already on their way.
+// maximum needs one or two shuffles.  A CTA takes kGroups groups of four rows:
+// one group for short calls (more CTAs, and the values are on their way while
+// the warps look the slots up), four for long ones, whose 16 look-ups then
+// overlap and whose loads are all in flight at once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -31,7 +33,7 @@ namespace mla {
 
 namespace {
 
-constexpr int kRowsPerCta = 4;
+constexpr int kGroupRows = 4;
 constexpr int kPiece = 8;   // values per thread
 
 template <RowFormat F> struct Fmt;
@@ -96,42 +98,36 @@ __device__ __forceinline__ int scale_exponent(uint32_t a) {
   return min(max(k, -127), Fmt<F>::kTopK);
 }
 
-template <RowFormat F>
-__global__ void __launch_bounds__(kRowsPerCta * Fmt<F>::kValues / kPiece)
-append_kernel(const RowsParams p) {
-  using T = Fmt<F>;
-  constexpr int kPieces = T::kValues / kPiece;
-  __shared__ int s_slot[kRowsPerCta];
+// The slots of this CTA's rows, one warp a row.
+template <int kGroups>
+__device__ __forceinline__ void look_up(const RowsParams& p, int row0, int* s_slot) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = threadIdx.x / kPieces, j = threadIdx.x - r * kPieces;
-  const int row = blockIdx.x * kRowsPerCta + r;
-  // V4.1 rows: values 0..447 are the latent's first 448, then the RoPE values
-  constexpr int kLatentPieces = (kIsV41<F> ? kV41Latent : kDc) / kPiece;
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (row < p.rows)
-    v = __ldg(reinterpret_cast<const uint4*>(
-        j < kLatentPieces ? p.c_kv + static_cast<size_t>(row) * p.c_stride + j * kPiece
-                          : p.k_rope + static_cast<size_t>(row) * p.r_stride + (j - kLatentPieces) * kPiece));
-  if (warp < kRowsPerCta) {
-    const int slot = row_slot(p, blockIdx.x * kRowsPerCta + warp, lane);
-    if (lane == 0) s_slot[warp] = slot;
+#pragma unroll 1
+  for (int i = warp; i < kGroups * kGroupRows; i += static_cast<int>(blockDim.x >> 5)) {
+    const int slot = row_slot(p, row0 + i, lane);
+    if (lane == 0) s_slot[i] = slot;
   }
   __syncthreads();
-  const int slot = s_slot[r];
+}
+
+// One piece of a quantised or bf16 row into its cache row.
+template <RowFormat F>
+__device__ __forceinline__ void append_piece(const RowsParams& p, uint4 v, int slot, int j) {
+  using T = Fmt<F>;
   uint8_t* dst = p.cache + static_cast<size_t>(slot < 0 ? 0 : slot) * T::kBytes;
   if constexpr (F == RowFormat::kBf16) {
     if (slot >= 0) *reinterpret_cast<uint4*>(dst + j * 16) = v;
   } else {
     // largest magnitude of the group as bf16 bits (their order as integers
     // is the order of the magnitudes, infinities and NaNs at the top)
-    uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                           __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    const uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                 __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
     uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
 #pragma unroll
     for (int o = 1; o < T::kGroup / kPiece; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const bool finite = m < 0x7F80u;
     const int k = finite ? scale_exponent<F>(m) : 0;
-    const float mul = finite ? __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : 0.f;   // 2^-k, normal: k <= 125
+    const float mul = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);   // 2^-k, normal: k <= 125
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t code[4];
 #pragma unroll
@@ -154,14 +150,41 @@ append_kernel(const RowsParams p) {
       *reinterpret_cast<uint32_t*>(dst + j * 4) = code[0] | (code[1] << 8) | (code[2] << 16) | (code[3] << 24);
     } else if constexpr (F == RowFormat::kFp8V41) {
       *reinterpret_cast<uint2*>(dst + j * 8) = make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+    } else if (slot & 1) {
+      // 594-byte rows: an odd slot starts between two words
+      *reinterpret_cast<uint16_t*>(dst + j * 8) = static_cast<uint16_t>(code[0]);
+      *reinterpret_cast<uint32_t*>(dst + j * 8 + 2) = code[1] | (code[2] << 16);
+      *reinterpret_cast<uint16_t*>(dst + j * 8 + 6) = static_cast<uint16_t>(code[3]);
     } else {
-      // 594-byte rows: 2-byte boundaries
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint16_t*>(dst + j * 8 + 2 * i) = static_cast<uint16_t>(code[i]);
+      *reinterpret_cast<uint32_t*>(dst + j * 8) = code[0] | (code[1] << 16);
+      *reinterpret_cast<uint32_t*>(dst + j * 8 + 4) = code[2] | (code[3] << 16);
     }
     if (j % (T::kGroup / kPiece) == 0)
       dst[T::kScales + j / (T::kGroup / kPiece)] = static_cast<uint8_t>(finite ? k + 127 : 255);
   }
+}
+
+template <RowFormat F, int kGroups>
+__global__ void __launch_bounds__(kGroupRows * Fmt<F>::kValues / kPiece) append_kernel(const RowsParams p) {
+  constexpr int kPieces = Fmt<F>::kValues / kPiece;
+  __shared__ int s_slot[kGroups * kGroupRows];
+  const int r = threadIdx.x / kPieces, j = threadIdx.x - r * kPieces;
+  const int row0 = blockIdx.x * kGroups * kGroupRows;
+  // V4.1 rows: values 0..447 are the latent's first 448, then the RoPE values
+  constexpr int kLatentPieces = (kIsV41<F> ? kV41Latent : kDc) / kPiece;
+  uint4 v[kGroups];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const int row = row0 + g * kGroupRows + r;
+    v[g] = make_uint4(0, 0, 0, 0);
+    if (row < p.rows)
+      v[g] = __ldg(reinterpret_cast<const uint4*>(
+          j < kLatentPieces ? p.c_kv + static_cast<size_t>(row) * p.c_stride + j * kPiece
+                            : p.k_rope + static_cast<size_t>(row) * p.r_stride + (j - kLatentPieces) * kPiece));
+  }
+  look_up<kGroups>(p, row0, s_slot);
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) append_piece<F>(p, v[g], s_slot[g * kGroupRows + r], j);
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -169,67 +192,108 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+// A stored piece (codes and their scale) as read, and as eight bf16 values.
+struct Piece {
+  uint4 raw;
+  uint32_t scale;
+};
+
 template <RowFormat F>
-__global__ void __launch_bounds__(kRowsPerCta * kRow / kPiece) gather_kernel(const RowsParams p) {
+__device__ __forceinline__ Piece read_piece(const RowsParams& p, int slot, int j) {
   using T = Fmt<F>;
-  constexpr int kPieces = kRow / kPiece;     // the output row has 576 values in every format
-  __shared__ int s_slot[kRowsPerCta];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = threadIdx.x / kPieces, j = threadIdx.x - r * kPieces;
-  const int row = blockIdx.x * kRowsPerCta + r;
-  if (warp < kRowsPerCta) {
-    const int slot = row_slot(p, blockIdx.x * kRowsPerCta + warp, lane);
-    if (lane == 0) s_slot[warp] = slot;
-  }
-  __syncthreads();
-  const int slot = s_slot[r];
-  if (slot == -1) return;                    // behind the last sequence: left as it was
-  uint4 o = make_uint4(0, 0, 0, 0);          // a row outside the cache reads as zeros
-  if (slot >= 0) {
-    const uint8_t* src = p.cache + static_cast<size_t>(slot) * T::kBytes;
-    if constexpr (F == RowFormat::kBf16) {
-      o = __ldg(reinterpret_cast<const uint4*>(src + j * 16));
+  Piece x;
+  x.raw = make_uint4(0, 0, 0, 0);            // a row outside the cache reads as zeros
+  x.scale = 127;
+  // V4.1 rows: latent dims 448..511 are zero, the RoPE values are the row's last 64
+  constexpr int kPad0 = kIsV41<F> ? kV41Latent / kPiece : kRow / kPiece, kPad1 = kDc / kPiece;
+  if (slot < 0 || (j >= kPad0 && j < kPad1)) return x;
+  const int q = kIsV41<F> && j >= kPad1 ? j - (kPad1 - kPad0) : j;         // piece of the stored row
+  const uint8_t* src = p.cache + static_cast<size_t>(slot) * T::kBytes;
+  if constexpr (F == RowFormat::kBf16) {
+    x.raw = __ldg(reinterpret_cast<const uint4*>(src + q * 16));
+  } else {
+    x.scale = __ldg(src + T::kScales + q / (T::kGroup / kPiece));
+    if constexpr (kIsFp4<F>) {
+      x.raw.x = __ldg(reinterpret_cast<const uint32_t*>(src + q * 4));
+    } else if constexpr (F == RowFormat::kFp8V41) {
+      const uint2 c = __ldg(reinterpret_cast<const uint2*>(src + q * 8));
+      x.raw.x = c.x;
+      x.raw.y = c.y;
+    } else if (slot & 1) {
+      // 594-byte rows: an odd slot starts between two words
+      const uint32_t a = __ldg(reinterpret_cast<const uint16_t*>(src + q * 8));
+      const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(src + q * 8 + 2));
+      const uint32_t c = __ldg(reinterpret_cast<const uint16_t*>(src + q * 8 + 6));
+      x.raw.x = a | (b << 16);
+      x.raw.y = (b >> 16) | (c << 16);
     } else {
-      // V4.1 rows: latent dims 448..511 are zero, the RoPE values are the row's last 64
-      constexpr int kPad0 = kIsV41<F> ? kV41Latent / kPiece : kPieces, kPad1 = kDc / kPiece;
-      const bool pad = j >= kPad0 && j < kPad1;
-      const int q = kIsV41<F> && j >= kPad1 ? j - (kPad1 - kPad0) : j;     // piece of the stored row
-      if (!pad) {
-        const uint32_t e = __ldg(src + T::kScales + q / (T::kGroup / kPiece));
-        const float sc = __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7FC00000u : e << 23));
-        uint32_t h[4];
-        if constexpr (kIsFp4<F>) {
-          const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(src + q * 4));
-          asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
-              " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
-              " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
-              : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(c));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const unsigned short c = __ldg(reinterpret_cast<const unsigned short*>(src + q * 8 + 2 * i));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[i]) : "h"(c));
-          }
-        }
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-          w[i] = bf16_pair(f.x * sc, f.y * sc);   // exact in fp32, rounded once
-        }
-        o = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      x.raw.x = __ldg(reinterpret_cast<const uint32_t*>(src + q * 8));
+      x.raw.y = __ldg(reinterpret_cast<const uint32_t*>(src + q * 8 + 4));
     }
   }
-  *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row) * kRow + j * kPiece) = o;
+  return x;
+}
+
+template <RowFormat F>
+__device__ __forceinline__ uint4 values_of(const Piece& x) {
+  if constexpr (F == RowFormat::kBf16) {
+    return x.raw;
+  } else {
+    const uint32_t e = x.scale;
+    const float sc = __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7FC00000u : e << 23));
+    uint32_t h[4], w[4];
+    if constexpr (kIsFp4<F>) {
+      asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+          " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+          " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+          : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(x.raw.x));
+    } else {
+      const uint32_t c[2] = {x.raw.x, x.raw.y};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[i]) : "h"(static_cast<unsigned short>(c[i >> 1] >> (16 * (i & 1)))));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+      w[i] = bf16_pair(f.x * sc, f.y * sc);   // exact in fp32, rounded once
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <RowFormat F, int kGroups>
+__global__ void __launch_bounds__(kGroupRows * kRow / kPiece) gather_kernel(const RowsParams p) {
+  constexpr int kPieces = kRow / kPiece;     // the output row has 576 values in every format
+  __shared__ int s_slot[kGroups * kGroupRows];
+  const int r = threadIdx.x / kPieces, j = threadIdx.x - r * kPieces;
+  const int row0 = blockIdx.x * kGroups * kGroupRows;
+  look_up<kGroups>(p, row0, s_slot);
+  Piece x[kGroups];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) x[g] = read_piece<F>(p, s_slot[g * kGroupRows + r], j);
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    if (s_slot[g * kGroupRows + r] == -1) continue;   // behind the last sequence: left as it was
+    const size_t row = static_cast<size_t>(row0) + g * kGroupRows + r;
+    *reinterpret_cast<uint4*>(p.out + row * kRow + j * kPiece) = values_of<F>(x[g]);
+  }
+}
+
+// Rows of a call from which a CTA takes four groups instead of one.
+constexpr int kLongCall = 8192;
+
+template <RowFormat F, int kGroups>
+cudaError_t launch(const RowsParams& p, bool append, cudaStream_t stream) {
+  const dim3 grid((p.rows + kGroups * kGroupRows - 1) / (kGroups * kGroupRows));
+  if (append)
+    return launch_kernel(append_kernel<F, kGroups>, grid, dim3(kGroupRows * Fmt<F>::kValues / kPiece), 0, stream, p);
+  return launch_kernel(gather_kernel<F, kGroups>, grid, dim3(kGroupRows * kRow / kPiece), 0, stream, p);
 }
 
 template <RowFormat F>
 cudaError_t launch(const RowsParams& p, bool append, cudaStream_t stream) {
-  const dim3 grid((p.rows + kRowsPerCta - 1) / kRowsPerCta);
-  if (append)
-    return launch_kernel(append_kernel<F>, grid, dim3(kRowsPerCta * Fmt<F>::kValues / kPiece), 0, stream, p);
-  return launch_kernel(gather_kernel<F>, grid, dim3(kRowsPerCta * kRow / kPiece), 0, stream, p);
+  return p.rows >= kLongCall ? launch<F, 4>(p, append, stream) : launch<F, 1>(p, append, stream);
 }
 
 }  // namespace
