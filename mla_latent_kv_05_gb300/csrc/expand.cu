@@ -79,11 +79,6 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {
                :: "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
 }
 // tiled loads whose bytes are counted on a barrier of either CTA of the pair (a cluster address)
-__device__ __forceinline__ void pair_load_2d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, uint64_t policy) {
-  asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-               " [%0], [%1, {%3, %4}], [%2], %5;"
-               :: "r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(y), "l"(policy) : "memory");
-}
 __device__ __forceinline__ void pair_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z,
                                              uint64_t policy) {
   asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
@@ -91,9 +86,9 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const void* tmap, uin
                :: "r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy) : "memory");
 }
 // tiled store from shared memory, in this thread's bulk group
-__device__ __forceinline__ void store_3d(const void* tmap, uint32_t src, int x, int y, int z, uint64_t policy) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;"
-               :: "l"(tmap), "r"(src), "r"(x), "r"(y), "r"(z), "l"(policy) : "memory");
+__device__ __forceinline__ void store_4d(const void* tmap, uint32_t src, int x, int y, int z, int w, uint64_t policy) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4, %5}], [%1], %6;"
+               :: "l"(tmap), "r"(src), "r"(x), "r"(y), "r"(z), "r"(w), "l"(policy) : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
@@ -167,8 +162,8 @@ expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, Plan
           ok = wait_short<true>(BAR(CEMPTY + s), ph ^ 1u, hdr);
           if (!ok) break;
           if (rank == 0) ptx::mbar_arrive_expect_tx(BAR(CFULL + s), 2 * kBlock);
-          pair_load_2d(sbase + kOffRing + static_cast<uint32_t>(s) * kBlock, &maps.c, ptx::mapa(BAR(CFULL + s), 0),
-                       kb * kKBlock, m * 256 + static_cast<int>(rank) * 128, pol);
+          pair_load_3d(sbase + kOffRing + static_cast<uint32_t>(s) * kBlock, &maps.c, ptx::mapa(BAR(CFULL + s), 0),
+                       kb * kKBlock, m * 256 + static_cast<int>(rank) * 128, 0, pol);
           ++nc;
           if (++s == kStages) { s = 0; ph ^= 1u; }
         }
@@ -275,7 +270,7 @@ expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, Plan
           }
           ptx::fence_proxy_async_cta();
           __syncwarp();
-          if (elect_one()) store_3d(&maps.out[half], stage, 64 * c, h, row0, pol);   // rows past n are clipped
+          if (elect_one()) store_4d(&maps.out[half], stage, 64 * c, h, row0, 0, pol);   // rows past n are clipped
           __syncwarp();
         }
       }
@@ -306,16 +301,16 @@ cudaError_t launch_expand(PFN_cuTensorMapEncodeTiled_v12000 encode, const void* 
   ExpandMaps maps;
   auto map = [&](CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
                  const cuuint32_t* box) {
-    const cuuint32_t es[3] = {1, 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
     return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   const cuuint64_t n = static_cast<cuuint64_t>(rows);
   {
-    const cuuint64_t dims[2] = {kDc, n}, strides[1] = {static_cast<cuuint64_t>(row_stride) * 2};
-    const cuuint32_t box[2] = {kKBlock, 128};
-    if (!map(&maps.c, latent, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    const cuuint64_t dims[3] = {kDc, n, 2}, strides[2] = {static_cast<cuuint64_t>(row_stride) * 2, kTmaFar};
+    const cuuint32_t box[3] = {kKBlock, 128, 1};
+    if (!map(&maps.c, latent, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
   {
     const cuuint64_t dims[3] = {kDc, 128, kHeads}, strides[2] = {kDc * 2, 128 * kDc * 2};
@@ -324,9 +319,9 @@ cudaError_t launch_expand(PFN_cuTensorMapEncodeTiled_v12000 encode, const void* 
       return cudaErrorInvalidValue;
   }
   {
-    const cuuint64_t dims[3] = {128, kHeads, n}, strides[2] = {256, kHeads * 256};
-    const cuuint32_t box[3] = {64, 1, 32};
-    if (!map(&maps.out[0], k_nope, 3, dims, strides, box) || !map(&maps.out[1], v, 3, dims, strides, box))
+    const cuuint64_t dims[4] = {128, kHeads, n, 2}, strides[3] = {256, kHeads * 256, kTmaFar};
+    const cuuint32_t box[4] = {64, 1, 32, 1};
+    if (!map(&maps.out[0], k_nope, 4, dims, strides, box) || !map(&maps.out[1], v, 4, dims, strides, box))
       return cudaErrorInvalidValue;
   }
   static std::atomic<uint64_t> configured{0};

@@ -304,7 +304,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         return ok;
       };
       auto chunk = [&](const CUtensorMap* map, int x, int y, int z) {
-        ptx::tma_load_3d(sbase + kOffRing + slot * kChunk, map, BAR(FULL + (seq & (kTiles - 1))), x, y, z, pol);
+        ptx::tma_load_4d(sbase + kOffRing + slot * kChunk, map, BAR(FULL + (seq & (kTiles - 1))), x, y, z, 0, pol);
         if (++slot == kRing) slot = 0;
       };
       auto query = [&](int t, uint32_t n, const Tile& it) {
@@ -313,9 +313,9 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         ptx::mbar_arrive_expect_tx(BAR(QFULL + t), kQTile);
         const uint32_t dst = sbase + static_cast<uint32_t>(t) * kQTile;
         const int row = it.q0 + 128 * t;
-        ptx::tma_load_3d(dst, &maps.qn, BAR(QFULL + t), 0, it.head, row, pol);
-        ptx::tma_load_3d(dst + kQChunk, &maps.qn, BAR(QFULL + t), 64, it.head, row, pol);
-        ptx::tma_load_3d(dst + 2 * kQChunk, &maps.qr, BAR(QFULL + t), 0, it.head, row, pol);
+        ptx::tma_load_4d(dst, &maps.qn, BAR(QFULL + t), 0, it.head, row, 0, pol);
+        ptx::tma_load_4d(dst + kQChunk, &maps.qn, BAR(QFULL + t), 64, it.head, row, 0, pol);
+        ptx::tma_load_4d(dst + 2 * kQChunk, &maps.qr, BAR(QFULL + t), 0, it.head, row, 0, pol);
       };
       const Tile* tiles = reinterpret_cast<const Tile*>(p.ws + L.tiles);
       const int n_tiles = *reinterpret_cast<const volatile int*>(&hdr->n_tiles);
@@ -670,14 +670,15 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
   }
 }
 
-// (values, heads, tokens) boxes of 64 x 1 x rows; strides in values.
+// (values, heads, tokens) boxes of 64 x 1 x rows; strides in values (see kTmaFar
+// for the fourth dimension).
 bool encode_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* base, int width, int heads,
                 int tokens, long long stride_t, long long stride_h, unsigned rows) {
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride_h) * 2, static_cast<cuuint64_t>(stride_t) * 2};
-  cuuint32_t box[3] = {64, 1, rows};
-  cuuint32_t es[3] = {1, 1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens), 2};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(stride_h) * 2, static_cast<cuuint64_t>(stride_t) * 2, kTmaFar};
+  cuuint32_t box[4] = {64, 1, rows, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
