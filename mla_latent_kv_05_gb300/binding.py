@@ -44,6 +44,7 @@ SIGNATURES = {
                                     ctypes.c_size_t, _P]),
     "mla_up_project_wuv": (_I, [_P, _P, _I, _I, _I, _P, _P, ctypes.c_size_t, _P]),
     "mla_workspace_size_tree": (_I, [_I, _I, _I, _I, ctypes.POINTER(_Z)]),
+    "mla_workspace_size_tree_widened": (_I, [_I, _I, _I, _I, _I, ctypes.POINTER(_Z)]),
     **{"mla_decode_tree_" + f: (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P,
                                      _Z, _P])
        for f in ("bf16", "fp8", "fp4", "fp8_v41", "fp4_v41")},
@@ -505,9 +506,27 @@ def mla_workspace_size_tree(batch: int, nodes: int, num_heads: int = 128, page_s
     return int(n.value)
 
 
-def alloc_workspace_tree(batch: int, nodes: int, device=None) -> torch.Tensor:
-    """A zeroed workspace buffer (uint8) for the tree decode."""
-    return torch.zeros(mla_workspace_size_tree(batch, nodes), dtype=torch.uint8, device=device or "cuda")
+def mla_workspace_size_tree_widened(batch: int, nodes: int, max_pages: int, num_heads: int = 128,
+                                    page_size: int = 64) -> int:
+    n = ctypes.c_size_t(0)
+    rc = load().mla_workspace_size_tree_widened(int(batch), int(nodes), int(num_heads), int(page_size),
+                                                int(max_pages), ctypes.byref(n))
+    if rc != MLA_OK:
+        raise MLAError(rc, "mla_workspace_size_tree_widened")
+    return int(n.value)
+
+
+def alloc_workspace_tree(batch: int, nodes: int, device=None, max_pages: int = 0) -> torch.Tensor:
+    """A zeroed workspace buffer (uint8) for the tree decode; with the width of
+    the block table as max_pages, one in which a quantised cache's rows are
+    widened to bf16 once for all nodes (faster, 72 KiB a page more)."""
+    size = (mla_workspace_size_tree_widened(batch, nodes, max_pages) if max_pages
+            else mla_workspace_size_tree(batch, nodes))
+    return torch.zeros(size, dtype=torch.uint8, device=device or "cuda")
+
+
+_WIDENED_PAGE = 64 * 576 * 2
+_WIDENED_DEFAULT = 1 << 30   # a call without a workspace of its own takes up to this much for widened rows
 
 
 def _tree(fmt, q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, scale, n_nodes, out, lse, workspace,
@@ -533,7 +552,9 @@ def _tree(fmt, q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, sca
     _check(out, "out", torch.bfloat16, (B, T, H, 512))
     _check(lse, "lse", torch.float32, (B, T, H))
     if workspace is None:
-        workspace = alloc_workspace_tree(B, T, q_absorbed.device)
+        pages = int(block_table.shape[1])
+        widen = fmt != "bf16" and T > 1 and B * pages * _WIDENED_PAGE <= _WIDENED_DEFAULT
+        workspace = alloc_workspace_tree(B, T, q_absorbed.device, pages if widen else 0)
     _check(workspace, "workspace", torch.uint8)
     _same_device(dict(q_absorbed=q_absorbed, q_rope=q_rope, kv_cache=kv_cache, block_table=block_table,
                       seq_lens=seq_lens, parents=parents, n_nodes=n_nodes, out=out, lse=lse, workspace=workspace),

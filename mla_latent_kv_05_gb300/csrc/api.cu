@@ -14,6 +14,7 @@
 #include "expand.cuh"
 #include "prefill.cuh"
 #include "rows.cuh"
+#include "tree.cuh"
 
 namespace {
 
@@ -82,8 +83,8 @@ enum class CacheKind { kBf16, kFp8, kFp4, kFp8V41, kFp4V41 };
 // row of a few pages is not split (no partial write, nothing to merge).  The
 // workspace stays sized for all resident pairs.
 constexpr long long kPagesPerPair = 8;
-int pairs_for(int max_pairs, long long page_bound) {
-  const long long want = (page_bound + kPagesPerPair - 1) / kPagesPerPair;
+int pairs_for(int max_pairs, long long page_bound, long long pages_per_pair = kPagesPerPair) {
+  const long long want = (page_bound + pages_per_pair - 1) / pages_per_pair;
   return static_cast<int>(want < 1 ? 1 : (want < max_pairs ? want : max_pairs));
 }
 
@@ -126,6 +127,7 @@ int run_decode(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rop
   p.sp_slots = nullptr;
   p.topk = 0;
   p.tree_nodes = 0;
+  p.skip_chunk7 = 0;
   p.block_table = block_table;
   p.batch = batch;
   p.sq = sq;
@@ -253,6 +255,21 @@ int run_sparse(const uint16_t* q_absorbed, const uint16_t* q_rope, const void* k
   return MLA_OK;
 }
 
+// Pages per pair of a small tree decode.  Eight nodes over 200 tokens take 26.1
+// us at eight pages a pair and 18.6 at four (1008 tokens: 26.9 and 24.8); at two
+// the merge of more parts costs more (4 x 8 nodes over 500 tokens: 22.7 and 28.8).
+constexpr long long kTreePagesPerPair = 4;
+
+// A quantised cache's tree decode first widens the live pages to bf16 rows, once
+// for all nodes, when the workspace has room for them: the attention then runs
+// at the bf16 rate.  Two nodes pay for it already: 64 x 2 nodes over 4096 fp8
+// tokens take 235 us so and 321 over the codes (fp4: 207 and 293), 64 x 4 334
+// and 582, 8 x 61 342 and 1080; small calls gain too (1 x 2 over 500: 22.8 us).
+constexpr int kWidenNodes = 2;
+size_t widened_bytes(int batch, int max_pages) {
+  return static_cast<size_t>(batch) * max_pages * kPage * kRow * 2;
+}
+
 // Tree decode: the drafted nodes' masks and lengths, then the split planner
 // over the batch * nodes rows with one query each, the attention, the merge.
 int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope, const void* kv_cache,
@@ -277,20 +294,31 @@ int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope,
   const int rows = batch * nodes;
   const WsLayout L = ws_layout(rows, 1, pairs, 0, true);
   if (workspace_bytes < L.total) return MLA_ERR_WORKSPACE;
-  const int ppg = pairs_for(pairs, static_cast<long long>(rows) * max_pages);
-  CacheMaps maps;
+  const int ppg = pairs_for(pairs, static_cast<long long>(rows) * max_pages, kTreePagesPerPair);
   const bool quant = kind != CacheKind::kBf16;
-  if (!quant) {
-    st = make_cache_tmap(&maps.k, kv_cache, num_pages, 5);
-    if (st == MLA_OK) st = make_cache_tmap(&maps.k8, kv_cache, num_pages, 5, 8);
-    if (st == MLA_OK) st = make_cache_tmap(&maps.kb, kv_cache, num_pages, 4);
-    if (st == MLA_OK) st = make_cache_tmap(&maps.kb8, kv_cache, num_pages, 4, 8);
-    if (st == MLA_OK) st = make_cache_tmap(&maps.v, kv_cache, num_pages, 8);
-    if (st != MLA_OK) return st;
-  }
+  const bool widen = quant && nodes >= kWidenNodes && workspace_bytes >= L.total + widened_bytes(batch, max_pages) &&
+                     static_cast<long long>(batch) * max_pages * kPage < INT_MAX / 2;
+  auto encode = encode_fn();
+  if (!encode) return MLA_ERR_CUDA;
   __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out);
   if (launch_tree_prep(parents, n_nodes, seq_lens, batch, nodes, max_pages, workspace, L, o, lse, stream) != cudaSuccess)
     return MLA_ERR_CUDA;
+  uint8_t* rows16 = static_cast<uint8_t*>(workspace) + L.total;
+  if (widen) {
+    RowsParams r;
+    memset(&r, 0, sizeof(r));
+    r.cache = static_cast<uint8_t*>(const_cast<void*>(kv_cache));
+    r.block_table = block_table;
+    r.seq_lens = seq_lens;
+    r.batch = batch;
+    r.num_pages = num_pages;
+    r.max_pages = max_pages;
+    r.out = reinterpret_cast<__nv_bfloat16*>(rows16);
+    r.status = &static_cast<PlanHeader*>(workspace)->status;
+    const RowFormat fmt = kind == CacheKind::kFp8 ? RowFormat::kFp8 : kind == CacheKind::kFp4 ? RowFormat::kFp4
+                        : kind == CacheKind::kFp8V41 ? RowFormat::kFp8V41 : RowFormat::kFp4V41;
+    if (launch_widen(fmt, r, stream) != cudaSuccess) return MLA_ERR_CUDA;
+  }
   const int32_t* row_lens = reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(workspace) + L.sp_lens);
   if (launch_plan(row_lens, rows, 1, max_pages, ppg, workspace, L, nullptr, nullptr, stream) != cudaSuccess)
     return MLA_ERR_CUDA;
@@ -299,12 +327,13 @@ int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope,
   p.q_abs = reinterpret_cast<const __nv_bfloat16*>(q_absorbed);
   p.q_rope = reinterpret_cast<const __nv_bfloat16*>(q_rope);
   p.kv_quant = quant ? static_cast<const uint8_t*>(kv_cache) : nullptr;
-  p.kv_bf16 = quant ? nullptr : static_cast<const uint8_t*>(kv_cache);
-  p.block_table = block_table;
+  p.kv_bf16 = widen ? rows16 : quant ? nullptr : static_cast<const uint8_t*>(kv_cache);
+  p.block_table = widen ? nullptr : block_table;
+  p.skip_chunk7 = widen && (kind == CacheKind::kFp8V41 || kind == CacheKind::kFp4V41);
   p.batch = rows;
   p.sq = 1;
   p.pairs_per_group = ppg;
-  p.num_pages = num_pages;
+  p.num_pages = widen ? batch * max_pages : num_pages;
   p.max_pages = max_pages;
   p.tree_nodes = nodes;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
@@ -317,11 +346,11 @@ int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope,
   const bool pdl = ev0 == nullptr;
   if (ev0 && cudaEventRecord(ev0, stream) != cudaSuccess) return MLA_ERR_CUDA;
   cudaError_t le;
-  if (kind == CacheKind::kFp8) le = launch_tree_fp8(p, ppg, pdl, stream);
+  if (widen || !quant) le = launch_tree(encode, p, ppg, pdl, stream);
+  else if (kind == CacheKind::kFp8) le = launch_tree_fp8(p, ppg, pdl, stream);
   else if (kind == CacheKind::kFp4) le = launch_tree_fp4(p, ppg, pdl, stream);
   else if (kind == CacheKind::kFp8V41) le = launch_tree_fp8_v41(p, ppg, pdl, stream);
-  else if (kind == CacheKind::kFp4V41) le = launch_tree_fp4_v41(p, ppg, pdl, stream);
-  else le = launch_tree_bf16(maps, p, ppg, pdl, stream);
+  else le = launch_tree_fp4_v41(p, ppg, pdl, stream);
   if (le != cudaSuccess) return MLA_ERR_CUDA;
   if (ev1 && cudaEventRecord(ev1, stream) != cudaSuccess) return MLA_ERR_CUDA;
   if (launch_combine_plan(workspace, L, rows, 1, o, lse, pdl, stream, true) != cudaSuccess) return MLA_ERR_CUDA;
@@ -654,6 +683,13 @@ int mla_workspace_size_tree(int batch, int nodes, int num_heads, int page_size, 
   if (pairs <= 0) return MLA_ERR_CUDA;
   *bytes = ws_layout(batch > 0 ? batch * nodes : 1, 1, pairs, 0, true).total;
   return MLA_OK;
+}
+
+int mla_workspace_size_tree_widened(int batch, int nodes, int num_heads, int page_size, int max_pages, size_t* bytes) {
+  if (max_pages <= 0) return MLA_ERR_INVALID_ARG;
+  const int rc = mla_workspace_size_tree(batch, nodes, num_heads, page_size, bytes);
+  if (rc == MLA_OK) *bytes += widened_bytes(batch, max_pages);
+  return rc;
 }
 
 int mla_decode_tree_bf16(const uint16_t* q_absorbed, const uint16_t* q_rope, const uint16_t* kv_cache,

@@ -74,6 +74,7 @@
 #include <cstring>
 
 #include "decode.cuh"
+#include "walk.cuh"
 
 namespace mla {
 
@@ -216,39 +217,6 @@ constexpr float kRescaleThreshold = kModeF16<kMode> ? 15.0f : 16.0f;
 // the f16 scale itself normal.
 constexpr uint32_t kF16ScaleLo = 113, kF16ScaleHi = 134;
 constexpr float kF16Max = 65504.0f;
-
-struct Segment {
-  int b;          // batch row
-  int t0, t1;     // row-local page range [t0, t1)
-};
-
-// Walks the segments of one pair: the pair's page range [lo, hi) cut at row
-// boundaries.  Every role of both ranks walks the same sequence; inside a
-// segment the half pages [2*t0, 2*t1) are taken kTileHalves at a time.
-struct SegWalker {
-  const int* tile_start;
-  int batch, b, lo, hi;
-  // b0: the row holding page lo (the planner's pair_b0)
-  __device__ void init(const int* ts, int nb, int lo_, int hi_, int b0) {
-    tile_start = ts; batch = nb; lo = lo_; hi = hi_;
-    b = lo >= hi ? nb : b0;
-  }
-  __device__ bool next(Segment& s) {
-    while (b < batch) {
-      const int a = __ldg(tile_start + b), e = __ldg(tile_start + b + 1);
-      if (a >= hi) { b = batch; return false; }
-      const int cb = b++;
-      if (e >= hi) b = batch;   // this segment reaches the end of the range: no read for the next call
-      if (e > a) {
-        s.b = cb;
-        s.t0 = max(lo, a) - a;
-        s.t1 = min(hi, e) - a;
-        if (s.t1 > s.t0) return true;
-      }
-    }
-    return false;
-  }
-};
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t d;
@@ -524,18 +492,6 @@ __device__ __forceinline__ void load_q_rolled(const uint8_t* qa, const uint8_t* 
     for (int v = 0; v < 4; ++v) ptx::ld_global_nc_v8(src + 32 * v, r0 + 8 * v);
     ptx::tmem_st32(taddr + 32u * c, r0);
   }
-}
-
-// Tree decode: bits of the columns starting at some token that a node sees,
-// `ctx` of them context (may be negative or large), `valid` of them at most;
-// draft token a is column ctx + a and seen when bit a of `seen` is set.
-__device__ __forceinline__ uint64_t tree_bits(uint64_t seen, int ctx, int valid) {
-  uint64_t m;
-  if (ctx >= 64) m = ~uint64_t{0};
-  else if (ctx > 0) m = (seen << ctx) | ((uint64_t{1} << ctx) - 1);
-  else m = ctx > -64 ? seen >> -ctx : 0;
-  if (valid <= 0) return 0;
-  return valid >= 64 ? m : m & ((uint64_t{1} << valid) - 1);
 }
 
 }  // namespace dk
@@ -937,6 +893,7 @@ mla_decode_pair_kernel(const __grid_constant__ CacheMaps maps, const DecodeParam
     bool ok = true, range_flagged = false;
     while (ok && w.next(sg)) {
       const int hp_end = 2 * sg.t1;
+      const int tree_len = kTree ? lens[sg.b] : 0;
       for (int h0 = 2 * sg.t0; h0 < hp_end && ok; h0 += TH) {
         const int nh = min(TH, hp_end - h0);
         // rank 1: the tile's slots are free once S of the tile two back is done
@@ -976,6 +933,14 @@ mla_decode_pair_kernel(const __grid_constant__ CacheMaps maps, const DecodeParam
             } else {
               r0 = dequant_group<kF16>(row, g, o0);
               r1 = dequant_group<kF16>(row + 16 * kQRow, g, o1);
+            }
+            // tree: what a page holds behind the row's last token is not read, so
+            // it may hold any scale (a fresh page's zeros sent every call to the
+            // exact pass, at half the speed)
+            if constexpr (kTree) {
+              const int left = tree_len - (h0 + j) * kHalf;
+              r0 = r0 || t >= left;
+              r1 = r1 || t + 16 >= left;
             }
             if (kF16 && !range_flagged && __any_sync(0xffffffffu, !(r0 && r1))) {
               if (lane == 0) atomicExch(&hdr->fp8_range, 1);
@@ -1609,11 +1574,6 @@ cudaError_t launch_decode_sparse(const DecodeParams& p, int n_pairs, bool pdl, c
   CacheMaps unused;
   memset(&unused, 0, sizeof(unused));
   return launch_decode_mode<3>(unused, p, n_pairs, pdl, stream);
-}
-
-cudaError_t launch_tree_bf16(const CacheMaps& maps, const DecodeParams& p, int n_pairs, bool pdl,
-                             cudaStream_t stream) {
-  return launch_decode_mode<0, true>(maps, p, n_pairs, pdl, stream);
 }
 
 namespace {

@@ -21,6 +21,7 @@ struct DecodeParams {
   const int32_t* sp_slots;       // sparse decode: compacted slot lists [rows, topk] (workspace)
   int topk;
   int tree_nodes;                // tree decode: rows are (sequence, node) pairs, this many per sequence
+  int skip_chunk7;               // tree decode over widened V4.1 rows: query dims 448..511 are ignored
   __nv_bfloat16* out;            // [B, Sq, 128, 512]
   float* lse;                    // [B, Sq, 128]
   uint8_t* ws;
@@ -60,9 +61,8 @@ cudaError_t launch_decode_fp4_v41(const DecodeParams& p, int n_pairs, bool pdl, 
 // Sparse decode over the bf16 cache (p.kv_bf16, p.sp_slots; rows planned
 // with one query each).
 cudaError_t launch_decode_sparse(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream);
-// Tree decode over each cache format (p.tree_nodes set; rows planned with one
-// query each).
-cudaError_t launch_tree_bf16(const CacheMaps& maps, const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream);
+// Tree decode over the quantised formats (p.tree_nodes set; rows planned with
+// one query each).
 cudaError_t launch_tree_fp8(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream);
 cudaError_t launch_tree_fp4(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream);
 cudaError_t launch_tree_fp8_v41(const DecodeParams& p, int n_pairs, bool pdl, cudaStream_t stream);

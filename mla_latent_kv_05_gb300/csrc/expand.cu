@@ -57,34 +57,6 @@ enum Bar {
   DEMPTY = DFULL + 2, DRAIN = DEMPTY + 2, NBAR
 };
 
-// ------------------------------------------------------------ cta_group::2 pieces
-__device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(dst_smem), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void pair_tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(ncols) : "memory");
-}
-// D (+)= A B^T over the pair: A and D rows 128 of each CTA, B rows half from each
-__device__ __forceinline__ void pair_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
-}
-// arrive on the barrier at this offset in both CTAs once this thread's MMAs are done
-__device__ __forceinline__ void pair_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-               :: "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
-}
-// tiled loads whose bytes are counted on a barrier of either CTA of the pair (a cluster address)
-__device__ __forceinline__ void pair_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z,
-                                             uint64_t policy) {
-  asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-               " [%0], [%1, {%3, %4, %5}], [%2], %6;"
-               :: "r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy) : "memory");
-}
 // tiled store from shared memory, in this thread's bulk group
 __device__ __forceinline__ void store_4d(const void* tmap, uint32_t src, int x, int y, int z, int w, uint64_t policy) {
   asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4, %5}], [%1], %6;"
@@ -123,8 +95,8 @@ expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, Plan
     ptx::fence_barrier_init();
   }
   if (warp == 2) {
-    pair_tmem_alloc(tmem_slot, 512);
-    pair_tmem_relinquish();
+    ptx::pair_tmem_alloc(tmem_slot, 512);
+    ptx::pair_tmem_relinquish();
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -157,12 +129,12 @@ expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, Plan
             ok = wait_short<true>(BAR(WEMPTY + kb), (nw & 1u) ^ 1u, hdr);
             if (!ok) break;
             if (rank == 0) ptx::mbar_arrive_expect_tx(BAR(WFULL + kb), 2 * kBlock);
-            pair_load_3d(sbase + kb * kBlock, &maps.w[rank], ptx::mapa(BAR(WFULL + kb), 0), kb * kKBlock, 0, h, pol);
+            ptx::pair_load_3d(sbase + kb * kBlock, &maps.w[rank], ptx::mapa(BAR(WFULL + kb), 0), kb * kKBlock, 0, h, pol);
           }
           ok = wait_short<true>(BAR(CEMPTY + s), ph ^ 1u, hdr);
           if (!ok) break;
           if (rank == 0) ptx::mbar_arrive_expect_tx(BAR(CFULL + s), 2 * kBlock);
-          pair_load_3d(sbase + kOffRing + static_cast<uint32_t>(s) * kBlock, &maps.c, ptx::mapa(BAR(CFULL + s), 0),
+          ptx::pair_load_3d(sbase + kOffRing + static_cast<uint32_t>(s) * kBlock, &maps.c, ptx::mapa(BAR(CFULL + s), 0),
                        kb * kKBlock, m * 256 + static_cast<int>(rank) * 128, 0, pol);
           ++nc;
           if (++s == kStages) { s = 0; ph ^= 1u; }
@@ -208,10 +180,10 @@ expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, Plan
           const uint64_t db = desc_w + static_cast<uint64_t>(kb) * (kBlock >> 4);
 #pragma unroll
           for (int k = 0; k < kKBlock / 16; ++k)
-            pair_mma_ss(tmem + 256u * d, da + 2u * k, db + 2u * k, kIdesc, (kb > 0 || k > 0) ? 1u : 0u);
-          pair_commit(BAR(CEMPTY + s));
-          if (last) pair_commit(BAR(WEMPTY + kb));
-          if (kb == kKBlocks - 1) pair_commit(BAR(DFULL + d));
+            ptx::pair_mma_ss(tmem + 256u * d, da + 2u * k, db + 2u * k, kIdesc, (kb > 0 || k > 0) ? 1u : 0u);
+          ptx::pair_commit(BAR(CEMPTY + s));
+          if (last) ptx::pair_commit(BAR(WEMPTY + kb));
+          if (kb == kKBlocks - 1) ptx::pair_commit(BAR(DFULL + d));
         }
         __syncwarp();
         if (++s == kStages) { s = 0; ph ^= 1u; }
@@ -222,7 +194,7 @@ expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, Plan
     }
     // every MMA (and commit to the other rank) completes before the pair may leave
     if (lo < hi && elect_one()) {   // the lane that issued them
-      pair_commit(BAR(DRAIN));
+      ptx::pair_commit(BAR(DRAIN));
       wait_drain(BAR(DRAIN), 0u, hdr);
     }
     __syncwarp();
@@ -288,7 +260,7 @@ expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, Plan
   ptx::cluster_sync();
   if (warp == 2) {
     ptx::tc_fence_after();
-    pair_tmem_dealloc(tmem, 512);
+    ptx::pair_tmem_dealloc(tmem, 512);
   }
 }
 

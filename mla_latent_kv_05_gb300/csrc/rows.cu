@@ -280,6 +280,35 @@ __global__ void __launch_bounds__(kGroupRows * kRow / kPiece) gather_kernel(cons
   }
 }
 
+// The pages of a batch of sequences as bf16 rows: token t of sequence b becomes
+// row b max_pages 64 + t, for the tokens of the pages that the sequence reaches
+// (zeros behind its end).  blockIdx.y is the sequence, whose pages the CTAs of
+// a column share.
+template <RowFormat F>
+__global__ void __launch_bounds__(kGroupRows * kRow / kPiece) widen_kernel(const RowsParams p) {
+  constexpr int kPieces = kRow / kPiece;
+  const int r = threadIdx.x / kPieces, j = threadIdx.x - r * kPieces;
+  const int b = blockIdx.y, len = min(__ldg(p.seq_lens + b), p.max_pages * kPage);
+  for (int t = blockIdx.x; t * kPage < len; t += gridDim.x) {
+    const size_t at = static_cast<size_t>(b) * p.max_pages + t;
+    const int page = __ldg(p.block_table + at);
+    const bool bad = page < 0 || page >= p.num_pages;
+    if (bad && threadIdx.x == 0) set_status(p.status, MLA_STATUS_BAD_PAGE);
+#pragma unroll 1
+    for (int i = r; i < kPage; i += 4 * kGroupRows) {
+      Piece x[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int row = i + g * kGroupRows;
+        x[g] = read_piece<F>(p, bad || t * kPage + row >= len ? -1 : page * kPage + row, j);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<uint4*>(p.out + (at * kPage + i + g * kGroupRows) * kRow + j * kPiece) = values_of<F>(x[g]);
+    }
+  }
+}
+
 // Rows of a call from which a CTA takes four groups instead of one.
 constexpr int kLongCall = 8192;
 
@@ -297,6 +326,22 @@ cudaError_t launch(const RowsParams& p, bool append, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t launch_widen(RowFormat fmt, const RowsParams& p, cudaStream_t stream) {
+  if (p.batch <= 0) return cudaSuccess;
+  // about 1000 CTAs are resident; at least eight columns for a batch of uneven lengths
+  const int share = (1024 + p.batch - 1) / p.batch;
+  const int columns = share < 8 ? 8 : share;
+  const dim3 grid(columns < p.max_pages ? columns : p.max_pages, p.batch), block(kGroupRows * kRow / kPiece);
+  switch (fmt) {
+    case RowFormat::kBf16: break;
+    case RowFormat::kFp8: return launch_kernel(widen_kernel<RowFormat::kFp8>, grid, block, 0, stream, p);
+    case RowFormat::kFp4: return launch_kernel(widen_kernel<RowFormat::kFp4>, grid, block, 0, stream, p);
+    case RowFormat::kFp8V41: return launch_kernel(widen_kernel<RowFormat::kFp8V41>, grid, block, 0, stream, p);
+    case RowFormat::kFp4V41: return launch_kernel(widen_kernel<RowFormat::kFp4V41>, grid, block, 0, stream, p);
+  }
+  return cudaErrorInvalidValue;
+}
 
 cudaError_t launch_rows(RowFormat fmt, const RowsParams& p, bool append, cudaStream_t stream) {
   if (p.rows <= 0) return cudaSuccess;

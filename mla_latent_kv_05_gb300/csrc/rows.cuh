@@ -17,10 +17,14 @@ struct RowsParams {
   const int32_t* seq_lens;       // [batch]
   const int32_t* cu_rows;        // [batch + 1]
   int batch, rows, num_pages, max_pages;
-  __nv_bfloat16* out;            // gather: [rows, 576]
+  __nv_bfloat16* out;            // gather and widen: rows of 576
   int* status;
 };
 
+// The sequences' pages in a quantised format as bf16 rows [batch, max_pages 64,
+// 576] in p.out (p.cache, block_table, seq_lens, batch, num_pages, max_pages
+// set; batch <= 65535).
+cudaError_t launch_widen(RowFormat fmt, const RowsParams& p, cudaStream_t stream);
 cudaError_t launch_rows(RowFormat fmt, const RowsParams& p, bool append, cudaStream_t stream);
 
 }  // namespace mla
