@@ -255,7 +255,7 @@ int run_sparse(const uint16_t* q_absorbed, const uint16_t* q_rope, const void* k
   return MLA_OK;
 }
 
-// Pages per pair of a small tree decode.  Eight nodes over 200 tokens take 26.1
+// Pages per pair of a small tree decode.  Eight nodes over 200 tokens took 26.1
 // us at eight pages a pair and 18.6 at four (1008 tokens: 26.9 and 24.8); at two
 // the merge of more parts costs more (4 x 8 nodes over 500 tokens: 22.7 and 28.8).
 constexpr long long kTreePagesPerPair = 4;
@@ -263,8 +263,8 @@ constexpr long long kTreePagesPerPair = 4;
 // A quantised cache's tree decode first widens the live pages to bf16 rows, once
 // for all nodes, when the workspace has room for them: the attention then runs
 // at the bf16 rate.  Two nodes pay for it already: 64 x 2 nodes over 4096 fp8
-// tokens take 235 us so and 321 over the codes (fp4: 207 and 293), 64 x 4 334
-// and 582, 8 x 61 342 and 1080; small calls gain too (1 x 2 over 500: 22.8 us).
+// tokens take 214 us so and 322 over the codes (fp4: 187 and 297), 64 x 4 282
+// and 583, 8 x 61 340 and 1080; small calls gain too (1 x 2 over 500: 23 and 44).
 constexpr int kWidenNodes = 2;
 size_t widened_bytes(int batch, int max_pages) {
   return static_cast<size_t>(batch) * max_pages * kPage * kRow * 2;
@@ -298,10 +298,14 @@ int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope,
   const bool quant = kind != CacheKind::kBf16;
   const bool widen = quant && nodes >= kWidenNodes && workspace_bytes >= L.total + widened_bytes(batch, max_pages) &&
                      static_cast<long long>(batch) * max_pages * kPage < INT_MAX / 2;
+  // The bf16 kernel's rows are planned node by node: pairs that work on
+  // different nodes of a sequence then read its rows at about the same time,
+  // and from L2, when the batch's rows together exceed it.
+  const bool by_node = widen || !quant;
   auto encode = encode_fn();
   if (!encode) return MLA_ERR_CUDA;
   __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out);
-  if (launch_tree_prep(parents, n_nodes, seq_lens, batch, nodes, max_pages, workspace, L, o, lse, stream) != cudaSuccess)
+  if (launch_tree_prep(parents, n_nodes, seq_lens, batch, nodes, max_pages, by_node, workspace, L, o, lse, stream) != cudaSuccess)
     return MLA_ERR_CUDA;
   uint8_t* rows16 = static_cast<uint8_t*>(workspace) + L.total;
   if (widen) {
@@ -336,6 +340,7 @@ int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope,
   p.num_pages = widen ? batch * max_pages : num_pages;
   p.max_pages = max_pages;
   p.tree_nodes = nodes;
+  p.tree_seqs = batch;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.out = o;
   p.lse = lse;
@@ -346,14 +351,14 @@ int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope,
   const bool pdl = ev0 == nullptr;
   if (ev0 && cudaEventRecord(ev0, stream) != cudaSuccess) return MLA_ERR_CUDA;
   cudaError_t le;
-  if (widen || !quant) le = launch_tree(encode, p, ppg, pdl, stream);
+  if (by_node) le = launch_tree(encode, p, ppg, pdl, stream);
   else if (kind == CacheKind::kFp8) le = launch_tree_fp8(p, ppg, pdl, stream);
   else if (kind == CacheKind::kFp4) le = launch_tree_fp4(p, ppg, pdl, stream);
   else if (kind == CacheKind::kFp8V41) le = launch_tree_fp8_v41(p, ppg, pdl, stream);
   else le = launch_tree_fp4_v41(p, ppg, pdl, stream);
   if (le != cudaSuccess) return MLA_ERR_CUDA;
   if (ev1 && cudaEventRecord(ev1, stream) != cudaSuccess) return MLA_ERR_CUDA;
-  if (launch_combine_plan(workspace, L, rows, 1, o, lse, pdl, stream, true) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_combine_plan(workspace, L, rows, 1, o, lse, pdl, stream, true, by_node ? batch : 0) != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }
 

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 // part) or the planner (no token).  Four parts' loads are in flight at a
 // time; the parts are summed in slot order.
 template <bool kF32>
-__global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __restrict__ ws, WsLayout Lw, int sq,
+__global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __restrict__ ws, WsLayout Lw, int sq, int seqs,
                                                            __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
   // The plan (part counts and slot bases) was written by the planner, which
   // completed before the attention kernel let this grid launch, so it is read
@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __rest
       for (int e = 0; e < 16; ++e) acc[e] *= r;
     }
     L = Ln;
-    const float wl = (v == -INFINITY || L == -INFINITY) ? 0.f : __expf(v - L);
+    // (tree decode: a part that is NaN makes the row NaN, also when all parts are)
+    const float wl = (v == -INFINITY || (!kF32 && L == -INFINITY)) ? 0.f : __expf(v - L);
     for (int j0 = 0; j0 < n; j0 += 4) {
       if (j0 > 0) {
 #pragma unroll
@@ -180,21 +181,24 @@ __global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __rest
       }
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum > 0.f ? 1.f / sum : kF32 ? sum : 0.f;
+  // rows planned node by node go back to their sequence's place
+  const int row = seqs > 0 ? k % seqs * static_cast<int>(gridDim.x / seqs) + k / seqs : k;
   uint32_t o[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     __nv_bfloat162 bb = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     o[e] = *reinterpret_cast<uint32_t*>(&bb);
   }
-  ptx::st_global_v8(out + (static_cast<size_t>(k) * kHeads + h) * kDc + 16 * lane, o);
-  if (lane == 0) lse[static_cast<size_t>(k) * kHeads + h] = sum > 0.f ? L + logf(sum) : -INFINITY;
+  ptx::st_global_v8(out + (static_cast<size_t>(row) * kHeads + h) * kDc + 16 * lane, o);
+  if (lane == 0)
+    lse[static_cast<size_t>(row) * kHeads + h] = sum > 0.f || (kF32 && sum != 0.f) ? L + logf(sum) : -INFINITY;
 }
 
 }  // namespace
 
 cudaError_t launch_combine_plan(const void* ws, const WsLayout& Lw, int batch, int sq, __nv_bfloat16* out, float* lse,
-                                bool pdl, cudaStream_t stream, bool f32) {
+                                bool pdl, cudaStream_t stream, bool f32, int seqs) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(batch * sq, kHeads / 8, 1);
   cfg.blockDim = dim3(256, 1, 1);
@@ -205,7 +209,7 @@ cudaError_t launch_combine_plan(const void* ws, const WsLayout& Lw, int batch, i
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, f32 ? combine_plan_kernel<true> : combine_plan_kernel<false>,
-                            static_cast<const uint8_t*>(ws), Lw, sq, out, lse);
+                            static_cast<const uint8_t*>(ws), Lw, sq, seqs, out, lse);
 }
 
 // Public merge: parts of row r are [indptr[r], indptr[r+1]).

@@ -21,6 +21,7 @@ struct DecodeParams {
   const int32_t* sp_slots;       // sparse decode: compacted slot lists [rows, topk] (workspace)
   int topk;
   int tree_nodes;                // tree decode: rows are (sequence, node) pairs, this many per sequence
+  int tree_seqs;                 // tree decode in launch_tree: planned row = node * tree_seqs + sequence
   int skip_chunk7;               // tree decode over widened V4.1 rows: query dims 448..511 are ignored
   __nv_bfloat16* out;            // [B, Sq, 128, 512]
   float* lse;                    // [B, Sq, 128]
@@ -39,8 +40,8 @@ cudaError_t launch_sparse_prep(const int32_t* token_slots, int rows, int topk, i
 // the draft nodes it sees, into the workspace; rows with nothing to see are
 // written here (out = 0, lse = -inf).
 cudaError_t launch_tree_prep(const int32_t* parents, const int32_t* n_nodes, const int32_t* seq_lens, int batch,
-                             int nodes, int max_pages, void* ws, const WsLayout& L, __nv_bfloat16* out, float* lse,
-                             cudaStream_t stream);
+                             int nodes, int max_pages, bool by_node, void* ws, const WsLayout& L, __nv_bfloat16* out,
+                             float* lse, cudaStream_t stream);
 // TMA descriptors of the bf16 cache (4-D: 64 columns, 8 rows, 9 chunks, row
 // groups).  The score SM loads chunks 0..4 (k) and 5..8 (kb) of a half page,
 // or of a whole page when a tile's two adjacent slots are the two halves of
@@ -71,9 +72,10 @@ int decode_max_pairs();
 // W^UV up-projection of latent outputs (see wuv.cu).
 cudaError_t launch_wuv(PFN_cuTensorMapEncodeTiled_v12000 encode, const void* o, const void* w, int rows, void* out,
                        void* hdr, cudaStream_t stream);
-// f32: the partials are fp32 (tree decode) instead of bf16.
+// f32: the partials are fp32 (tree decode) instead of bf16.  seqs > 0: planned
+// row k is node k / seqs of sequence k % seqs.
 cudaError_t launch_combine_plan(const void* ws, const WsLayout& Lw, int batch, int sq, __nv_bfloat16* out, float* lse,
-                                bool pdl, cudaStream_t stream, bool f32 = false);
+                                bool pdl, cudaStream_t stream, bool f32 = false, int seqs = 0);
 cudaError_t launch_combine_indptr(const float* part_out, const float* part_lse, const int32_t* indptr, int rows,
                                   __nv_bfloat16* out, float* lse, cudaStream_t stream);
 

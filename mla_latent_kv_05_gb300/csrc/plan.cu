@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(256) sparse_prep_kernel(const int32_t* __restr
 // have length 0; this CTA writes their output.
 __global__ void __launch_bounds__(128) tree_prep_kernel(const int32_t* __restrict__ parents,
                                                         const int32_t* __restrict__ n_nodes,
-                                                        const int32_t* __restrict__ seq_lens, int nodes, int max_len,
+                                                        const int32_t* __restrict__ seq_lens, int nodes, int max_len, bool by_node,
                                                         uint8_t* __restrict__ ws, WsLayout L,
                                                         __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
   __shared__ int s_parent[kMaxNodes];
@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(128) tree_prep_kernel(const int32_t* __restric
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(ws);
   const int b = blockIdx.y, i = blockIdx.x;
   const size_t row = static_cast<size_t>(b) * nodes + i;
+  const size_t planned = by_node ? static_cast<size_t>(i) * gridDim.y + b : row;
   if (threadIdx.x <= i) s_parent[threadIdx.x] = parents[static_cast<size_t>(b) * nodes + threadIdx.x];
   const int n = n_nodes ? n_nodes[b] : nodes;
   const int seq = seq_lens[b];
@@ -348,8 +349,8 @@ __global__ void __launch_bounds__(128) tree_prep_kernel(const int32_t* __restric
         a = up;
       }
     }
-    reinterpret_cast<int*>(ws + L.sp_lens)[row] = len;
-    reinterpret_cast<uint64_t*>(ws + L.tree_seen)[row] = seen;
+    reinterpret_cast<int*>(ws + L.sp_lens)[planned] = len;
+    reinterpret_cast<uint64_t*>(ws + L.tree_seen)[planned] = seen;
     s_len = len;
   }
   __syncthreads();
@@ -363,10 +364,10 @@ __global__ void __launch_bounds__(128) tree_prep_kernel(const int32_t* __restric
 }  // namespace
 
 cudaError_t launch_tree_prep(const int32_t* parents, const int32_t* n_nodes, const int32_t* seq_lens, int batch,
-                             int nodes, int max_pages, void* ws, const WsLayout& L, __nv_bfloat16* out, float* lse,
-                             cudaStream_t stream) {
+                             int nodes, int max_pages, bool by_node, void* ws, const WsLayout& L, __nv_bfloat16* out,
+                             float* lse, cudaStream_t stream) {
   return launch_kernel(tree_prep_kernel, dim3(nodes, batch), dim3(128), 0, stream, parents, n_nodes, seq_lens, nodes,
-                       max_pages * kPage, static_cast<uint8_t*>(ws), L, out, lse);
+                       max_pages * kPage, by_node, static_cast<uint8_t*>(ws), L, out, lse);
 }
 
 cudaError_t launch_sparse_prep(const int32_t* token_slots, int rows, int topk, int num_slots, void* ws,

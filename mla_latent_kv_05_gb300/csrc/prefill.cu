@@ -181,13 +181,6 @@ struct Maps {
 };
 
 // 32 lanes x 16 columns to tensor memory.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32"
-               " [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-                  "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-               : "memory");
-}
 
 // Registers (128 a thread at launch): 80 for warps 0..3, 96 for the output
 // warps, 168 for the softmax warps (4 * 80 + 4 * 96 + 8 * 168 = 16 * 128),

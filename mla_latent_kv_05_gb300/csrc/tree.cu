@@ -38,11 +38,15 @@
 // here, so a bf16 rounding of each would be as large as the result's own.
 // Every wait is bounded, as in the decode kernel.
 //
-// Measured, whole call: 8 x 61 nodes over 4096 tokens 344 us (1630 TFLOP/s; the
-// decode kernel's form of it 554), 16 x 16 over up to 8192 205 us (1387), 8 nodes
-// over 1000 25 us (four kernels of 2 to 6 us and their gaps).  A tile takes about
-// 2560 cycles, 2184 of them MMAs; what remains is waiting for V's second page
-// (272 KiB of rows a tile and pair, 48 bytes a cycle for each SM from L2).
+// Rows are planned node by node, not sequence by sequence: pairs then work on
+// different nodes of one sequence at a time and find its rows in L2 (64 x 4
+// nodes over 4096 tokens: 247 us by sequence, 199 by node).
+//
+// Measured, whole call: 8 x 61 nodes over 4096 tokens 339 us (1655 TFLOP/s; the
+// decode kernel's form of it 554), 16 x 16 over up to 8192 199 us (1429), 8 nodes
+// over 1000 23 us (four kernels of 2 to 11 us).  A tile takes about 2500 cycles,
+// 2184 of them MMAs; what remains is waiting for V's second page (272 KiB of
+// rows a tile and pair, 50 bytes a cycle for each SM from L2).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -155,6 +159,8 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
   const int lo = pair_lo[pl], hi = pair_lo[pl + 1];
   const int b0 = reinterpret_cast<const int*>(p.ws + p.L.pair_b0)[pl];
 
+  // rows are planned node by node (see api.cu); queries and results lie by sequence
+  auto out_row = [&](int row) { return row % p.tree_seqs * p.tree_nodes + row / p.tree_seqs; };
   // a tile's page (row of its first token): one past the segment, or a bad one, is
   // read outside the cache, which fills zeros
   auto page_row = [&](int b, int t, int t1) {
@@ -175,11 +181,11 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
         ok = wait_short<true>(BAR(QEMPTY), (nq & 1u) ^ 1u, hdr);
         if (!ok) break;
         if (rank == 0) ptx::mbar_arrive_expect_tx(BAR(QFULL), 2 * 9 * kChunk);
-        const int head = sg.b * kHeads + static_cast<int>(rank) * 64;
+        const int head = out_row(sg.b) * kHeads + static_cast<int>(rank) * 64;
         ptx::pair_load_3d(sbase, &maps.q, LEAD(QFULL), 0, head, 0, pol);
         ptx::pair_load_3d(sbase + 8 * kChunk, &maps.qr, LEAD(QFULL), 0, head, 0, pol);
         ++nq;
-        const int seq = sg.b / p.tree_nodes;
+        const int seq = sg.b % p.tree_seqs;
         for (int t = sg.t0; t < sg.t1 && ok; t += 2) {
           const int row = page_row(seq, t + static_cast<int>(rank), sg.t1);
 #pragma unroll 1
@@ -210,7 +216,7 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
       uint32_t nt = 0;
       bool ok = true;
       while (ok && w.next(sg)) {
-        const int seq = sg.b / p.tree_nodes;
+        const int seq = sg.b % p.tree_seqs;
         for (int t = sg.t0; t < sg.t1 && ok; t += 2) {
 #pragma unroll 1
           for (int a = 0; a < 2 && ok; ++a) {
@@ -327,8 +333,11 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
     // (a wait that gave up) takes effect only once the others have heard of it.
     while (w.next(sg)) {
       const int row = sg.b, len = lens[row];
-      const int ctx = len - 1 - row % p.tree_nodes;        // tokens of the context
+      const int ctx = len - 1 - row / p.tree_seqs;         // tokens of the context
       const uint64_t seen = tree_seen[row];
+      // where the result goes: read here, so that its latency passes beside the first tile's
+      const int parts = n_parts[row];
+      const int slot = parts > 1 ? slot_base[row] + pair_rank[pl] - pair_rank[first_pair[row]] : 0;
       float mc = 0.f, m_ref = -INFINITY, l = 0.f;
       bool quit = false;
       for (int t = sg.t0; t < sg.t1; t += 2) {
@@ -400,12 +409,13 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
         // V has landed; rows the node does not see get V = 0 (P = 0 alone would
         // turn an infinity or a NaN there into NaN)
         if (!wait_short_warp(BAR(VFULL + hf), n & 1u, hdr)) ok = false;
-        for (uint32_t hide = __shfl_sync(0xffffffffu, ~see, 0); hide != 0; hide &= hide - 1) {
-          // half of the row by each of the two warps (heads) that know of it, a chunk by eight lanes
-          const int r = 32 * cf + __ffs(static_cast<int>(hide)) - 1, q = 16 * (wq & 1) + lane;
-          if (lane < 16)
-            *reinterpret_cast<uint4*>(smem + kOffV + hf * kVPage + (q >> 3) * kChunk + r * 128 + (q & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
+        if (see != 0xffffffffu) {              // the same for every thread of the warp
+          // half of each row by either of the two warps that know of it, two rows at a time
+          const int q = 16 * (wq & 1) + (lane & 15);
+          uint8_t* dst = smem + kOffV + hf * kVPage + (q >> 3) * kChunk + (32 * cf + (lane >> 4)) * 128 + (q & 7) * 16;
+#pragma unroll
+          for (int r = 0; r < 32; r += 2)
+            if (!((see >> (r + (lane >> 4))) & 1u)) *reinterpret_cast<uint4*>(dst + r * 128) = make_uint4(0, 0, 0, 0);
         }
         ptx::fence_proxy_async_cta();
         ptx::tc_fence_before();
@@ -421,16 +431,14 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
       if (any_of_group(group, !ok)) break;
       l = (shared[0] + shared[64]) + (shared[128] + shared[192]);
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays NaN
-      const int parts = n_parts[row];
-      const int slot = parts > 1 ? slot_base[row] + pair_rank[pl] - pair_rank[first_pair[row]] : 0;
       if (hf == 0 && cf == 0) {
         const float lse = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
         if (parts > 1) reinterpret_cast<float*>(p.ws + p.L.part_lse)[static_cast<size_t>(slot) * kHeads + h] = lse;
-        else p.lse[static_cast<size_t>(row) * kHeads + h] = lse;
+        else p.lse[static_cast<size_t>(out_row(row)) * kHeads + h] = lse;
       }
       // this thread's quarter of the latent columns: [256 hf + 128 cf, +128)
       float* part = reinterpret_cast<float*>(p.ws + p.L.part_out) + (static_cast<size_t>(slot) * kHeads + h) * kDc + 256 * hf + 128 * cf;
-      __nv_bfloat16* dst = p.out + (static_cast<size_t>(row) * kHeads + h) * kDc + 256 * hf + 128 * cf;
+      __nv_bfloat16* dst = p.out + (static_cast<size_t>(out_row(row)) * kHeads + h) * kDc + 256 * hf + 128 * cf;
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         uint32_t o[32];
@@ -479,7 +487,7 @@ cudaError_t launch_tree(PFN_cuTensorMapEncodeTiled_v12000 encode, const DecodePa
   TreeMaps maps;
   auto map = [&](CUtensorMap* m, const void* base, cuuint64_t rows, cuuint64_t chunks, cuuint64_t row_bytes,
                  cuuint32_t box_chunks) {
-    const cuuint64_t dims[3] = {64, rows, chunks}, strides[2] = {row_bytes, chunks > 1 ? 128 : kTmaFar};
+    const cuuint64_t dims[3] = {64, rows, chunks > 1 ? chunks : 2}, strides[2] = {row_bytes, chunks > 1 ? 128 : kTmaFar};
     const cuuint32_t box[3] = {64, 64, box_chunks}, es[3] = {1, 1, 1};
     return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -10,7 +10,8 @@ struct TreeMaps {
   CUtensorMap q, qr, k, v;
 };
 
-// p.kv_bf16, p.tree_nodes set; rows planned with one query each.  p.block_table
+// p.kv_bf16, p.tree_nodes and p.tree_seqs set; rows planned with one query each,
+// node by node.  p.block_table
 // may be null: page t of sequence b is page b p.max_pages + t.
 cudaError_t launch_tree(PFN_cuTensorMapEncodeTiled_v12000 encode, const DecodeParams& p, int n_pairs, bool pdl,
                         cudaStream_t stream);

@@ -275,3 +275,27 @@ def test_prompt_chunk_draft_and_decode_together(cuda_device):
     # 1e-2 of sum p|v|), P, V or the latent, and the result (2^-8 each)
     mag = torch.einsum("hnm,hmd->nhd", p, v.abs())
     assert bool(((got - ref).abs() <= (1e-2 + 3 * 2.0 ** -8) * mag + 2.0 ** -8 * ref.abs()).all())
+
+
+@pytest.mark.parametrize("length", [40, 5000])
+def test_a_nan_query_gives_nan_rows_only_for_itself(cuda_device, length):
+    # 5000 tokens on one sequence: rows are split over several parts and merged
+    inp = gen.make_inputs(1, 4, [length], seed=13)
+    inp.q_absorbed[0, 2, 5] = float("nan")
+    out, lse = run(inp, chain(1, 4))
+    bad = torch.zeros((4, 128), dtype=torch.bool, device="cuda")
+    bad[2, 5] = True
+    assert torch.equal(torch.isnan(out[0]).all(-1), bad) and torch.equal(torch.isnan(out[0]).any(-1), bad)
+    assert torch.equal(torch.isnan(lse[0]), bad)
+
+
+def test_many_sequences_whose_rows_exceed_the_cache(cuda_device):
+    # several rows a pair, uneven lengths, an empty sequence and one without nodes
+    lens = [700 + 61 * b for b in range(40)]
+    lens[7], lens[11] = 6, 0
+    inp = gen.make_inputs(40, 6, lens, seed=14)
+    n = [6] * 40
+    n[11], n[20] = 0, 0
+    parents = random_tree(40, 6, 15)
+    rows = [(b, i) for b in (0, 7, 11, 20, 39) for i in (0, 5)]
+    check(*run(inp, parents, n), *reference(inp, parents, n, rows_only=rows), rows_only=rows)
