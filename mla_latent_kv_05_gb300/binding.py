@@ -117,6 +117,9 @@ def _stream(stream) -> ctypes.c_void_p:
 
 
 def _check(t: torch.Tensor, name: str, dtype, shape=None):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_cuda
+            and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if not t.is_cuda:
@@ -374,6 +377,43 @@ def _stride(t, dim: int, default: int) -> int:
     return int(t.stride(dim)) if t.shape[dim] > 1 else default
 
 
+# The two below pass an ordinary tensor with few attribute reads (a call's checks
+# cost the host several times its launches); every other goes through
+# _check_rows, which has the rules and the messages.
+def _rows_arg(t, name: str, width: int, rows: int | None = None):
+    """Address and row stride of a checked [rows, width] bf16 tensor or view."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda:
+        shape = t.shape
+        if len(shape) == 2 and shape[1] == width and shape[0] > 1 and (rows is None or shape[0] == rows):
+            s0, s1 = t.stride()
+            at = t.data_ptr()
+            if s1 == 1 and s0 > 0 and s0 % 8 == 0 and at % 16 == 0:
+                return at, s0
+    _check_rows(t, name, (width,), rows)
+    return t.data_ptr(), _stride(t, 0, width)
+
+
+def _heads_arg(t, name: str, width: int, rows: int | None = None):
+    """Address, row and head stride of a checked [rows, 128, width] bf16 tensor or view."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda:
+        shape = t.shape
+        if (len(shape) == 3 and shape[2] == width and shape[1] == 128 and shape[0] > 1
+                and (rows is None or shape[0] == rows)):
+            s0, s1, s2 = t.stride()
+            at = t.data_ptr()
+            if s2 == 1 and s0 > 0 and s1 > 0 and s0 % 8 == 0 and s1 % 8 == 0 and at % 16 == 0:
+                return at, s0, s1
+    _check_rows(t, name, (128, width), rows)
+    return t.data_ptr(), _stride(t, 0, 128 * width), int(t.stride(1))
+
+
+def _handle(stream, device: int) -> int:
+    """The stream's handle, of the device's current stream for None."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
 def _status_workspace(device) -> torch.Tensor:
     return torch.zeros(256, dtype=torch.uint8, device=device)
 
@@ -388,26 +428,31 @@ def _check_cache(fmt, kv_cache, block_table, seq_lens, cu_rows):
     _check(block_table, "block_table", torch.int32)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
-    _check(seq_lens, "seq_lens", torch.int32, (block_table.shape[0],))
-    _check(cu_rows, "cu_rows", torch.int32, (block_table.shape[0] + 1,))
+    batch = block_table.shape[0]
+    _check(seq_lens, "seq_lens", torch.int32, (batch,))
+    _check(cu_rows, "cu_rows", torch.int32, (batch + 1,))
 
 
 def _append(fmt, c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace, stream):
     name = "mla_cache_append_" + fmt
-    _check_rows(c_kv, "c_kv", (512,))
-    rows = int(c_kv.shape[0])
-    _check_rows(k_rope, "k_rope", (64,), rows)
+    c_at, c_stride = _rows_arg(c_kv, "c_kv", 512)
+    rows = c_kv.shape[0]
+    r_at, r_stride = _rows_arg(k_rope, "k_rope", 64, rows)
     _check_cache(fmt, kv_cache, block_table, seq_lens, cu_rows)
     if workspace is None:
         workspace = _status_workspace(kv_cache.device)
     _check(workspace, "workspace", torch.uint8)
-    _same_device(dict(kv_cache=kv_cache, c_kv=c_kv, k_rope=k_rope, block_table=block_table, seq_lens=seq_lens,
-                      cu_rows=cu_rows, workspace=workspace), torch.cuda.current_device())
+    dev = torch.cuda.current_device()
+    if not (kv_cache.device == c_kv.device == k_rope.device == block_table.device == seq_lens.device == cu_rows.device
+            == workspace.device and kv_cache.device.index == dev):
+        _same_device(dict(kv_cache=kv_cache, c_kv=c_kv, k_rope=k_rope, block_table=block_table, seq_lens=seq_lens,
+                          cu_rows=cu_rows, workspace=workspace), dev)
+    batch, max_pages = block_table.shape
+    pages, page_size, _ = kv_cache.shape
     rc = getattr(load(), name)(
-        _ptr(c_kv), _stride(c_kv, 0, 512), _ptr(k_rope), _stride(k_rope, 0, 64), _ptr(kv_cache), _ptr(block_table),
-        _ptr(seq_lens), _ptr(cu_rows), int(block_table.shape[0]), rows, int(kv_cache.shape[0]),
-        int(kv_cache.shape[1]), int(block_table.shape[1]), _ptr(workspace), ctypes.c_size_t(workspace.numel()),
-        _stream(stream))
+        c_at, c_stride, r_at, r_stride, kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        cu_rows.data_ptr(), batch, rows, pages, page_size, max_pages, workspace.data_ptr(), workspace.numel(),
+        _handle(stream, dev))
     if rc != MLA_OK and rows:       # empty tensors have null pointers: nothing to do
         raise MLAError(rc, name)
     return kv_cache
@@ -421,16 +466,21 @@ def _gather(fmt, kv_cache, block_table, seq_lens, cu_rows, n_rows, out, workspac
         raise ValueError("n_rows must not be negative")
     if out is None:
         out = torch.empty((rows, 576), dtype=torch.bfloat16, device=kv_cache.device)
-    _check(out, "out", torch.bfloat16, (rows, 576))
+    else:
+        _check(out, "out", torch.bfloat16, (rows, 576))
     if workspace is None:
         workspace = _status_workspace(kv_cache.device)
     _check(workspace, "workspace", torch.uint8)
-    _same_device(dict(kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, cu_rows=cu_rows, out=out,
-                      workspace=workspace), torch.cuda.current_device())
+    dev = torch.cuda.current_device()
+    if not (kv_cache.device == block_table.device == seq_lens.device == cu_rows.device == out.device
+            == workspace.device and kv_cache.device.index == dev):
+        _same_device(dict(kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, cu_rows=cu_rows, out=out,
+                          workspace=workspace), dev)
+    batch, max_pages = block_table.shape
+    pages, page_size, _ = kv_cache.shape
     rc = getattr(load(), name)(
-        _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens), _ptr(cu_rows), int(block_table.shape[0]), rows,
-        int(kv_cache.shape[0]), int(kv_cache.shape[1]), int(block_table.shape[1]), _ptr(out), _ptr(workspace),
-        ctypes.c_size_t(workspace.numel()), _stream(stream))
+        kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_rows.data_ptr(), batch, rows, pages,
+        page_size, max_pages, out.data_ptr(), workspace.data_ptr(), workspace.numel(), _handle(stream, dev))
     if rc != MLA_OK and rows:
         raise MLAError(rc, name)
     return out
@@ -547,23 +597,29 @@ def _tree(fmt, q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, sca
         _check(n_nodes, "n_nodes", torch.int32, (B,))
     if out is None:
         out = torch.empty((B, T, H, 512), dtype=torch.bfloat16, device=q_absorbed.device)
+    else:
+        _check(out, "out", torch.bfloat16, (B, T, H, 512))
     if lse is None:
         lse = torch.empty((B, T, H), dtype=torch.float32, device=q_absorbed.device)
-    _check(out, "out", torch.bfloat16, (B, T, H, 512))
-    _check(lse, "lse", torch.float32, (B, T, H))
+    else:
+        _check(lse, "lse", torch.float32, (B, T, H))
+    max_pages = block_table.shape[1]
     if workspace is None:
-        pages = int(block_table.shape[1])
-        widen = fmt != "bf16" and T > 1 and B * pages * _WIDENED_PAGE <= _WIDENED_DEFAULT
-        workspace = alloc_workspace_tree(B, T, q_absorbed.device, pages if widen else 0)
+        widen = fmt != "bf16" and T > 1 and B * max_pages * _WIDENED_PAGE <= _WIDENED_DEFAULT
+        workspace = alloc_workspace_tree(B, T, q_absorbed.device, max_pages if widen else 0)
     _check(workspace, "workspace", torch.uint8)
-    _same_device(dict(q_absorbed=q_absorbed, q_rope=q_rope, kv_cache=kv_cache, block_table=block_table,
-                      seq_lens=seq_lens, parents=parents, n_nodes=n_nodes, out=out, lse=lse, workspace=workspace),
-                 torch.cuda.current_device())
+    dev = torch.cuda.current_device()
+    if not (q_absorbed.device == q_rope.device == kv_cache.device == block_table.device == seq_lens.device
+            == parents.device == out.device == lse.device == workspace.device
+            and (n_nodes is None or n_nodes.device == out.device) and out.device.index == dev):
+        _same_device(dict(q_absorbed=q_absorbed, q_rope=q_rope, kv_cache=kv_cache, block_table=block_table,
+                          seq_lens=seq_lens, parents=parents, n_nodes=n_nodes, out=out, lse=lse, workspace=workspace),
+                     dev)
+    pages, page_size, _ = kv_cache.shape
     rc = getattr(load(), name)(
-        _ptr(q_absorbed), _ptr(q_rope), _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens), _ptr(parents),
-        _ptr(n_nodes), int(B), int(T), int(H), int(kv_cache.shape[0]), int(kv_cache.shape[1]),
-        int(block_table.shape[1]), ctypes.c_float(float(scale)), _ptr(out), _ptr(lse), _ptr(workspace),
-        ctypes.c_size_t(workspace.numel()), _stream(stream))
+        q_absorbed.data_ptr(), q_rope.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        parents.data_ptr(), None if n_nodes is None else n_nodes.data_ptr(), B, T, H, pages, page_size, max_pages,
+        float(scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _handle(stream, dev))
     if rc != MLA_OK:
         raise MLAError(rc, name)
     return out, lse
@@ -612,26 +668,33 @@ def mla_expand_kv(latent, w_uk, w_uv, k_nope=None, v=None, workspace=None, strea
     """k_nope[t, h] = w_uk[h] @ latent[t], v[t, h] = w_uv[h] @ latent[t]:
     latent [n, 512] bf16 (a view with a 16-byte row stride, such as gathered
     rows' [:, :512]), w_uk, w_uv [128, 128, 512] bf16 -> two [n, 128, 128]."""
-    _check_rows(latent, "latent", (512,))
+    at, stride = _rows_arg(latent, "latent", 512)
     _check(w_uk, "w_uk", torch.bfloat16, (128, 128, 512))
     _check(w_uv, "w_uv", torch.bfloat16, (128, 128, 512))
-    n = int(latent.shape[0])
+    n = latent.shape[0]
     if k_nope is None:
         k_nope = torch.empty((n, 128, 128), dtype=torch.bfloat16, device=latent.device)
+    else:
+        _check(k_nope, "k_nope", torch.bfloat16, (n, 128, 128))
     if v is None:
         v = torch.empty((n, 128, 128), dtype=torch.bfloat16, device=latent.device)
-    _check(k_nope, "k_nope", torch.bfloat16, (n, 128, 128))
-    _check(v, "v", torch.bfloat16, (n, 128, 128))
+    else:
+        _check(v, "v", torch.bfloat16, (n, 128, 128))
     if workspace is None:
         workspace = _status_workspace(latent.device)
     _check(workspace, "workspace", torch.uint8)
-    _same_device(dict(latent=latent, w_uk=w_uk, w_uv=w_uv, k_nope=k_nope, v=v, workspace=workspace),
-                 torch.cuda.current_device())
-    rc = load().mla_expand_kv(_ptr(latent), _stride(latent, 0, 512), _ptr(w_uk), _ptr(w_uv), n, 128, 128, _ptr(k_nope),
-                              _ptr(v), _ptr(workspace), ctypes.c_size_t(workspace.numel()), _stream(stream))
+    dev = torch.cuda.current_device()
+    if not (latent.device == w_uk.device == w_uv.device == k_nope.device == v.device == workspace.device
+            and latent.device.index == dev):
+        _same_device(dict(latent=latent, w_uk=w_uk, w_uv=w_uv, k_nope=k_nope, v=v, workspace=workspace), dev)
+    rc = load().mla_expand_kv(at, stride, w_uk.data_ptr(), w_uv.data_ptr(), n, 128, 128, k_nope.data_ptr(),
+                              v.data_ptr(), workspace.data_ptr(), workspace.numel(), _handle(stream, dev))
     if rc != MLA_OK and n:
         raise MLAError(rc, "mla_expand_kv")
     return k_nope, v
+
+
+_Strides = ctypes.c_size_t * 9
 
 
 def mla_workspace_size_prefill(batch: int, num_q: int) -> int:
@@ -656,39 +719,41 @@ def mla_prefill_bf16(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, scale, causa
     allowed), cu_q, cu_k int32 [B + 1].  causal: query i of a sequence's n_q
     sees keys j <= i + n_k - n_q.  Returns (out [nq, 128, 128] bf16, lse
     [nq, 128] fp32); rows past cu_q[B] are left as they were."""
-    _check_rows(q_nope, "q_nope", (128, 128))
-    nq = int(q_nope.shape[0])
-    _check_rows(q_rope, "q_rope", (128, 64), nq)
-    _check_rows(k_nope, "k_nope", (128, 128))
-    nk = int(k_nope.shape[0])
-    _check_rows(k_rope, "k_rope", (64,), nk)
-    _check_rows(v, "v", (128, 128), nk)
+    qn = _heads_arg(q_nope, "q_nope", 128)
+    nq = q_nope.shape[0]
+    qr = _heads_arg(q_rope, "q_rope", 64, nq)
+    kn = _heads_arg(k_nope, "k_nope", 128)
+    nk = k_nope.shape[0]
+    kr = _rows_arg(k_rope, "k_rope", 64, nk)
+    vv = _heads_arg(v, "v", 128, nk)
     _check(cu_q, "cu_q", torch.int32)
     if cu_q.dim() != 1 or cu_q.numel() < 1:
         raise ValueError("cu_q must be [B + 1]")
-    B = int(cu_q.numel()) - 1
+    B = cu_q.numel() - 1
     _check(cu_k, "cu_k", torch.int32, (B + 1,))
     if out is None:
         out = torch.empty((nq, 128, 128), dtype=torch.bfloat16, device=q_nope.device)
+    else:
+        _check(out, "out", torch.bfloat16, (nq, 128, 128))
     if lse is None:
         lse = torch.empty((nq, 128), dtype=torch.float32, device=q_nope.device)
-    _check(out, "out", torch.bfloat16, (nq, 128, 128))
-    _check(lse, "lse", torch.float32, (nq, 128))
+    else:
+        _check(lse, "lse", torch.float32, (nq, 128))
     if workspace is None:
         workspace = alloc_workspace_prefill(B, nq, q_nope.device)
     _check(workspace, "workspace", torch.uint8)
-    _same_device(dict(q_nope=q_nope, q_rope=q_rope, k_nope=k_nope, k_rope=k_rope, v=v, cu_q=cu_q, cu_k=cu_k, out=out,
-                      lse=lse, workspace=workspace), torch.cuda.current_device())
+    dev = torch.cuda.current_device()
+    if not (q_nope.device == q_rope.device == k_nope.device == k_rope.device == v.device == cu_q.device == cu_k.device
+            == out.device == lse.device == workspace.device and q_nope.device.index == dev):
+        _same_device(dict(q_nope=q_nope, q_rope=q_rope, k_nope=k_nope, k_rope=k_rope, v=v, cu_q=cu_q, cu_k=cu_k,
+                          out=out, lse=lse, workspace=workspace), dev)
     if nq == 0:
         return out, lse
-    strides = (ctypes.c_size_t * 9)(
-        _stride(q_nope, 0, 128 * 128), int(q_nope.stride(1)), _stride(q_rope, 0, 128 * 64), int(q_rope.stride(1)),
-        _stride(k_nope, 0, 128 * 128), int(k_nope.stride(1)), _stride(k_rope, 0, 64),
-        _stride(v, 0, 128 * 128), int(v.stride(1)))
+    strides = _Strides(qn[1], qn[2], qr[1], qr[2], kn[1], kn[2], kr[1], vv[1], vv[2])
     rc = load().mla_prefill_bf16(
-        _ptr(q_nope), _ptr(q_rope), _ptr(k_nope), _ptr(k_rope), _ptr(v), strides, _ptr(cu_q), _ptr(cu_k), B, nq, nk,
-        128, 1 if causal else 0, ctypes.c_float(float(scale)), _ptr(out), _ptr(lse), _ptr(workspace),
-        ctypes.c_size_t(workspace.numel()), _stream(stream))
+        qn[0], qr[0], kn[0], kr[0], vv[0], strides, cu_q.data_ptr(), cu_k.data_ptr(), B, nq, nk, 128,
+        1 if causal else 0, float(scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _handle(stream, dev))
     if rc != MLA_OK:
         raise MLAError(rc, "mla_prefill_bf16")
     return out, lse
