@@ -22,8 +22,16 @@
 // the bf16 side is one coalesced 16-byte access a thread and a group's
 // maximum needs one or two shuffles.  A CTA takes kGroups groups of four rows:
 // one group for short calls (more CTAs, and the values are on their way while
-// the warps look the slots up), four for long ones, whose 16 look-ups then
-// overlap and whose loads are all in flight at once.
+// a warp looks the slots up), four for long ones, whose loads are all in
+// flight at once.
+//
+// Measured (bytes read and written a second; a copy reaches 6670 GB/s), 262,144
+// rows: bf16 append 89 us (6810 GB/s) and gather 90, fp8 81 (5640) and 84, fp4
+// 72 (5400) and 62 (6180), V4.1 rows 66, 63 (6670, 5950) and 68, 61; the 594-
+// and 324-byte rows are off 16-byte boundaries, so their accesses are smaller.
+// 16,384 rows: 5.2 to 7.2 us; 64 rows: 2.3 us.
+#include <climits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -55,36 +63,59 @@ template <> struct Fmt<RowFormat::kFp4V41> {
 template <RowFormat F> constexpr bool kIsFp4 = F == RowFormat::kFp4 || F == RowFormat::kFp4V41;
 template <RowFormat F> constexpr bool kIsV41 = F == RowFormat::kFp8V41 || F == RowFormat::kFp4V41;
 
-// Cache slot (page * 64 + offset) of packed row i, by one warp: -1 for a row
-// past the last sequence (left alone), -2 for one whose token or page lies
-// outside the cache (recorded in the status word; never read or written).
-__device__ int row_slot(const RowsParams& p, int i, int lane) {
-  if (i >= p.rows) return -1;
-  // largest b with cu[b] <= i, 32 probes a round
-  int lo = 0, hi = p.batch;              // cu[lo] <= i is assumed, cu[hi + 1] is not probed
-  while (lo < hi) {
-    const int step = (hi - lo + 31) / 32;
-    const int probe = lo + (lane + 1) * step;
-    const bool le = probe <= hi && __ldg(p.cu_rows + probe) <= i;
-    const unsigned m = __ballot_sync(0xffffffffu, le);
-    const int n = __popc(m);             // cu is non-decreasing, so the probes that hold come first
-    const int nlo = lo + n * step;
-    hi = min(hi, nlo + step - 1);
-    lo = min(nlo, hi);
-  }
-  if (lo >= p.batch) return -1;          // cu[batch] <= i: behind the last sequence
-  const int c0 = __ldg(p.cu_rows + lo), c1 = __ldg(p.cu_rows + lo + 1);
-  int slot = -2, code = MLA_STATUS_BAD_SEQ_LEN;
-  if (i >= c0 && i < c1) {
-    const long long pos = static_cast<long long>(__ldg(p.seq_lens + lo)) - c1 + i;
-    if (pos >= 0 && pos < static_cast<long long>(p.max_pages) * kPage) {
-      const int page = __ldg(p.block_table + static_cast<size_t>(lo) * p.max_pages + (pos >> 6));
-      if (page >= 0 && page < p.num_pages) slot = page * kPage + static_cast<int>(pos & 63);
-      else code = MLA_STATUS_BAD_PAGE;
+// Cache slots (page * 64 + offset) of this CTA's rows, by its first warp, a lane
+// a row: -1 for a row past the last sequence (left alone), -2 for one whose
+// token or page lies outside the cache (recorded in the status word; never read
+// or written).  One search for all rows: a warp's search for each took more
+// instructions than the rows' values (131,072 rows: fp8 append 56 us).
+template <int kRows>
+__device__ __forceinline__ void look_up(const RowsParams& p, int row0, int* s_slot) {
+  static_assert(kRows <= 32, "a lane a row");
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    // a sequence b with cu[b] <= row0 and cu[b + 32] > row0 or b + 32 > batch, 32 probes a round
+    int lo = 0, hi = p.batch;            // cu[lo] <= row0 is assumed, cu[hi + 1] is not probed
+    while (hi - lo > 31) {
+      const int step = (hi - lo + 31) / 32;
+      const int probe = lo + (lane + 1) * step;
+      const bool le = probe <= hi && __ldg(p.cu_rows + probe) <= row0;
+      const int n = __popc(__ballot_sync(0xffffffffu, le));   // cu is non-decreasing: the probes that hold come first
+      const int nlo = lo + n * step;
+      hi = min(hi, nlo + step - 1);
+      lo = min(nlo, hi);
+    }
+    // each row's sequence: the largest b with cu[b] <= row
+    const int next = lo + 1 + lane <= p.batch ? __ldg(p.cu_rows + lo + 1 + lane) : INT_MAX;
+    int b = lo;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int n = __popc(__ballot_sync(0xffffffffu, next <= row0 + r));
+      if (lane == r) b = lo + n;
+    }
+    const int i = row0 + lane;
+    if (lane < kRows) {
+      // (32 sequences begin in these rows, most of them empty: look further)
+      if (b == lo + 32)
+        while (b < p.batch && __ldg(p.cu_rows + b + 1) <= i) ++b;
+      int slot = -1;
+      if (i < p.rows && b < p.batch) {   // (cu[batch] <= i: behind the last sequence)
+        const int c0 = __ldg(p.cu_rows + b), c1 = __ldg(p.cu_rows + b + 1);
+        int code = MLA_STATUS_BAD_SEQ_LEN;
+        slot = -2;
+        if (i >= c0 && i < c1) {
+          const long long pos = static_cast<long long>(__ldg(p.seq_lens + b)) - c1 + i;
+          if (pos >= 0 && pos < static_cast<long long>(p.max_pages) * kPage) {
+            const int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + (pos >> 6));
+            if (page >= 0 && page < p.num_pages) slot = page * kPage + static_cast<int>(pos & 63);
+            else code = MLA_STATUS_BAD_PAGE;
+          }
+        }
+        if (slot < 0) set_status(p.status, code);
+      }
+      s_slot[lane] = slot;
     }
   }
-  if (slot < 0 && lane == 0) set_status(p.status, code);
-  return slot;
+  __syncthreads();
 }
 
 // Scale exponent of a group whose largest magnitude has the bf16 bits `a`
@@ -96,18 +127,6 @@ __device__ __forceinline__ int scale_exponent(uint32_t a) {
   const uint32_t man = a & 0x7Fu;
   const int k = kIsFp4<F> ? e - 3 + (man > 0x40u) : e - 9 + (man > 0x60u);
   return min(max(k, -127), Fmt<F>::kTopK);
-}
-
-// The slots of this CTA's rows, one warp a row.
-template <int kGroups>
-__device__ __forceinline__ void look_up(const RowsParams& p, int row0, int* s_slot) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int i = warp; i < kGroups * kGroupRows; i += static_cast<int>(blockDim.x >> 5)) {
-    const int slot = row_slot(p, row0 + i, lane);
-    if (lane == 0) s_slot[i] = slot;
-  }
-  __syncthreads();
 }
 
 // One piece of a quantised or bf16 row into its cache row.
@@ -182,7 +201,7 @@ __global__ void __launch_bounds__(kGroupRows * Fmt<F>::kValues / kPiece) append_
           j < kLatentPieces ? p.c_kv + static_cast<size_t>(row) * p.c_stride + j * kPiece
                             : p.k_rope + static_cast<size_t>(row) * p.r_stride + (j - kLatentPieces) * kPiece));
   }
-  look_up<kGroups>(p, row0, s_slot);
+  look_up<kGroups * kGroupRows>(p, row0, s_slot);
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) append_piece<F>(p, v[g], s_slot[g * kGroupRows + r], j);
 }
@@ -268,7 +287,7 @@ __global__ void __launch_bounds__(kGroupRows * kRow / kPiece) gather_kernel(cons
   __shared__ int s_slot[kGroups * kGroupRows];
   const int r = threadIdx.x / kPieces, j = threadIdx.x - r * kPieces;
   const int row0 = blockIdx.x * kGroups * kGroupRows;
-  look_up<kGroups>(p, row0, s_slot);
+  look_up<kGroups * kGroupRows>(p, row0, s_slot);
   Piece x[kGroups];
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) x[g] = read_piece<F>(p, s_slot[g * kGroupRows + r], j);
