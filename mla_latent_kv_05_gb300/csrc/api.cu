@@ -263,8 +263,8 @@ constexpr long long kTreePagesPerPair = 4;
 // A quantised cache's tree decode first widens the live pages to bf16 rows, once
 // for all nodes, when the workspace has room for them: the attention then runs
 // at the bf16 rate.  Two nodes pay for it already: 64 x 2 nodes over 4096 fp8
-// tokens take 214 us so and 322 over the codes (fp4: 187 and 297), 64 x 4 282
-// and 583, 8 x 61 340 and 1080; small calls gain too (1 x 2 over 500: 23 and 44).
+// tokens take 209 us so and 322 over the codes (fp4: 185 and 297), 64 x 4 276
+// and 583, 8 x 61 340 and 1080; small calls gain too (1 x 2 over 500: 21 and 44).
 constexpr int kWidenNodes = 2;
 size_t widened_bytes(int batch, int max_pages) {
   return static_cast<size_t>(batch) * max_pages * kPage * kRow * 2;

@@ -300,31 +300,27 @@ __global__ void __launch_bounds__(kGroupRows * kRow / kPiece) gather_kernel(cons
 }
 
 // The pages of a batch of sequences as bf16 rows: token t of sequence b becomes
-// row b max_pages 64 + t, for the tokens of the pages that the sequence reaches
-// (zeros behind its end).  blockIdx.y is the sequence, whose pages the CTAs of
-// a column share.
+// row b max_pages 64 + t.  blockIdx.y is the sequence, whose tokens the CTAs of
+// a column take 16 at a time (the last 16 are filled up with zero rows).
 template <RowFormat F>
 __global__ void __launch_bounds__(kGroupRows * kRow / kPiece) widen_kernel(const RowsParams p) {
-  constexpr int kPieces = kRow / kPiece;
+  constexpr int kPieces = kRow / kPiece, kRows = 4 * kGroupRows;
   const int r = threadIdx.x / kPieces, j = threadIdx.x - r * kPieces;
   const int b = blockIdx.y, len = min(__ldg(p.seq_lens + b), p.max_pages * kPage);
-  for (int t = blockIdx.x; t * kPage < len; t += gridDim.x) {
-    const size_t at = static_cast<size_t>(b) * p.max_pages + t;
-    const int page = __ldg(p.block_table + at);
+  for (int t = blockIdx.x * kRows + r; t - r < len; t += gridDim.x * kRows) {
+    const size_t at = static_cast<size_t>(b) * p.max_pages;
+    const int page = __ldg(p.block_table + at + (t - r) / kPage);
     const bool bad = page < 0 || page >= p.num_pages;
     if (bad && threadIdx.x == 0) set_status(p.status, MLA_STATUS_BAD_PAGE);
-#pragma unroll 1
-    for (int i = r; i < kPage; i += 4 * kGroupRows) {
-      Piece x[4];
+    Piece x[4];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int row = i + g * kGroupRows;
-        x[g] = read_piece<F>(p, bad || t * kPage + row >= len ? -1 : page * kPage + row, j);
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<uint4*>(p.out + (at * kPage + i + g * kGroupRows) * kRow + j * kPiece) = values_of<F>(x[g]);
+    for (int g = 0; g < 4; ++g) {
+      const int row = t + g * kGroupRows;
+      x[g] = read_piece<F>(p, bad || row >= len ? -1 : page * kPage + row % kPage, j);
     }
+    __nv_bfloat16* dst = p.out + (at * kPage + t) * kRow + j * kPiece;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) *reinterpret_cast<uint4*>(dst + g * kGroupRows * kRow) = values_of<F>(x[g]);
   }
 }
 
@@ -348,10 +344,10 @@ cudaError_t launch(const RowsParams& p, bool append, cudaStream_t stream) {
 
 cudaError_t launch_widen(RowFormat fmt, const RowsParams& p, cudaStream_t stream) {
   if (p.batch <= 0) return cudaSuccess;
-  // about 1000 CTAs are resident; at least eight columns for a batch of uneven lengths
-  const int share = (1024 + p.batch - 1) / p.batch;
-  const int columns = share < 8 ? 8 : share;
-  const dim3 grid(columns < p.max_pages ? columns : p.max_pages, p.batch), block(kGroupRows * kRow / kPiece);
+  // about 1000 CTAs are resident; at least 32 columns for a batch of uneven lengths
+  const int share = (2048 + p.batch - 1) / p.batch;
+  const int columns = share < 32 ? 32 : share, most = p.max_pages * (kPage / (4 * kGroupRows));
+  const dim3 grid(columns < most ? columns : most, p.batch), block(kGroupRows * kRow / kPiece);
   switch (fmt) {
     case RowFormat::kBf16: break;
     case RowFormat::kFp8: return launch_kernel(widen_kernel<RowFormat::kFp8>, grid, block, 0, stream, p);

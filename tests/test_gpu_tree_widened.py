@@ -51,7 +51,7 @@ def test_rows_behind_the_end_and_other_pages_may_hold_anything(cuda_device, fmt)
         for tok in range(n):
             live[int(inp.block_table[b, tok // 64]), tok % 64] = True
     inp.kv_cache[~live] = 0xFF                         # NaN scales and codes
-    ws[-4096:] = 0xFF
+    ws[binding.mla_workspace_size_tree(3, 6):] = 0xFF
     got = run(inp, parents, ws=ws)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
