@@ -47,6 +47,16 @@
 // exceeds it by more than 2^kLazy, so O is rescaled rarely; its softmax warps
 // do that themselves, after the previous P.V of the tile has completed.
 //
+// Measured: 8192 causal tokens 1.74 ms (1580 TFLOP/s; 1.8 to 1.9 in a loop of
+// seconds, under the power cap), eight prompts of 54 to 1523 tokens 265 us (940;
+// HBM alone takes 130), 2 x 512 queries over 15,000 keys 900 us (1420), five
+// prompts of up to 33 tokens 18.6 us.  A step takes about 2200 cycles, 1852 of
+// them MMAs: K tiles land 1400 cycles after they are asked for (1900 from HBM),
+// and an item's queries about 1900 after the last item's scores, because a
+// second copy of them does not fit beside the ring.  Tried and no faster: K and
+// V ahead of the queries, and prefetches of either into L2 (0 to 10 % slower on
+// ragged prompts).
+//
 // Every wait is bounded: a timeout records MLA_STATUS_TIMEOUT and raises the
 // abort flag, all roles leave, and the kernel ends through its teardown.
 #include <climits>
@@ -179,8 +189,6 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
 struct Maps {
   CUtensorMap qn, qr, kn, kr, v;
 };
-
-// 32 lanes x 16 columns to tensor memory.
 
 // Registers (128 a thread at launch): 80 for warps 0..3, 96 for the output
 // warps, 168 for the softmax warps (4 * 80 + 4 * 96 + 8 * 168 = 16 * 128),

@@ -23,6 +23,8 @@ Modules:
   mla_oracle    absorbed and un-absorbed attention, paged gather, LSE merge,
                 the query as two e4m3 terms
   closed_forms  the pages' cache-size arithmetic
+  row_codec     the row quantisers (e4m3 per 32, e2m1 per 16) of cache append
+  expanded      expanded-form keys, values and attention; what a tree node sees
 
 Every function here is pinned by a CPU test against something other than
 itself (closed forms printed on the pages, torch's float8 casts, torch's
