@@ -305,7 +305,8 @@ int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope,
   auto encode = encode_fn();
   if (!encode) return MLA_ERR_CUDA;
   __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out);
-  if (launch_tree_prep(parents, n_nodes, seq_lens, batch, nodes, max_pages, by_node, workspace, L, o, lse, stream) != cudaSuccess)
+  if (launch_tree_prep(parents, n_nodes, seq_lens, batch, nodes, max_pages, by_node, workspace, L, o, lse, stream) !=
+      cudaSuccess)
     return MLA_ERR_CUDA;
   uint8_t* rows16 = static_cast<uint8_t*>(workspace) + L.total;
   if (widen) {
@@ -358,7 +359,8 @@ int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope,
   else le = launch_tree_fp4_v41(p, ppg, pdl, stream);
   if (le != cudaSuccess) return MLA_ERR_CUDA;
   if (ev1 && cudaEventRecord(ev1, stream) != cudaSuccess) return MLA_ERR_CUDA;
-  if (launch_combine_plan(workspace, L, rows, 1, o, lse, pdl, stream, true, by_node ? batch : 0) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_combine_plan(workspace, L, rows, 1, o, lse, pdl, stream, true, by_node ? batch : 0) != cudaSuccess)
+    return MLA_ERR_CUDA;
   return MLA_OK;
 }
 

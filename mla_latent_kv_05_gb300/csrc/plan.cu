@@ -325,9 +325,9 @@ __global__ void __launch_bounds__(128) tree_prep_kernel(const int32_t* __restric
   __shared__ int s_parent[kMaxNodes];
   __shared__ int s_len;
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(ws);
-  const int b = blockIdx.y, i = blockIdx.x;
+  const int b = blockIdx.x, i = blockIdx.y;   // (the sequences may exceed a grid's y)
   const size_t row = static_cast<size_t>(b) * nodes + i;
-  const size_t planned = by_node ? static_cast<size_t>(i) * gridDim.y + b : row;
+  const size_t planned = by_node ? static_cast<size_t>(i) * gridDim.x + b : row;
   if (threadIdx.x <= i) s_parent[threadIdx.x] = parents[static_cast<size_t>(b) * nodes + threadIdx.x];
   const int n = n_nodes ? n_nodes[b] : nodes;
   const int seq = seq_lens[b];
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(128) tree_prep_kernel(const int32_t* __restric
 cudaError_t launch_tree_prep(const int32_t* parents, const int32_t* n_nodes, const int32_t* seq_lens, int batch,
                              int nodes, int max_pages, bool by_node, void* ws, const WsLayout& L, __nv_bfloat16* out,
                              float* lse, cudaStream_t stream) {
-  return launch_kernel(tree_prep_kernel, dim3(nodes, batch), dim3(128), 0, stream, parents, n_nodes, seq_lens, nodes,
+  return launch_kernel(tree_prep_kernel, dim3(batch, nodes), dim3(128), 0, stream, parents, n_nodes, seq_lens, nodes,
                        max_pages * kPage, by_node, static_cast<uint8_t*>(ws), L, out, lse);
 }
 

@@ -299,3 +299,22 @@ def test_many_sequences_whose_rows_exceed_the_cache(cuda_device):
     parents = random_tree(40, 6, 15)
     rows = [(b, i) for b in (0, 7, 11, 20, 39) for i in (0, 5)]
     check(*run(inp, parents, n), *reference(inp, parents, n, rows_only=rows), rows_only=rows)
+
+
+def test_the_most_sequences_a_call_takes(cuda_device):
+    batch = 1 << 16
+    q = torch.zeros((batch, 1, 128, 512), dtype=torch.bfloat16, device="cuda")
+    qr = torch.zeros((batch, 1, 128, 64), dtype=torch.bfloat16, device="cuda")
+    cache = torch.arange(4 * 64, device="cuda").to(torch.bfloat16)[:, None].expand(256, 576).reshape(4, 64, 576).contiguous()
+    b = torch.arange(batch, device="cuda")
+    table = (b % 4).to(torch.int32)[:, None].contiguous()
+    lens = (b % 65).to(torch.int32)                       # a node of an empty sequence is none
+    nodes = (lens > 0).to(torch.int32)
+    out, lse = binding.mla_decode_tree_bf16(q, qr, cache, table, lens, torch.full((batch, 1), -1, dtype=torch.int32, device="cuda"),
+                                            192 ** -0.5, n_nodes=nodes)
+    # all scores are 0: the mean of tokens 64 p .. 64 p + len - 1 (below 256), rounded once
+    mean = torch.where(lens > 0, (64 * table[:, 0] + (lens - 1) / 2).float(), torch.zeros((), device="cuda"))
+    assert float((out[:, 0, ::31, ::73].float() - mean[:, None, None]).abs().max()) <= 2.0 ** -8 * 256
+    want = torch.log(lens.float())
+    assert torch.equal(torch.isneginf(lse[:, 0, 5]), lens == 0)
+    assert float((lse[:, 0, 5] - want)[lens > 0].abs().max()) <= 1e-3
