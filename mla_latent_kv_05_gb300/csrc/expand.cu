@@ -216,7 +216,7 @@ expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, Plan
       int m, h;
       item_of(i, tiles, m, h);
       const int row0 = m * 256 + static_cast<int>(rank) * 128 + (warp & 3) * 32;     // the warp's first token
-      if (!wait_short_warp<true>(BAR(DFULL + d), dph, hdr)) break;
+      if (!wait_short_warp(BAR(DFULL + d), dph, hdr)) break;
       ptx::tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {                      // 64 columns at a time
@@ -228,7 +228,7 @@ expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, Plan
           // this warp has read its part of D
           ptx::tc_fence_before();
           __syncwarp();
-          if (elect_one()) ptx::mbar_arrive_remote(ptx::mapa(BAR(DEMPTY + d), 0));
+          if (elect_one()) ptx::arrive_leader(ptx::mapa(BAR(DEMPTY + d), 0));
         }
         if (row0 < rows) {
           // the last store must have read the staging rows

@@ -90,13 +90,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Tell the pair's leader.  What the arrival hands over lies in this CTA's own
-// tensor and shared memory and has been read, or made visible to the MMAs
-// (fence.proxy.async), before it; a release at cluster scope would also wait
-// for the CTA's writes to global memory and took 1000 cycles a tile.
-__device__ __forceinline__ void arrive_leader(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -348,7 +341,7 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
         ptx::tmem_wait_ld();
         ptx::tc_fence_before();
         __syncwarp();
-        if (elect_one()) arrive_leader(LEAD(SEMPTY + (n & 1u)));
+        if (elect_one()) ptx::arrive_leader(LEAD(SEMPTY + (n & 1u)));
         // this thread's tokens that the node sees (a page past the segment: none)
         const int tok = (t + hf) * kPage + 32 * cf;
         const uint32_t see = t + hf < sg.t1 ? static_cast<uint32_t>(tree_bits(seen, ctx - tok, len - tok)) : 0u;
@@ -420,7 +413,7 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
         ptx::fence_proxy_async_cta();
         ptx::tc_fence_before();
         __syncwarp();
-        if (elect_one()) arrive_leader(LEAD(PREADY + hf));
+        if (elect_one()) ptx::arrive_leader(LEAD(PREADY + hf));
         ++n;
         if (quit) break;
       }
@@ -448,7 +441,7 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
           // O is read: the next segment's first P.V may overwrite it
           ptx::tc_fence_before();
           __syncwarp();
-          if (elect_one()) arrive_leader(LEAD(OFREE));
+          if (elect_one()) ptx::arrive_leader(LEAD(OFREE));
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
