@@ -305,8 +305,7 @@ int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope,
   auto encode = encode_fn();
   if (!encode) return MLA_ERR_CUDA;
   __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out);
-  if (launch_tree_prep(parents, n_nodes, seq_lens, batch, nodes, max_pages, by_node, workspace, L, o, lse, stream) !=
-      cudaSuccess)
+  if (launch_tree_prep(parents, n_nodes, seq_lens, batch, nodes, max_pages, by_node, workspace, L, stream) != cudaSuccess)
     return MLA_ERR_CUDA;
   uint8_t* rows16 = static_cast<uint8_t*>(workspace) + L.total;
   if (widen) {

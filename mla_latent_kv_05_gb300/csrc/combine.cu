@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __rest
   // the next call's planner may begin launching (it waits for this grid
   // before it reads or writes anything)
   ptx::grid_dep_launch();
-  if (parts <= 1) return;
+  if (kF32 ? parts == 1 : parts <= 1) return;
   const int start = i * spq + base;
   const float* part_lse = reinterpret_cast<const float*>(ws + Lw.part_lse);
   // fp32 partials (tree decode): the same 16 values a lane, in two 32-byte loads
@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __rest
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
   float sum = 0.f, L = -INFINITY;
+  // (no part: a row of the tree decode that has no token, sum = 0)
   // Parts in groups of 32 (one lse per lane); within a group the partial
   // rows are read four at a time, and the first four are requested together
   // with the group's lse values.  Each group's weights are taken against the

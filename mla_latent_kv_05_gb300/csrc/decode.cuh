@@ -37,11 +37,9 @@ cudaError_t launch_plan(const int32_t* seq_lens, int batch, int sq, int max_page
 cudaError_t launch_sparse_prep(const int32_t* token_slots, int rows, int topk, int num_slots, void* ws,
                                const WsLayout& L, cudaStream_t stream);
 // Tree decode: per (sequence, node) row its visible length and the bits of
-// the draft nodes it sees, into the workspace; rows with nothing to see are
-// written here (out = 0, lse = -inf).
+// the draft nodes it sees, into the workspace.
 cudaError_t launch_tree_prep(const int32_t* parents, const int32_t* n_nodes, const int32_t* seq_lens, int batch,
-                             int nodes, int max_pages, bool by_node, void* ws, const WsLayout& L, __nv_bfloat16* out,
-                             float* lse, cudaStream_t stream);
+                             int nodes, int max_pages, bool by_node, void* ws, const WsLayout& L, cudaStream_t stream);
 // TMA descriptors of the bf16 cache (4-D: 64 columns, 8 rows, 9 chunks, row
 // groups).  The score SM loads chunks 0..4 (k) and 5..8 (kb) of a half page,
 // or of a whole page when a tile's two adjacent slots are the two halves of
@@ -72,7 +70,8 @@ int decode_max_pairs();
 // W^UV up-projection of latent outputs (see wuv.cu).
 cudaError_t launch_wuv(PFN_cuTensorMapEncodeTiled_v12000 encode, const void* o, const void* w, int rows, void* out,
                        void* hdr, cudaStream_t stream);
-// f32: the partials are fp32 (tree decode) instead of bf16.  seqs > 0: planned
+// f32: tree decode, whose partials are fp32 instead of bf16 and whose rows with no
+// token are written here (out = 0, lse = -inf).  seqs > 0: planned
 // row k is node k / seqs of sequence k % seqs.
 cudaError_t launch_combine_plan(const void* ws, const WsLayout& Lw, int batch, int sq, __nv_bfloat16* out, float* lse,
                                 bool pdl, cudaStream_t stream, bool f32 = false, int seqs = 0);

@@ -311,63 +311,57 @@ __global__ void __launch_bounds__(256) sparse_prep_kernel(const int32_t* __restr
   if (threadIdx.x == 0) reinterpret_cast<int*>(ws + L.sp_lens)[row] = base;
 }
 
-// Tree decode: one CTA per (sequence b, node i) row.  Node i's token is ctx + i
-// (ctx = seq_len - n_nodes), so the row's length is ctx + i + 1: a parent comes
-// before its child, and nothing after the node is visible.  Within the drafted
-// tokens the row sees the nodes on the path to the root, as bits.  A padding
-// node (i >= n_nodes) and every node of a sequence whose numbers do not fit
-// have length 0; this CTA writes their output.
-__global__ void __launch_bounds__(128) tree_prep_kernel(const int32_t* __restrict__ parents,
-                                                        const int32_t* __restrict__ n_nodes,
-                                                        const int32_t* __restrict__ seq_lens, int nodes, int max_len, bool by_node,
-                                                        uint8_t* __restrict__ ws, WsLayout L,
-                                                        __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
-  __shared__ int s_parent[kMaxNodes];
-  __shared__ int s_len;
+// Tree decode: one CTA per sequence b, one thread per node i.  Node i's token is
+// ctx + i (ctx = seq_len - n_nodes), so the row's length is ctx + i + 1: a parent
+// comes before its child, and nothing after the node is visible.  Within the
+// drafted tokens the row sees the nodes on the path to the root, as bits.  A
+// padding node (i >= n_nodes) and every node of a sequence whose numbers do not
+// fit have length 0; the merge writes their output.
+__global__ void __launch_bounds__(kMaxNodes) tree_prep_kernel(const int32_t* __restrict__ parents,
+                                                              const int32_t* __restrict__ n_nodes,
+                                                              const int32_t* __restrict__ seq_lens, int nodes,
+                                                              int max_len, bool by_node, uint8_t* __restrict__ ws,
+                                                              WsLayout L) {
+  __shared__ uint64_t s_seen[kMaxNodes];
+  __shared__ int s_up[kMaxNodes];
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(ws);
-  const int b = blockIdx.x, i = blockIdx.y;   // (the sequences may exceed a grid's y)
-  const size_t row = static_cast<size_t>(b) * nodes + i;
-  const size_t planned = by_node ? static_cast<size_t>(i) * gridDim.x + b : row;
-  if (threadIdx.x <= i) s_parent[threadIdx.x] = parents[static_cast<size_t>(b) * nodes + threadIdx.x];
+  const int b = blockIdx.x, i = threadIdx.x;
   const int n = n_nodes ? n_nodes[b] : nodes;
   const int seq = seq_lens[b];
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const bool ok = n >= 0 && n <= nodes && seq >= n && seq <= max_len;
-    if (!ok && i == 0) set_status(&hdr->status, MLA_STATUS_BAD_SEQ_LEN);
-    const int len = ok && i < n ? seq - n + i + 1 : 0;
-    uint64_t seen = 0;
-    if (len > 0) {
-      // every step goes to an earlier node, so the walk ends
-      for (int a = i; a >= 0;) {
-        seen |= uint64_t{1} << a;
-        const int up = s_parent[a];
-        if (up < -1 || up >= a) {
-          set_status(&hdr->status, MLA_STATUS_BAD_INDEX);
-          break;
-        }
-        a = up;
-      }
-    }
-    reinterpret_cast<int*>(ws + L.sp_lens)[planned] = len;
-    reinterpret_cast<uint64_t*>(ws + L.tree_seen)[planned] = seen;
-    s_len = len;
+  const bool ok = n >= 0 && n <= nodes && seq >= n && seq <= max_len;
+  if (!ok && i == 0) set_status(&hdr->status, MLA_STATUS_BAD_SEQ_LEN);
+  const bool live = ok && i < n;
+  int up = live ? parents[static_cast<size_t>(b) * nodes + i] : -1;
+  if (up < -1 || up >= i) {
+    set_status(&hdr->status, MLA_STATUS_BAD_INDEX);
+    up = -1;
   }
-  __syncthreads();
-  if (s_len == 0) {
-    uint4* dst = reinterpret_cast<uint4*>(out + row * kHeads * kDc);
-    for (int e = threadIdx.x; e < kHeads * kDc * 2 / 16; e += blockDim.x) dst[e] = make_uint4(0, 0, 0, 0);
-    lse[row * kHeads + threadIdx.x] = -INFINITY;
+  uint64_t seen = live ? uint64_t{1} << i : 0;
+  // each round takes in what the farthest ancestor so far has seen: paths of
+  // 1, 2, 4 .. 64 nodes (every step goes to an earlier node)
+  while (true) {
+    s_seen[i] = seen;
+    s_up[i] = up;
+    if (!__syncthreads_or(up >= 0)) break;
+    if (up >= 0) {
+      seen |= s_seen[up];
+      up = s_up[up];
+    }
+    __syncthreads();
+  }
+  if (i < nodes) {
+    const size_t row = by_node ? static_cast<size_t>(i) * gridDim.x + b : static_cast<size_t>(b) * nodes + i;
+    reinterpret_cast<int*>(ws + L.sp_lens)[row] = live ? seq - n + i + 1 : 0;
+    reinterpret_cast<uint64_t*>(ws + L.tree_seen)[row] = seen;
   }
 }
 
 }  // namespace
 
 cudaError_t launch_tree_prep(const int32_t* parents, const int32_t* n_nodes, const int32_t* seq_lens, int batch,
-                             int nodes, int max_pages, bool by_node, void* ws, const WsLayout& L, __nv_bfloat16* out,
-                             float* lse, cudaStream_t stream) {
-  return launch_kernel(tree_prep_kernel, dim3(batch, nodes), dim3(128), 0, stream, parents, n_nodes, seq_lens, nodes,
-                       max_pages * kPage, by_node, static_cast<uint8_t*>(ws), L, out, lse);
+                             int nodes, int max_pages, bool by_node, void* ws, const WsLayout& L, cudaStream_t stream) {
+  return launch_kernel(tree_prep_kernel, dim3(batch), dim3(kMaxNodes), 0, stream, parents, n_nodes, seq_lens, nodes,
+                       max_pages * kPage, by_node, static_cast<uint8_t*>(ws), L);
 }
 
 cudaError_t launch_sparse_prep(const int32_t* token_slots, int rows, int topk, int num_slots, void* ws,
