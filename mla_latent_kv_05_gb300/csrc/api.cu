@@ -358,8 +358,9 @@ int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope,
   else le = launch_tree_fp4_v41(p, ppg, pdl, stream);
   if (le != cudaSuccess) return MLA_ERR_CUDA;
   if (ev1 && cudaEventRecord(ev1, stream) != cudaSuccess) return MLA_ERR_CUDA;
-  if (launch_combine_plan(workspace, L, rows, 1, o, lse, pdl, stream, true, by_node ? batch : 0) != cudaSuccess)
-    return MLA_ERR_CUDA;
+  le = by_node ? launch_combine_tree(workspace, L, rows, batch, o, lse, pdl, stream)
+               : launch_combine_plan(workspace, L, rows, 1, o, lse, pdl, stream, true);
+  if (le != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }
 

@@ -6,7 +6,7 @@
 // partials, caller's indptr).  One warp per (output row, head), bf16 out.
 #include <cuda_bf16.h>
 
-#include "common.cuh"
+#include "tree.cuh"
 
 namespace mla {
 
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 // part) or the planner (no token).  Four parts' loads are in flight at a
 // time; the parts are summed in slot order.
 template <bool kF32>
-__global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __restrict__ ws, WsLayout Lw, int sq, int seqs,
+__global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __restrict__ ws, WsLayout Lw, int sq,
                                                            __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
   // The plan (part counts and slot bases) was written by the planner, which
   // completed before the attention kernel let this grid launch, so it is read
@@ -183,23 +183,97 @@ __global__ void __launch_bounds__(256) combine_plan_kernel(const uint8_t* __rest
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : kF32 ? sum : 0.f;
-  // rows planned node by node go back to their sequence's place
-  const int row = seqs > 0 ? k % seqs * static_cast<int>(gridDim.x / seqs) + k / seqs : k;
   uint32_t o[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     __nv_bfloat162 bb = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     o[e] = *reinterpret_cast<uint32_t*>(&bb);
   }
-  ptx::st_global_v8(out + (static_cast<size_t>(row) * kHeads + h) * kDc + 16 * lane, o);
+  ptx::st_global_v8(out + (static_cast<size_t>(k) * kHeads + h) * kDc + 16 * lane, o);
   if (lane == 0)
-    lse[static_cast<size_t>(row) * kHeads + h] = sum > 0.f || (kF32 && sum != 0.f) ? L + logf(sum) : -INFINITY;
+    lse[static_cast<size_t>(k) * kHeads + h] = sum > 0.f || (kF32 && sum != 0.f) ? L + logf(sum) : -INFINITY;
+}
+
+// The merge of launch_tree's rows, on the decode merge's grid and terms: warp W of
+// a row's 128 takes 32 heads (lane = head) and 16 latent columns, so that a part
+// is read as it was written (two kilobytes in a row, see part_piece) and a
+// head's weights stay in its lane.  Planned row k is node k / seqs of sequence k
+// % seqs; rows with no token get out = 0, lse = -inf.
+__global__ void __launch_bounds__(256) combine_tree_kernel(const uint8_t* __restrict__ ws, WsLayout Lw, int seqs,
+                                                           __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+  const int k = blockIdx.x;
+  const int parts = __ldcg(reinterpret_cast<const int*>(ws + Lw.n_parts) + k);
+  const int base = __ldcg(reinterpret_cast<const int*>(ws + Lw.slot_base) + k);
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  if (parts == 1) return;                // written by the attention kernel
+  const int w = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int group = w >> 5, cols = w & 31, h = group * 32 + lane;
+  const float* src = reinterpret_cast<const float*>(ws + Lw.part_out) + static_cast<size_t>(max(base, 0)) * kHeads * kDc +
+                     part_piece(group, cols >> 3, 2 * (cols & 7)) + 8 * lane;
+  const float* part_lse = reinterpret_cast<const float*>(ws + Lw.part_lse) + static_cast<size_t>(max(base, 0)) * kHeads + h;
+  float L = -INFINITY, sum = 0.f, acc[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  for (int s0 = 0; s0 < parts; s0 += 4) {
+    uint32_t x[4][16];
+    float v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      v[u] = -INFINITY;
+      if (s0 + u < parts) {
+        v[u] = __ldcg(part_lse + static_cast<size_t>(s0 + u) * kHeads);
+        ptx::ld_global_cg_v8(src + static_cast<size_t>(s0 + u) * kHeads * kDc, x[u]);
+        ptx::ld_global_cg_v8(src + static_cast<size_t>(s0 + u) * kHeads * kDc + 256, x[u] + 8);
+      }
+    }
+    const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), m = fmaxf(L, top);
+    if (m != L && L != -INFINITY) {
+      const float r = __expf(L - m);
+      sum *= r;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[e] *= r;
+    }
+    L = m;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (s0 + u >= parts) break;
+      const float wt = v[u] == -INFINITY ? 0.f : __expf(v[u] - L);   // a part that is NaN makes the row NaN
+      sum += wt;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[e] = fmaf(wt, __uint_as_float(x[u][e]), acc[e]);
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : sum;
+  uint32_t o[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    o[e] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  const size_t row = static_cast<size_t>(k % seqs) * (gridDim.x / seqs) + k / seqs;
+  ptx::st_global_v8(out + (row * kHeads + h) * kDc + 16 * cols, o);
+  if (cols == 0) lse[row * kHeads + h] = sum == 0.f ? -INFINITY : L + logf(sum);
 }
 
 }  // namespace
 
+cudaError_t launch_combine_tree(const void* ws, const WsLayout& Lw, int rows, int seqs, __nv_bfloat16* out, float* lse,
+                                bool pdl, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(rows, kHeads / 8, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_tree_kernel, static_cast<const uint8_t*>(ws), Lw, seqs, out, lse);
+}
+
 cudaError_t launch_combine_plan(const void* ws, const WsLayout& Lw, int batch, int sq, __nv_bfloat16* out, float* lse,
-                                bool pdl, cudaStream_t stream, bool f32, int seqs) {
+                                bool pdl, cudaStream_t stream, bool f32) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(batch * sq, kHeads / 8, 1);
   cfg.blockDim = dim3(256, 1, 1);
@@ -210,7 +284,7 @@ cudaError_t launch_combine_plan(const void* ws, const WsLayout& Lw, int batch, i
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, f32 ? combine_plan_kernel<true> : combine_plan_kernel<false>,
-                            static_cast<const uint8_t*>(ws), Lw, sq, seqs, out, lse);
+                            static_cast<const uint8_t*>(ws), Lw, sq, out, lse);
 }
 
 // Public merge: parts of row r are [indptr[r], indptr[r+1]).

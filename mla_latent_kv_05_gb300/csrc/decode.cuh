@@ -71,10 +71,9 @@ int decode_max_pairs();
 cudaError_t launch_wuv(PFN_cuTensorMapEncodeTiled_v12000 encode, const void* o, const void* w, int rows, void* out,
                        void* hdr, cudaStream_t stream);
 // f32: tree decode, whose partials are fp32 instead of bf16 and whose rows with no
-// token are written here (out = 0, lse = -inf).  seqs > 0: planned
-// row k is node k / seqs of sequence k % seqs.
+// token are written here (out = 0, lse = -inf).
 cudaError_t launch_combine_plan(const void* ws, const WsLayout& Lw, int batch, int sq, __nv_bfloat16* out, float* lse,
-                                bool pdl, cudaStream_t stream, bool f32 = false, int seqs = 0);
+                                bool pdl, cudaStream_t stream, bool f32 = false);
 cudaError_t launch_combine_indptr(const float* part_out, const float* part_lse, const int32_t* indptr, int rows,
                                   __nv_bfloat16* out, float* lse, cudaStream_t stream);
 

@@ -430,7 +430,8 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
         else p.lse[static_cast<size_t>(out_row(row)) * kHeads + h] = lse;
       }
       // this thread's quarter of the latent columns: [256 hf + 128 cf, +128)
-      float* part = reinterpret_cast<float*>(p.ws + p.L.part_out) + (static_cast<size_t>(slot) * kHeads + h) * kDc + 256 * hf + 128 * cf;
+      float* part = reinterpret_cast<float*>(p.ws + p.L.part_out) + static_cast<size_t>(slot) * kHeads * kDc +
+                    part_piece(2 * static_cast<int>(rank) + (wq & 1), 2 * hf + cf, 0) + 8 * lane;
       __nv_bfloat16* dst = p.out + (static_cast<size_t>(out_row(row)) * kHeads + h) * kDc + 256 * hf + 128 * cf;
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
@@ -447,7 +448,7 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
         if (parts > 1) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) ptx::st_global_v8(part + 32 * q + e, o + e);
+          for (int e = 0; e < 4; ++e) ptx::st_global_v8(part + (4 * q + e) * 256, o + 8 * e);
         } else {
           uint32_t b16[16];
 #pragma unroll
