@@ -30,9 +30,11 @@ struct DecodeParams {
 };
 
 // out / lse: the rows with no token are written here (out = 0, lse = -inf),
-// unless out is null.
+// unless out is null.  seg_cost: what starting a row segment costs in pages, -1
+// for the tuned value.
 cudaError_t launch_plan(const int32_t* seq_lens, int batch, int sq, int max_pages, int pairs_per_group,
-                        void* ws, const WsLayout& L, __nv_bfloat16* out, float* lse, cudaStream_t stream);
+                        void* ws, const WsLayout& L, __nv_bfloat16* out, float* lse, cudaStream_t stream,
+                        int seg_cost = -1);
 // Sparse decode: compact each query row's listed slots into the workspace.
 cudaError_t launch_sparse_prep(const int32_t* token_slots, int rows, int topk, int num_slots, void* ws,
                                const WsLayout& L, cudaStream_t stream);

@@ -99,7 +99,7 @@ __device__ void block_exclusive_scan2(int a, int b, unsigned long long* smem_war
 constexpr int kPlanSmemRows = 2048;   // 4 mirrors of [batch + 1] ints: 32 KiB, under the 48 KiB default
 
 __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ seq_lens, int batch, int sq,
-                                                    int max_pages, int pairs_per_group,
+                                                    int max_pages, int pairs_per_group, int seg_cost,
                                                     uint8_t* __restrict__ ws, WsLayout L,
                                                     __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
   __shared__ int s_warp[32];
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
     local_ne += s > 0 ? 1 : 0;
   }
   // Row costs for the partition: a row with pages costs its pages plus
-  // kSegCost pages' worth for its segment start (query load, output write,
+  // seg_cost pages' worth for its segment start (query load, output write,
   // pipeline refill).
   int total = 0, ne_total = 0, excl = 0, ne_excl = 0;
   block_exclusive_scan2(local, local_ne, s_warp2, &excl, &ne_excl, &total, &ne_total);
@@ -162,14 +162,14 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
     const int n = (r_len[b] + kPage - 1) / kPage;
     r_ts[b] = excl;
     if (rows_in_smem) tile_start[b] = excl;
-    r_cost[b] = excl + kSegCost * ne_excl;
+    r_cost[b] = excl + seg_cost * ne_excl;
     excl += n;
     ne_excl += n > 0 ? 1 : 0;
   }
   if (tid == 0) {
     r_ts[batch] = total;
     tile_start[batch] = total;
-    r_cost[batch] = total + kSegCost * ne_total;
+    r_cost[batch] = total + seg_cost * ne_total;
     s_chunk = total > 0 ? (total + ppg - 1) / ppg : 1;
   }
   __syncthreads();
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
   // the row whose cost range holds that point, past the row's start cost.
   // pair_b0[p]: the row holding the pair's first page (the last row whose
   // pages start at or before it), where the attention kernel begins walking.
-  const long long cost_total = static_cast<long long>(total) + static_cast<long long>(kSegCost) * ne_total;
+  const long long cost_total = static_cast<long long>(total) + static_cast<long long>(seg_cost) * ne_total;
   for (int pp = tid; pp <= ppg; pp += blockDim.x) {
     int x = pp == 0 ? 0 : total;
     if (pp > 0 && pp < ppg) {
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
         if (r_cost[mid] <= target) l = mid; else r = mid - 1;
       }
       const int n = r_ts[l + 1] - r_ts[l];
-      const long long off = target - r_cost[l] - (n > 0 ? kSegCost : 0);
+      const long long off = target - r_cost[l] - (n > 0 ? seg_cost : 0);
       x = r_ts[l] + static_cast<int>(off < 0 ? 0 : (off > n ? n : off));
     }
     s_lo[pp] = x;
@@ -372,7 +372,9 @@ cudaError_t launch_sparse_prep(const int32_t* token_slots, int rows, int topk, i
 }
 
 cudaError_t launch_plan(const int32_t* seq_lens, int batch, int sq, int max_pages, int pairs_per_group,
-                        void* ws, const WsLayout& L, __nv_bfloat16* out, float* lse, cudaStream_t stream) {
+                        void* ws, const WsLayout& L, __nv_bfloat16* out, float* lse, cudaStream_t stream,
+                        int seg_cost) {
+  if (seg_cost < 0) seg_cost = kSegCost;
   const size_t smem = sizeof(int) * (2 * static_cast<size_t>(pairs_per_group + 1) +
                                      (batch <= kPlanSmemRows ? 4 * static_cast<size_t>(batch + 1) : 0));
   // one thread per row (or pair boundary), at least four warps: a small
@@ -391,7 +393,7 @@ cudaError_t launch_plan(const int32_t* seq_lens, int batch, int sq, int max_page
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, plan_kernel, seq_lens, batch, sq, max_pages, pairs_per_group,
+  return cudaLaunchKernelEx(&cfg, plan_kernel, seq_lens, batch, sq, max_pages, pairs_per_group, seg_cost,
                             static_cast<uint8_t*>(ws), L, out, lse);
 }
 
