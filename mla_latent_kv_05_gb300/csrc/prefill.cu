@@ -19,8 +19,8 @@
 // M = 128 tiles that share each K/V tile of 80 keys:
 //   tensor memory (512 columns): O0 | O1 (128 fp32 columns each), S0 | S1 (80
 //       each), P0 | P1 (bf16, 40 each);
-//   shared memory: Q0 | Q1 (48 KiB each), and a ring of twelve 10-KiB chunks
-//       (80 keys x 64 values), three per K tile and two per V tile;
+//   shared memory: Q0 | Q1 (48 KiB each), two K tiles (three 10-KiB chunks of 80
+//       keys x 64 values each) and three V tiles (two chunks each);
 //   warp 0 fetches the items and issues the TMA loads, warps 1 and 2 the
 //   scores' MMAs of tile 0 and tile 1, warp 3 the P.V MMAs of both, warps
 //   4..7 and 8..11 are the softmax of tile 0 and tile 1 (thread = row), warps
@@ -73,13 +73,15 @@ constexpr int kKeys = 80;                          // keys per K/V tile
 constexpr uint32_t kQChunk = 128u * 128u;          // 16 KiB: 128 query rows x 64 values
 constexpr uint32_t kQTile = 3 * kQChunk;           // 128 query rows x 192
 constexpr uint32_t kChunk = kKeys * 128u;          // 10 KiB: 80 keys x 64 values
-constexpr uint32_t kRing = 12;                     // chunks
-constexpr uint32_t kOffRing = 2 * kQTile;
-constexpr uint32_t kOffBar = kOffRing + kRing * kChunk;   // 216 KiB
-constexpr uint32_t kTiles = 8;                     // K or V tiles in flight at most (barriers)
+constexpr uint32_t kKTiles = 2, kVTiles = 3;       // K and V tiles held
+constexpr uint32_t kKTile = 3 * kChunk, kVTile = 2 * kChunk;
+constexpr uint32_t kOffK = 2 * kQTile;
+constexpr uint32_t kOffV = kOffK + kKTiles * kKTile;
+constexpr uint32_t kOffBar = kOffV + kVTiles * kVTile;    // 216 KiB
 constexpr int kItemSlots = 2;
 enum Bar {
-  QFULL = 0, QEMPTY = QFULL + 2, FULL = QEMPTY + 2, EMPTY = FULL + kTiles, SFULL = EMPTY + kTiles, SREAD = SFULL + 2,
+  QFULL = 0, QEMPTY = QFULL + 2, KFULL = QEMPTY + 2, KEMPTY = KFULL + kKTiles, VFULL = KEMPTY + kKTiles,
+  VEMPTY = VFULL + kVTiles, SFULL = VEMPTY + kVTiles, SREAD = SFULL + 2,
   PREADY = SREAD + 2, PVDONE = PREADY + 2, LFULL = PVDONE + 2, LEMPTY = LFULL + 2, OFREE = LEMPTY + 2,
   IFULL = OFREE + 2, IEMPTY = IFULL + kItemSlots, DRAIN = IEMPTY + kItemSlots, NBAR = DRAIN + 3
 };
@@ -93,7 +95,6 @@ constexpr uint32_t kOCol = 0, kSCol = 256, kPCol = kSCol + 2 * kKeys;   // + 128
 static_assert(kPCol + kKeys <= 512, "tensor memory columns");
 constexpr uint32_t kIdescS = ptx::idesc_bf16(128, kKeys, 0, 0);  // Q, K: K-major
 constexpr uint32_t kIdescPV = ptx::idesc_bf16(128, 128, 0, 1);   // P in tensor memory, V: MN-major
-constexpr uint32_t kIdescPVHalf = ptx::idesc_bf16(128, 64, 0, 1);
 // log2 units: P <= 2^12, exact in relative terms, and far from fp32 overflow in O and l
 constexpr float kLazy = 12.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -250,7 +251,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       ptx::mbar_init(BAR(DRAIN + t), 1);
     }
     ptx::mbar_init(BAR(DRAIN + 2), 1);
-    for (uint32_t s = 0; s < kTiles; ++s) { ptx::mbar_init(BAR(FULL + s), 1); ptx::mbar_init(BAR(EMPTY + s), s & 1 ? 1 : 2); }   // V: one warp reads it
+    for (uint32_t s = 0; s < kKTiles; ++s) { ptx::mbar_init(BAR(KFULL + s), 1); ptx::mbar_init(BAR(KEMPTY + s), 2); }
+    for (uint32_t s = 0; s < kVTiles; ++s) { ptx::mbar_init(BAR(VFULL + s), 1); ptx::mbar_init(BAR(VEMPTY + s), 1); }
     for (int s = 0; s < kItemSlots; ++s) {
       ptx::mbar_init(BAR(IFULL + s), 1);
       ptx::mbar_init(BAR(IEMPTY + s), 15);         // three MMA, eight softmax, four output warps
@@ -293,21 +295,10 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     if (lane == 0) {
       const uint64_t pol = ptx::policy_evict_normal();
       Walk w;
-      uint32_t slot = 0, seq = 0;              // next chunk of the ring, tiles queued so far
+      uint32_t kb = 0, k_phase = 0, vb = 0, v_phase = 0;   // next K and V buffer
+      uint32_t k_tiles = 0, v_tiles = 0;       // tiles queued so far
       uint32_t nq0 = 0, nq1 = 0;               // Q tiles queued so far
       bool ok = true;
-      // The ring holds twelve chunks, so a K tile's slots were last used by the
-      // fourth (K) and fifth (V) tiles before it, a V tile's by the fifth (K).
-      auto slot_free = [&](bool k_tile) {
-        if (seq >= 5) ok = wait_short(BAR(EMPTY + ((seq - 5) & (kTiles - 1))), ((seq - 5) >> 3) & 1u, hdr);
-        if (ok && k_tile && seq >= 4)
-          ok = wait_short(BAR(EMPTY + ((seq - 4) & (kTiles - 1))), ((seq - 4) >> 3) & 1u, hdr);
-        return ok;
-      };
-      auto chunk = [&](const CUtensorMap* map, int x, int y, int z) {
-        ptx::tma_load_4d(sbase + kOffRing + slot * kChunk, map, BAR(FULL + (seq & (kTiles - 1))), x, y, z, 0, pol);
-        if (++slot == kRing) slot = 0;
-      };
       auto query = [&](int t, uint32_t n, const Tile& it) {
         ok = wait_short(BAR(QEMPTY + t), (n & 1u) ^ 1u, hdr);
         if (!ok) return;
@@ -350,21 +341,28 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         }
         for (int j = 0; j < n && ok; ++j) {
           const int k = it.k0 + j * kKeys;
-          if (!slot_free(true)) break;
-          ptx::mbar_arrive_expect_tx(BAR(FULL + (seq & (kTiles - 1))), 3 * kChunk);
-          chunk(&maps.kn, 0, it.head, k);
-          chunk(&maps.kn, 64, it.head, k);
-          chunk(&maps.kr, 0, 0, k);
-          ++seq;
+          ok = wait_short(BAR(KEMPTY + kb), k_phase ^ 1u, hdr);
+          if (!ok) break;
+          ptx::mbar_arrive_expect_tx(BAR(KFULL + kb), kKTile);
+          const uint32_t k_dst = sbase + kOffK + kb * kKTile;
+          ptx::tma_load_4d(k_dst, &maps.kn, BAR(KFULL + kb), 0, it.head, k, 0, pol);
+          ptx::tma_load_4d(k_dst + kChunk, &maps.kn, BAR(KFULL + kb), 64, it.head, k, 0, pol);
+          ptx::tma_load_4d(k_dst + 2 * kChunk, &maps.kr, BAR(KFULL + kb), 0, 0, k, 0, pol);
+          if (++kb == kKTiles) { kb = 0; k_phase ^= 1u; }
           if (j == 0 && n1 > 0) {
             query(1, nq1, it);
             if (ok) ++nq1;
           }
-          if (!ok || !slot_free(false)) break;
-          ptx::mbar_arrive_expect_tx(BAR(FULL + (seq & (kTiles - 1))), 2 * kChunk);
-          chunk(&maps.v, 0, it.head, k);
-          chunk(&maps.v, 64, it.head, k);
-          ++seq;
+          // (a K tile without its V is waited for all the same)
+          ++k_tiles;
+          if (ok) ok = wait_short(BAR(VEMPTY + vb), v_phase ^ 1u, hdr);
+          if (!ok) break;
+          ptx::mbar_arrive_expect_tx(BAR(VFULL + vb), kVTile);
+          const uint32_t v_dst = sbase + kOffV + vb * kVTile;
+          ptx::tma_load_4d(v_dst, &maps.v, BAR(VFULL + vb), 0, it.head, k, 0, pol);
+          ptx::tma_load_4d(v_dst + kChunk, &maps.v, BAR(VFULL + vb), 64, it.head, k, 0, pol);
+          if (++vb == kVTiles) { vb = 0; v_phase ^= 1u; }
+          ++v_tiles;
         }
         it = ahead;
       }
@@ -372,9 +370,14 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       if (nq0 > 0) wait_drain(BAR(QFULL), (nq0 - 1) & 1u, hdr);
       if (nq1 > 0) wait_drain(BAR(QFULL + 1), (nq1 - 1) & 1u, hdr);
 #pragma unroll 1
-      for (uint32_t s = 0; s < kTiles; ++s) {
-        const uint32_t n = (seq + kTiles - 1 - s) / kTiles;
-        if (n > 0) wait_drain(BAR(FULL + s), (n - 1) & 1u, hdr);
+      for (uint32_t s = 0; s < kKTiles; ++s) {
+        const uint32_t n = (k_tiles + kKTiles - 1 - s) / kKTiles;
+        if (n > 0) wait_drain(BAR(KFULL + s), (n - 1) & 1u, hdr);
+      }
+#pragma unroll 1
+      for (uint32_t s = 0; s < kVTiles; ++s) {
+        const uint32_t n = (v_tiles + kVTiles - 1 - s) / kVTiles;
+        if (n > 0) wait_drain(BAR(VFULL + s), (n - 1) & 1u, hdr);
       }
     }
   } else if (smem_ok && warp < 3) {
@@ -387,17 +390,16 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     Tile it;
     const uint32_t s_col = tmem + kSCol + kKeys * t;
     const uint64_t desc_q = ptx::sdesc_sw128(sbase + static_cast<uint32_t>(t) * kQTile, 16, 1024);   // + chunks, K-steps
-    const uint64_t desc_k = ptx::sdesc_sw128(sbase + kOffRing, 16, 1024);
+    const uint64_t desc_k = ptx::sdesc_sw128(sbase + kOffK, 16, 1024);
     constexpr uint64_t kQChunkD = kQChunk >> 4, kChunkD = kChunk >> 4;           // in descriptor units
-    uint32_t slot = 0, seq = 0;              // ring slot and number of the next K tile
+    uint32_t kb = 0, k_phase = 0;
     uint32_t q_phase = 0, n_s = 0;           // S tiles issued so far
     bool ok = true;
     while (ok && next_warp(w, it)) {
       const int n0 = kv_tiles(it, 0, causal), n1 = kv_tiles(it, 1, causal);
       const int n_all = __shfl_sync(0xffffffffu, max(n0, n1), 0), n_mine = __shfl_sync(0xffffffffu, t ? n1 : n0, 0);
       for (int j = 0; j < n_all && ok; ++j) {
-        const uint32_t full = seq & (kTiles - 1);
-        ok = wait_short_warp(BAR(FULL + full), (seq >> 3) & 1u, hdr);
+        ok = wait_short_warp(BAR(KFULL + kb), k_phase, hdr);
         if (ok && j < n_mine) {
           if (j == 0) {
             ok = wait_short_warp(BAR(QFULL + t), q_phase, hdr);
@@ -409,25 +411,22 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           ++n_s;
           ptx::tc_fence_after();
           if (elect_one()) {
-            uint32_t sl = slot;
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
               const uint64_t da = desc_q + c * kQChunkD;
-              const uint64_t db = desc_k + sl * kChunkD;
+              const uint64_t db = desc_k + (3u * kb + c) * kChunkD;
 #pragma unroll
               for (int k = 0; k < 4; ++k) ptx::mma_ss(s_col, da + 2u * k, db + 2u * k, kIdescS, (c > 0 || k > 0) ? 1u : 0u);
-              if (++sl == kRing) sl = 0;
             }
             ptx::mma_commit(BAR(SFULL + t));
-            ptx::mma_commit(BAR(EMPTY + full));
+            ptx::mma_commit(BAR(KEMPTY + kb));
             if (j == n_mine - 1) ptx::mma_commit(BAR(QEMPTY + t));
           }
           __syncwarp();
         } else if (ok && elect_one()) {
-          ptx::mbar_arrive(BAR(EMPTY + full));
+          ptx::mbar_arrive(BAR(KEMPTY + kb));
         }
-        slot = slot + 5 < kRing ? slot + 5 : slot + 5 - kRing;
-        seq += 2;
+        if (++kb == kKTiles) { kb = 0; k_phase ^= 1u; }
       }
     }
     // every MMA this warp issued completes before the CTA may leave
@@ -441,9 +440,9 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     regs_issue();
     Walk w;
     Tile it;
-    const uint64_t desc_v = ptx::sdesc_sw128(sbase + kOffRing, kChunk, 1024);
+    const uint64_t desc_v = ptx::sdesc_sw128(sbase + kOffV, kChunk, 1024);
     constexpr uint64_t kChunkD = kChunk >> 4;
-    uint32_t slot = 3, seq = 1;              // ring slot and number of the next V tile
+    uint32_t vb = 0, v_phase = 0;
     uint32_t p_phase = 0, o_phase = 3;       // bit t: parity to wait for on PREADY, OFREE (the first item waits for none)
     bool ok = true, issued = false;
     while (ok && next_warp(w, it)) {
@@ -451,16 +450,14 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       const int n1 = __shfl_sync(0xffffffffu, kv_tiles(it, 1, causal), 0);
       const int n_all = max(n0, n1), nk = __shfl_sync(0xffffffffu, it.nk, 0);
       for (int j = 0; j < n_all && ok; ++j) {
-        const uint32_t full = seq & (kTiles - 1);
-        ok = wait_short_warp(BAR(FULL + full), (seq >> 3) & 1u, hdr);
+        ok = wait_short_warp(BAR(VFULL + vb), v_phase, hdr);
         const int valid = nk - j * kKeys;
         if (ok && valid < kKeys) {
           // keys past the sequence's end have P = 0; make their V rows 0 too
           // (they may be another sequence's, and hold NaN)
 #pragma unroll 1
           for (uint32_t c = 0; c < 2; ++c) {
-            const uint32_t sl = slot + c == kRing ? 0 : slot + c;
-            uint4* dst = reinterpret_cast<uint4*>(smem + kOffRing + sl * kChunk);
+            uint4* dst = reinterpret_cast<uint4*>(smem + kOffV + vb * kVTile + c * kChunk);
             for (int i = valid * 8 + lane; i < kKeys * 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
           }
           ptx::fence_proxy_async_cta();
@@ -480,29 +477,18 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           ptx::tc_fence_after();
           issued = true;
           if (elect_one()) {
-            const uint64_t db = desc_v + slot * kChunkD;
+            const uint64_t db = desc_v + 2u * vb * kChunkD;
             const uint32_t o_col = tmem + kOCol + 128u * t, p_col = tmem + kPCol + kKeys / 2 * t;
-            if (slot != kRing - 1) {
 #pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
-                ptx::mma_ts(o_col, p_col + 8u * k, db + 128u * k, kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
-            } else {
-              // the tile's second chunk wrapped to the ring's start: two halves
-#pragma unroll 1
-              for (int k = 0; k < kKeys / 16; ++k) {
-                const uint32_t acc = (j > 0 || k > 0) ? 1u : 0u;
-                ptx::mma_ts(o_col, p_col + 8u * k, db + 128u * k, kIdescPVHalf, acc);
-                ptx::mma_ts(o_col + 64u, p_col + 8u * k, desc_v + 128u * k, kIdescPVHalf, acc);
-              }
-            }
+            for (int k = 0; k < kKeys / 16; ++k)
+              ptx::mma_ts(o_col, p_col + 8u * k, db + 128u * k, kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
             ptx::mma_commit(BAR(PVDONE + t));
           }
           __syncwarp();
         }
-        if (ok && elect_one()) ptx::mma_commit(BAR(EMPTY + full));
+        if (ok && elect_one()) ptx::mma_commit(BAR(VEMPTY + vb));
         __syncwarp();
-        slot = slot + 5 < kRing ? slot + 5 : slot + 5 - kRing;
-        seq += 2;
+        if (++vb == kVTiles) { vb = 0; v_phase ^= 1u; }
       }
     }
     if (issued && elect_one()) {
