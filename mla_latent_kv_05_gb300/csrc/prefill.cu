@@ -15,7 +15,12 @@
 //
 // One persistent CTA per SM, work items (head, 256 query rows) handed out by
 // a counter, head by head (a head's K and V are then in L2 while its tiles
-// run) and within a head the longest tiles first.  An item's rows are two
+// run) and within a head the longest tiles first; the last heads, about five
+// items a CTA, are taken together, so that the longest tiles of the last one do
+// not start when everything else is done (4096 causal tokens 499 and 456 us,
+// 2048 155 and 134, 8 x up to 256 over up to 4096 290 and 235).  Not where all
+// tiles are about as long: there is nothing to balance, and the tiles of a head
+// that run together share its K and V in L2.  An item's rows are two
 // M = 128 tiles that share each K/V tile of 80 keys:
 //   tensor memory (512 columns): O0 | O1 (128 fp32 columns each), S0 | S1 (80
 //       each), P0 | P1 (bf16, 40 each);
@@ -47,15 +52,17 @@
 // exceeds it by more than 2^kLazy, so O is rescaled rarely; its softmax warps
 // do that themselves, after the previous P.V of the tile has completed.
 //
-// Measured: 8192 causal tokens 1.74 ms (1580 TFLOP/s; 1.8 to 1.9 in a loop of
-// seconds, under the power cap), eight prompts of 54 to 1523 tokens 265 us (940;
-// HBM alone takes 130), 2 x 512 queries over 15,000 keys 900 us (1420), five
-// prompts of up to 33 tokens 18.6 us.  A step takes about 2200 cycles, 1852 of
-// them MMAs: K tiles land 1400 cycles after they are asked for (1900 from HBM),
-// and an item's queries about 1900 after the last item's scores, because a
-// second copy of them does not fit beside the ring.  Tried and no faster: K and
-// V ahead of the queries, and prefetches of either into L2 (0 to 10 % slower on
-// ragged prompts).
+// K and V have rings of their own: in one ring a K tile waited for the V tile
+// whose slots it reused, which is read 600 cycles later (8192 causal 1.85 ms in
+// a loop against 1.62; with two V tiles instead of three 1.95).
+//
+// Measured: 8192 causal tokens 1.60 ms (1715 TFLOP/s; 1.65 to 1.7 in a loop of
+// seconds, under the power cap), eight prompts of 54 to 1523 tokens 235 us
+// (1050; HBM alone takes 130), 2 x 512 queries over 15,000 keys 840 us (1520),
+// five prompts of up to 33 tokens 18.6 us.  An item's queries land about 1900
+// cycles after the last item's scores, because a second copy of them does not
+// fit beside K and V.  Tried and no faster: K and V ahead of the queries (0 to 3 %
+// either way), prefetches of K and V into L2 (3 % slower on ragged prompts).
 //
 // Every wait is bounded: a timeout records MLA_STATUS_TIMEOUT and raises the
 // abort flag, all roles leave, and the kernel ends through its teardown.
@@ -79,6 +86,7 @@ constexpr uint32_t kOffK = 2 * kQTile;
 constexpr uint32_t kOffV = kOffK + kKTiles * kKTile;
 constexpr uint32_t kOffBar = kOffV + kVTiles * kVTile;    // 216 KiB
 constexpr int kItemSlots = 2;
+constexpr int kTailItems = 5;                      // items per CTA of the heads that are taken together at the end
 enum Bar {
   QFULL = 0, QEMPTY = QFULL + 2, KFULL = QEMPTY + 2, KEMPTY = KFULL + kKTiles, VFULL = KEMPTY + kKTiles,
   VEMPTY = VFULL + kVTiles, SFULL = VEMPTY + kVTiles, SREAD = SFULL + 2,
@@ -99,8 +107,9 @@ constexpr uint32_t kIdescPV = ptx::idesc_bf16(128, 128, 0, 1);   // P in tensor 
 constexpr float kLazy = 12.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Header fields this operator uses: n_tiles (tiles in the list) and chunk
-// (the next work item).
+// Header fields this operator uses: n_tiles (tiles in the list), chunk (the next
+// work item after each CTA's first) and slots_per_query (heads taken together at
+// the end).
 struct Tile {
   int q0, rows;   // first packed query row, query rows (1..256)
   int k0, nk;     // first packed key, keys of the sequence
@@ -127,13 +136,18 @@ constexpr int kClasses = 1024;
 
 __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __restrict__ cu_q,
                                                             const int32_t* __restrict__ cu_k, int batch, int nq, int nk,
-                                                            int causal, uint8_t* __restrict__ ws, PrefillWs L) {
+                                                            int causal, int first, uint8_t* __restrict__ ws, PrefillWs L) {
   __shared__ int s_count[kClasses];
   __shared__ int s_warp[32];
+  __shared__ int s_longest, s_shortest;
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(ws);
   Tile* tiles = reinterpret_cast<Tile*>(ws + L.tiles);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   s_count[tid] = 0;
+  if (tid == 0) {
+    s_longest = 0;
+    s_shortest = kClasses;
+  }
   ptx::grid_dep_launch();   // the attention kernel may set itself up; it waits for this grid before it reads the list
   __syncthreads();
   for (int pass = 0; pass < 2; ++pass) {
@@ -153,7 +167,12 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
         t.lim = causal ? i * kPrefillTile + 1 + (n_k - n_q) : n_k;
         t.head = 0;
         t.pad[0] = t.pad[1] = 0;
-        const int c = kClasses - 1 - min(kClasses - 1, max(kv_tiles(t, 0, causal), kv_tiles(t, 1, causal)));
+        const int steps = min(kClasses - 1, max(kv_tiles(t, 0, causal), kv_tiles(t, 1, causal)));
+        const int c = kClasses - 1 - steps;
+        if (pass == 0) {
+          atomicMax(&s_longest, steps);
+          atomicMin(&s_shortest, steps);
+        }
         const int pos = atomicAdd(&s_count[c], 1);
         if (pass == 1) {
           if (pos < L.max_tiles) tiles[pos] = t;
@@ -177,8 +196,12 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
       for (int w = 0; w < warp; ++w) before += s_warp[w];
       s_count[tid] = before + x - v;
       if (tid == 1023) {
-        hdr->n_tiles = min(before + x, L.max_tiles);
-        hdr->chunk = 0;
+        const int n_tiles = min(before + x, L.max_tiles);
+        hdr->n_tiles = n_tiles;
+        hdr->chunk = first;
+        // heads taken together at the end: one where all tiles are about as long
+        hdr->slots_per_query =
+            2 * s_longest > 3 * s_shortest ? min(kHeads, (kTailItems * first + n_tiles - 1) / max(n_tiles, 1)) : 1;
         hdr->abort_flag = 0;
       }
       __syncthreads();
@@ -311,18 +334,26 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       };
       const Tile* tiles = reinterpret_cast<const Tile*>(p.ws + L.tiles);
       const int n_tiles = *reinterpret_cast<const volatile int*>(&hdr->n_tiles);
+      const int tail = max(1, *reinterpret_cast<const volatile int*>(&hdr->slots_per_query));
+      const int first_late = n_tiles * (kHeads - tail);
       auto record = [&](int item) {
         Tile t;
         t.q0 = t.rows = t.k0 = t.nk = t.lim = 0;
         t.head = -1;
         if (item < n_tiles * kHeads) {
-          t = tiles[item % n_tiles];
-          t.head = item / n_tiles;
+          const bool late = item >= first_late;
+          const int left = late ? item - first_late : item, by = late ? tail : n_tiles;
+          const int q = left / by, r = left - q * by;
+          t = tiles[late ? q : r];
+          t.head = late ? kHeads - tail + r : q;
         }
         return t;
       };
-      // one record and one item number ahead, so that neither's latency is waited for
-      Tile it = record(atomicAdd(&hdr->chunk, 1));
+      // The first item is the CTA's own number; the next one is claimed at the last
+      // tile of the one before, early enough that its latency is not waited for
+      // and no earlier: items held in advance leave other CTAs idle (256 items
+      // of 1.7 ms took 4.7 ms instead of 3.5 in some runs).
+      Tile it = record(static_cast<int>(blockIdx.x));
       int item = atomicAdd(&hdr->chunk, 1);
       while (ok) {
         ok = wait_short(BAR(IEMPTY + w.slot), w.phase ^ 1u, hdr);
@@ -333,7 +364,6 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
         if (it.head < 0) break;
         const Tile ahead = record(item);
-        item = atomicAdd(&hdr->chunk, 1);
         const int n0 = kv_tiles(it, 0, causal), n1 = kv_tiles(it, 1, causal), n = max(n0, n1);
         if (n0 > 0) {
           query(0, nq0, it);
@@ -341,6 +371,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         }
         for (int j = 0; j < n && ok; ++j) {
           const int k = it.k0 + j * kKeys;
+          if (j == n - 1) item = atomicAdd(&hdr->chunk, 1);
           ok = wait_short(BAR(KEMPTY + kb), k_phase ^ 1u, hdr);
           if (!ok) break;
           ptx::mbar_arrive_expect_tx(BAR(KFULL + kb), kKTile);
@@ -364,6 +395,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           if (++vb == kVTiles) { vb = 0; v_phase ^= 1u; }
           ++v_tiles;
         }
+        if (n == 0) item = atomicAdd(&hdr->chunk, 1);
         it = ahead;
       }
       // no copy may land after the CTA has left: wait for the last phase armed on each barrier
@@ -688,12 +720,13 @@ cudaError_t launch_prefill(PFN_cuTensorMapEncodeTiled_v12000 encode, const Prefi
   static std::atomic<uint64_t> configured{0};
   cudaError_t e = allow_smem(prefill_kernel, kSmem, configured);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(prefill_plan_kernel, dim3(1), dim3(1024), 0, stream, p.cu_q, p.cu_k, p.batch, p.nq, p.nk, p.causal,
-                    p.ws, L);
-  if (e != cudaSuccess) return e;
   const long long items = static_cast<long long>(L.max_tiles) * kHeads;
+  const int ctas = static_cast<int>(items < sms ? items : sms);
+  e = launch_kernel(prefill_plan_kernel, dim3(1), dim3(1024), 0, stream, p.cu_q, p.cu_k, p.batch, p.nq, p.nk, p.causal,
+                    ctas, p.ws, L);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items < sms ? items : sms));
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
