@@ -56,9 +56,9 @@
 // whose slots it reused, which is read 600 cycles later (8192 causal 1.85 ms in
 // a loop against 1.62; with two V tiles instead of three 1.95).
 //
-// Measured: 8192 causal tokens 1.60 ms (1715 TFLOP/s; 1.65 to 1.7 in a loop of
+// Measured: 8192 causal tokens 1.53 ms (1800 TFLOP/s; 1.6 to 1.7 in a loop of
 // seconds, under the power cap), eight prompts of 54 to 1523 tokens 235 us
-// (1050; HBM alone takes 130), 2 x 512 queries over 15,000 keys 840 us (1520),
+// (1060; HBM alone takes 130), 2 x 512 queries over 15,000 keys 840 us (1520),
 // five prompts of up to 33 tokens 18.6 us.  An item's queries land about 1900
 // cycles after the last item's scores, because a second copy of them does not
 // fit beside K and V.  Tried and no faster: K and V ahead of the queries (0 to 3 %

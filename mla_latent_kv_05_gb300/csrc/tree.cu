@@ -42,11 +42,11 @@
 // different nodes of one sequence at a time and find its rows in L2 (64 x 4
 // nodes over 4096 tokens: 247 us by sequence, 199 by node).
 //
-// Measured, whole call: 8 x 61 nodes over 4096 tokens 339 us (1655 TFLOP/s; the
-// decode kernel's form of it 554), 16 x 16 over up to 8192 199 us (1429), 8 nodes
-// over 1000 23 us (four kernels of 2 to 11 us).  A tile takes about 2500 cycles,
-// 2184 of them MMAs; what remains is waiting for V's second page (272 KiB of
-// rows a tile and pair, 50 bytes a cycle for each SM from L2).
+// Measured, whole call: 8 x 61 nodes over 4096 tokens 329 us (1690 TFLOP/s; the
+// decode kernel's form of it 554), 16 x up to 16 over up to 8192 120 us (1180),
+// 64 x 16 over 4096 720 us (1620), 8 nodes over 1000 18.6 us (four kernels of 2 to
+// 9 us).  A tile takes about 2300 cycles, 2184 of them MMAs; a segment's output
+// another 4500, while the next segment's first scores wait.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
