@@ -20,7 +20,9 @@
 // not start when everything else is done (4096 causal tokens 499 and 456 us,
 // 2048 155 and 134, 8 x up to 256 over up to 4096 290 and 235).  Not where all
 // tiles are about as long: there is nothing to balance, and the tiles of a head
-// that run together share its K and V in L2.  An item's rows are two
+// that run together share its K and V in L2.  There the last round's items go
+// out in halves if it would leave half of the SMs idle (2 x 512 queries over
+// 15,000 keys 879 and 815 us).  An item's rows are two
 // M = 128 tiles that share each K/V tile of 80 keys:
 //   tensor memory (512 columns): O0 | O1 (128 fp32 columns each), S0 | S1 (80
 //       each), P0 | P1 (bf16, 40 each);
@@ -56,9 +58,9 @@
 // whose slots it reused, which is read 600 cycles later (8192 causal 1.85 ms in
 // a loop against 1.62; with two V tiles instead of three 1.95).
 //
-// Measured: 8192 causal tokens 1.53 ms (1800 TFLOP/s; 1.6 to 1.7 in a loop of
+// Measured: 8192 causal tokens 1.52 ms (1815 TFLOP/s; 1.6 to 1.7 in a loop of
 // seconds, under the power cap), eight prompts of 54 to 1523 tokens 235 us
-// (1060; HBM alone takes 130), 2 x 512 queries over 15,000 keys 840 us (1520),
+// (1060; HBM alone takes 130), 2 x 512 queries over 15,000 keys 798 us (1605),
 // five prompts of up to 33 tokens 18.6 us.  An item's queries land about 1900
 // cycles after the last item's scores, because a second copy of them does not
 // fit beside K and V.  Tried and no faster: K and V ahead of the queries (0 to 3 %
@@ -86,6 +88,7 @@ constexpr uint32_t kOffK = 2 * kQTile;
 constexpr uint32_t kOffV = kOffK + kKTiles * kKTile;
 constexpr uint32_t kOffBar = kOffV + kVTiles * kVTile;    // 216 KiB
 constexpr int kItemSlots = 2;
+constexpr int kHalvesFrom = 8;                     // K tiles from which a last round's items are halved
 constexpr int kTailItems = 5;                      // items per CTA of the heads that are taken together at the end
 enum Bar {
   QFULL = 0, QEMPTY = QFULL + 2, KFULL = QEMPTY + 2, KEMPTY = KFULL + kKTiles, VFULL = KEMPTY + kKTiles,
@@ -108,8 +111,8 @@ constexpr float kLazy = 12.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // Header fields this operator uses: n_tiles (tiles in the list), chunk (the next
-// work item after each CTA's first) and slots_per_query (heads taken together at
-// the end).
+// work item after each CTA's first), slots_per_query (heads taken together at
+// the end) and n_empty (the first item that goes out in halves).
 struct Tile {
   int q0, rows;   // first packed query row, query rows (1..256)
   int k0, nk;     // first packed key, keys of the sequence
@@ -199,9 +202,13 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
         const int n_tiles = min(before + x, L.max_tiles);
         hdr->n_tiles = n_tiles;
         hdr->chunk = first;
-        // heads taken together at the end: one where all tiles are about as long
-        hdr->slots_per_query =
-            2 * s_longest > 3 * s_shortest ? min(kHeads, (kTailItems * first + n_tiles - 1) / max(n_tiles, 1)) : 1;
+        // heads taken together at the end: one where all tiles are about as long.
+        // There, if the last round would leave half of the CTAs idle and its items
+        // are not short, they go out as two halves of 128 rows.
+        const bool even = 2 * s_longest <= 3 * s_shortest;
+        const int items = n_tiles * kHeads, rest = items % first;
+        hdr->slots_per_query = even ? 1 : min(kHeads, (kTailItems * first + n_tiles - 1) / max(n_tiles, 1));
+        hdr->n_empty = even && s_longest >= kHalvesFrom && 2 * rest <= first ? items - rest : INT_MAX;
         hdr->abort_flag = 0;
       }
       __syncthreads();
@@ -334,18 +341,27 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       };
       const Tile* tiles = reinterpret_cast<const Tile*>(p.ws + L.tiles);
       const int n_tiles = *reinterpret_cast<const volatile int*>(&hdr->n_tiles);
-      const int tail = max(1, *reinterpret_cast<const volatile int*>(&hdr->slots_per_query));
-      const int first_late = n_tiles * (kHeads - tail);
+      const int tail = *reinterpret_cast<const volatile int*>(&hdr->slots_per_query);
+      const int first_half = *reinterpret_cast<const volatile int*>(&hdr->n_empty);
+      const int items = n_tiles * kHeads, first_late = items - n_tiles * tail;
       auto record = [&](int item) {
         Tile t;
         t.q0 = t.rows = t.k0 = t.nk = t.lim = 0;
         t.head = -1;
-        if (item < n_tiles * kHeads) {
+        const int half = item >= first_half ? (item - first_half) & 1 : -1;
+        if (half >= 0) item = first_half + ((item - first_half) >> 1);
+        if (item < items) {
           const bool late = item >= first_late;
           const int left = late ? item - first_late : item, by = late ? tail : n_tiles;
           const int q = left / by, r = left - q * by;
           t = tiles[late ? q : r];
           t.head = late ? kHeads - tail + r : q;
+          if (half == 0) t.rows = min(t.rows, 128);
+          if (half == 1) {                     // (none of a tile of 128 rows or fewer)
+            t.q0 += 128;
+            t.rows = max(t.rows - 128, 0);
+            t.lim += causal ? 128 : 0;
+          }
         }
         return t;
       };
