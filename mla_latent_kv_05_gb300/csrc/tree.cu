@@ -353,7 +353,8 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
         float mx = max32(s);
         const bool up = !ok || t == sg.t0 || (m_ref == -INFINITY ? mx != -INFINITY : (mx - m_ref) * c > kLazy);
         float alpha = 1.f;
-        if (any_of_group(group, up)) {
+        const bool moving = any_of_group(group, up);
+        if (moving) {
           // rare: agree on the heads' maxima and move the references that need it
           *own = mx;
           quit = any_of_group(group, !ok);
@@ -383,17 +384,26 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
         // the previous P.V has read P (and completed O)
         if (n > 0 && !wait_short_warp(BAR(PVDONE), (n - 1) & 1u, hdr)) ok = false;
         ptx::tc_fence_after();
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+        if (moving && t != sg.t0) {            // (a segment's first tile finds O empty)
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-          for (int q = 4 * cf; q < 4 * cf + 4; ++q) {
-            uint32_t o[32];
-            ptx::tmem_ld32(tmem + lane_base + kOCol + 32u * q, o);
-            ptx::tmem_wait_ld();
+            for (int q = 4 * cf; q < 4 * cf + 4; ++q) {
+              uint32_t o[32];
+              ptx::tmem_ld32(tmem + lane_base + kOCol + 32u * q, o);
+              ptx::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            ptx::tmem_st32(tmem + lane_base + kOCol + 32u * q, o);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              ptx::tmem_st32(tmem + lane_base + kOCol + 32u * q, o);
+            }
+            ptx::tmem_wait_st();
           }
-          ptx::tmem_wait_st();
+          // A page's P.V adds to all columns of a head, lanes 0..63 and 64..127,
+          // and starts on that page's P, which two of the four warps write (hf).
+          // So each of them arrives only when all four have rescaled their lanes:
+          // this barrier orders the other page's warps before the arrival below.
+          ptx::tc_fence_before();
+          any_of_group(group, false);
+          ptx::tc_fence_after();
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)          // 64 tokens = one 128-byte swizzled row
