@@ -148,16 +148,22 @@ expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, Plan
       }
       // no copy may land after the CTA has left: rank 0's barriers count both
       // ranks' bytes (after a wait that gave up, the pause at the end covers
-      // what was not waited for here)
-      if (rank == 0 && ok) {
+      // what was not waited for here).  Nor any arrival: rank 0's commits arrive in
+      // both ranks, and that it has seen its own says nothing about the other's;
+      // the commit to DRAIN is the last one.
+      if (ok && nc > 0) {
 #pragma unroll 1
-        for (int b = 0; b < kKBlocks; ++b)
-          if (nw > 0) wait_drain(BAR(WFULL + b), (nw - 1) & 1, hdr);
+        for (int b = 0; b < kKBlocks; ++b) {
+          if (rank == 0) wait_drain(BAR(WFULL + b), (nw - 1) & 1, hdr);
+          wait_short<true>(BAR(WEMPTY + b), (nw - 1) & 1, hdr);
+        }
 #pragma unroll 1
         for (int b = 0; b < kStages; ++b) {
           const int n = (nc + kStages - 1 - b) / kStages;     // times stage b was armed
-          if (n > 0) wait_drain(BAR(CFULL + b), (n - 1) & 1, hdr);
+          if (rank == 0) wait_drain(BAR(CFULL + b), (n - 1) & 1, hdr);
+          wait_short<true>(BAR(CEMPTY + b), (n - 1) & 1, hdr);
         }
+        if (rank == 1) wait_short<true>(BAR(DRAIN), 0u, hdr);
       }
     }
   } else if (warp == 1 && rank == 0) {
@@ -197,7 +203,8 @@ expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, Plan
       d ^= 1;
       if (d == 0) dph ^= 1u;
     }
-    // every MMA (and commit to the other rank) completes before the pair may leave
+    // every MMA completes before the pair may leave (the commits to rank 1 are
+    // waited for there, by its loader)
     if (lo < hi && elect_one()) {   // the lane that issued them
       ptx::pair_commit(BAR(DRAIN));
       wait_drain(BAR(DRAIN), 0u, hdr);

@@ -199,6 +199,13 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
         for (int g = 0; g < 3; ++g)
           if (nt > 0) wait_drain(BAR(KFULL + g), (nt - 1) & 1u, hdr);
       }
+      // nor any arrival: rank 0's commits arrive in both ranks, and that it has seen
+      // its own says nothing about the other's
+      if (ok && nt > 0) {
+#pragma unroll 1
+        for (int g = 0; g < 3; ++g) wait_short<true>(BAR(KEMPTY + g), (nt - 1) & 1u, hdr);
+        wait_short<true>(BAR(QEMPTY), (nq - 1) & 1u, hdr);
+      }
     }
   } else if (smem_ok && warp == 3) {
     // ------------------------------------------------------------ loads of V
@@ -222,9 +229,16 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
           if (ok) ++nt;
         }
       }
+      // no copy or arrival may land after the CTA has left (as for Q and K); the
+      // commit to DRAIN is the last one
+      if (ok && nt > 0) {
 #pragma unroll 1
-      for (int a = 0; a < 2; ++a)
-        if (ok && nt > 0) wait_drain(BAR(VFULL + a), (nt - 1) & 1u, hdr);
+        for (int a = 0; a < 2; ++a) {
+          wait_drain(BAR(VFULL + a), (nt - 1) & 1u, hdr);
+          wait_short<true>(BAR(VEMPTY + a), (nt - 1) & 1u, hdr);
+        }
+        if (rank == 1) wait_short<true>(BAR(DRAIN), 0u, hdr);   // (here, not from the start: the limit is for a wait)
+      }
     }
   } else if (smem_ok && warp == 1 && rank == 0) {
     // ------------------------------------------------------------ MMA issuer
@@ -295,7 +309,8 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
       }
       ++n_seg;
     }
-    // every MMA (and commit to the other rank) completes before the pair may leave
+    // every MMA completes before the pair may leave (the commits to rank 1 are
+    // waited for there, by its loaders)
     if (n_s > 0 && elect_one()) {   // the lane that issued them
       ptx::pair_commit(BAR(DRAIN));
       wait_drain(BAR(DRAIN), 0u, hdr);
