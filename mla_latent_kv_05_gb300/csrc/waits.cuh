@@ -30,12 +30,15 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                :: "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
 }
-// Tell the pair's leader.  What the arrival hands over lies in this CTA's own
-// tensor and shared memory and has been read, or made visible to the MMAs
-// (fence.proxy.async), before it; a release at cluster scope would also wait
-// for the CTA's writes to global memory and took 1000 cycles a tile.
+// Tell the pair's leader, in the other CTA or in this one.  What the arrival
+// hands over lies in this CTA's own shared memory (written, and made visible to
+// the MMAs by fence.proxy.async, before it) or tensor memory (read or written,
+// tcgen05.fence).  So the release at cluster scope, which the waiter's acquire
+// needs to see this CTA's writes, is restricted to shared memory; an unrestricted
+// one also waits for the CTA's writes to global memory, 1000 cycles a tile.
 __device__ __forceinline__ void arrive_leader(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n\t"
+               "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
 }
 // tiled loads whose bytes are counted on a barrier of either CTA of the pair (a cluster address)
 __device__ __forceinline__ void pair_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z,
