@@ -366,11 +366,12 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         return t;
       };
       // The first item is the CTA's own number; the next one is claimed at the last
-      // tile of the one before, early enough that its latency is not waited for
-      // and no earlier: items held in advance leave other CTAs idle (256 items
-      // of 1.7 ms took 4.7 ms instead of 3.5 in some runs).
+      // tile but one of the one before, early enough that its latency is not waited
+      // for and no earlier: an item held in advance leaves other CTAs idle, and goes
+      // to the CTA that asked first, not to the one that is done first (one held all
+      // along: 8 x up to 700 over up to 4000 tokens 390 us instead of 379, 16 x up
+      // to 200 55 instead of 53; two: 256 items of 1.7 ms 4.7 ms instead of 3.5).
       Tile it = record(static_cast<int>(blockIdx.x));
-      int item = atomicAdd(&hdr->chunk, 1);
       while (ok) {
         ok = wait_short(BAR(IEMPTY + w.slot), w.phase ^ 1u, hdr);
         if (!ok) break;
@@ -379,7 +380,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         ptx::mbar_arrive(BAR(IFULL + w.slot));
         if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
         if (it.head < 0) break;
-        const Tile ahead = record(item);
+        int item = 0;
         const int n0 = kv_tiles(it, 0, causal), n1 = kv_tiles(it, 1, causal), n = max(n0, n1);
         if (n0 > 0) {
           query(0, nq0, it);
@@ -387,7 +388,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         }
         for (int j = 0; j < n && ok; ++j) {
           const int k = it.k0 + j * kKeys;
-          if (j == n - 1) item = atomicAdd(&hdr->chunk, 1);
+          if (j == max(n - 2, 0)) item = atomicAdd(&hdr->chunk, 1);
           ok = wait_short(BAR(KEMPTY + kb), k_phase ^ 1u, hdr);
           if (!ok) break;
           ptx::mbar_arrive_expect_tx(BAR(KFULL + kb), kKTile);
@@ -412,7 +413,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           ++v_tiles;
         }
         if (n == 0) item = atomicAdd(&hdr->chunk, 1);
-        it = ahead;
+        it = record(item);
       }
       // no copy may land after the CTA has left: wait for the last phase armed on each barrier
       if (nq0 > 0) wait_drain(BAR(QFULL), (nq0 - 1) & 1u, hdr);
