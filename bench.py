@@ -59,7 +59,7 @@ def load_peaks():
 # the headers it includes, and the planner (its partition sets the split
 # partials the kernel writes).  The merge, W^UV and API files are not among
 # them.
-KERNEL_SOURCES = ("decode.cu", "decode.cuh", "common.cuh", "ptx.cuh", "plan.cu")
+KERNEL_SOURCES = ("decode.cu", "decode.cuh", "common.cuh", "ptx.cuh", "walk.cuh", "plan.cu")
 
 
 def kernel_source_hash():
