@@ -4,6 +4,11 @@ Argument marshalling only: tensors are checked for device, dtype, shape and
 contiguity, their raw pointers and the current CUDA stream are handed to the
 library, and every step of the decode runs in the library's kernels.  There
 is no fallback: if the library is missing or a call fails, an error is raised.
+
+stream: the stream of a call's kernels, None for the current one.  On another
+stream than the current one, the caller's tensors have to be ready there and to
+live until the kernels are done; what a call allocates itself (outputs and a
+workspace that were not given) is that stream's memory.
 """
 from __future__ import annotations
 
@@ -146,6 +151,29 @@ def _same_device(tensors: dict, current: int) -> None:
                          f"call under torch.cuda.device({first})")
 
 
+def _status_workspace(device) -> torch.Tensor:
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def _new(stream, make, *args, **kwargs) -> torch.Tensor:
+    """A tensor that a call allocates itself, for kernels that run on `stream`:
+    its memory is that stream's, so that neither what a free block was last used
+    for nor its next use after the call lies on another stream than they do, and
+    a fill (a zeroed workspace) comes before them.  The caller's current stream may
+    use the tensor as well (after it has waited for `stream`)."""
+    if stream is None:
+        return make(*args, **kwargs)
+    current = torch.cuda.current_stream()
+    if current.cuda_stream == stream.cuda_stream:
+        return make(*args, **kwargs)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kwargs)
+    t.record_stream(current)
+    return t
+
+
 def mla_workspace_size(batch: int, sq: int, num_heads: int = 128, page_size: int = 64) -> int:
     n = ctypes.c_size_t(0)
     rc = load().mla_workspace_size(int(batch), int(sq), int(num_heads), int(page_size), ctypes.byref(n))
@@ -173,13 +201,13 @@ def _decode(fn_name, q_absorbed, q_rope, kv_cache, block_table, seq_lens, scale,
         raise ValueError("block_table must be [B, max_pages]")
     _check(seq_lens, "seq_lens", torch.int32, (B,))
     if out is None:
-        out = torch.empty((B, Sq, H, 512), dtype=torch.bfloat16, device=q_absorbed.device)
+        out = _new(stream, torch.empty, (B, Sq, H, 512), dtype=torch.bfloat16, device=q_absorbed.device)
     if lse is None:
-        lse = torch.empty((B, Sq, H), dtype=torch.float32, device=q_absorbed.device)
+        lse = _new(stream, torch.empty, (B, Sq, H), dtype=torch.float32, device=q_absorbed.device)
     _check(out, "out", torch.bfloat16, (B, Sq, H, 512))
     _check(lse, "lse", torch.float32, (B, Sq, H))
     if workspace is None:
-        workspace = alloc_workspace(B, Sq, q_absorbed.device)
+        workspace = _new(stream, alloc_workspace, B, Sq, q_absorbed.device)
     _check(workspace, "workspace", torch.uint8)
     _same_device(dict(q_absorbed=q_absorbed, q_rope=q_rope, kv_cache=kv_cache, block_table=block_table,
                       seq_lens=seq_lens, out=out, lse=lse, workspace=workspace), torch.cuda.current_device())
@@ -218,9 +246,9 @@ def mla_decode_bf16_noalloc(q_absorbed, q_rope, kv_cache, block_table, seq_lens,
         raise ValueError("block_table must be [B, max_pages]")
     _check(seq_lens, "seq_lens", torch.int32, (B,))
     if out is None:
-        out = torch.empty((B, Sq, H, 512), dtype=torch.bfloat16, device=q_absorbed.device)
+        out = _new(stream, torch.empty, (B, Sq, H, 512), dtype=torch.bfloat16, device=q_absorbed.device)
     if lse is None:
-        lse = torch.empty((B, Sq, H), dtype=torch.float32, device=q_absorbed.device)
+        lse = _new(stream, torch.empty, (B, Sq, H), dtype=torch.float32, device=q_absorbed.device)
     _check(out, "out", torch.bfloat16, (B, Sq, H, 512))
     _check(lse, "lse", torch.float32, (B, Sq, H))
     if device_status is not None:
@@ -307,13 +335,13 @@ def mla_decode_sparse_bf16(q_absorbed, q_rope, kv_cache, token_slots, scale, out
         raise ValueError("token_slots must be [B, Sq, topk]")
     topk = int(token_slots.shape[2])
     if out is None:
-        out = torch.empty((B, Sq, H, 512), dtype=torch.bfloat16, device=q_absorbed.device)
+        out = _new(stream, torch.empty, (B, Sq, H, 512), dtype=torch.bfloat16, device=q_absorbed.device)
     if lse is None:
-        lse = torch.empty((B, Sq, H), dtype=torch.float32, device=q_absorbed.device)
+        lse = _new(stream, torch.empty, (B, Sq, H), dtype=torch.float32, device=q_absorbed.device)
     _check(out, "out", torch.bfloat16, (B, Sq, H, 512))
     _check(lse, "lse", torch.float32, (B, Sq, H))
     if workspace is None:
-        workspace = alloc_workspace_sparse(B, Sq, topk, q_absorbed.device)
+        workspace = _new(stream, alloc_workspace_sparse, B, Sq, topk, q_absorbed.device)
     _check(workspace, "workspace", torch.uint8)
     _same_device(dict(q_absorbed=q_absorbed, q_rope=q_rope, kv_cache=kv_cache, token_slots=token_slots, out=out,
                       lse=lse, workspace=workspace), torch.cuda.current_device())
@@ -338,10 +366,10 @@ def mla_up_project_wuv(latent, w_uv, out=None, workspace=None, stream=None):
     for x in lead:
         rows *= int(x)
     if out is None:
-        out = torch.empty(lead + (128, 128), dtype=torch.bfloat16, device=latent.device)
+        out = _new(stream, torch.empty, lead + (128, 128), dtype=torch.bfloat16, device=latent.device)
     _check(out, "out", torch.bfloat16, lead + (128, 128))
     if workspace is None:
-        workspace = torch.zeros(256, dtype=torch.uint8, device=latent.device)
+        workspace = _new(stream, _status_workspace, latent.device)
     _check(workspace, "workspace", torch.uint8)
     _same_device(dict(latent=latent, w_uv=w_uv, out=out, workspace=workspace), torch.cuda.current_device())
     rc = load().mla_up_project_wuv(_ptr(latent), _ptr(w_uv), rows, 128, 128, _ptr(out), _ptr(workspace),
@@ -414,10 +442,6 @@ def _handle(stream, device: int) -> int:
     return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
-def _status_workspace(device) -> torch.Tensor:
-    return torch.zeros(256, dtype=torch.uint8, device=device)
-
-
 _ROW_WIDTH = {"bf16": 576, "fp8": 594, "fp4": 324, "fp8_v41": 528, "fp4_v41": 288}
 
 
@@ -440,7 +464,7 @@ def _append(fmt, c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspa
     r_at, r_stride = _rows_arg(k_rope, "k_rope", 64, rows)
     _check_cache(fmt, kv_cache, block_table, seq_lens, cu_rows)
     if workspace is None:
-        workspace = _status_workspace(kv_cache.device)
+        workspace = _new(stream, _status_workspace, kv_cache.device)
     _check(workspace, "workspace", torch.uint8)
     dev = torch.cuda.current_device()
     if not (kv_cache.device == c_kv.device == k_rope.device == block_table.device == seq_lens.device == cu_rows.device
@@ -465,11 +489,11 @@ def _gather(fmt, kv_cache, block_table, seq_lens, cu_rows, n_rows, out, workspac
     if rows < 0:
         raise ValueError("n_rows must not be negative")
     if out is None:
-        out = torch.empty((rows, 576), dtype=torch.bfloat16, device=kv_cache.device)
+        out = _new(stream, torch.empty, (rows, 576), dtype=torch.bfloat16, device=kv_cache.device)
     else:
         _check(out, "out", torch.bfloat16, (rows, 576))
     if workspace is None:
-        workspace = _status_workspace(kv_cache.device)
+        workspace = _new(stream, _status_workspace, kv_cache.device)
     _check(workspace, "workspace", torch.uint8)
     dev = torch.cuda.current_device()
     if not (kv_cache.device == block_table.device == seq_lens.device == cu_rows.device == out.device
@@ -596,17 +620,17 @@ def _tree(fmt, q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, sca
     if n_nodes is not None:
         _check(n_nodes, "n_nodes", torch.int32, (B,))
     if out is None:
-        out = torch.empty((B, T, H, 512), dtype=torch.bfloat16, device=q_absorbed.device)
+        out = _new(stream, torch.empty, (B, T, H, 512), dtype=torch.bfloat16, device=q_absorbed.device)
     else:
         _check(out, "out", torch.bfloat16, (B, T, H, 512))
     if lse is None:
-        lse = torch.empty((B, T, H), dtype=torch.float32, device=q_absorbed.device)
+        lse = _new(stream, torch.empty, (B, T, H), dtype=torch.float32, device=q_absorbed.device)
     else:
         _check(lse, "lse", torch.float32, (B, T, H))
     max_pages = block_table.shape[1]
     if workspace is None:
         widen = fmt != "bf16" and T > 1 and B * max_pages * _WIDENED_PAGE <= _WIDENED_DEFAULT
-        workspace = alloc_workspace_tree(B, T, q_absorbed.device, max_pages if widen else 0)
+        workspace = _new(stream, alloc_workspace_tree, B, T, q_absorbed.device, max_pages if widen else 0)
     _check(workspace, "workspace", torch.uint8)
     dev = torch.cuda.current_device()
     if not (q_absorbed.device == q_rope.device == kv_cache.device == block_table.device == seq_lens.device
@@ -673,15 +697,15 @@ def mla_expand_kv(latent, w_uk, w_uv, k_nope=None, v=None, workspace=None, strea
     _check(w_uv, "w_uv", torch.bfloat16, (128, 128, 512))
     n = latent.shape[0]
     if k_nope is None:
-        k_nope = torch.empty((n, 128, 128), dtype=torch.bfloat16, device=latent.device)
+        k_nope = _new(stream, torch.empty, (n, 128, 128), dtype=torch.bfloat16, device=latent.device)
     else:
         _check(k_nope, "k_nope", torch.bfloat16, (n, 128, 128))
     if v is None:
-        v = torch.empty((n, 128, 128), dtype=torch.bfloat16, device=latent.device)
+        v = _new(stream, torch.empty, (n, 128, 128), dtype=torch.bfloat16, device=latent.device)
     else:
         _check(v, "v", torch.bfloat16, (n, 128, 128))
     if workspace is None:
-        workspace = _status_workspace(latent.device)
+        workspace = _new(stream, _status_workspace, latent.device)
     _check(workspace, "workspace", torch.uint8)
     dev = torch.cuda.current_device()
     if not (latent.device == w_uk.device == w_uv.device == k_nope.device == v.device == workspace.device
@@ -732,15 +756,15 @@ def mla_prefill_bf16(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, scale, causa
     B = cu_q.numel() - 1
     _check(cu_k, "cu_k", torch.int32, (B + 1,))
     if out is None:
-        out = torch.empty((nq, 128, 128), dtype=torch.bfloat16, device=q_nope.device)
+        out = _new(stream, torch.empty, (nq, 128, 128), dtype=torch.bfloat16, device=q_nope.device)
     else:
         _check(out, "out", torch.bfloat16, (nq, 128, 128))
     if lse is None:
-        lse = torch.empty((nq, 128), dtype=torch.float32, device=q_nope.device)
+        lse = _new(stream, torch.empty, (nq, 128), dtype=torch.float32, device=q_nope.device)
     else:
         _check(lse, "lse", torch.float32, (nq, 128))
     if workspace is None:
-        workspace = alloc_workspace_prefill(B, nq, q_nope.device)
+        workspace = _new(stream, alloc_workspace_prefill, B, nq, q_nope.device)
     _check(workspace, "workspace", torch.uint8)
     dev = torch.cuda.current_device()
     if not (q_nope.device == q_rope.device == k_nope.device == k_rope.device == v.device == cu_q.device == cu_k.device
@@ -772,9 +796,9 @@ def mla_combine_splits(partial_out, partial_lse, split_indptr, out=None, lse=Non
     rows = split_indptr.numel() - 1
     H = partial_out.shape[1]
     if out is None:
-        out = torch.empty((rows, H, 512), dtype=torch.bfloat16, device=partial_out.device)
+        out = _new(stream, torch.empty, (rows, H, 512), dtype=torch.bfloat16, device=partial_out.device)
     if lse is None:
-        lse = torch.empty((rows, H), dtype=torch.float32, device=partial_out.device)
+        lse = _new(stream, torch.empty, (rows, H), dtype=torch.float32, device=partial_out.device)
     _check(out, "out", torch.bfloat16, (rows, H, 512))
     _check(lse, "lse", torch.float32, (rows, H))
     _same_device(dict(partial_out=partial_out, partial_lse=partial_lse, split_indptr=split_indptr, out=out, lse=lse),
