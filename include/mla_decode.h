@@ -384,9 +384,8 @@ int mla_expand_kv(const uint16_t* latent, size_t row_stride, const uint16_t* w_u
  * is cached before it.  A query that sees no key gets out = 0, lse = -inf.
  * Queries past cu_q[batch] are left alone.  A sequence whose bounds are out
  * of order or out of range is skipped and sets MLA_STATUS_BAD_SEQ_LEN.
- * A masked key's K never matters, whatever it holds, nor does another
- * sequence's K or V; a non-finite V value of a masked key of the same
- * sequence may reach the queries within 255 tokens before it.
+ * A masked key's K and V never matter, whatever they hold (including NaN),
+ * nor do another sequence's.
  * q_nope [num_q, 128, 128], q_rope [num_q, 128, 64], k_nope [num_k, 128,
  * 128], k_rope [num_k, 64] (shared by the heads), v [num_k, 128, 128], all
  * bf16 with their last dimension contiguous; strides (host memory, values,

@@ -66,8 +66,8 @@
 // fit beside K and V.  Tried and no faster: K and V ahead of the queries (0 to 3 %
 // either way), prefetches of K and V into L2 (3 % slower on ragged prompts).
 //
-// Every wait is bounded: a timeout records MLA_STATUS_TIMEOUT and raises the
-// abort flag, all roles leave, and the kernel ends through its teardown.
+// Every wait is bounded: after a timeout all roles of the CTA leave, and it ends
+// through its teardown, which records MLA_STATUS_TIMEOUT.
 #include <climits>
 
 #include "prefill.cuh"
@@ -94,12 +94,20 @@ enum Bar {
   QFULL = 0, QEMPTY = QFULL + 2, KFULL = QEMPTY + 2, KEMPTY = KFULL + kKTiles, VFULL = KEMPTY + kKTiles,
   VEMPTY = VFULL + kVTiles, SFULL = VEMPTY + kVTiles, SREAD = SFULL + 2,
   PREADY = SREAD + 2, PVDONE = PREADY + 2, LFULL = PVDONE + 2, LEMPTY = LFULL + 2, OFREE = LEMPTY + 2,
-  IFULL = OFREE + 2, IEMPTY = IFULL + kItemSlots, DRAIN = IEMPTY + kItemSlots, NBAR = DRAIN + 3
+  IFULL = OFREE + 2, IEMPTY = IFULL + kItemSlots, DRAIN = IEMPTY + kItemSlots, VASK = DRAIN + 3,
+  NBAR = VASK + 2 * kVTiles
 };
 constexpr uint32_t kOffTmem = kOffBar + 8 * NBAR;
 constexpr uint32_t kOffItems = (kOffTmem + 16 + 15) & ~15u;     // kItemSlots x 32 bytes
 constexpr uint32_t kOffInv = kOffItems + 32 * kItemSlots;       // fp32 1/l [2 tiles][128 rows]
-constexpr uint32_t kSmem = kOffInv + 2 * 128 * 4;
+constexpr uint32_t kOffQuit = kOffInv + 2 * 128 * 4;            // uint32: a wait gave up
+// the second pass (see clean): the number of an item with values that were taken
+// out, and the first key of each column with +inf and with -inf; for three items,
+// because a role is at most two ahead of another
+constexpr uint32_t kOffFound = kOffQuit + 16;                   // uint32 [3], padded
+constexpr uint32_t kOffFirst = kOffFound + 16;                  // uint64 [3][2 signs][128 columns]
+constexpr uint32_t kSmem = kOffFirst + 3 * 2 * 128 * 8;
+static_assert(kOffFirst % 8 == 0, "alignment");
 static_assert(kSmem <= 232448, "shared memory budget");
 
 constexpr uint32_t kOCol = 0, kSCol = 256, kPCol = kSCol + 2 * kKeys;   // + 128 t, kKeys t, kKeys / 2 t
@@ -112,13 +120,15 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 // Header fields this operator uses: n_tiles (tiles in the list), chunk (the next
 // work item after each CTA's first), slots_per_query (heads taken together at
-// the end) and n_empty (the first item that goes out in halves).
+// the end), n_empty (the first item that goes out in halves) and fp8_range (an
+// item has to be done again).
 struct Tile {
   int q0, rows;   // first packed query row, query rows (1..256)
   int k0, nk;     // first packed key, keys of the sequence
   int lim;        // keys that row 0 sees before clamping to nk (row r: lim + r if causal)
   int head;       // filled in for a fetched item; -1: no more items
-  int pad[2];
+  int index;      // of the tile in the list, filled in too
+  int pad;
 };
 static_assert(sizeof(Tile) == 32, "tile record");
 
@@ -168,8 +178,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
         t.k0 = k0;
         t.nk = n_k;
         t.lim = causal ? i * kPrefillTile + 1 + (n_k - n_q) : n_k;
-        t.head = 0;
-        t.pad[0] = t.pad[1] = 0;
+        t.head = t.index = t.pad = 0;
         const int steps = min(kClasses - 1, max(kv_tiles(t, 0, causal), kv_tiles(t, 1, causal)));
         const int c = kClasses - 1 - steps;
         if (pass == 0) {
@@ -178,7 +187,10 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
         }
         const int pos = atomicAdd(&s_count[c], 1);
         if (pass == 1) {
-          if (pos < L.max_tiles) tiles[pos] = t;
+          if (pos < L.max_tiles) {
+            tiles[pos] = t;
+            reinterpret_cast<uint4*>(ws + L.again)[pos] = make_uint4(0, 0, 0, 0);
+          }
           else set_status(&hdr->status, MLA_STATUS_BAD_SEQ_LEN);   // overlapping sequences: cu_q decreased somewhere
         }
       }
@@ -209,6 +221,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
         const int items = n_tiles * kHeads, rest = items % first;
         hdr->slots_per_query = even ? 1 : min(kHeads, (kTailItems * first + n_tiles - 1) / max(n_tiles, 1));
         hdr->n_empty = even && s_longest >= kHalvesFrom && 2 * rest <= first ? items - rest : INT_MAX;
+        hdr->fp8_range = 0;
         hdr->abort_flag = 0;
       }
       __syncthreads();
@@ -221,11 +234,11 @@ struct Maps {
   CUtensorMap qn, qr, kn, kr, v;
 };
 
-// Registers (128 a thread at launch): 80 for warps 0..3, 96 for the output
-// warps, 168 for the softmax warps (4 * 80 + 4 * 96 + 8 * 168 = 16 * 128),
+// Registers (128 a thread at launch): 72 for warps 0..3, 104 for the output
+// warps, 168 for the softmax warps (4 * 72 + 4 * 104 + 8 * 168 = 16 * 128),
 // each role's branch setting its own.
-__device__ __forceinline__ void regs_issue() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
-__device__ __forceinline__ void regs_output() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
+__device__ __forceinline__ void regs_issue() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
+__device__ __forceinline__ void regs_output() { asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); }
 __device__ __forceinline__ void regs_softmax() { asm volatile("setmaxnreg.inc.sync.aligned.u32 168;"); }
 
 // 32 lanes x 8 columns to tensor memory.
@@ -258,6 +271,87 @@ __device__ __forceinline__ float row_max(const uint32_t* s) {
   return max3(fmaxf(m[0], m[1]), m[2], m[3]);
 }
 
+// Waits as in waits.cuh, with less code: CTAs of this kernel do not wait for one
+// another, so a wait that gives up tells its own CTA only, through shared memory,
+// and the status is written at the end.  (Thirty waits in line; the kernel's
+// code must stay in the instruction caches: with 62 KB instead of 52, 64 prompts
+// of up to 512 tokens took 610 us instead of 477.)
+static_assert(MLA_WAIT_TIMEOUT_NS < (1ull << 31), "a difference of 32-bit times");
+__device__ __forceinline__ uint32_t timer32() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool wait_cta(uint32_t bar, uint32_t parity, volatile uint32_t* quit) {
+  uint32_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t n = 1; !ptx::mbar_try_wait(bar, parity); ++n) {
+    if ((n & 1023u) != 0) continue;
+    const uint32_t now = timer32();
+    if (n == 1024u) t0 = now;
+    if (now - t0 > static_cast<uint32_t>(MLA_WAIT_TIMEOUT_NS)) *quit = 1u;
+    if (*quit != 0) return false;
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_cta_warp(uint32_t bar, uint32_t parity, volatile uint32_t* quit) {
+  return __all_sync(0xffffffffu, wait_cta(bar, parity, quit));
+}
+// For what was issued and completes by itself, whether the CTA gave up or not.
+__device__ __forceinline__ void wait_issued(uint32_t bar, uint32_t parity, volatile uint32_t* quit) {
+  const uint32_t t0 = timer32();
+#pragma unroll 1
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (timer32() - t0 > static_cast<uint32_t>(kDrainTimeoutNs)) {
+      *quit = 1u;
+      return;
+    }
+  }
+}
+
+// sum += a b in bf16 pairs: not finite once a value was not.  (In its place behind
+// the stores, which the compiler delays for it otherwise.)
+__device__ __forceinline__ void add_product(uint32_t& sum, uint32_t a, uint32_t b) {
+  asm volatile("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(a), "r"(b));
+}
+
+// A key that a row does not see has P = 0 there, which an infinity or a NaN in
+// its V turns into NaN.  Looking for such values in every V tile at the mask's
+// diagonal took up to half of a short item's time (64 prompts of up to 512 tokens
+// 474 and 690 us), so they are looked for in the results: a tile and head with a
+// row whose sum of weights is finite and whose output is not is marked, and done
+// once more by a second launch of the kernel, which returns at once if there is
+// none.  It runs this function over each V tile before its P.V.
+//
+// Rows [lo, hi) of a V tile, keys k0 + row of the sequence, by the 128 threads of
+// a query tile's softmax: values that are not finite become 0, and `first` takes
+// the smallest key of each column with +inf and with -inf (a NaN counts as both)
+// under the item's number: `tag` has its complement in the high half, so that an
+// entry of a later item is smaller and none needs a reset.  The output gives them
+// back to the rows that see the key.  True if this thread found any.  (The other
+// query tile's threads may do the same at the same time.)
+__device__ __forceinline__ bool clean(uint8_t* tile, int lo, int hi, int k0, int tid, uint64_t tag,
+                                      unsigned long long* first) {
+  bool found = false;
+#pragma unroll 1
+  for (int i = 0; i < kKeys / 16 * 2 * 8; ++i) {     // (row, chunk, value) of this thread's share
+    const int r = lo + (tid >> 3) + 16 * (i >> 4), c = (i >> 3) & 1, e = i & 7;
+    if (r >= hi) break;
+    volatile uint16_t* at = reinterpret_cast<volatile uint16_t*>(tile + c * kChunk + r * 128 + (tid & 7) * 16) + e;
+    const uint32_t v = *at;
+    if ((v & 0x7F80u) != 0x7F80u) continue;
+    const bool nan = (v & 0x7Fu) != 0;
+    unsigned long long* entry = first + 64 * c + 8 * ((tid & 7) ^ (r & 7)) + e;   // 128-byte swizzle
+    if (nan || v < 0x8000u) atomicMin(entry, tag | static_cast<uint32_t>(k0 + r));
+    if (nan || v >= 0x8000u) atomicMin(entry + 128, tag | static_cast<uint32_t>(k0 + r));
+    *at = 0;
+    found = true;
+  }
+  return found;
+}
+
+// kAgain: the second pass, over the items that the first one marked.
+template <bool kAgain>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const PrefillWs L) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -266,8 +360,14 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
   // depend on it otherwise takes about 90 cycles to issue instead of 24)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws);
+  if constexpr (kAgain) {
+    ptx::grid_dep_wait();
+    if (*reinterpret_cast<const volatile int*>(&hdr->fp8_range) == 0) return;   // nothing was marked
+  }
+  volatile uint32_t* const quit = reinterpret_cast<volatile uint32_t*>(smem + kOffQuit);
   auto BAR = [&](int i) { return sbase + kOffBar + 8u * static_cast<uint32_t>(i); };
   if (threadIdx.x == 0) {
+    *quit = 0;
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(BAR(QFULL + t), 1);
       ptx::mbar_init(BAR(QEMPTY + t), 1);
@@ -283,11 +383,16 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     ptx::mbar_init(BAR(DRAIN + 2), 1);
     for (uint32_t s = 0; s < kKTiles; ++s) { ptx::mbar_init(BAR(KFULL + s), 1); ptx::mbar_init(BAR(KEMPTY + s), 2); }
     for (uint32_t s = 0; s < kVTiles; ++s) { ptx::mbar_init(BAR(VFULL + s), 1); ptx::mbar_init(BAR(VEMPTY + s), 1); }
+    for (uint32_t s = 0; s < 2 * kVTiles; ++s) ptx::mbar_init(BAR(VASK + s), 1);
     for (int s = 0; s < kItemSlots; ++s) {
       ptx::mbar_init(BAR(IFULL + s), 1);
       ptx::mbar_init(BAR(IEMPTY + s), 15);         // three MMA, eight softmax, four output warps
     }
     ptx::fence_barrier_init();
+  }
+  if (kAgain && warp == 1) {                         // (items are numbered from 1)
+    for (int i = lane; i < 3 * 2 * 128; i += 32) reinterpret_cast<unsigned long long*>(smem + kOffFirst)[i] = ~0ull;
+    if (lane < 3) reinterpret_cast<uint32_t*>(smem + kOffFound)[lane] = 0;
   }
   if (warp == 2) {
     ptx::tmem_alloc(sbase + kOffTmem, 512);
@@ -298,7 +403,10 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem), 0);
   // everything above overlaps the plan kernel, whose list is read from here on
-  ptx::grid_dep_wait();
+  if constexpr (!kAgain) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();   // the second pass may be launched where a CTA has left
+  }
   const bool smem_ok = (sbase & 1023u) == 0;
   if (threadIdx.x == 0 && !smem_ok) set_status(&hdr->status, MLA_ERR_UNSUPPORTED);
   const int causal = p.causal;
@@ -308,10 +416,10 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
   struct Walk { int slot = 0; uint32_t phase = 0; };
   auto read_item = [&](Walk& w, Tile& t) {
     const volatile int* src = reinterpret_cast<const volatile int*>(smem + kOffItems + 32 * w.slot);
-    t.q0 = src[0]; t.rows = src[1]; t.k0 = src[2]; t.nk = src[3]; t.lim = src[4]; t.head = src[5];
+    t.q0 = src[0]; t.rows = src[1]; t.k0 = src[2]; t.nk = src[3]; t.lim = src[4]; t.head = src[5]; t.index = src[6];
   };
   auto next_warp = [&](Walk& w, Tile& t) {
-    if (!wait_short_warp(BAR(IFULL + w.slot), w.phase, hdr)) { t.head = -1; t.nk = 0; return false; }
+    if (!wait_cta_warp(BAR(IFULL + w.slot), w.phase, quit)) { t.head = -1; t.nk = 0; return false; }
     read_item(w, t);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(BAR(IEMPTY + w.slot));
@@ -330,7 +438,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       uint32_t nq0 = 0, nq1 = 0;               // Q tiles queued so far
       bool ok = true;
       auto query = [&](int t, uint32_t n, const Tile& it) {
-        ok = wait_short(BAR(QEMPTY + t), (n & 1u) ^ 1u, hdr);
+        ok = wait_cta(BAR(QEMPTY + t), (n & 1u) ^ 1u, quit);
         if (!ok) return;
         ptx::mbar_arrive_expect_tx(BAR(QFULL + t), kQTile);
         const uint32_t dst = sbase + static_cast<uint32_t>(t) * kQTile;
@@ -346,8 +454,19 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       const int items = n_tiles * kHeads, first_late = items - n_tiles * tail;
       auto record = [&](int item) {
         Tile t;
-        t.q0 = t.rows = t.k0 = t.nk = t.lim = 0;
+        t.q0 = t.rows = t.k0 = t.nk = t.lim = t.index = 0;
         t.head = -1;
+        if constexpr (kAgain) {
+          // `item` and every gridDim.x'th behind it, as far as it is not marked
+          const uint32_t* again = reinterpret_cast<const uint32_t*>(p.ws + L.again);
+          while (item < items && ((again[item >> 5] >> (item & 31)) & 1u) == 0) item += static_cast<int>(gridDim.x);
+          if (item < items) {
+            t = tiles[item / kHeads];
+            t.head = item % kHeads;
+            t.index = item;                    // (its number in the second pass: where the next search begins)
+          }
+          return t;
+        }
         const int half = item >= first_half ? (item - first_half) & 1 : -1;
         if (half >= 0) item = first_half + ((item - first_half) >> 1);
         if (item < items) {
@@ -356,6 +475,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           const int q = left / by, r = left - q * by;
           t = tiles[late ? q : r];
           t.head = late ? kHeads - tail + r : q;
+          t.index = late ? q : r;
           if (half == 0) t.rows = min(t.rows, 128);
           if (half == 1) {                     // (none of a tile of 128 rows or fewer)
             t.q0 += 128;
@@ -373,10 +493,10 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       // to 200 55 instead of 53; two: 256 items of 1.7 ms 4.7 ms instead of 3.5).
       Tile it = record(static_cast<int>(blockIdx.x));
       while (ok) {
-        ok = wait_short(BAR(IEMPTY + w.slot), w.phase ^ 1u, hdr);
+        ok = wait_cta(BAR(IEMPTY + w.slot), w.phase ^ 1u, quit);
         if (!ok) break;
         volatile int* dst = reinterpret_cast<volatile int*>(smem + kOffItems + 32 * w.slot);
-        dst[0] = it.q0; dst[1] = it.rows; dst[2] = it.k0; dst[3] = it.nk; dst[4] = it.lim; dst[5] = it.head;
+        dst[0] = it.q0; dst[1] = it.rows; dst[2] = it.k0; dst[3] = it.nk; dst[4] = it.lim; dst[5] = it.head; dst[6] = it.index;
         ptx::mbar_arrive(BAR(IFULL + w.slot));
         if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
         if (it.head < 0) break;
@@ -388,8 +508,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         }
         for (int j = 0; j < n && ok; ++j) {
           const int k = it.k0 + j * kKeys;
-          if (j == max(n - 2, 0)) item = atomicAdd(&hdr->chunk, 1);
-          ok = wait_short(BAR(KEMPTY + kb), k_phase ^ 1u, hdr);
+          if (!kAgain && j == max(n - 2, 0)) item = atomicAdd(&hdr->chunk, 1);
+          ok = wait_cta(BAR(KEMPTY + kb), k_phase ^ 1u, quit);
           if (!ok) break;
           ptx::mbar_arrive_expect_tx(BAR(KFULL + kb), kKTile);
           const uint32_t k_dst = sbase + kOffK + kb * kKTile;
@@ -403,30 +523,30 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           }
           // (a K tile without its V is waited for all the same)
           ++k_tiles;
-          if (ok) ok = wait_short(BAR(VEMPTY + vb), v_phase ^ 1u, hdr);
+          if (ok) ok = wait_cta(BAR(VEMPTY + vb), v_phase ^ 1u, quit);
           if (!ok) break;
           ptx::mbar_arrive_expect_tx(BAR(VFULL + vb), kVTile);
           const uint32_t v_dst = sbase + kOffV + vb * kVTile;
           ptx::tma_load_4d(v_dst, &maps.v, BAR(VFULL + vb), 0, it.head, k, 0, pol);
           ptx::tma_load_4d(v_dst + kChunk, &maps.v, BAR(VFULL + vb), 64, it.head, k, 0, pol);
+          if constexpr (kAgain) {   // tells a query tile's softmax that the phase of VFULL in progress is this V tile's
+            if (j < n0) ptx::mbar_arrive(BAR(VASK + vb));
+            if (j < n1) ptx::mbar_arrive(BAR(VASK + kVTiles + vb));
+          }
           if (++vb == kVTiles) { vb = 0; v_phase ^= 1u; }
           ++v_tiles;
         }
-        if (n == 0) item = atomicAdd(&hdr->chunk, 1);
-        it = record(item);
+        if (!kAgain && n == 0) item = atomicAdd(&hdr->chunk, 1);
+        it = record(kAgain ? it.index + static_cast<int>(gridDim.x) : item);
       }
       // no copy may land after the CTA has left: wait for the last phase armed on each barrier
-      if (nq0 > 0) wait_drain(BAR(QFULL), (nq0 - 1) & 1u, hdr);
-      if (nq1 > 0) wait_drain(BAR(QFULL + 1), (nq1 - 1) & 1u, hdr);
 #pragma unroll 1
-      for (uint32_t s = 0; s < kKTiles; ++s) {
-        const uint32_t n = (k_tiles + kKTiles - 1 - s) / kKTiles;
-        if (n > 0) wait_drain(BAR(KFULL + s), (n - 1) & 1u, hdr);
-      }
-#pragma unroll 1
-      for (uint32_t s = 0; s < kVTiles; ++s) {
-        const uint32_t n = (v_tiles + kVTiles - 1 - s) / kVTiles;
-        if (n > 0) wait_drain(BAR(VFULL + s), (n - 1) & 1u, hdr);
+      for (uint32_t i = 0; i < 2 + kKTiles + kVTiles; ++i) {
+        const uint32_t s = i < 2 ? i : i < 2 + kKTiles ? i - 2 : i - 2 - kKTiles;
+        const uint32_t n = i < 2 ? (i == 0 ? nq0 : nq1)
+                         : i < 2 + kKTiles ? (k_tiles + kKTiles - 1 - s) / kKTiles : (v_tiles + kVTiles - 1 - s) / kVTiles;
+        const int bar = (i < 2 ? QFULL : i < 2 + kKTiles ? KFULL : VFULL) + static_cast<int>(s);
+        if (n > 0) wait_issued(BAR(bar), (n - 1) & 1u, quit);
       }
     }
   } else if (smem_ok && warp < 3) {
@@ -448,14 +568,14 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       const int n0 = kv_tiles(it, 0, causal), n1 = kv_tiles(it, 1, causal);
       const int n_all = __shfl_sync(0xffffffffu, max(n0, n1), 0), n_mine = __shfl_sync(0xffffffffu, t ? n1 : n0, 0);
       for (int j = 0; j < n_all && ok; ++j) {
-        ok = wait_short_warp(BAR(KFULL + kb), k_phase, hdr);
+        ok = wait_cta_warp(BAR(KFULL + kb), k_phase, quit);
         if (ok && j < n_mine) {
           if (j == 0) {
-            ok = wait_short_warp(BAR(QFULL + t), q_phase, hdr);
+            ok = wait_cta_warp(BAR(QFULL + t), q_phase, quit);
             q_phase ^= 1u;
           }
           // the softmax has the scores before these in its registers
-          if (ok && n_s > 0) ok = wait_short_warp(BAR(SREAD + t), (n_s - 1) & 1u, hdr);
+          if (ok && n_s > 0) ok = wait_cta_warp(BAR(SREAD + t), (n_s - 1) & 1u, quit);
           if (!ok) break;
           ++n_s;
           ptx::tc_fence_after();
@@ -481,7 +601,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     // every MMA this warp issued completes before the CTA may leave
     if (n_s > 0 && elect_one()) {   // the lane that issued them
       ptx::mma_commit(BAR(DRAIN + t));
-      wait_drain(BAR(DRAIN + t), 0u, hdr);
+      wait_issued(BAR(DRAIN + t), 0u, quit);
     }
     __syncwarp();
   } else if (smem_ok && warp == 3) {
@@ -499,7 +619,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       const int n1 = __shfl_sync(0xffffffffu, kv_tiles(it, 1, causal), 0);
       const int n_all = max(n0, n1), nk = __shfl_sync(0xffffffffu, it.nk, 0);
       for (int j = 0; j < n_all && ok; ++j) {
-        ok = wait_short_warp(BAR(VFULL + vb), v_phase, hdr);
+        ok = wait_cta_warp(BAR(VFULL + vb), v_phase, quit);
         const int valid = nk - j * kKeys;
         if (ok && valid < kKeys) {
           // keys past the sequence's end have P = 0; make their V rows 0 too
@@ -517,10 +637,10 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           if (j >= (t ? n1 : n0)) continue;
           // an item's first P.V overwrites O: the output warps must have read the last one's
           if (j == 0) {
-            ok = wait_short_warp(BAR(OFREE + t), (o_phase >> t) & 1u, hdr);
+            ok = wait_cta_warp(BAR(OFREE + t), (o_phase >> t) & 1u, quit);
             o_phase ^= 1u << t;
           }
-          if (ok) ok = wait_short_warp(BAR(PREADY + t), (p_phase >> t) & 1u, hdr);
+          if (ok) ok = wait_cta_warp(BAR(PREADY + t), (p_phase >> t) & 1u, quit);
           if (!ok) break;
           p_phase ^= 1u << t;
           ptx::tc_fence_after();
@@ -542,7 +662,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     }
     if (issued && elect_one()) {
       ptx::mma_commit(BAR(DRAIN + 2));
-      wait_drain(BAR(DRAIN + 2), 0u, hdr);
+      wait_issued(BAR(DRAIN + 2), 0u, quit);
     }
     __syncwarp();
   } else if (smem_ok && warp < 12) {
@@ -558,8 +678,15 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     Walk w;
     Tile it;
     uint32_t steps = 0, outs = 0;            // tiles turned into P so far (phase of SFULL, PVDONE), outputs handed over
+    uint32_t number = 0, v_next = 0;         // second pass: items, and their V tiles, so far
+    uint32_t ask_phase = 0;                  // second pass, bit s: parity to wait for on VASK + s
     bool ok = true;
     while (ok && next_warp(w, it)) {
+      const uint32_t v_first = v_next;
+      if constexpr (kAgain) {
+        ++number;
+        v_next += static_cast<uint32_t>(max(kv_tiles(it, 0, causal), kv_tiles(it, 1, causal)));
+      }
       if (it.rows <= 128 * t) continue;
       const int n = kv_tiles(it, t, causal);
       const int vis = visible(it, r, causal);
@@ -576,7 +703,21 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       float mc = 0.f;                        // reference maximum * c (0 while nothing was seen)
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
-        if (!wait_short_warp(BAR(SFULL + t), steps & 1u, hdr)) { ok = false; break; }
+        if constexpr (kAgain) {
+          const uint32_t at = v_first + static_cast<uint32_t>(j), vb = at % kVTiles;
+          if (!wait_cta_warp(BAR(VASK + kVTiles * t + vb), (ask_phase >> vb) & 1u, quit) ||
+              !wait_cta_warp(BAR(VFULL + vb), (at / kVTiles) & 1u, quit)) { ok = false; break; }
+          ask_phase ^= 1u << vb;
+          // the keys that a row of the tile does not see: row 0 sees the fewest
+          if (clean(smem + kOffV + vb * kVTile, max(visible(it, 128 * t, causal) - j * kKeys, 0),
+                    min(it.nk - j * kKeys, kKeys), j * kKeys, rt, static_cast<uint64_t>(~number) << 32,
+                    reinterpret_cast<unsigned long long*>(smem + kOffFirst) + number % 3u * 256u)) {
+            reinterpret_cast<volatile uint32_t*>(smem + kOffFound)[number % 3u] = number;
+            ptx::fence_proxy_async_cta();
+          }
+          __syncwarp();
+        }
+        if (!wait_cta_warp(BAR(SFULL + t), steps & 1u, quit)) { ok = false; break; }
         ptx::tc_fence_after();
         uint32_t s[kKeys];
         ptx::tmem_ld32(s_addr, s);
@@ -619,7 +760,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
         acc0 = __fadd2_rn(acc0, acc1);
         l += acc0.x + acc0.y;
         // the previous P.V has read P (and completed O)
-        if (steps > 0 && !wait_short_warp(BAR(PVDONE + t), (steps - 1) & 1u, hdr)) { ok = false; break; }
+        if (steps > 0 && !wait_cta_warp(BAR(PVDONE + t), (steps - 1) & 1u, quit)) { ok = false; break; }
         ptx::tc_fence_after();
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
@@ -642,7 +783,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       }
       if (!ok) break;
       // hand 1/l to the output warps
-      if (!wait_short_warp(BAR(LEMPTY + t), (outs & 1u) ^ 1u, hdr)) break;
+      if (!wait_cta_warp(BAR(LEMPTY + t), (outs & 1u) ^ 1u, quit)) break;
       ++outs;
       *inv_l = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays NaN
       __syncwarp();
@@ -658,20 +799,22 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     Walk w;
     Tile it;
     uint32_t outs = 0, steps = 0;            // bit t / half-words t: outputs and P.V steps of tile t so far, mod 2
+    uint32_t number = 0;                     // second pass: items so far
     bool ok = true;
     while (ok && next_warp(w, it)) {
+      ++number;
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const int n = kv_tiles(it, t, causal);
         if (n == 0) continue;
-        if (!wait_short_warp(BAR(LFULL + t), (outs >> t) & 1u, hdr)) { ok = false; break; }
+        if (!wait_cta_warp(BAR(LFULL + t), (outs >> t) & 1u, quit)) { ok = false; break; }
         outs ^= 1u << t;
         const float inv = reinterpret_cast<const volatile float*>(smem + kOffInv)[128 * t + rt];
         __syncwarp();
         if (elect_one()) ptx::mbar_arrive(BAR(LEMPTY + t));
         steps ^= (static_cast<uint32_t>(n) & 1u) << t;
         // its last P.V: number steps - 1 of the tile's
-        if (!wait_short_warp(BAR(PVDONE + t), ((steps >> t) & 1u) ^ 1u, hdr)) { ok = false; break; }
+        if (!wait_cta_warp(BAR(PVDONE + t), ((steps >> t) & 1u) ^ 1u, quit)) { ok = false; break; }
         ptx::tc_fence_after();
         uint32_t o16[64];
 #pragma unroll
@@ -693,6 +836,28 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
           __nv_bfloat16* dst = p.out + ((static_cast<size_t>(it.q0) + r) * kHeads + it.head) * 128;
 #pragma unroll
           for (int q = 0; q < 8; ++q) ptx::st_global_v8(dst + 16 * q, o16 + 8 * q);
+          if constexpr (!kAgain) {
+            // a result that is not finite, of weights that are (1/l is not NaN): once more
+            uint32_t sum[2] = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) add_product(sum[(e >> 1) & 1], o16[e], o16[e + 1]);
+            const uint32_t bad = ((sum[0] & 0x7F807F80u) + 0x00800080u) | ((sum[1] & 0x7F807F80u) + 0x00800080u);
+            if (causal && inv >= 0.f && (bad & 0x80008000u)) {   // an exponent of ones carries into the sign's place
+              atomicOr(reinterpret_cast<uint32_t*>(p.ws + L.again) + 4 * it.index + (it.head >> 5), 1u << (it.head & 31));
+              *reinterpret_cast<volatile int*>(&hdr->fp8_range) = 1;
+            }
+          } else if (reinterpret_cast<const volatile uint32_t*>(smem + kOffFound)[number % 3u] == number) {
+            // values that were taken out, of keys that the row sees (an entry of
+            // another item is larger than any of this one)
+            const volatile unsigned long long* first =
+                reinterpret_cast<const volatile unsigned long long*>(smem + kOffFirst) + number % 3u * 256u;
+            const unsigned long long end = static_cast<uint64_t>(~number) << 32 | static_cast<uint32_t>(visible(it, r, causal));
+#pragma unroll 1
+            for (int d = 0; d < 128; ++d) {
+              const float up = first[d] < end ? INFINITY : 0.f, down = first[128 + d] < end ? -INFINITY : 0.f;
+              if (up != down) dst[d] = __float2bfloat16(__bfloat162float(dst[d]) + up + down);
+            }
+          }
         }
       }
     }
@@ -700,6 +865,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
   // ------------------------------------------------------------ teardown
   ptx::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *quit != 0) set_status(&hdr->status, MLA_STATUS_TIMEOUT);
   if (warp == 2) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
@@ -734,8 +900,9 @@ cudaError_t launch_prefill(PFN_cuTensorMapEncodeTiled_v12000 encode, const Prefi
       !encode_map(encode, &maps.kr, p.k_rope, 64, 1, nk, p.kr_t, 64, kKeys) ||
       !encode_map(encode, &maps.v, p.v, 128, kHeads, nk, p.v_t, p.v_h, kKeys))
     return cudaErrorInvalidValue;
-  static std::atomic<uint64_t> configured{0};
-  cudaError_t e = allow_smem(prefill_kernel, kSmem, configured);
+  static std::atomic<uint64_t> configured{0}, configured_again{0};
+  cudaError_t e = allow_smem(prefill_kernel<false>, kSmem, configured);
+  if (e == cudaSuccess) e = allow_smem(prefill_kernel<true>, kSmem, configured_again);
   if (e != cudaSuccess) return e;
   const long long items = static_cast<long long>(L.max_tiles) * kHeads;
   const int ctas = static_cast<int>(items < sms ? items : sms);
@@ -752,7 +919,9 @@ cudaError_t launch_prefill(PFN_cuTensorMapEncodeTiled_v12000 encode, const Prefi
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_kernel, maps, p, L);
+  e = cudaLaunchKernelEx(&cfg, prefill_kernel<false>, maps, p, L);
+  // (without the mask a row sees every key)
+  return e != cudaSuccess || !p.causal ? e : cudaLaunchKernelEx(&cfg, prefill_kernel<true>, maps, p, L);
 }
 
 }  // namespace mla

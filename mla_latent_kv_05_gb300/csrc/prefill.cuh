@@ -22,16 +22,18 @@ struct PrefillParams {
   uint8_t* ws;
 };
 
-// Workspace: the plan header, then the tile list.
+// Workspace: the plan header, then the tile list, then 128 bits a tile: the heads
+// whose results the second pass computes again.
 struct PrefillWs {
-  size_t tiles, total;
+  size_t tiles, again, total;
   int max_tiles;
 };
 __host__ __device__ inline PrefillWs prefill_ws(int batch, int nq) {
   PrefillWs w;
   w.max_tiles = nq / kPrefillTile + (batch < nq ? batch : nq);   // every sequence ends at most one tile early
   w.tiles = align256(sizeof(PlanHeader));
-  w.total = align256(w.tiles + 32 * static_cast<size_t>(w.max_tiles));
+  w.again = align256(w.tiles + 32 * static_cast<size_t>(w.max_tiles));
+  w.total = align256(w.again + 16 * static_cast<size_t>(w.max_tiles));
   return w;
 }
 
