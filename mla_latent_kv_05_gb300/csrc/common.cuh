@@ -43,7 +43,10 @@ struct PlanHeader {
   int pairs_per_group;   // pairs that serve one query index
   int abort_flag;        // set by the first wait that times out; all waits then give up
   int fp8_range;         // FP8/FP4 f16 pass: an input lies outside the f16-exact range (the exact pass recomputes)
-  int pad[8];
+  // prefill: heads taken together at the end, the first item that goes out in
+  // halves, and whether a result has to be computed again
+  int prefill_tail, prefill_halves, prefill_again;
+  int pad[5];
 };
 
 // Offsets (bytes) of the plan arrays and split partials inside the workspace.
@@ -125,6 +128,19 @@ __device__ __forceinline__ void set_status(int* status, int code) {
 
 __device__ __forceinline__ int read_status(const int* status) {
   return *reinterpret_cast<const volatile int*>(status);
+}
+
+// One instruction each: 2^x (results below 2^-126 are 0), and the largest of three.
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 #ifndef MLA_WAIT_TIMEOUT_NS

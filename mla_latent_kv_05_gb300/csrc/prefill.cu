@@ -118,10 +118,8 @@ constexpr uint32_t kIdescPV = ptx::idesc_bf16(128, 128, 0, 1);   // P in tensor 
 constexpr float kLazy = 12.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Header fields this operator uses: n_tiles (tiles in the list), chunk (the next
-// work item after each CTA's first), slots_per_query (heads taken together at
-// the end), n_empty (the first item that goes out in halves) and fp8_range (an
-// item has to be done again).
+// The header's n_tiles are the tiles in the list, chunk the next work item after
+// each CTA's first.
 struct Tile {
   int q0, rows;   // first packed query row, query rows (1..256)
   int k0, nk;     // first packed key, keys of the sequence
@@ -219,9 +217,9 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
         // are not short, they go out as two halves of 128 rows.
         const bool even = 2 * s_longest <= 3 * s_shortest;
         const int items = n_tiles * kHeads, rest = items % first;
-        hdr->slots_per_query = even ? 1 : min(kHeads, (kTailItems * first + n_tiles - 1) / max(n_tiles, 1));
-        hdr->n_empty = even && s_longest >= kHalvesFrom && 2 * rest <= first ? items - rest : INT_MAX;
-        hdr->fp8_range = 0;
+        hdr->prefill_tail = even ? 1 : min(kHeads, (kTailItems * first + n_tiles - 1) / max(n_tiles, 1));
+        hdr->prefill_halves = even && s_longest >= kHalvesFrom && 2 * rest <= first ? items - rest : INT_MAX;
+        hdr->prefill_again = 0;
         hdr->abort_flag = 0;
       }
       __syncthreads();
@@ -246,17 +244,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
-}
-
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 
 // Maximum of a row's scores.
@@ -362,7 +349,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws);
   if constexpr (kAgain) {
     ptx::grid_dep_wait();
-    if (*reinterpret_cast<const volatile int*>(&hdr->fp8_range) == 0) return;   // nothing was marked
+    if (*reinterpret_cast<const volatile int*>(&hdr->prefill_again) == 0) return;   // nothing was marked
   }
   volatile uint32_t* const quit = reinterpret_cast<volatile uint32_t*>(smem + kOffQuit);
   auto BAR = [&](int i) { return sbase + kOffBar + 8u * static_cast<uint32_t>(i); };
@@ -449,8 +436,8 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
       };
       const Tile* tiles = reinterpret_cast<const Tile*>(p.ws + L.tiles);
       const int n_tiles = *reinterpret_cast<const volatile int*>(&hdr->n_tiles);
-      const int tail = *reinterpret_cast<const volatile int*>(&hdr->slots_per_query);
-      const int first_half = *reinterpret_cast<const volatile int*>(&hdr->n_empty);
+      const int tail = *reinterpret_cast<const volatile int*>(&hdr->prefill_tail);
+      const int first_half = *reinterpret_cast<const volatile int*>(&hdr->prefill_halves);
       const int items = n_tiles * kHeads, first_late = items - n_tiles * tail;
       auto record = [&](int item) {
         Tile t;
@@ -844,7 +831,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
             const uint32_t bad = ((sum[0] & 0x7F807F80u) + 0x00800080u) | ((sum[1] & 0x7F807F80u) + 0x00800080u);
             if (causal && inv >= 0.f && (bad & 0x80008000u)) {   // an exponent of ones carries into the sign's place
               atomicOr(reinterpret_cast<uint32_t*>(p.ws + L.again) + 4 * it.index + (it.head >> 5), 1u << (it.head & 31));
-              *reinterpret_cast<volatile int*>(&hdr->fp8_range) = 1;
+              *reinterpret_cast<volatile int*>(&hdr->prefill_again) = 1;
             }
           } else if (reinterpret_cast<const volatile uint32_t*>(smem + kOffFound)[number % 3u] == number) {
             // values that were taken out, of keys that the row sees (an entry of

@@ -85,16 +85,6 @@ constexpr uint32_t kIdescPV = ptx::idesc_bf16(128, 256, 0, 1);
 constexpr float kLazy = 12.0f;                          // log2 units: P <= 2^12
 constexpr float kLn2 = 0.69314718055994530942f;
 
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 __device__ __forceinline__ float max32(const uint32_t* s) {
   float m[4];
 #pragma unroll
