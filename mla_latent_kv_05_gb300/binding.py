@@ -639,6 +639,8 @@ def _tree(fmt, q_absorbed, q_rope, kv_cache, block_table, seq_lens, parents, sca
         _same_device(dict(q_absorbed=q_absorbed, q_rope=q_rope, kv_cache=kv_cache, block_table=block_table,
                           seq_lens=seq_lens, parents=parents, n_nodes=n_nodes, out=out, lse=lse, workspace=workspace),
                      dev)
+    if B == 0:
+        return out, lse
     pages, page_size, _ = kv_cache.shape
     rc = getattr(load(), name)(
         q_absorbed.data_ptr(), q_rope.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
