@@ -392,7 +392,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
   // everything above overlaps the plan kernel, whose list is read from here on
   if constexpr (!kAgain) {
     ptx::grid_dep_wait();
-    ptx::grid_dep_launch();   // the second pass may be launched where a CTA has left
+    if (p.causal) ptx::grid_dep_launch();   // the second pass may be launched where a CTA has left
   }
   const bool smem_ok = (sbase & 1023u) == 0;
   if (threadIdx.x == 0 && !smem_ok) set_status(&hdr->status, MLA_ERR_UNSUPPORTED);
