@@ -171,6 +171,12 @@ expand_kernel(const __grid_constant__ ExpandMaps maps, int rows, int tiles, Plan
     int s = 0, d = 0;
     uint32_t ph = 0, wph = 0, dph = 0;
     bool ok = true;
+#ifdef MLA_TEST_STALL_WAIT
+    // Test builds only: a wait on a barrier that nothing arrives on before the end
+    // of the kernel, so that its limit runs out and every role leaves through the
+    // abort path.
+    ok = wait_short_warp<true>(BAR(DRAIN), 0u, hdr);
+#endif
     const uint64_t desc_w = ptx::sdesc_sw128(sbase, 16, 1024), desc_c = ptx::sdesc_sw128(sbase + kOffRing, 16, 1024);
     int m, h = -1, h_next = -1, h_last = -1;
     if (lo < hi) item_of(lo, tiles, m, h_next);

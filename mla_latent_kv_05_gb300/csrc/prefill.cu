@@ -551,6 +551,12 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     uint32_t kb = 0, k_phase = 0;
     uint32_t q_phase = 0, n_s = 0;           // S tiles issued so far
     bool ok = true;
+#ifdef MLA_TEST_STALL_WAIT
+    // Test builds only: a wait on a barrier that nothing arrives on before the end
+    // of the kernel, so that its limit runs out and every role leaves through the
+    // abort path.
+    if (t == 0) ok = wait_cta_warp(BAR(DRAIN), 0u, quit);
+#endif
     while (ok && next_warp(w, it)) {
       const int n0 = kv_tiles(it, 0, causal), n1 = kv_tiles(it, 1, causal);
       const int n_all = __shfl_sync(0xffffffffu, max(n0, n1), 0), n_mine = __shfl_sync(0xffffffffu, t ? n1 : n0, 0);

@@ -240,6 +240,12 @@ tree_kernel(const __grid_constant__ TreeMaps maps, const DecodeParams p) {
     Segment sg;
     uint32_t n_s = 0, n_p = 0, n_seg = 0;    // S tiles, P.V tiles and segments begun so far
     bool ok = true;
+#ifdef MLA_TEST_STALL_WAIT
+    // Test builds only: a wait on a barrier that nothing arrives on before the end
+    // of the kernel, so that its limit runs out and every role leaves through the
+    // abort path.
+    ok = wait_short_warp<true>(BAR(DRAIN), 0u, hdr);
+#endif
     auto score = [&](bool last) {
       // S buffer n_s & 1 is free once its last scores were read
       ok = wait_short_warp<true>(BAR(SEMPTY + (n_s & 1u)), ((n_s >> 1) & 1u) ^ 1u, hdr);
