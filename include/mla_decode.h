@@ -261,8 +261,11 @@ int mla_decode_sparse_bf16(const uint16_t* q_absorbed, const uint16_t* q_rope,
  * workspace: mla_workspace_size_tree(...) bytes, as for the decode.  With
  * mla_workspace_size_tree_widened(...) bytes, and two nodes or more, the
  * quantised forms write each sequence's rows into it as bf16 once and let all
- * nodes attend to those: up to six times faster (the results differ from
- * those in the smaller workspace by rounding). */
+ * nodes attend to those: 1.5 (two nodes) to 3 times faster (16 nodes over
+ * 16,384 tokens).  The softmax weights are then rounded to bf16 (2^-8
+ * relative) before the sum over V, where the smaller workspace rounds them to
+ * f16 (2^-11) unless an input lies beyond f16: the size of the workspace
+ * decides which of the two results a call gives. */
 int mla_workspace_size_tree(int batch, int nodes, int num_heads, int page_size, size_t* bytes);
 int mla_workspace_size_tree_widened(int batch, int nodes, int num_heads, int page_size, int max_pages, size_t* bytes);
 int mla_decode_tree_bf16(const uint16_t* q_absorbed, const uint16_t* q_rope, const uint16_t* kv_cache,

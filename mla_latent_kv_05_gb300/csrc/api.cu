@@ -255,16 +255,18 @@ int run_sparse(const uint16_t* q_absorbed, const uint16_t* q_rope, const void* k
   return MLA_OK;
 }
 
-// Pages per pair of a small tree decode.  Eight nodes over 200 tokens took 26.1
-// us at eight pages a pair and 18.6 at four (1008 tokens: 26.9 and 24.8); at two
-// the merge of more parts costs more (4 x 8 nodes over 500 tokens: 22.7 and 28.8).
+// Pages per pair of a small tree decode, at eight, four and two: eight nodes over
+// 200 tokens 22.7, 16.6 and 16.6 us, over 1008 24.7, 18.7 and 20.8, over 4096 24.8,
+// 26.7 and 25.3; 4 x 8 over 500 20.7, 20.7 and 24.7, over 1008 28.7, 27.0 and 27.6.
 constexpr long long kTreePagesPerPair = 4;
 
 // A quantised cache's tree decode first widens the live pages to bf16 rows, once
 // for all nodes, when the workspace has room for them: the attention then runs
 // at the bf16 rate.  Two nodes pay for it already: 64 x 2 nodes over 4096 fp8
-// tokens take 209 us so and 322 over the codes (fp4: 185 and 297), 64 x 4 276
-// and 583, 8 x 61 340 and 1080; small calls gain too (1 x 2 over 500: 21 and 44).
+// tokens take 205 us so and 322 over the codes (fp4: 182 and 298), 64 x 4 272 and
+// 583, 8 x 16 over 16,384 361 and 1070; small calls gain too (1 x 2 over 500: 21 and
+// 45).  The weights P are rounded to bf16 so, and to f16 over the codes (to bf16
+// where f16 does not hold an input), as in the decode.
 constexpr int kWidenNodes = 2;
 size_t widened_bytes(int batch, int max_pages) {
   return static_cast<size_t>(batch) * max_pages * kPage * kRow * 2;

@@ -30,10 +30,13 @@
 // of rank 0 the MMAs, warps 4..11 of each rank write (4..7 the keys, 8..11 the
 // values; thread = token).  Rows past n are read as zeros and not written.
 //
-// Measured: 8192 tokens 164 us (1680 TFLOP/s, 3.5 TB/s of HBM), 2048 50, 1000 27,
-// 130 and fewer 12.5 (the 33.5 MB of weights alone take 5 us from HBM).  Alone
-// and cold, at 4096 tokens, the tensor pipe is active 71 % of the time and HBM
-// at 35 % of its rate.
+// Measured: 8192 tokens 165 us (1660 TFLOP/s, 3.5 TB/s of HBM), 2048 48, 1000 26.5,
+// 130 and fewer 12 (the 33.5 MB of weights alone take 5 us from HBM: 128 heads
+// over 76 pairs are two rounds, and the second head's weights are asked for only
+// as the first one's products end; with one token tile the roles could swap,
+// latents resident and weights streaming, which is not built).  Alone and cold, at
+// 4096 tokens, the tensor pipe is active 71 % of the time and HBM at 43 % of its
+// rate.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>

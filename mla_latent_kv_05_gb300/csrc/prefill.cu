@@ -58,13 +58,15 @@
 // whose slots it reused, which is read 600 cycles later (8192 causal 1.85 ms in
 // a loop against 1.62; with two V tiles instead of three 1.95).
 //
-// Measured: 8192 causal tokens 1.52 ms (1815 TFLOP/s; 1.6 to 1.7 in a loop of
-// seconds, under the power cap), eight prompts of 54 to 1523 tokens 235 us
-// (1060; HBM alone takes 130), 2 x 512 queries over 15,000 keys 798 us (1605),
-// five prompts of up to 33 tokens 18.6 us.  An item's queries land about 1900
-// cycles after the last item's scores, because a second copy of them does not
-// fit beside K and V.  Tried and no faster: K and V ahead of the queries (0 to 3 %
-// either way), prefetches of K and V into L2 (3 % slower on ragged prompts).
+// Measured: 8192 causal tokens 1.47 to 1.52 ms (1815 to 1870 TFLOP/s; 1.6 to 1.7 in a
+// loop of seconds, under the power cap), eight prompts of 54 to 1523 tokens 227 to
+// 250 us by machine (1000 to 1100; HBM alone takes 130), 2 x 512 queries over 15,000
+// keys 785 to 870 us (1630 to 1470), five prompts of up to 33 tokens 18.6 us.  An
+// item's queries land about 1900 cycles after the last item's scores: a second
+// copy of 256 of them does not fit beside K and V.  (An item of 128 rows or fewer
+// uses query tile 0 alone, and waits for it although tile 1's half idles.)  Tried
+// and no faster: K and V ahead of the queries (0 to 3 % either way), prefetches of
+// K and V into L2 (3 % slower on ragged prompts).
 //
 // Every wait is bounded: after a timeout all roles of the CTA leave, and it ends
 // through its teardown, which records MLA_STATUS_TIMEOUT.

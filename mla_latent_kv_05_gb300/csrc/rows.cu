@@ -27,8 +27,9 @@
 //
 // Measured (bytes read and written a second; a copy reaches 6670 GB/s), 262,144
 // rows: bf16 append 89 us (6810 GB/s) and gather 90, fp8 81 (5640) and 84, fp4
-// 72 (5400) and 62 (6180), V4.1 rows 66, 63 (6670, 5950) and 68, 61; the 594-
-// and 324-byte rows are off 16-byte boundaries, so their accesses are smaller.
+// 72 (5380) and 63 (6180), V4.1 rows 66, 64 (6150, 5410: they read 1024 of a row's
+// 1152 bytes) and 68, 61 (6470, 6190); the 594- and 324-byte rows are off 16-byte
+// boundaries, so their accesses are smaller.
 // 16,384 rows: 5.2 to 7.2 us; 64 rows: 2.3 us.
 #include <climits>
 

@@ -42,11 +42,13 @@
 // different nodes of one sequence at a time and find its rows in L2 (64 x 4
 // nodes over 4096 tokens: 247 us by sequence, 199 by node).
 //
-// Measured, whole call: 8 x 61 nodes over 4096 tokens 329 us (1690 TFLOP/s; the
+// Measured, whole call: 8 x 61 nodes over 4096 tokens 332 us (1690 TFLOP/s; the
 // decode kernel's form of it 554), 16 x up to 16 over up to 8192 120 us (1180),
-// 64 x 16 over 4096 720 us (1620), 8 nodes over 1000 18.6 us (four kernels of 2 to
-// 9 us).  A tile takes about 2300 cycles, 2184 of them MMAs; a segment's output
-// another 4500, while the next segment's first scores wait.
+// 64 x 16 over 4096 720 us (1620), 8 nodes over 1000 18.7 us (four kernels of 2 to
+// 9 us).  Scores that rise, so that every head's reference moves in every tile,
+// cost a tenth: 8 x 61 369 us, 16 x 16 over 4096 193 and 207, 8 nodes 20.2.  A tile
+// takes about 2300 cycles, 2184 of them MMAs; a segment's output another 4500,
+// while the next segment's first scores wait.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
