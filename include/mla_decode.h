@@ -361,6 +361,74 @@ int mla_cache_gather_fp4_v41(const uint8_t* kv_cache, const int32_t* block_table
                           const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size, int max_pages,
                           uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Rotary positions.  Pair i of a vector's 64 RoPE values is turned by the
+ * angle position * inv_freq[i] ("DeepSeek R1 Architecture & Deployment Guide",
+ * section 1.1: the decoupled key k_R = RoPE(W^KR h)): with its values (a, b),
+ *   a' = scale (a cos - b sin),   b' = scale (a sin + b cos),
+ * where pair i is the values (2i, 2i+1) (interleaved) or (i, i+32).
+ * The table below is host memory, made by mla_rope_init from 32 frequencies in
+ * radians a token (finite, at most 1024) and the scale of the rotated vectors;
+ * calls copy it.  Its frequencies are 64-bit fractions of a turn, so that an
+ * angle is exact to position * 2^-65 turns however far the position. */
+typedef struct {
+  uint64_t turns[32];
+  float scale;
+  int interleaved;
+} mla_rope;
+int mla_rope_init(mla_rope* rope, const double* inv_freq, float scale, int interleaved);
+
+/* inv_freq[32] (host): base^(-i/32), for factor > 1 scaled to contexts `factor`
+ * times the original_tokens a model was trained on (YaRN): with r(n) =
+ * 64 ln(original_tokens / (2 pi n)) / (2 ln base) the pair that turns n times
+ * over them, pairs up to floor(r(beta_fast)) keep their frequency, pairs from
+ * ceil(r(beta_slow)) have it divided by factor, and a linear ramp joins them.
+ * base > 1, factor >= 1, beta_fast > beta_slow > 0. */
+int mla_rope_frequencies(float base, float factor, int original_tokens, float beta_fast, float beta_slow,
+                         double* inv_freq);
+
+/* Rotate packed vectors: x [rows, heads, 64] bf16 (a query's q_rope, a part of
+ * wider heads through its strides, or with one head k_rope) by positions[row]
+ * (int32 [rows], device, any value) into out, rounded to nearest.  inverse != 0
+ * negates the angles: the gradient of the rotation, and for scale 1 its
+ * inverse.  strides (host memory, values, positive multiples of 8): token and
+ * head stride of x, then of out.  x and out are 16-byte aligned; they may be the
+ * same memory with the same strides, and must not overlap otherwise.  rows at
+ * most 2^24, heads at most 4096.  No workspace, no device status. */
+int mla_rope_bf16(const uint16_t* x, const size_t* strides, const int32_t* positions, int rows, int heads,
+                  const mla_rope* rope, int inverse, uint16_t* out, void* stream);
+
+/* mla_cache_append_* with k_rope arriving unrotated: row i's 64 values are
+ * rotated by positions[i] (int32 [rows], device, any value; NULL: the row's
+ * token index) and rounded once, to bf16 or straight to the codes (as the exact
+ * rotated values would be, to about 2^-40 of their pair).  A drafted tree's rows
+ * stand at token indexes that are not their positions, and need the array.
+ * Everything else is as for mla_cache_append_*. */
+int mla_cache_append_rope_bf16(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                               const int32_t* positions, const mla_rope* rope, uint16_t* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_rows, int batch,
+                               int rows, int num_pages, int page_size, int max_pages, void* workspace,
+                               size_t workspace_bytes, void* stream);
+int mla_cache_append_rope_fp8(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                               const int32_t* positions, const mla_rope* rope, uint8_t* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_rows, int batch,
+                               int rows, int num_pages, int page_size, int max_pages, void* workspace,
+                               size_t workspace_bytes, void* stream);
+int mla_cache_append_rope_fp4(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                               const int32_t* positions, const mla_rope* rope, uint8_t* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_rows, int batch,
+                               int rows, int num_pages, int page_size, int max_pages, void* workspace,
+                               size_t workspace_bytes, void* stream);
+int mla_cache_append_rope_fp8_v41(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                               const int32_t* positions, const mla_rope* rope, uint8_t* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_rows, int batch,
+                               int rows, int num_pages, int page_size, int max_pages, void* workspace,
+                               size_t workspace_bytes, void* stream);
+int mla_cache_append_rope_fp4_v41(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                               const int32_t* positions, const mla_rope* rope, uint8_t* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_rows, int batch,
+                               int rows, int num_pages, int page_size, int max_pages, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* Keys and values of the expanded form ("DeepSeek R1 Architecture &
  * Deployment Guide", section 1.1, before absorption):
  *   k_nope[t][h][:] = W_uk[h] . c_t,   v[t][h][:] = W_uv[h] . c_t,

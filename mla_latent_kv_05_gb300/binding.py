@@ -57,6 +57,11 @@ SIGNATURES = {
        for f in ("bf16", "fp8", "fp4", "fp8_v41", "fp4_v41")},
     **{"mla_cache_gather_" + f: (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _Z, _P])
        for f in ("bf16", "fp8", "fp4", "fp8_v41", "fp4_v41")},
+    "mla_rope_init": (_I, [_P, _P, ctypes.c_float, _I]),
+    "mla_rope_frequencies": (_I, [ctypes.c_float, ctypes.c_float, _I, ctypes.c_float, ctypes.c_float, _P]),
+    "mla_rope_bf16": (_I, [_P, ctypes.POINTER(_Z), _P, _I, _I, _P, _I, _P, _P]),
+    **{"mla_cache_append_rope_" + f: (_I, [_P, _Z, _P, _Z, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _Z, _P])
+       for f in ("bf16", "fp8", "fp4", "fp8_v41", "fp4_v41")},
     "mla_expand_kv": (_I, [_P, _Z, _P, _P, _I, _I, _I, _P, _P, _P, _Z, _P]),
     "mla_workspace_size_prefill": (_I, [_I, _I, ctypes.POINTER(_Z)]),
     "mla_prefill_bf16": (_I, [_P, _P, _P, _P, _P, ctypes.POINTER(_Z), _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P,
@@ -482,6 +487,113 @@ def _append(fmt, c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspa
     return kv_cache
 
 
+class Rope(ctypes.Structure):
+    """A rotation's table (host memory, made by mla_rope_init; calls copy it)."""
+    _fields_ = [("turns", ctypes.c_uint64 * 32), ("scale", ctypes.c_float), ("interleaved", ctypes.c_int)]
+
+
+def mla_rope_frequencies(base: float = 10000.0, factor: float = 1.0, original_tokens: int = 4096,
+                         beta_fast: float = 32.0, beta_slow: float = 1.0) -> list:
+    """The 32 frequencies (radians a token) base^(-i/32), for factor > 1 scaled
+    (YaRN) to contexts `factor` times the original_tokens."""
+    f = (ctypes.c_double * 32)()
+    rc = load().mla_rope_frequencies(float(base), float(factor), int(original_tokens), float(beta_fast),
+                                     float(beta_slow), f)
+    if rc != MLA_OK:
+        raise MLAError(rc, "mla_rope_frequencies")
+    return list(f)
+
+
+def mla_rope_init(inv_freq, scale: float = 1.0, interleaved: bool = True) -> Rope:
+    """The table of a rotation: pair i of a vector's 64 values, (2i, 2i+1) if
+    interleaved, else (i, i+32), turns by position * inv_freq[i]; rotated vectors
+    are multiplied by `scale`."""
+    f = [float(v) for v in inv_freq]
+    if len(f) != 32:
+        raise ValueError(f"inv_freq must have 32 values, got {len(f)}")
+    rope = Rope()
+    rc = load().mla_rope_init(ctypes.addressof(rope), (ctypes.c_double * 32)(*f), float(scale), 1 if interleaved else 0)
+    if rc != MLA_OK:
+        raise MLAError(rc, "mla_rope_init")
+    return rope
+
+
+def _rope_arg(rope) -> int:
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope (of mla_rope_init)")
+    return ctypes.addressof(rope)
+
+
+_RopeStrides = ctypes.c_size_t * 4
+
+
+def _vectors_arg(t, name: str, shape=None):
+    """Address, token and head stride of a checked [rows, 64] or [rows, heads, 64] bf16 tensor or view."""
+    if isinstance(t, torch.Tensor) and t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [rows, 64] or [rows, heads, 64], got {tuple(t.shape)}")
+    if isinstance(t, torch.Tensor) and shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _check_rows(t, name, (64,) if not isinstance(t, torch.Tensor) or t.dim() == 2 else (t.shape[1], 64))
+    if t.dim() == 2:
+        return t.data_ptr(), _stride(t, 0, 64), 64
+    head = _stride(t, 1, 64)
+    return t.data_ptr(), _stride(t, 0, head * t.shape[1] or 64), head
+
+
+def mla_rope_bf16(x, positions, rope, out=None, inverse=False, stream=None):
+    """Rotate x [rows, heads, 64] or [rows, 64] bf16 (views with 16-byte strides
+    and a contiguous last dimension allowed, such as the last 64 values of wider
+    heads) by positions [rows] int32.  inverse: by the negated angles (the
+    gradient).  out: None for a new tensor, x itself to rotate in place, or
+    another that does not overlap x.  Returns out."""
+    at, x_t, x_h = _vectors_arg(x, "x")
+    table = _rope_arg(rope)
+    rows, heads = x.shape[0], x.shape[1] if x.dim() == 3 else 1
+    _check(positions, "positions", torch.int32, (rows,))
+    if out is None:
+        out = _new(stream, torch.empty, x.shape, dtype=torch.bfloat16, device=x.device)
+    to, o_t, o_h = (at, x_t, x_h) if out is x else _vectors_arg(out, "out", x.shape)
+    dev = torch.cuda.current_device()
+    if not (x.device == positions.device == out.device and x.device.index == dev):
+        _same_device(dict(x=x, positions=positions, out=out), dev)
+    if rows == 0 or heads == 0:
+        return out
+    rc = load().mla_rope_bf16(at, _RopeStrides(x_t, x_h, o_t, o_h), positions.data_ptr(), rows, heads, table,
+                              1 if inverse else 0, to, _handle(stream, dev))
+    if rc != MLA_OK:
+        raise MLAError(rc, "mla_rope_bf16")
+    return out
+
+
+def _append_rope(fmt, c_kv, k_rope, rope, kv_cache, block_table, seq_lens, cu_rows, positions, workspace, stream):
+    name = "mla_cache_append_rope_" + fmt
+    c_at, c_stride = _rows_arg(c_kv, "c_kv", 512)
+    rows = c_kv.shape[0]
+    r_at, r_stride = _rows_arg(k_rope, "k_rope", 64, rows)
+    table = _rope_arg(rope)
+    _check_cache(fmt, kv_cache, block_table, seq_lens, cu_rows)
+    if positions is not None:
+        _check(positions, "positions", torch.int32, (rows,))
+    if workspace is None:
+        workspace = _new(stream, _status_workspace, kv_cache.device)
+    _check(workspace, "workspace", torch.uint8)
+    dev = torch.cuda.current_device()
+    if not (kv_cache.device == c_kv.device == k_rope.device == block_table.device == seq_lens.device == cu_rows.device
+            == workspace.device and (positions is None or positions.device == c_kv.device)
+            and kv_cache.device.index == dev):
+        _same_device(dict(kv_cache=kv_cache, c_kv=c_kv, k_rope=k_rope, block_table=block_table, seq_lens=seq_lens,
+                          cu_rows=cu_rows, positions=positions, workspace=workspace), dev)
+    batch, max_pages = block_table.shape
+    pages, page_size, _ = kv_cache.shape
+    rc = getattr(load(), name)(
+        c_at, c_stride, r_at, r_stride, None if positions is None else positions.data_ptr(), table,
+        kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_rows.data_ptr(), batch, rows, pages,
+        page_size, max_pages, workspace.data_ptr(), workspace.numel(), _handle(stream, dev))
+    if rc != MLA_OK and rows:       # empty tensors have null pointers: nothing to do
+        raise MLAError(rc, name)
+    return kv_cache
+
+
 def _gather(fmt, kv_cache, block_table, seq_lens, cu_rows, n_rows, out, workspace, stream):
     name = "mla_cache_gather_" + fmt
     _check_cache(fmt, kv_cache, block_table, seq_lens, cu_rows)
@@ -540,6 +652,48 @@ def mla_cache_append_fp4_v41(c_kv, k_rope, kv_cache, block_table, seq_lens, cu_r
     """mla_cache_append_fp4 into the V4.1 rows [num_pages, 64, 288]: the first
     448 latent values and the 64 RoPE values (c_kv[:, 448:] is ignored)."""
     return _append("fp4_v41", c_kv, k_rope, kv_cache, block_table, seq_lens, cu_rows, workspace, stream)
+
+
+def mla_cache_append_rope_bf16(c_kv, k_rope, rope, kv_cache, block_table, seq_lens, cu_rows, positions=None,
+                               workspace=None, stream=None):
+    """mla_cache_append_bf16 with k_rope arriving unrotated: row i's 64 values are
+    rotated by positions[i] (int32 [n]; None: the row's token index in its
+    sequence) on their way into a bf16 cache [num_pages, 64, 576], and rounded once.
+    Returns kv_cache."""
+    return _append_rope("bf16", c_kv, k_rope, rope, kv_cache, block_table, seq_lens, cu_rows, positions, workspace,
+                        stream)
+
+
+def mla_cache_append_rope_fp8(c_kv, k_rope, rope, kv_cache, block_table, seq_lens, cu_rows, positions=None,
+                               workspace=None, stream=None):
+    """mla_cache_append_fp8 into an FP8 cache [num_pages, 64, 594], k_rope rotated
+    as by mla_cache_append_rope_bf16 and rounded straight to the codes."""
+    return _append_rope("fp8", c_kv, k_rope, rope, kv_cache, block_table, seq_lens, cu_rows, positions, workspace,
+                        stream)
+
+
+def mla_cache_append_rope_fp4(c_kv, k_rope, rope, kv_cache, block_table, seq_lens, cu_rows, positions=None,
+                               workspace=None, stream=None):
+    """mla_cache_append_fp4 into an FP4 cache [num_pages, 64, 324], k_rope rotated
+    as by mla_cache_append_rope_bf16 and rounded straight to the codes."""
+    return _append_rope("fp4", c_kv, k_rope, rope, kv_cache, block_table, seq_lens, cu_rows, positions, workspace,
+                        stream)
+
+
+def mla_cache_append_rope_fp8_v41(c_kv, k_rope, rope, kv_cache, block_table, seq_lens, cu_rows, positions=None,
+                               workspace=None, stream=None):
+    """mla_cache_append_fp8_v41 into V4.1 rows [num_pages, 64, 528], k_rope rotated
+    as by mla_cache_append_rope_bf16 and rounded straight to the codes."""
+    return _append_rope("fp8_v41", c_kv, k_rope, rope, kv_cache, block_table, seq_lens, cu_rows, positions, workspace,
+                        stream)
+
+
+def mla_cache_append_rope_fp4_v41(c_kv, k_rope, rope, kv_cache, block_table, seq_lens, cu_rows, positions=None,
+                               workspace=None, stream=None):
+    """mla_cache_append_fp4_v41 into V4.1 rows [num_pages, 64, 288], k_rope rotated
+    as by mla_cache_append_rope_bf16 and rounded straight to the codes."""
+    return _append_rope("fp4_v41", c_kv, k_rope, rope, kv_cache, block_table, seq_lens, cu_rows, positions, workspace,
+                        stream)
 
 
 def mla_cache_gather_bf16(kv_cache, block_table, seq_lens, cu_rows, n_rows, out=None, workspace=None, stream=None):

@@ -13,6 +13,7 @@
 #include "decode.cuh"
 #include "expand.cuh"
 #include "prefill.cuh"
+#include "rope.cuh"
 #include "rows.cuh"
 #include "tree.cuh"
 
@@ -373,6 +374,8 @@ int run_tree(CacheKind kind, const uint16_t* q_absorbed, const uint16_t* q_rope,
 }
 
 // Row strides (values) a 16-byte access or a TMA map takes.
+constexpr int kMaxRopeRows = 1 << 24, kMaxRopeHeads = 4096;
+
 bool stride_ok(size_t s) { return s > 0 && s % 8 == 0 && s < (size_t{1} << 38); }
 
 int sm_count() {
@@ -386,7 +389,7 @@ int sm_count() {
 int run_rows(RowFormat fmt, const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
              const void* cache, const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_rows, int batch,
              int rows, int num_pages, int page_size, int max_pages, uint16_t* out, bool append, void* workspace,
-             size_t workspace_bytes, void* stream) {
+             size_t workspace_bytes, void* stream, const RowsRope* rope = nullptr) {
   if (!cache || !block_table || !seq_lens || !cu_rows || !workspace || (append ? !c_kv || !k_rope : !out))
     return MLA_ERR_INVALID_ARG;
   if (batch < 0 || rows < 0 || num_pages <= 0 || max_pages <= 0) return MLA_ERR_INVALID_ARG;
@@ -420,7 +423,21 @@ int run_rows(RowFormat fmt, const uint16_t* c_kv, size_t c_stride, const uint16_
   p.max_pages = max_pages;
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
   p.status = &static_cast<PlanHeader*>(workspace)->status;
-  return launch_rows(fmt, p, append, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = rope ? launch_append_rope(fmt, p, *rope, st) : launch_rows(fmt, p, append, st);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+bool rope_ok(const mla_rope* rope) { return rope && std::isfinite(rope->scale); }
+
+int run_append_rope(RowFormat fmt, const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                    const int32_t* positions, const mla_rope* rope, void* cache, const int32_t* block_table,
+                    const int32_t* seq_lens, const int32_t* cu_rows, int batch, int rows, int num_pages, int page_size,
+                    int max_pages, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!rope_ok(rope) || !aligned(positions, 4)) return MLA_ERR_INVALID_ARG;
+  const RowsRope r = {positions, *rope};
+  return run_rows(fmt, c_kv, c_stride, k_rope, r_stride, cache, block_table, seq_lens, cu_rows, batch, rows, num_pages,
+                  page_size, max_pages, nullptr, true, workspace, workspace_bytes, stream, &r);
 }
 
 }  // namespace
@@ -522,6 +539,116 @@ int mla_cache_gather_fp4_v41(const uint8_t* kv_cache, const int32_t* block_table
                           uint16_t* out, void* workspace, size_t workspace_bytes, void* stream) {
   return run_rows(RowFormat::kFp4V41, nullptr, 0, nullptr, 0, kv_cache, block_table, seq_lens, cu_rows, batch, rows,
                   num_pages, page_size, max_pages, out, false, workspace, workspace_bytes, stream);
+}
+
+int mla_cache_append_rope_bf16(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                               const int32_t* positions, const mla_rope* rope, uint16_t* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_rows, int batch,
+                               int rows, int num_pages, int page_size, int max_pages, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return run_append_rope(RowFormat::kBf16, c_kv, c_stride, k_rope, r_stride, positions, rope, kv_cache, block_table,
+                         seq_lens, cu_rows, batch, rows, num_pages, page_size, max_pages, workspace, workspace_bytes,
+                         stream);
+}
+
+int mla_cache_append_rope_fp8(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                               const int32_t* positions, const mla_rope* rope, uint8_t* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_rows, int batch,
+                               int rows, int num_pages, int page_size, int max_pages, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return run_append_rope(RowFormat::kFp8, c_kv, c_stride, k_rope, r_stride, positions, rope, kv_cache, block_table,
+                         seq_lens, cu_rows, batch, rows, num_pages, page_size, max_pages, workspace, workspace_bytes,
+                         stream);
+}
+
+int mla_cache_append_rope_fp4(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                               const int32_t* positions, const mla_rope* rope, uint8_t* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_rows, int batch,
+                               int rows, int num_pages, int page_size, int max_pages, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return run_append_rope(RowFormat::kFp4, c_kv, c_stride, k_rope, r_stride, positions, rope, kv_cache, block_table,
+                         seq_lens, cu_rows, batch, rows, num_pages, page_size, max_pages, workspace, workspace_bytes,
+                         stream);
+}
+
+int mla_cache_append_rope_fp8_v41(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                               const int32_t* positions, const mla_rope* rope, uint8_t* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_rows, int batch,
+                               int rows, int num_pages, int page_size, int max_pages, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return run_append_rope(RowFormat::kFp8V41, c_kv, c_stride, k_rope, r_stride, positions, rope, kv_cache, block_table,
+                         seq_lens, cu_rows, batch, rows, num_pages, page_size, max_pages, workspace, workspace_bytes,
+                         stream);
+}
+
+int mla_cache_append_rope_fp4_v41(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,
+                               const int32_t* positions, const mla_rope* rope, uint8_t* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_rows, int batch,
+                               int rows, int num_pages, int page_size, int max_pages, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return run_append_rope(RowFormat::kFp4V41, c_kv, c_stride, k_rope, r_stride, positions, rope, kv_cache, block_table,
+                         seq_lens, cu_rows, batch, rows, num_pages, page_size, max_pages, workspace, workspace_bytes,
+                         stream);
+}
+
+int mla_rope_init(mla_rope* rope, const double* inv_freq, float scale, int interleaved) {
+  if (!rope || !inv_freq || !std::isfinite(scale)) return MLA_ERR_INVALID_ARG;
+  for (int i = 0; i < kRopePairs; ++i)
+    if (!(std::fabs(inv_freq[i]) <= 1024.0)) return MLA_ERR_INVALID_ARG;
+  // 1 / (2 pi) in two parts; the turns a token, modulo one, in units of 2^-64
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+  for (int i = 0; i < kRopePairs; ++i) {
+    const double p = inv_freq[i] * kHi, rest = std::fma(inv_freq[i], kLo, std::fma(inv_freq[i], kHi, -p));
+    double whole;
+    const double turn = std::ldexp(std::modf(p, &whole), 32), upper = std::floor(turn);
+    const double lower = std::nearbyint(std::ldexp(turn - upper, 32) + std::ldexp(rest, 64));
+    rope->turns[i] = (static_cast<uint64_t>(static_cast<int64_t>(upper)) << 32) +
+                     static_cast<uint64_t>(static_cast<int64_t>(lower));
+  }
+  rope->scale = scale;
+  rope->interleaved = interleaved != 0;
+  return MLA_OK;
+}
+
+int mla_rope_frequencies(float base, float factor, int original_tokens, float beta_fast, float beta_slow,
+                         double* inv_freq) {
+  if (!inv_freq || !(base > 1.f) || !std::isfinite(base) || !(factor >= 1.f) || !std::isfinite(factor) ||
+      original_tokens <= 0 || !(beta_slow > 0.f) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast))
+    return MLA_ERR_INVALID_ARG;
+  const double ln_base = std::log(static_cast<double>(base));
+  // the pair that turns `n` times over the original length
+  auto pair = [&](double n) { return kDr * std::log(original_tokens / (n * 6.283185307179586)) / (2 * ln_base); };
+  const double low = std::fmax(std::floor(pair(beta_fast)), 0.0);
+  const double high = std::fmin(std::ceil(pair(beta_slow)), kDr - 1.0);
+  for (int i = 0; i < kRopePairs; ++i) {
+    const double f = std::exp(-ln_base * i / kRopePairs);
+    const double ramp = std::fmin(std::fmax((i - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
+    inv_freq[i] = f / factor * ramp + f * (1.0 - ramp);
+  }
+  return MLA_OK;
+}
+
+int mla_rope_bf16(const uint16_t* x, const size_t* strides, const int32_t* positions, int rows, int heads,
+                  const mla_rope* rope, int inverse, uint16_t* out, void* stream) {
+  if (!x || !strides || !positions || !out || !rope_ok(rope) || rows < 0 || heads < 0) return MLA_ERR_INVALID_ARG;
+  if (rows > kMaxRopeRows || heads > kMaxRopeHeads) return MLA_ERR_UNSUPPORTED;
+  for (int i = 0; i < 4; ++i)
+    if (!stride_ok(strides[i])) return MLA_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(positions, 4)) return MLA_ERR_INVALID_ARG;
+  if (rows == 0 || heads == 0) return MLA_OK;
+  RopeParams p;
+  p.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  p.x_t = static_cast<long long>(strides[0]);
+  p.x_h = static_cast<long long>(strides[1]);
+  p.out_t = static_cast<long long>(strides[2]);
+  p.out_h = static_cast<long long>(strides[3]);
+  p.positions = positions;
+  p.rows = rows;
+  p.heads = heads;
+  p.inverse = inverse != 0;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.rope = *rope;
+  return launch_rope(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 int mla_expand_kv(const uint16_t* latent, size_t row_stride, const uint16_t* w_uk, const uint16_t* w_uv, int rows,

@@ -31,11 +31,17 @@
 // 1152 bytes) and 68, 61 (6470, 6190); the 594- and 324-byte rows are off 16-byte
 // boundaries, so their accesses are smaller.
 // 16,384 rows: 5.2 to 7.2 us; 64 rows: 2.3 us.
+//
+// The append may rotate the RoPE values on their way (rope.cuh): the CTA's rows
+// have 32 pairs each, which its threads take in turn into shared memory, as floats
+// that round to the cache's format as the exact rotated values would.  They are
+// rounded once, straight to bf16 or to the codes.
 #include <climits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "rope.cuh"
 #include "rows.cuh"
 
 namespace mla {
@@ -69,8 +75,9 @@ template <RowFormat F> constexpr bool kIsV41 = F == RowFormat::kFp8V41 || F == R
 // token or page lies outside the cache (recorded in the status word; never read
 // or written).  One search for all rows: a warp's search for each took more
 // instructions than the rows' values (131,072 rows: fp8 append 56 us).
+// s_token: where not null, the rows' token indexes (0 for a row without a slot).
 template <int kRows>
-__device__ __forceinline__ void look_up(const RowsParams& p, int row0, int* s_slot) {
+__device__ __forceinline__ void look_up(const RowsParams& p, int row0, int* s_slot, int* s_token = nullptr) {
   static_assert(kRows <= 32, "a lane a row");
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
@@ -98,7 +105,7 @@ __device__ __forceinline__ void look_up(const RowsParams& p, int row0, int* s_sl
       // (32 sequences begin in these rows, most of them empty: look further)
       if (b == lo + 32)
         while (b < p.batch && __ldg(p.cu_rows + b + 1) <= i) ++b;
-      int slot = -1;
+      int slot = -1, token = 0;
       if (i < p.rows && b < p.batch) {   // (cu[batch] <= i: behind the last sequence)
         const int c0 = __ldg(p.cu_rows + b), c1 = __ldg(p.cu_rows + b + 1);
         int code = MLA_STATUS_BAD_SEQ_LEN;
@@ -107,6 +114,7 @@ __device__ __forceinline__ void look_up(const RowsParams& p, int row0, int* s_sl
           const long long pos = static_cast<long long>(__ldg(p.seq_lens + b)) - c1 + i;
           if (pos >= 0 && pos < static_cast<long long>(p.max_pages) * kPage) {
             const int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + (pos >> 6));
+            token = static_cast<int>(pos);
             if (page >= 0 && page < p.num_pages) slot = page * kPage + static_cast<int>(pos & 63);
             else code = MLA_STATUS_BAD_PAGE;
           }
@@ -114,6 +122,7 @@ __device__ __forceinline__ void look_up(const RowsParams& p, int row0, int* s_sl
         if (slot < 0) set_status(p.status, code);
       }
       s_slot[lane] = slot;
+      if (s_token) s_token[lane] = token;
     }
   }
   __syncthreads();
@@ -128,6 +137,61 @@ __device__ __forceinline__ int scale_exponent(uint32_t a) {
   const uint32_t man = a & 0x7Fu;
   const int k = kIsFp4<F> ? e - 3 + (man > 0x40u) : e - 9 + (man > 0x60u);
   return min(max(k, -127), Fmt<F>::kTopK);
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// The same from the fp32 bits of a magnitude.
+template <RowFormat F>
+__device__ __forceinline__ int scale_exponent_fp32(uint32_t a) {
+  if (a == 0) return 0;
+  const int e = static_cast<int>(a >> 23) - 126;
+  const uint32_t man = a & 0x7FFFFFu;
+  const int k = kIsFp4<F> ? e - 3 + (man > 0x400000u) : e - 9 + (man > 0x600000u);
+  return min(max(k, -127), Fmt<F>::kTopK);
+}
+
+// Eight codes from fp32 values that `mul` = 2^-k brings into the format's range.
+template <RowFormat F>
+__device__ __forceinline__ void encode(const float* x, float mul, bool finite, uint32_t* code) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // exact: a product that is not (below 2^-126) is far under the smallest code
+    const float lo = finite ? x[2 * i] * mul : 0.f;
+    const float hi = finite ? x[2 * i + 1] * mul : 0.f;
+    if constexpr (kIsFp4<F>) {
+      asm("{\n .reg .b8 c;\n cvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n cvt.u32.u8 %0, c;\n}"
+          : "=r"(code[i]) : "f"(lo), "f"(hi));
+    } else {
+      unsigned short c;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(lo), "f"(hi));
+      code[i] = c;
+    }
+  }
+}
+
+// Codes of piece j, and with the group's first piece the scale byte.
+template <RowFormat F>
+__device__ __forceinline__ void store_codes(uint8_t* dst, int slot, int j, const uint32_t* code, uint8_t scale) {
+  using T = Fmt<F>;
+  if constexpr (kIsFp4<F>) {
+    // rows start on 4-byte boundaries
+    *reinterpret_cast<uint32_t*>(dst + j * 4) = code[0] | (code[1] << 8) | (code[2] << 16) | (code[3] << 24);
+  } else if constexpr (F == RowFormat::kFp8V41) {
+    *reinterpret_cast<uint2*>(dst + j * 8) = make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+  } else if (slot & 1) {
+    // 594-byte rows: an odd slot starts between two words
+    *reinterpret_cast<uint16_t*>(dst + j * 8) = static_cast<uint16_t>(code[0]);
+    *reinterpret_cast<uint32_t*>(dst + j * 8 + 2) = code[1] | (code[2] << 16);
+    *reinterpret_cast<uint16_t*>(dst + j * 8 + 6) = static_cast<uint16_t>(code[3]);
+  } else {
+    *reinterpret_cast<uint32_t*>(dst + j * 8) = code[0] | (code[1] << 16);
+    *reinterpret_cast<uint32_t*>(dst + j * 8 + 4) = code[2] | (code[3] << 16);
+  }
+  if (j % (T::kGroup / kPiece) == 0) dst[T::kScales + j / (T::kGroup / kPiece)] = scale;
 }
 
 // One piece of a quantised or bf16 row into its cache row.
@@ -149,38 +213,16 @@ __device__ __forceinline__ void append_piece(const RowsParams& p, uint4 v, int s
     const int k = finite ? scale_exponent<F>(m) : 0;
     const float mul = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);   // 2^-k, normal: k <= 125
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t code[4];
+    float x[kPiece];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // exact: a product that is not (below 2^-126) is far under the smallest code
-      const float lo = finite ? __uint_as_float(w[i] << 16) * mul : 0.f;
-      const float hi = finite ? __uint_as_float(w[i] & 0xFFFF0000u) * mul : 0.f;
-      if constexpr (kIsFp4<F>) {
-        asm("{\n .reg .b8 c;\n cvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n cvt.u32.u8 %0, c;\n}"
-            : "=r"(code[i]) : "f"(lo), "f"(hi));
-      } else {
-        unsigned short c;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(lo), "f"(hi));
-        code[i] = c;
-      }
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
+    uint32_t code[4];
+    encode<F>(x, mul, finite, code);
     if (slot < 0) return;
-    if constexpr (kIsFp4<F>) {
-      // rows start on 4-byte boundaries
-      *reinterpret_cast<uint32_t*>(dst + j * 4) = code[0] | (code[1] << 8) | (code[2] << 16) | (code[3] << 24);
-    } else if constexpr (F == RowFormat::kFp8V41) {
-      *reinterpret_cast<uint2*>(dst + j * 8) = make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
-    } else if (slot & 1) {
-      // 594-byte rows: an odd slot starts between two words
-      *reinterpret_cast<uint16_t*>(dst + j * 8) = static_cast<uint16_t>(code[0]);
-      *reinterpret_cast<uint32_t*>(dst + j * 8 + 2) = code[1] | (code[2] << 16);
-      *reinterpret_cast<uint16_t*>(dst + j * 8 + 6) = static_cast<uint16_t>(code[3]);
-    } else {
-      *reinterpret_cast<uint32_t*>(dst + j * 8) = code[0] | (code[1] << 16);
-      *reinterpret_cast<uint32_t*>(dst + j * 8 + 4) = code[2] | (code[3] << 16);
-    }
-    if (j % (T::kGroup / kPiece) == 0)
-      dst[T::kScales + j / (T::kGroup / kPiece)] = static_cast<uint8_t>(finite ? k + 127 : 255);
+    store_codes<F>(dst, slot, j, code, static_cast<uint8_t>(finite ? k + 127 : 255));
   }
 }
 
@@ -207,10 +249,96 @@ __global__ void __launch_bounds__(kGroupRows * Fmt<F>::kValues / kPiece) append_
   for (int g = 0; g < kGroups; ++g) append_piece<F>(p, v[g], s_slot[g * kGroupRows + r], j);
 }
 
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
+// A piece of eight fp32 values (rotated ones), as append_piece.
+template <RowFormat F>
+__device__ __forceinline__ void append_values(const RowsParams& p, const float* x, int slot, int j) {
+  using T = Fmt<F>;
+  uint8_t* dst = p.cache + static_cast<size_t>(slot < 0 ? 0 : slot) * T::kBytes;
+  if constexpr (F == RowFormat::kBf16) {
+    if (slot >= 0)
+      *reinterpret_cast<uint4*>(dst + j * 16) =
+          make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 1; o < T::kGroup / kPiece; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool finite = m < 0x7F800000u;
+    const int k = finite ? scale_exponent_fp32<F>(m) : 0;
+    uint32_t code[4];
+    encode<F>(x, __uint_as_float(static_cast<uint32_t>(127 - k) << 23), finite, code);
+    if (slot >= 0) store_codes<F>(dst, slot, j, code, static_cast<uint8_t>(finite ? k + 127 : 255));
+  }
 }
+
+// append_kernel with the RoPE values rotated by their row's position.
+template <RowFormat F, int kGroups>
+__global__ void __launch_bounds__(kGroupRows * Fmt<F>::kValues / kPiece)
+append_rope_kernel(const RowsParams p, const __grid_constant__ RowsRope rope) {
+  constexpr int kPieces = Fmt<F>::kValues / kPiece, kThreads = kGroupRows * kPieces, kRows = kGroups * kGroupRows;
+  constexpr int kLatentPieces = (kIsV41<F> ? kV41Latent : kDc) / kPiece;
+  constexpr int kTurns = (kRows * kRopePairs + kThreads - 1) / kThreads;   // pairs a thread rotates
+  __shared__ int s_slot[kRows], s_token[kRows];
+  __shared__ float4 s_table[64];
+  __shared__ float s_rope[kRows][kDr];
+  const int r = threadIdx.x / kPieces, j = threadIdx.x - r * kPieces;
+  const int row0 = blockIdx.x * kRows;
+  const int near = rope.table.interleaved ? 2 : 1, far = rope.table.interleaved ? 1 : kRopePairs;   // pair i: near i, near i + far
+  uint4 v[kGroups];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const int row = row0 + g * kGroupRows + r;
+    v[g] = make_uint4(0, 0, 0, 0);
+    if (row < p.rows && j < kLatentPieces)
+      v[g] = __ldg(reinterpret_cast<const uint4*>(p.c_kv + static_cast<size_t>(row) * p.c_stride + j * kPiece));
+  }
+  float a[kTurns], b[kTurns];
+#pragma unroll
+  for (int n = 0; n < kTurns; ++n) {
+    const int i = static_cast<int>(threadIdx.x) + n * kThreads, row = row0 + i / kRopePairs, pair = i % kRopePairs;
+    a[n] = b[n] = 0.f;
+    if (i < kRows * kRopePairs && row < p.rows) {
+      const __nv_bfloat16* src = p.k_rope + static_cast<size_t>(row) * p.r_stride + near * pair;
+      a[n] = __bfloat162float(src[0]);
+      b[n] = __bfloat162float(src[far]);
+    }
+  }
+  if (threadIdx.x < 64) s_table[threadIdx.x] = turn_entry(threadIdx.x);
+  look_up<kRows>(p, row0, s_slot, s_token);
+#pragma unroll
+  for (int n = 0; n < kTurns; ++n) {
+    const int i = static_cast<int>(threadIdx.x) + n * kThreads, at = i / kRopePairs, pair = i % kRopePairs;
+    if (i >= kRows * kRopePairs || s_slot[at] < 0) continue;
+    const int64_t position = rope.positions ? __ldg(rope.positions + row0 + at) : s_token[at];
+    Two c, s;
+    turn_cos_sin(static_cast<uint64_t>(position) * rope.table.turns[pair], s_table, c, s);
+    if (rope.table.scale != 1.f) {
+      c = product(c, Two{rope.table.scale, 0.f});
+      s = product(s, Two{rope.table.scale, 0.f});
+    }
+    s_rope[at][near * pair] = odd_sum(a[n], c, b[n], Two{-s.hi, -s.lo});
+    s_rope[at][near * pair + far] = odd_sum(a[n], s, b[n], c);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const int at = g * kGroupRows + r, slot = s_slot[at];
+    float x[kPiece];
+    const uint32_t w[4] = {v[g].x, v[g].y, v[g].z, v[g].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    if (j >= kLatentPieces && slot >= 0) {
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) x[i] = s_rope[at][(j - kLatentPieces) * kPiece + i];
+    }
+    append_values<F>(p, x, slot, j);
+  }
+}
+
 
 // A stored piece (codes and their scale) as read, and as eight bf16 values.
 struct Piece {
@@ -328,6 +456,14 @@ __global__ void __launch_bounds__(kGroupRows * kRow / kPiece) widen_kernel(const
 // Rows of a call from which a CTA takes four groups instead of one.
 constexpr int kLongCall = 8192;
 
+template <RowFormat F>
+cudaError_t launch_append_rope(const RowsParams& p, const RowsRope& rope, cudaStream_t stream) {
+  const int rows = (p.rows >= kLongCall ? 4 : 1) * kGroupRows;
+  const dim3 grid((p.rows + rows - 1) / rows), block(kGroupRows * Fmt<F>::kValues / kPiece);
+  if (p.rows >= kLongCall) return launch_kernel(append_rope_kernel<F, 4>, grid, block, 0, stream, p, rope);
+  return launch_kernel(append_rope_kernel<F, 1>, grid, block, 0, stream, p, rope);
+}
+
 template <RowFormat F, int kGroups>
 cudaError_t launch(const RowsParams& p, bool append, cudaStream_t stream) {
   const dim3 grid((p.rows + kGroups * kGroupRows - 1) / (kGroups * kGroupRows));
@@ -367,6 +503,18 @@ cudaError_t launch_rows(RowFormat fmt, const RowsParams& p, bool append, cudaStr
     case RowFormat::kFp4: return launch<RowFormat::kFp4>(p, append, stream);
     case RowFormat::kFp8V41: return launch<RowFormat::kFp8V41>(p, append, stream);
     case RowFormat::kFp4V41: return launch<RowFormat::kFp4V41>(p, append, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_append_rope(RowFormat fmt, const RowsParams& p, const RowsRope& rope, cudaStream_t stream) {
+  if (p.rows <= 0) return cudaSuccess;
+  switch (fmt) {
+    case RowFormat::kBf16: return launch_append_rope<RowFormat::kBf16>(p, rope, stream);
+    case RowFormat::kFp8: return launch_append_rope<RowFormat::kFp8>(p, rope, stream);
+    case RowFormat::kFp4: return launch_append_rope<RowFormat::kFp4>(p, rope, stream);
+    case RowFormat::kFp8V41: return launch_append_rope<RowFormat::kFp8V41>(p, rope, stream);
+    case RowFormat::kFp4V41: return launch_append_rope<RowFormat::kFp4V41>(p, rope, stream);
   }
   return cudaErrorInvalidValue;
 }

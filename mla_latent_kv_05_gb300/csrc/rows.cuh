@@ -21,10 +21,18 @@ struct RowsParams {
   int* status;
 };
 
+// The rotation of an append's RoPE values: the rows' positions (null: their
+// token indexes) and the table.
+struct RowsRope {
+  const int32_t* positions;      // [rows]
+  mla_rope table;
+};
+
 // The sequences' pages in a quantised format as bf16 rows [batch, max_pages 64,
 // 576] in p.out (p.cache, block_table, seq_lens, batch, num_pages, max_pages
 // set; batch <= 65535).
 cudaError_t launch_widen(RowFormat fmt, const RowsParams& p, cudaStream_t stream);
 cudaError_t launch_rows(RowFormat fmt, const RowsParams& p, bool append, cudaStream_t stream);
+cudaError_t launch_append_rope(RowFormat fmt, const RowsParams& p, const RowsRope& rope, cudaStream_t stream);
 
 }  // namespace mla
