@@ -42,6 +42,7 @@
 #include <cuda_bf16.h>
 
 #include "expand.cuh"
+#include "spans.cuh"
 #include "waits.cuh"
 
 namespace mla {
@@ -301,7 +302,8 @@ cudaError_t launch_expand(PFN_cuTensorMapEncodeTiled_v12000 encode, const void* 
   };
   const cuuint64_t n = static_cast<cuuint64_t>(rows);
   {
-    const cuuint64_t dims[3] = {kDc, n, 2}, strides[2] = {static_cast<cuuint64_t>(row_stride) * 2, kTmaFar};
+    const cuuint64_t far = tma_far(latent, 2 * ((n - 1) * static_cast<cuuint64_t>(row_stride) + kDc));
+    const cuuint64_t dims[3] = {kDc, n, far ? 2u : 1u}, strides[2] = {static_cast<cuuint64_t>(row_stride) * 2, far ? far : 16u};
     const cuuint32_t box[3] = {kKBlock, 128, 1};
     if (!map(&maps.c, latent, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
@@ -312,10 +314,13 @@ cudaError_t launch_expand(PFN_cuTensorMapEncodeTiled_v12000 encode, const void* 
       return cudaErrorInvalidValue;
   }
   {
-    const cuuint64_t dims[4] = {128, kHeads, n, 2}, strides[3] = {256, kHeads * 256, kTmaFar};
     const cuuint32_t box[4] = {64, 1, 32, 1};
-    if (!map(&maps.out[0], k_nope, 4, dims, strides, box) || !map(&maps.out[1], v, 4, dims, strides, box))
-      return cudaErrorInvalidValue;
+    for (int i = 0; i < 2; ++i) {
+      void* out = i ? v : k_nope;
+      const cuuint64_t far = tma_far(out, n * kHeads * 256);
+      const cuuint64_t dims[4] = {128, kHeads, n, far ? 2u : 1u}, strides[3] = {256, kHeads * 256, far ? far : 16u};
+      if (!map(&maps.out[i], out, 4, dims, strides, box)) return cudaErrorInvalidValue;
+    }
   }
   static std::atomic<uint64_t> configured{0};
   const cudaError_t e = allow_smem(expand_kernel, kSmem, configured);

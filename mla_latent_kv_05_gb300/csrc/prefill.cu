@@ -260,44 +260,6 @@ __device__ __forceinline__ float row_max(const uint32_t* s) {
   return max3(fmaxf(m[0], m[1]), m[2], m[3]);
 }
 
-// Waits as in waits.cuh, with less code: CTAs of this kernel do not wait for one
-// another, so a wait that gives up tells its own CTA only, through shared memory,
-// and the status is written at the end.  (Thirty waits in line; the kernel's
-// code must stay in the instruction caches: with 62 KB instead of 52, 64 prompts
-// of up to 512 tokens took 610 us instead of 477.)
-static_assert(MLA_WAIT_TIMEOUT_NS < (1ull << 31), "a difference of 32-bit times");
-__device__ __forceinline__ uint32_t timer32() {
-  uint32_t t;
-  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
-  return t;
-}
-__device__ __forceinline__ bool wait_cta(uint32_t bar, uint32_t parity, volatile uint32_t* quit) {
-  uint32_t t0 = 0;
-#pragma unroll 1
-  for (uint32_t n = 1; !ptx::mbar_try_wait(bar, parity); ++n) {
-    if ((n & 1023u) != 0) continue;
-    const uint32_t now = timer32();
-    if (n == 1024u) t0 = now;
-    if (now - t0 > static_cast<uint32_t>(MLA_WAIT_TIMEOUT_NS)) *quit = 1u;
-    if (*quit != 0) return false;
-  }
-  return true;
-}
-__device__ __forceinline__ bool wait_cta_warp(uint32_t bar, uint32_t parity, volatile uint32_t* quit) {
-  return __all_sync(0xffffffffu, wait_cta(bar, parity, quit));
-}
-// For what was issued and completes by itself, whether the CTA gave up or not.
-__device__ __forceinline__ void wait_issued(uint32_t bar, uint32_t parity, volatile uint32_t* quit) {
-  const uint32_t t0 = timer32();
-#pragma unroll 1
-  while (!ptx::mbar_try_wait(bar, parity)) {
-    if (timer32() - t0 > static_cast<uint32_t>(kDrainTimeoutNs)) {
-      *quit = 1u;
-      return;
-    }
-  }
-}
-
 // sum += a b in bf16 pairs: not finite once a value was not.  (In its place behind
 // the stores, which the compiler delays for it otherwise.)
 __device__ __forceinline__ void add_product(uint32_t& sum, uint32_t a, uint32_t b) {
@@ -865,19 +827,6 @@ prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams p, const P
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
-}
-
-// (values, heads, tokens) boxes of 64 x 1 x rows; strides in values (see kTmaFar
-// for the fourth dimension).
-bool encode_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* base, int width, int heads,
-                int tokens, long long stride_t, long long stride_h, unsigned rows) {
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens), 2};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(stride_h) * 2, static_cast<cuuint64_t>(stride_t) * 2, kTmaFar};
-  cuuint32_t box[4] = {64, 1, rows, 1};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace

@@ -4,7 +4,8 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
-#include "common.cuh"
+#include "spans.cuh"
+#include "waits.cuh"
 
 namespace mla {
 
@@ -35,6 +36,21 @@ __host__ __device__ inline PrefillWs prefill_ws(int batch, int nq) {
   w.again = align256(w.tiles + 32 * static_cast<size_t>(w.max_tiles));
   w.total = align256(w.again + 16 * static_cast<size_t>(w.max_tiles));
   return w;
+}
+
+// (values, heads, tokens) boxes of 64 x 1 x rows; strides in values (see spans.cuh
+// for the fourth dimension).
+inline bool encode_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* base, int width, int heads,
+                       int tokens, long long stride_t, long long stride_h, unsigned rows) {
+  const uint64_t far = tma_far(base, 2 * static_cast<uint64_t>((tokens - 1) * stride_t + (heads - 1) * stride_h + width));
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens),
+                        far ? 2u : 1u};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(stride_h) * 2, static_cast<cuuint64_t>(stride_t) * 2, far ? far : 16u};
+  cuuint32_t box[4] = {64, 1, rows, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_prefill(PFN_cuTensorMapEncodeTiled_v12000 encode, const PrefillParams& p, int sms,

@@ -52,6 +52,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "spans.cuh"
 #include "tree.cuh"
 #include "waits.cuh"
 #include "walk.cuh"
@@ -504,7 +505,8 @@ cudaError_t launch_tree(PFN_cuTensorMapEncodeTiled_v12000 encode, const DecodePa
   TreeMaps maps;
   auto map = [&](CUtensorMap* m, const void* base, cuuint64_t rows, cuuint64_t chunks, cuuint64_t row_bytes,
                  cuuint32_t box_chunks) {
-    const cuuint64_t dims[3] = {64, rows, chunks > 1 ? chunks : 2}, strides[2] = {row_bytes, chunks > 1 ? 128 : kTmaFar};
+    const cuuint64_t far = chunks > 1 ? 0 : tma_far(base, rows * row_bytes);   // (chunks > 1: 128 rows of 1 KiB at least)
+    const cuuint64_t dims[3] = {64, rows, far ? 2 : chunks}, strides[2] = {row_bytes, far ? far : 128};
     const cuuint32_t box[3] = {64, 64, box_chunks}, es[3] = {1, 1, 1};
     return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

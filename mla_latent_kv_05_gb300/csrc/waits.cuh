@@ -49,13 +49,6 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const void* tmap, uin
 }
 }  // namespace ptx
 
-// TMA boxes from a tensor map that spans less than 128 KiB load about three
-// times slower (a 100-row expansion took 30 us, a 128-row one 13 us, and the
-// 100 rows with a wider stride 13 us).  Maps over tensors that may be that
-// small get one more dimension of two entries this many bytes apart; only its
-// entry 0 is ever addressed.
-constexpr uint64_t kTmaFar = uint64_t{1} << 24;
-
 // As wait_bounded<false> (common.cuh): false, with MLA_STATUS_TIMEOUT recorded
 // and the abort flag raised, when the phase did not complete in time; false
 // too once another thread of the grid gave up.  kCluster: acquire at cluster
@@ -82,6 +75,44 @@ __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity, PlanHe
 template <bool kCluster = false>
 __device__ __forceinline__ bool wait_short_warp(uint32_t bar, uint32_t parity, PlanHeader* hdr) {
   return __all_sync(0xffffffffu, wait_short<kCluster>(bar, parity, hdr));
+}
+
+// The same with less code, for kernels whose CTAs do not wait for one another: a
+// wait that gives up tells its own CTA only, through shared memory, and the status
+// is written at the end.  (Thirty waits in line in prefill, whose code must stay in
+// the instruction caches: with 62 KB instead of 52, 64 prompts of up to 512 tokens
+// took 610 us instead of 477.)
+static_assert(MLA_WAIT_TIMEOUT_NS < (1ull << 31), "a difference of 32-bit times");
+__device__ __forceinline__ uint32_t timer32() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool wait_cta(uint32_t bar, uint32_t parity, volatile uint32_t* quit) {
+  uint32_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t n = 1; !ptx::mbar_try_wait(bar, parity); ++n) {
+    if ((n & 1023u) != 0) continue;
+    const uint32_t now = timer32();
+    if (n == 1024u) t0 = now;
+    if (now - t0 > static_cast<uint32_t>(MLA_WAIT_TIMEOUT_NS)) *quit = 1u;
+    if (*quit != 0) return false;
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_cta_warp(uint32_t bar, uint32_t parity, volatile uint32_t* quit) {
+  return __all_sync(0xffffffffu, wait_cta(bar, parity, quit));
+}
+// For what was issued and completes by itself, whether the CTA gave up or not.
+__device__ __forceinline__ void wait_issued(uint32_t bar, uint32_t parity, volatile uint32_t* quit) {
+  const uint32_t t0 = timer32();
+#pragma unroll 1
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (timer32() - t0 > static_cast<uint32_t>(kDrainTimeoutNs)) {
+      *quit = 1u;
+      return;
+    }
+  }
 }
 
 // One lane of a converged warp.  The compiler knows that a branch on it is
