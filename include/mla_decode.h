@@ -472,6 +472,35 @@ int mla_prefill_bf16(const uint16_t* q_nope, const uint16_t* q_rope, const uint1
                      int num_q, int num_k, int num_heads, int causal, float softmax_scale, uint16_t* out, float* lse,
                      void* workspace, size_t workspace_bytes, void* stream);
 
+/* Gradients of mla_prefill_bf16 ("DeepSeek R1 Architecture & Deployment Guide",
+ * section 1.1, the expanded form).  With d_out, the gradient of out, and d_lse,
+ * that of lse (fp32 [num_q, 128], or NULL for none), for query i, key j that it
+ * sees, and head h:
+ *   p     = exp(s_ij - lse_i),   ds = p (d_out_i . v_j - d_out_i . out_i + d_lse_i)
+ *   dq_i  = scale sum_j ds k_j,  dk_j = scale sum_i ds q_i,  dv_j = sum_i p d_out_i
+ * where q, k are the 192 values of both parts, and the RoPE part of dk is summed
+ * over the heads.  p and ds are rounded to bf16 for the products, all sums are
+ * fp32, results rounded to nearest; the order of every sum is fixed, so equal
+ * calls give equal bits.  out and lse are what the forward call gave for the same
+ * inputs, cu_q, cu_k, causal and scale.  A pair outside the mask takes no part,
+ * whatever its rows hold (including NaN); a query that sees no key, and a key that
+ * no query sees, get zeros.  Rows of no sequence are left alone.
+ * Inputs as for mla_prefill_bf16, d_out [num_q, 128, 128] bf16 likewise; gradients
+ * bf16 of the shapes of what they belong to, 16-byte aligned.  strides (host
+ * memory, values, positive multiples of 8): the nine of mla_prefill_bf16; token and
+ * head stride of d_out; then the same nine for dq_nope, dq_rope, dk_nope, dk_rope,
+ * dv.  out and lse are contiguous.  Gradients overlap neither inputs nor one
+ * another.  Limits and device status as for mla_prefill_bf16.
+ * workspace: mla_workspace_size_prefill_backward(...) bytes, zeroed before its
+ * first use, 256-byte aligned, not shared with a call that may run concurrently. */
+int mla_workspace_size_prefill_backward(int batch, int num_q, int num_k, size_t* bytes);
+int mla_prefill_backward_bf16(const uint16_t* d_out, const float* d_lse, const uint16_t* q_nope, const uint16_t* q_rope,
+                              const uint16_t* k_nope, const uint16_t* k_rope, const uint16_t* v, const uint16_t* out,
+                              const float* lse, const size_t* strides, const int32_t* cu_q, const int32_t* cu_k,
+                              int batch, int num_q, int num_k, int num_heads, int causal, float softmax_scale,
+                              uint16_t* dq_nope, uint16_t* dq_rope, uint16_t* dk_nope, uint16_t* dk_rope, uint16_t* dv,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* Up-projection of latent attention outputs through W^UV ("DeepSeek R1
  * Architecture & Deployment Guide", section 1.1: the value up-projection is
  * folded out of the attention, which returns the 512-value latent output

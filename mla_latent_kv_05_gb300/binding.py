@@ -66,6 +66,9 @@ SIGNATURES = {
     "mla_workspace_size_prefill": (_I, [_I, _I, ctypes.POINTER(_Z)]),
     "mla_prefill_bf16": (_I, [_P, _P, _P, _P, _P, ctypes.POINTER(_Z), _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P,
                               _P, _P, _Z, _P]),
+    "mla_workspace_size_prefill_backward": (_I, [_I, _I, _I, ctypes.POINTER(_Z)]),
+    "mla_prefill_backward_bf16": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(_Z), _P, _P, _I, _I, _I, _I, _I,
+                                       ctypes.c_float, _P, _P, _P, _P, _P, _P, _Z, _P]),
     "mla_combine_splits": (_I, [_P, _P, _P, _I, _I, _P, _P, _P]),
     "mla_get_status": (_I, [_P, _P]),
     "mla_profile_next_decode": (_I, [_P, _P]),
@@ -937,6 +940,86 @@ def mla_prefill_bf16(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, scale, causa
     if rc != MLA_OK:
         raise MLAError(rc, "mla_prefill_bf16")
     return out, lse
+
+
+_BackwardStrides = ctypes.c_size_t * 20
+
+
+def mla_workspace_size_prefill_backward(batch: int, num_q: int, num_k: int) -> int:
+    n = ctypes.c_size_t(0)
+    rc = load().mla_workspace_size_prefill_backward(int(batch), int(num_q), int(num_k), ctypes.byref(n))
+    if rc != MLA_OK:
+        raise MLAError(rc, "mla_workspace_size_prefill_backward")
+    return int(n.value)
+
+
+def alloc_workspace_prefill_backward(batch: int, num_q: int, num_k: int, device=None) -> torch.Tensor:
+    """A zeroed workspace buffer (uint8) for the gradients of a prefill of
+    `batch` sequences with `num_q` queries and `num_k` keys together."""
+    return torch.zeros(mla_workspace_size_prefill_backward(batch, num_q, num_k), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def mla_prefill_backward_bf16(d_out, q_nope, q_rope, k_nope, k_rope, v, out, lse, cu_q, cu_k, scale, causal=True,
+                              d_lse=None, dq_nope=None, dq_rope=None, dk_nope=None, dk_rope=None, dv=None,
+                              workspace=None, stream=None):
+    """Gradients of mla_prefill_bf16: d_out [nq, 128, 128] bf16 (a view as the
+    inputs may be) and d_lse [nq, 128] fp32 (None: zero) are the gradients of out
+    and lse; the other inputs, cu_q, cu_k, scale and causal are the forward call's,
+    out and lse its results.  Returns (dq_nope, dq_rope, dk_nope, dk_rope, dv) bf16,
+    new tensors where none is given (given ones may be views with 16-byte strides,
+    such as two parts of one [nq, 128, 192]); rows of no sequence are left as they
+    were.  dk_rope is summed over the heads.  Equal calls give equal bits."""
+    qn = _heads_arg(q_nope, "q_nope", 128)
+    nq = q_nope.shape[0]
+    qr = _heads_arg(q_rope, "q_rope", 64, nq)
+    do = _heads_arg(d_out, "d_out", 128, nq)
+    kn = _heads_arg(k_nope, "k_nope", 128)
+    nk = k_nope.shape[0]
+    kr = _rows_arg(k_rope, "k_rope", 64, nk)
+    vv = _heads_arg(v, "v", 128, nk)
+    _check(out, "out", torch.bfloat16, (nq, 128, 128))
+    _check(lse, "lse", torch.float32, (nq, 128))
+    if d_lse is not None:
+        _check(d_lse, "d_lse", torch.float32, (nq, 128))
+    _check(cu_q, "cu_q", torch.int32)
+    if cu_q.dim() != 1 or cu_q.numel() < 1:
+        raise ValueError("cu_q must be [B + 1]")
+    B = cu_q.numel() - 1
+    _check(cu_k, "cu_k", torch.int32, (B + 1,))
+
+    def new(*shape):
+        return _new(stream, torch.empty, shape, dtype=torch.bfloat16, device=q_nope.device)
+
+    dq_nope = new(nq, 128, 128) if dq_nope is None else dq_nope
+    dq_rope = new(nq, 128, 64) if dq_rope is None else dq_rope
+    dk_nope = new(nk, 128, 128) if dk_nope is None else dk_nope
+    dk_rope = new(nk, 64) if dk_rope is None else dk_rope
+    dv = new(nk, 128, 128) if dv is None else dv
+    gqn = _heads_arg(dq_nope, "dq_nope", 128, nq)
+    gqr = _heads_arg(dq_rope, "dq_rope", 64, nq)
+    gkn = _heads_arg(dk_nope, "dk_nope", 128, nk)
+    gkr = _rows_arg(dk_rope, "dk_rope", 64, nk)
+    gv = _heads_arg(dv, "dv", 128, nk)
+    if workspace is None:
+        workspace = _new(stream, alloc_workspace_prefill_backward, B, nq, nk, q_nope.device)
+    _check(workspace, "workspace", torch.uint8)
+    dev = torch.cuda.current_device()
+    tensors = dict(d_out=d_out, d_lse=d_lse, q_nope=q_nope, q_rope=q_rope, k_nope=k_nope, k_rope=k_rope, v=v, out=out,
+                   lse=lse, cu_q=cu_q, cu_k=cu_k, dq_nope=dq_nope, dq_rope=dq_rope, dk_nope=dk_nope, dk_rope=dk_rope,
+                   dv=dv, workspace=workspace)
+    _same_device(tensors, dev)
+    if nq == 0 and nk == 0:
+        return dq_nope, dq_rope, dk_nope, dk_rope, dv
+    strides = _BackwardStrides(qn[1], qn[2], qr[1], qr[2], kn[1], kn[2], kr[1], vv[1], vv[2], do[1], do[2], gqn[1], gqn[2],
+                               gqr[1], gqr[2], gkn[1], gkn[2], gkr[1], gv[1], gv[2])
+    rc = load().mla_prefill_backward_bf16(
+        do[0], None if d_lse is None else d_lse.data_ptr(), qn[0], qr[0], kn[0], kr[0], vv[0], out.data_ptr(),
+        lse.data_ptr(), strides, cu_q.data_ptr(), cu_k.data_ptr(), B, nq, nk, 128, 1 if causal else 0, float(scale),
+        gqn[0], gqr[0], gkn[0], gkr[0], gv[0], workspace.data_ptr(), workspace.numel(), _handle(stream, dev))
+    if rc != MLA_OK:
+        raise MLAError(rc, "mla_prefill_backward_bf16")
+    return dq_nope, dq_rope, dk_nope, dk_rope, dv
 
 
 def mla_combine_splits(partial_out, partial_lse, split_indptr, out=None, lse=None, stream=None):

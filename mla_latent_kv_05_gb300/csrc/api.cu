@@ -10,6 +10,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "backward.cuh"
 #include "decode.cuh"
 #include "expand.cuh"
 #include "prefill.cuh"
@@ -720,6 +721,72 @@ int mla_prefill_bf16(const uint16_t* q_nope, const uint16_t* q_rope, const uint1
   p.lse = lse;
   p.ws = static_cast<uint8_t*>(workspace);
   return launch_prefill(fn, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_workspace_size_prefill_backward(int batch, int num_q, int num_k, size_t* bytes) {
+  if (!bytes || batch < 0 || num_q < 0 || num_k < 0) return MLA_ERR_INVALID_ARG;
+  if (batch > kMaxRows || num_q > kMaxPrefillRows || num_k > kMaxPrefillRows) return MLA_ERR_UNSUPPORTED;
+  *bytes = backward_ws(batch, num_q, num_k).total;
+  return MLA_OK;
+}
+
+int mla_prefill_backward_bf16(const uint16_t* d_out, const float* d_lse, const uint16_t* q_nope, const uint16_t* q_rope,
+                              const uint16_t* k_nope, const uint16_t* k_rope, const uint16_t* v, const uint16_t* out,
+                              const float* lse, const size_t* strides, const int32_t* cu_q, const int32_t* cu_k,
+                              int batch, int num_q, int num_k, int num_heads, int causal, float softmax_scale,
+                              uint16_t* dq_nope, uint16_t* dq_rope, uint16_t* dk_nope, uint16_t* dk_rope, uint16_t* dv,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  if (!strides || !cu_q || !cu_k || !workspace) return MLA_ERR_INVALID_ARG;
+  if (batch < 0 || num_q < 0 || num_k < 0 || !std::isfinite(softmax_scale) || !(softmax_scale > 0.f))
+    return MLA_ERR_INVALID_ARG;
+  if (num_q > 0 && (!d_out || !q_nope || !q_rope || !out || !lse || !dq_nope || !dq_rope)) return MLA_ERR_INVALID_ARG;
+  if (num_k > 0 && (!k_nope || !k_rope || !v || !dk_nope || !dk_rope || !dv)) return MLA_ERR_INVALID_ARG;
+  if (num_heads != kHeads) return MLA_ERR_UNSUPPORTED;
+  if (batch > kMaxRows || num_q > kMaxPrefillRows || num_k > kMaxPrefillRows) return MLA_ERR_UNSUPPORTED;
+  for (int i = 0; i < 20; ++i)
+    if (!stride_ok(strides[i])) return MLA_ERR_INVALID_ARG;
+  for (const void* ptr : {static_cast<const void*>(d_out), static_cast<const void*>(q_nope), static_cast<const void*>(q_rope),
+                          static_cast<const void*>(k_nope), static_cast<const void*>(k_rope), static_cast<const void*>(v),
+                          static_cast<const void*>(out), static_cast<const void*>(dq_nope), static_cast<const void*>(dq_rope),
+                          static_cast<const void*>(dk_nope), static_cast<const void*>(dk_rope), static_cast<const void*>(dv)})
+    if (!aligned(ptr, 16)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_lse, 4) || !aligned(lse, 4) || !aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(workspace, 256))
+    return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < backward_ws(batch, num_q, num_k).total) return MLA_ERR_WORKSPACE;
+  if (batch == 0 || (num_q == 0 && num_k == 0)) return MLA_OK;
+  auto fn = encode_fn();
+  const int sms = sm_count();
+  if (!fn || sms <= 0) return MLA_ERR_CUDA;
+  BackwardParams p;
+  // with no query or no key nothing is read through those pointers; the maps need valid addresses all the same
+  const uint16_t* any = num_q > 0 ? q_nope : k_nope;
+  auto in = [&](const uint16_t* ptr, int n) { return reinterpret_cast<const __nv_bfloat16*>(n > 0 ? ptr : any); };
+  p.d_out = in(d_out, num_q);
+  p.q_nope = in(q_nope, num_q);
+  p.q_rope = in(q_rope, num_q);
+  p.k_nope = in(k_nope, num_k);
+  p.k_rope = in(k_rope, num_k);
+  p.v = in(v, num_k);
+  p.out = in(out, num_q);
+  p.d_lse = d_lse;
+  p.lse = lse;
+  long long* s[20] = {&p.qn_t, &p.qn_h, &p.qr_t, &p.qr_h, &p.kn_t, &p.kn_h, &p.kr_t, &p.v_t, &p.v_h, &p.do_t, &p.do_h,
+                      &p.dqn_t, &p.dqn_h, &p.dqr_t, &p.dqr_h, &p.dkn_t, &p.dkn_h, &p.dkr_t, &p.dv_t, &p.dv_h};
+  for (int i = 0; i < 20; ++i) *s[i] = static_cast<long long>(strides[i]);
+  p.cu_q = cu_q;
+  p.cu_k = cu_k;
+  p.batch = batch;
+  p.nq = num_q;
+  p.nk = num_k;
+  p.causal = causal != 0;
+  p.scale = softmax_scale;
+  p.dq_nope = reinterpret_cast<__nv_bfloat16*>(dq_nope);
+  p.dq_rope = reinterpret_cast<__nv_bfloat16*>(dq_rope);
+  p.dk_nope = reinterpret_cast<__nv_bfloat16*>(dk_nope);
+  p.dk_rope = reinterpret_cast<__nv_bfloat16*>(dk_rope);
+  p.dv = reinterpret_cast<__nv_bfloat16*>(dv);
+  p.ws = static_cast<uint8_t*>(workspace);
+  return launch_backward(fn, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 int mla_workspace_size_sparse(int batch, int sq, int topk, int num_heads, int page_size, size_t* bytes) {

@@ -1,0 +1,55 @@
+// Backward pass of the expanded-form (prefill) attention: parameters, workspace
+// and launcher.
+#pragma once
+#include "prefill.cuh"
+
+namespace mla {
+
+constexpr int kBackwardTile = 128;   // rows and columns of a step's tile of scores
+constexpr int kMaxRopeGroup = 8;     // heads whose key-RoPE gradients are summed in one work item, at most
+
+struct BackwardParams {
+  const __nv_bfloat16 *d_out, *q_nope, *q_rope, *k_nope, *k_rope, *v, *out;
+  const float *d_lse, *lse;     // d_lse may be null
+  long long do_t, do_h, qn_t, qn_h, qr_t, qr_h, kn_t, kn_h, kr_t, v_t, v_h;
+  const int32_t *cu_q, *cu_k;
+  int batch, nq, nk, causal;
+  float scale;
+  __nv_bfloat16 *dq_nope, *dq_rope, *dk_nope, *dk_rope, *dv;
+  long long dqn_t, dqn_h, dqr_t, dqr_h, dkn_t, dkn_h, dkr_t, dv_t, dv_h;
+  uint8_t* ws;
+};
+
+// Behind the plan header.
+struct BackwardPlan {
+  int tiles[2], next[2], tail[2];   // [0] key tiles, [1] query tiles
+};
+
+// Workspace: header and plan; the first query tile of each sequence; the key tiles
+// and the query tiles; per query tile and head 128 values lse log2(e) and 128 values
+// of sum(d_out out) - d_lse; the key-RoPE gradients of `group` heads each, fp32.
+struct BackwardWs {
+  size_t plan, base, tiles[2], stats, rope, total;
+  int max_tiles[2], group;
+};
+__host__ __device__ inline BackwardWs backward_ws(int batch, int nq, int nk) {
+  BackwardWs w;
+  // every sequence ends at most one tile early
+  w.max_tiles[0] = nk / kBackwardTile + (batch < nk ? batch : nk);
+  w.max_tiles[1] = nq / kBackwardTile + (batch < nq ? batch : nq);
+  w.group = kMaxRopeGroup;
+  while (w.group > 1 && static_cast<long long>(w.max_tiles[0]) * kHeads / w.group < 8 * 152) w.group /= 2;
+  w.plan = align256(sizeof(PlanHeader));
+  w.base = align256(w.plan + sizeof(BackwardPlan));
+  w.tiles[0] = align256(w.base + sizeof(int) * static_cast<size_t>(batch));
+  w.tiles[1] = align256(w.tiles[0] + 32 * static_cast<size_t>(w.max_tiles[0]));
+  w.stats = align256(w.tiles[1] + 32 * static_cast<size_t>(w.max_tiles[1]));
+  w.rope = align256(w.stats + sizeof(float) * 2 * kBackwardTile * kHeads * static_cast<size_t>(w.max_tiles[1]));
+  w.total = align256(w.rope + sizeof(float) * kDr * (kHeads / w.group) * static_cast<size_t>(nk));
+  return w;
+}
+
+cudaError_t launch_backward(PFN_cuTensorMapEncodeTiled_v12000 encode, const BackwardParams& p, int sms,
+                            cudaStream_t stream);
+
+}  // namespace mla

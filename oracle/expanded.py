@@ -53,6 +53,23 @@ def prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, scale, causal, heads)
     return out, lse, mag
 
 
+def attend_backward(q, k, v, see, scale, out, lse, d_out, d_lse=None):
+    """Gradients of one head's `attend` by the softmax's derivative, from its results
+    out [n, e], lse [n] and their gradients d_out, d_lse (None: zero) -> dq [n, d],
+    dk [m, d], dv [m, e].  Pairs that are not seen take no part."""
+    dq, dk, dv = np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)
+    for i in range(q.shape[0]):
+        j = np.nonzero(see[i])[0]
+        if j.size == 0:
+            continue
+        p = np.exp(scale * (k[j] @ q[i]) - lse[i])
+        g = p * (v[j] @ d_out[i] - out[i] @ d_out[i] + (0.0 if d_lse is None else d_lse[i])) * scale
+        dq[i] = g @ k[j]
+        dk[j] += np.outer(g, q[i])
+        dv[j] += np.outer(p, d_out[i])
+    return dq, dk, dv
+
+
 def tree_sees(parents, n_nodes: int, i: int, ctx: int):
     """Token positions node i of a drafted tree sees: the context [0, ctx),
     itself, and its ancestors (node a is token ctx + a)."""
