@@ -25,31 +25,45 @@
 // shared-memory tile, read along the other axis (MN-major).
 //   tensor memory (512 columns): ACC1 192 | ACC2 128 | X 128 | Y 64.  Keys: X holds
 //       S, then dP; Y holds P, then dS.  Queries: S is in X, dP in ACC2's place.
-//   shared memory: R1 48 KiB, R2 32, two C1 tiles, one C2 tile.
-//   warp 0: work items and TMA loads; warp 1 issues S and dP, warp 2 the second
-//   products; warps 4..11 compute P and dS (thread = half a row) and write the
-//   results.  S of the next step runs while dS of this one is computed, and the
-//   second products of this one while the next one's P is.
+//   shared memory: R1 48 KiB, R2 32, two C1 tiles, one C2 tile, two query tiles' lse
+//   and delta.
+//   warp 0: work items, R1 and R2; warps 3 to 5 a chunk of C1 each and warp 6 C2 (a copy
+//   costs its thread 160 cycles to issue), each chunk with its own barrier, warp 7 the
+//   statistics; warp 1 issues S and dP, warp 2 the second products; warps 8..23 compute
+//   P and dS (thread = a quarter row of 32 columns) and write the results.  S of the
+//   next step runs while dS of this one is computed, and the second products of this
+//   one while the next one's P is.
+// Long sequences' query pass runs on CTA pairs instead (backward_pair.cu).
+//
+// Measured (4096 causal tokens, 1.79 TFLOP of the five products, 952 us at the peak):
+// 1,598 us, 1,120 TFLOP/s; 3 x 777 full 595 (a floor of 205), 8 x up to 1024 613 (162),
+// 2 x 512 queries over 8,012 keys 1,676 (900), 5 x up to 33 66.7.  The key pass takes 940
+// of the first, of 599 that its MMAs need: S, its reading, dP and its reading follow one
+// another in one place of tensor memory, and S's MMAs find shared memory busy with the
+// copies (1,150 cycles of 768).  Tried for it and slower: two sets of eight warps on
+// alternate steps (2,110), streamed tiles multicast to clusters of two (1,830 instead of
+// 1,765), reading S and dP together (1,836 instead of 1,770), one warp that issues all
+// products (1,672 instead of 1,605).
 //
 // Every wait is bounded, as in prefill.cu.
-#include <climits>
+#include <cmath>
 
-#include "backward.cuh"
+#include "backward_tile.cuh"
 
 namespace mla {
 
 namespace {
 
-constexpr int kTile = kBackwardTile;
-constexpr int kThreads = 384;
-constexpr uint32_t kChunk = kTile * 128u;          // 16 KiB: 128 rows x 64 values
+using namespace bwd;
+
+constexpr int kHelpers = 8;                            // warps that load and issue
+constexpr int kThreads = 32 * (kHelpers + kWarps);
 constexpr uint32_t kOffR1 = 0, kOffR2 = 3 * kChunk, kOffC1 = 5 * kChunk, kOffC2 = 11 * kChunk, kOffStats = 13 * kChunk;
-constexpr uint32_t kStatBytes = 2 * kTile * 4;     // lse and delta of a query tile
 constexpr uint32_t kOffBar = kOffStats + 2 * kStatBytes;
 constexpr int kItemSlots = 2;
 enum Bar {
-  R1FULL, R1EMPTY, R2FULL, R2EMPTY, C1FULL, C1EMPTY = C1FULL + 2, C2FULL = C1EMPTY + 2, C2EMPTY, SFULL, SREAD, DPFULL,
-  DPREAD, PREADY, PDONE, DSREADY, DSDONE, ACCFREE, IFULL, IEMPTY = IFULL + kItemSlots, DRAIN = IEMPTY + kItemSlots,
+  R1FULL, R1EMPTY, R2FULL, R2EMPTY, C1FULL, C1EMPTY = C1FULL + 6, C2FULL = C1EMPTY + 2, C2EMPTY = C2FULL + 2, SFULL, SREAD, DPFULL,
+  DPREAD, PREADY, PDONE, DSREADY, DSDONE, ACCFREE, STATFULL, IFULL = STATFULL + 2, IEMPTY = IFULL + kItemSlots, DRAIN = IEMPTY + kItemSlots,
   NBAR = DRAIN + 2
 };
 constexpr uint32_t kOffTmem = kOffBar + 8 * NBAR;
@@ -58,23 +72,9 @@ constexpr uint32_t kOffItems = (kOffQuit + 4 + 15) & ~15u;
 constexpr uint32_t kSmem = kOffItems + 48 * kItemSlots;
 static_assert(kSmem <= 232448, "shared memory budget");
 
-constexpr uint32_t kAcc1 = 0, kAcc2 = 192, kX = 320, kY = 448;   // tensor memory columns
 constexpr uint32_t kIdescS = ptx::idesc_bf16(128, 128, 0, 0);    // both K-major
 constexpr uint32_t kIdesc192 = ptx::idesc_bf16(128, 192, 0, 1), kIdesc128 = ptx::idesc_bf16(128, 128, 0, 1),
                    kIdesc64 = ptx::idesc_bf16(128, 64, 0, 1);    // A in tensor memory, B MN-major
-constexpr float kLog2e = 1.4426950408889634f;
-
-// A tile of rows: keys (key pass) or queries (query pass).
-struct Tile {
-  int r0, rows;   // first packed row, rows (1..128)
-  int c0, nc;     // first packed column of the sequence, its columns
-  int lim;        // row r sees the columns from lim + r (keys), or those below lim + r (queries), where causal
-  int first;      // first column tile
-  int steps;      // column tiles
-  int stat;       // query tile number of column tile 0 (keys), or of the tile itself (queries)
-};
-static_assert(sizeof(Tile) == 32, "tile record");
-
 // ---------------------------------------------------------------- plan
 // One CTA: the sequences' first query tiles, and the lists of key tiles and of
 // query tiles, those with most steps first (counting sort; every tile is computed
@@ -82,12 +82,13 @@ static_assert(sizeof(Tile) == 32, "tile record");
 constexpr int kClasses = 1024;
 constexpr int kTailItems = 5;   // items per CTA of the heads that are taken together at the end
 
-__global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParams p, const BackwardWs L, int ctas_k, int ctas_q) {
+__global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParams p, const BackwardWs L, int ctas_k, int ctas_q, int query_rows) {
   __shared__ int s_count[kClasses], s_warp[32], s_longest, s_shortest;
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws);
   BackwardPlan* plan = reinterpret_cast<BackwardPlan*>(p.ws + L.plan);
   int* base = reinterpret_cast<int*>(p.ws + L.base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  ptx::grid_dep_launch();   // (what follows waits for this grid before it reads the plan)
   // inclusive sum over the CTA
   auto scan = [&](int v) {
 #pragma unroll
@@ -134,11 +135,11 @@ __global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParam
       for (int b = warp; b < p.batch; b += 32) {
         const Seq s = sequence(b);
         if (!s.ok) continue;
-        const int n = side ? s.nq : s.nk, off = s.nk - s.nq;
-        for (int i = lane; i * kTile < n; i += 32) {
+        const int n = side ? s.nq : s.nk, rows = side ? query_rows : kTile, off = s.nk - s.nq;
+        for (int i = lane; i * rows < n; i += 32) {
           Tile t;
-          const int at = i * kTile;
-          t.rows = min(kTile, n - at);
+          const int at = i * rows;
+          t.rows = min(rows, n - at);
           t.first = 0;
           if (side == 0) {
             t.r0 = s.k0 + at;
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParam
             t.lim = at + off + 1;
             const int sees = p.causal ? max(0, min(s.nk, t.lim + t.rows - 1)) : s.nk;   // its last row
             t.steps = (sees + kTile - 1) / kTile;
-            t.stat = base[b] + i;
+            t.stat = base[b] + at / kTile;
           }
           const int steps = min(kClasses - 1, t.steps), c = kClasses - 1 - steps;
           if (pass == 0) {
@@ -197,56 +198,76 @@ __global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParam
 }
 
 // ---------------------------------------------------------------- delta
-// lse log2(e) and sum(d_out out) - d_lse per query tile and head, 8 heads a CTA.
-__global__ void __launch_bounds__(256) backward_delta_kernel(const BackwardParams p, const BackwardWs L) {
-  __shared__ float s_delta[8][kTile];
+// lse log2(e) and sum(d_out out) - d_lse per query tile and head: 32 rows and 8 heads a
+// CTA, 16 threads a row and head, whose loads are all in flight together.
+constexpr int kDeltaRows = 32;
+
+__global__ void __launch_bounds__(256) backward_delta_kernel(const BackwardParams p, const BackwardWs L, int query_rows) {
+  __shared__ float s_delta[8][kDeltaRows];
   const BackwardPlan* plan = reinterpret_cast<const BackwardPlan*>(p.ws + L.plan);
-  if (static_cast<int>(blockIdx.x) >= plan->tiles[1]) return;
-  const Tile t = reinterpret_cast<const Tile*>(p.ws + L.tiles[1])[blockIdx.x];
-  const int h0 = 8 * blockIdx.y, lane16 = threadIdx.x & 15;
-#pragma unroll 4
-  for (int i = threadIdx.x >> 4; i < 8 * kTile; i += 16) {
-    const int r = i >> 3, h = i & 7;
-    float sum = 0.f;
-    if (r < t.rows) {
-      const size_t row = static_cast<size_t>(t.r0) + r;
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.d_out + row * p.do_t + (h0 + h) * p.do_h) + lane16);
-      const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.out + (row * kHeads + h0 + h) * 128) + lane16);
-      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  const int parts = query_rows / kDeltaRows, i_tile = static_cast<int>(blockIdx.x) / parts, part = static_cast<int>(blockIdx.x) % parts;
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  if (i_tile >= *reinterpret_cast<const volatile int*>(&plan->tiles[1])) return;
+  const Tile t = reinterpret_cast<const Tile*>(p.ws + L.tiles[1])[i_tile];
+  // (a stat tile is 128 rows: those past the sequence's end get zeros)
+  const int r0 = part * kDeltaRows;
+  if ((t.rows + kTile - 1) / kTile * kTile <= r0) return;
+  const int h0 = 8 * blockIdx.y, lane16 = threadIdx.x & 15, first = threadIdx.x >> 4;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint4 a[8], b[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = first + 16 * (8 * half + k), r = r0 + (i >> 3), h = h0 + (i & 7);
+      a[k] = b[k] = make_uint4(0, 0, 0, 0);
+      if (r < t.rows) {
+        const size_t row = static_cast<size_t>(t.r0) + r;
+        a[k] = __ldg(reinterpret_cast<const uint4*>(p.d_out + row * p.do_t + h * p.do_h) + lane16);
+        b[k] = __ldg(reinterpret_cast<const uint4*>(p.out + (row * kHeads + h) * 128) + lane16);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t x[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, y[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+      float sum = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         sum += __uint_as_float(x[e] << 16) * __uint_as_float(y[e] << 16);
         sum += __uint_as_float(x[e] & 0xFFFF0000u) * __uint_as_float(y[e] & 0xFFFF0000u);
       }
-    }
 #pragma unroll
-    for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane16 == 0) s_delta[h][r] = sum;
+      for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const int i = first + 16 * (8 * half + k);
+      if (lane16 == 0) s_delta[i & 7][i >> 3] = sum;
+    }
   }
   __syncthreads();
-  float* stats = reinterpret_cast<float*>(p.ws + L.stats) + (static_cast<size_t>(t.stat) * kHeads + h0) * 2 * kTile;
-  for (int i = threadIdx.x; i < 8 * kTile; i += 256) {
-    const int h = i / kTile, r = i % kTile;
-    float l = 0.f, d = 0.f;
-    if (r < t.rows) {
-      const size_t at = (static_cast<size_t>(t.r0) + r) * kHeads + h0 + h;
-      l = __ldg(p.lse + at) * kLog2e;
-      d = s_delta[h][r] - (p.d_lse ? __ldg(p.d_lse + at) : 0.f);
-    }
-    stats[h * 2 * kTile + r] = l;
-    stats[h * 2 * kTile + kTile + r] = d;
+  const int h = threadIdx.x / kDeltaRows, r = threadIdx.x % kDeltaRows;
+  float* stats = reinterpret_cast<float*>(p.ws + L.stats) +
+                 (static_cast<size_t>(t.stat + r0 / kTile) * kHeads + h0 + h) * 2 * kTile + r0 % kTile + r;
+  float l = 0.f, d = 0.f;
+  if (r0 + r < t.rows) {
+    const size_t at = (static_cast<size_t>(t.r0) + r0 + r) * kHeads + h0 + h;
+    l = __ldg(p.lse + at) * kLog2e;
+    d = s_delta[h][r] - (p.d_lse ? __ldg(p.d_lse + at) : 0.f);
   }
+  stats[0] = l;
+  stats[kTile] = d;
 }
 
 // ---------------------------------------------------------------- the two passes
-struct Maps {
-  CUtensorMap qn, qr, kn, kr, v, d_out;
-};
+// (Without a cache hint, with which concurrent copies of all SMs reached 110 GB/s an SM
+// instead of 190.)
+__device__ __forceinline__ void load_4d(uint32_t dst, const void* tmap, uint32_t bar, int x, int row, int chunk, int head) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+               :: "r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(row), "r"(chunk), "r"(head) : "memory");
+}
 
 // kKeys: rows are keys (dk, dv), else queries (dq).
 template <bool kKeys>
 __global__ void __launch_bounds__(kThreads, 1)
-backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ BackwardParams p, const BackwardWs L) {
+backward_kernel(const __grid_constant__ PassMaps maps, const __grid_constant__ BackwardParams p, const BackwardWs L) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = ptx::smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -261,9 +282,10 @@ backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Backw
     *quit = 0;
     for (int i = 0; i < NBAR; ++i) {
       int n = 1;                                   // copies, MMA commits
-      if (i == SREAD || i == DPREAD || i == PREADY || i == DSREADY || i == ACCFREE) n = 8;   // one arrival a warp
+      if (i == SREAD || i == DPREAD || i == PREADY || i == DSREADY || i == ACCFREE) n = kWarps;   // one arrival a warp
+      // (roles that walk the items: the C copies, the two that issue)
       if (i == C2EMPTY && kKeys) n = 2;            // dP and dv
-      if (i >= IEMPTY && i < IEMPTY + kItemSlots) n = 10;
+      if (i >= IEMPTY && i < IEMPTY + kItemSlots) n = kWarps + (kKeys ? 7 : 6);
       ptx::mbar_init(BAR(i), n);
     }
     ptx::fence_barrier_init();
@@ -276,6 +298,7 @@ backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Backw
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem), 0);
+  begin_pass<kKeys>(p);
   const bool smem_ok = (sbase & 1023u) == 0;
   if (threadIdx.x == 0 && !smem_ok) set_status(&hdr->status, MLA_ERR_UNSUPPORTED);
   const int causal = p.causal;
@@ -284,113 +307,137 @@ backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Backw
   // The next item of this role's walk: its tile and first head, false when there is none.
   auto next_warp = [&](Walk& w, Tile& t, int& head) {
     if (!wait_cta_warp(BAR(IFULL + w.slot), w.phase, quit)) return false;
-    const volatile int* src = reinterpret_cast<const volatile int*>(smem + kOffItems + 48 * w.slot);
-    t.r0 = src[0]; t.rows = src[1]; t.c0 = src[2]; t.nc = src[3]; t.lim = src[4]; t.first = src[5]; t.steps = src[6];
-    t.stat = src[7];
-    head = src[8];
+    read_item(smem + kOffItems + 48 * w.slot, t, head);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(BAR(IEMPTY + w.slot));
     if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
     return head >= 0;
   };
 
+  // A role's walk over the steps of all items: f(tile, head, step of the head, number
+  // of the step so far) is false when a wait gave up.  Returns the number of steps.
+  auto walk_steps = [&](auto f) {
+    Walk w;
+    Tile t;
+    int head0;
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && next_warp(w, t, head0)) {
+      for (int g = 0; g < group && ok; ++g)
+        for (int i = 0; i < t.steps && ok; ++i) {
+          ok = f(t, head0 + g, i, n);
+          if (ok) ++n;
+        }
+    }
+    return n;
+  };
+
   if (smem_ok && warp == 0) {
-    // ------------------------------------------------------------ items and TMA loads
-    if (lane == 0) {
-      const uint64_t pol = ptx::policy_evict_normal();
+    // ------------------------------------------------------------ items, and the loads of R1 and R2
+    regs_issue();
+    if (elect_one()) {
       const Tile* tiles = reinterpret_cast<const Tile*>(p.ws + L.tiles[kSide]);
-      const int n_tiles = *reinterpret_cast<const volatile int*>(&plan->tiles[kSide]);
-      const int tail = *reinterpret_cast<const volatile int*>(&plan->tail[kSide]);
-      const int items = n_tiles * groups, first_late = items - n_tiles * tail;
-      const float* stats = reinterpret_cast<const float*>(p.ws + L.stats);
+      const Schedule sched(plan, kSide, groups);
       Walk w;
-      uint32_t n = 0, n2 = 0;                  // C1 and C2 tiles queued so far
-      uint32_t loads = 0, loads2 = 0;          // R1 and R2 tiles
+      uint32_t loads = 0, loads2 = 0;
       bool ok = true;
-      // 192 values of 128 rows: queries, or keys with the shared RoPE part
-      auto load_qk = [&](uint32_t dst, int bar, bool keys, int head, int row) {
-        const CUtensorMap* nope = keys ? &maps.kn : &maps.qn;
-        ptx::tma_load_4d(dst, nope, BAR(bar), 0, head, row, 0, pol);
-        ptx::tma_load_4d(dst + kChunk, nope, BAR(bar), 64, head, row, 0, pol);
-        ptx::tma_load_4d(dst + 2 * kChunk, keys ? &maps.kr : &maps.qr, BAR(bar), 0, keys ? 0 : head, row, 0, pol);
-      };
-      auto load_vo = [&](uint32_t dst, int bar, bool keys, int head, int row) {
-        const CUtensorMap* m = keys ? &maps.v : &maps.d_out;
-        ptx::tma_load_4d(dst, m, BAR(bar), 0, head, row, 0, pol);
-        ptx::tma_load_4d(dst + kChunk, m, BAR(bar), 64, head, row, 0, pol);
-      };
       int item = static_cast<int>(blockIdx.x);
       while (ok) {
-        // head by head, and the last heads tile by tile (as in prefill)
         Tile t = {0, 0, 0, 0, 0, 0, 0, 0};
-        int head0 = -1;
-        if (item < items) {
-          const bool late = item >= first_late;
-          const int left = late ? item - first_late : item, by = late ? tail : n_tiles;
-          const int q = left / by, r = left - q * by;
-          t = tiles[late ? q : r];
-          head0 = (late ? groups - tail + r : q) * group;
+        int tile, head0 = -1;
+        if (sched.find(item, tile, head0)) {
+          t = read_tile(tiles + tile);
+          head0 *= group;
         }
         ok = wait_cta(BAR(IEMPTY + w.slot), w.phase ^ 1u, quit);
         if (!ok) break;
-        volatile int* dst = reinterpret_cast<volatile int*>(smem + kOffItems + 48 * w.slot);
-        dst[0] = t.r0; dst[1] = t.rows; dst[2] = t.c0; dst[3] = t.nc; dst[4] = t.lim; dst[5] = t.first; dst[6] = t.steps;
-        dst[7] = t.stat;
-        dst[8] = head0;
+        write_item(smem + kOffItems + 48 * w.slot, t, head0);
         ptx::mbar_arrive(BAR(IFULL + w.slot));
         if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
         if (head0 < 0) break;
-        const int total = group * t.steps;
-        for (int g = 0; g < group && ok; ++g) {
+        for (int g = 0; g < group && t.steps > 0 && ok; ++g) {
           const int head = head0 + g;
-          for (int i = 0; i < t.steps && ok; ++i) {
-            if (g * t.steps + i == max(total - 2, 0)) item = atomicAdd(&plan->next[kSide], 1);
-            if (i == 0) {
-              ok = wait_cta(BAR(R1EMPTY), (loads & 1u) ^ 1u, quit);
-              if (!ok) break;
-              ++loads;
-              ptx::mbar_arrive_expect_tx(BAR(R1FULL), 3 * kChunk);
-              load_qk(sbase + kOffR1, R1FULL, kKeys, head, t.r0);
-            }
-            const int col = t.c0 + (t.first + i) * kTile;
-            const uint32_t buf = n & 1u;
-            ok = wait_cta(BAR(C1EMPTY + buf), ((n >> 1) & 1u) ^ 1u, quit);
-            if (ok) {
-              ptx::mbar_arrive_expect_tx(BAR(C1FULL + buf), 3 * kChunk + (kKeys ? kStatBytes : 0u));
-              load_qk(sbase + kOffC1 + buf * 3 * kChunk, C1FULL + buf, !kKeys, head, col);
-              if constexpr (kKeys)
-                ptx::bulk_load(sbase + kOffStats + buf * kStatBytes,
-                               stats + (static_cast<size_t>(t.stat + t.first + i) * kHeads + head) * 2 * kTile, kStatBytes,
-                               BAR(C1FULL + buf), pol);
-            }
-            if (ok) ++n;
-            if (i == 0 && ok) {
-              ok = wait_cta(BAR(R2EMPTY), (loads2 & 1u) ^ 1u, quit);
-              if (ok) {
-                ++loads2;
-                ptx::mbar_arrive_expect_tx(BAR(R2FULL), 2 * kChunk);
-                load_vo(sbase + kOffR2, R2FULL, kKeys, head, t.r0);
-              }
-            }
-            if (ok) ok = wait_cta(BAR(C2EMPTY), (n2 & 1u) ^ 1u, quit);
-            if (ok) {
-              ++n2;
-              ptx::mbar_arrive_expect_tx(BAR(C2FULL), 2 * kChunk);
-              load_vo(sbase + kOffC2, C2FULL, !kKeys, head, col);
-            }
-          }
+          ok = wait_cta(BAR(R1EMPTY), (loads & 1u) ^ 1u, quit);
+          if (!ok) break;
+          ++loads;
+          ptx::mbar_arrive_expect_tx(BAR(R1FULL), 3 * kChunk);
+          load_4d(sbase + kOffR1, &maps.r1n, BAR(R1FULL), 0, t.r0, 0, head);
+          load_4d(sbase + kOffR1 + 2 * kChunk, &maps.r1r, BAR(R1FULL), 0, t.r0, 0, kKeys ? 0 : head);
+          ok = wait_cta(BAR(R2EMPTY), (loads2 & 1u) ^ 1u, quit);
+          if (!ok) break;
+          ++loads2;
+          ptx::mbar_arrive_expect_tx(BAR(R2FULL), 2 * kChunk);
+          load_4d(sbase + kOffR2, &maps.r2, BAR(R2FULL), 0, t.r0, 0, head);
         }
-        if (t.steps == 0) item = atomicAdd(&plan->next[kSide], 1);
+        // Claimed when the item's last rows are on their way: its steps are still to come.
+        item = atomicAdd(&plan->next[kSide], 1);
       }
-      // no copy may land after the CTA has left: wait for the last phase armed on each barrier
-#pragma unroll 1
-      for (int b = 0; b < 5; ++b) {
-        const uint32_t count = b == 0 ? loads : b == 1 ? loads2 : b == 2 ? n2 : (n + 4u - static_cast<uint32_t>(b)) / 2u;
-        const int bar = b == 0 ? R1FULL : b == 1 ? R2FULL : b == 2 ? C2FULL : C1FULL + b - 3;
-        if (count > 0) wait_issued(BAR(bar), (count - 1) & 1u, quit);
-      }
+      // no copy may land after the CTA has left
+      if (loads > 0) wait_issued(BAR(R1FULL), (loads - 1) & 1u, quit);
+      if (loads2 > 0) wait_issued(BAR(R2FULL), (loads2 - 1) & 1u, quit);
     }
+    __syncwarp();
+  } else if (smem_ok && warp >= 3 && warp < 6) {
+    // ------------------------------------------------------------ loads of C1, a chunk of 64 values each
+    // (A copy costs its thread 160 cycles to issue, and one thread that waited for all
+    // buffers in turn held up one copy for another's sake.  The products of a chunk
+    // begin when it has landed.)
+    regs_issue();
+    const int chunk = warp - 3;
+    uint32_t queued = 0;
+    walk_steps([&](const Tile& t, int head, int i, uint32_t n) {
+      const uint32_t buf = n & 1u;
+      const int bar = C1FULL + 3 * static_cast<int>(buf) + chunk;
+      if (!wait_cta_warp(BAR(C1EMPTY + buf), ((n >> 1) & 1u) ^ 1u, quit)) return false;
+      ++queued;
+      if (elect_one()) {
+        ptx::mbar_arrive_expect_tx(BAR(bar), kChunk);
+        load_4d(sbase + kOffC1 + (buf * 3 + chunk) * kChunk, chunk < 2 ? &maps.c1n : &maps.c1r, BAR(bar), 0,
+                t.c0 + (t.first + i) * kTile, chunk & 1, kKeys || chunk < 2 ? head : 0);
+      }
+      __syncwarp();
+      return true;
+    });
+    for (uint32_t b = 0; b < 2 && b < queued; ++b)
+      wait_issued(BAR(C1FULL + 3 * b + chunk), ((queued + 1 - b) / 2 - 1) & 1u, quit);
+  } else if (smem_ok && warp == 6) {
+    // ------------------------------------------------------------ loads of C2, a chunk each
+    regs_issue();
+    uint32_t queued = 0;
+    walk_steps([&](const Tile& t, int head, int i, uint32_t n) {
+      if (!wait_cta_warp(BAR(C2EMPTY), (n & 1u) ^ 1u, quit)) return false;
+      ++queued;
+      if (elect_one()) {
+        for (int c = 0; c < 2; ++c) {
+          ptx::mbar_arrive_expect_tx(BAR(C2FULL + c), kChunk);
+          load_4d(sbase + kOffC2 + c * kChunk, &maps.c2, BAR(C2FULL + c), 0, t.c0 + (t.first + i) * kTile, c, head);
+        }
+      }
+      __syncwarp();
+      return true;
+    });
+    for (int c = 0; c < 2 && queued > 0; ++c) wait_issued(BAR(C2FULL + c), (queued - 1) & 1u, quit);
+  } else if (kKeys && smem_ok && warp == 7) {
+    // ------------------------------------------------------------ lse and delta of the streamed queries
+    regs_issue();
+    const float* stats = reinterpret_cast<const float*>(p.ws + L.stats);
+    walk_steps([&](const Tile& t, int head, int i, uint32_t n) {
+      // read while the step before the last, whose place they take, is still at work
+      const uint32_t buf = n & 1u;
+      const float4* src = reinterpret_cast<const float4*>(
+          stats + (static_cast<size_t>(t.stat + t.first + i) * kHeads + head) * 2 * kTile) + lane;
+      const float4 lse = __ldcg(src), delta = __ldcg(src + kTile / 4);
+      // (its dS has been computed when the product with it is done)
+      if (!wait_cta_warp(BAR(C1EMPTY + buf), ((n >> 1) & 1u) ^ 1u, quit)) return false;
+      float4* dst = reinterpret_cast<float4*>(smem + kOffStats + buf * kStatBytes) + lane;
+      dst[0] = lse;
+      dst[kTile / 4] = delta;
+      __syncwarp();
+      if (elect_one()) ptx::mbar_arrive(BAR(STATFULL + static_cast<int>(buf)));
+      return true;
+    });
   } else if (smem_ok && warp == 1) {
+    regs_issue();
     // ------------------------------------------------------------ S = R1 C1^T, dP = R2 C2^T
     Walk w;
     Tile t;
@@ -411,40 +458,47 @@ backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Backw
         for (int i = 0; i < steps && ok; ++i, ++n) {
           const uint32_t buf = n & 1u;
           if (i == 0) ok = wait_cta_warp(BAR(R1FULL), loads & 1u, quit);
-          if (ok) ok = wait_cta_warp(BAR(C1FULL + buf), (n >> 1) & 1u, quit);
+          // (who sees S finds the statistics)
+          if (kKeys && ok) ok = wait_cta_warp(BAR(STATFULL + buf), (n >> 1) & 1u, quit);
           // S's place: the last dP has been read from it (keys), or the last S
           if (ok && n > 0) ok = wait_cta_warp(BAR(kKeys ? DPREAD : SREAD), (n - 1) & 1u, quit);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          issued = true;
-          if (elect_one()) {
+#pragma unroll 1
+          for (int c = 0; c < 3 && ok; ++c) {
+            ok = wait_cta_warp(BAR(C1FULL + 3 * static_cast<int>(buf) + c), (n >> 1) & 1u, quit);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            issued = true;
+            if (elect_one()) {
+              const uint64_t a = r1 + c * kChunkD, b = c1 + (3u * buf + c) * kChunkD;
 #pragma unroll
-            for (int c = 0; c < 3; ++c)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                ptx::mma_ss(tmem + kX, r1 + c * kChunkD + 2u * k, c1 + (3u * buf + c) * kChunkD + 2u * k, kIdescS,
-                            (c > 0 || k > 0) ? 1u : 0u);
-            ptx::mma_commit(BAR(SFULL));
-            if (i == steps - 1) ptx::mma_commit(BAR(R1EMPTY));
+              for (int k = 0; k < 4; ++k) ptx::mma_ss(tmem + kX, a + 2u * k, b + 2u * k, kIdescS, (c > 0 || k > 0) ? 1u : 0u);
+              if (c == 2) {
+                ptx::mma_commit(BAR(SFULL));
+                if (i == steps - 1) ptx::mma_commit(BAR(R1EMPTY));
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
           if (i == 0) ok = wait_cta_warp(BAR(R2FULL), loads & 1u, quit);
-          if (ok) ok = wait_cta_warp(BAR(C2FULL), n & 1u, quit);
           if (ok && (kKeys || n > 0)) ok = wait_cta_warp(BAR(kKeys ? SREAD : DPREAD), (kKeys ? n : n - 1) & 1u, quit);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          if (elect_one()) {
+#pragma unroll 1
+          for (int c = 0; c < 2 && ok; ++c) {
+            ok = wait_cta_warp(BAR(C2FULL + c), n & 1u, quit);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (elect_one()) {
+              const uint64_t a = r2 + c * kChunkD, b = c2 + c * kChunkD;
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                ptx::mma_ss(tmem + kDp, r2 + c * kChunkD + 2u * k, c2 + c * kChunkD + 2u * k, kIdescS,
-                            (c > 0 || k > 0) ? 1u : 0u);
-            ptx::mma_commit(BAR(DPFULL));
-            ptx::mma_commit(BAR(C2EMPTY));
-            if (i == steps - 1) ptx::mma_commit(BAR(R2EMPTY));
+              for (int k = 0; k < 4; ++k) ptx::mma_ss(tmem + kDp, a + 2u * k, b + 2u * k, kIdescS, (c > 0 || k > 0) ? 1u : 0u);
+              if (c == 1) {
+                ptx::mma_commit(BAR(DPFULL));
+                ptx::mma_commit(BAR(C2EMPTY));
+                if (i == steps - 1) ptx::mma_commit(BAR(R2EMPTY));
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
         if (steps > 0) ++loads;
       }
@@ -456,6 +510,7 @@ backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Backw
     }
     __syncwarp();
   } else if (smem_ok && warp == 2) {
+    regs_issue();
     // ------------------------------------------------------------ ACC2 += P C2 (keys), ACC1 += dS C1
     Walk w;
     Tile t;
@@ -484,7 +539,7 @@ backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Backw
           // a head's first products overwrite the accumulators: they must have been read
           if (i == 0) ok = wait_cta_warp(BAR(ACCFREE), (heads & 1u) ^ 1u, quit);
           if constexpr (kKeys) {
-            if (ok) ok = wait_cta_warp(BAR(C2FULL), n & 1u, quit);
+            for (int c = 0; c < 2 && ok; ++c) ok = wait_cta_warp(BAR(C2FULL + c), n & 1u, quit);
             if (ok) ok = wait_cta_warp(BAR(PREADY), n & 1u, quit);
             if (!ok) break;
             if (valid < kTile) clear(kOffC2, 2, valid);
@@ -499,7 +554,7 @@ backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Backw
             }
             __syncwarp();
           }
-          if (ok) ok = wait_cta_warp(BAR(C1FULL + buf), (n >> 1) & 1u, quit);
+          for (int c = 0; c < 3 && ok; ++c) ok = wait_cta_warp(BAR(C1FULL + 3 * static_cast<int>(buf) + c), (n >> 1) & 1u, quit);
           if (ok) ok = wait_cta_warp(BAR(DSREADY), n & 1u, quit);
           if (!ok) break;
           if (valid < kTile) clear(kOffC1 + buf * 3 * kChunk, 3, valid);
@@ -529,12 +584,15 @@ backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Backw
       wait_issued(BAR(DRAIN + 1), 0u, quit);
     }
     __syncwarp();
-  } else if (smem_ok && warp >= 4) {
-    // ------------------------------------------------------------ P and dS (thread = half a row), results
-    const int half = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
+  } else if (smem_ok && warp < kHelpers) {
+    regs_issue();   // (idle: a register split is the whole warpgroup's)
+  } else if (smem_ok) {
+    // ------------------------------------------------------------ P and dS (thread = a quarter row), results
+    regs_compute();
+    const int quarter = (warp - kHelpers) >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t x_addr = tmem + lane_base + kX + 64u * half, dp_addr = tmem + lane_base + kDp + 64u * half;
-    const uint32_t y_addr = tmem + lane_base + kY + 32u * half;
+    const uint32_t x_addr = tmem + lane_base + kX + 32u * quarter, dp_addr = tmem + lane_base + kDp + 32u * quarter;
+    const uint32_t y_addr = tmem + lane_base + kY + 16u * quarter;
     const float c = p.scale * kLog2e;
     Walk w;
     Tile t;
@@ -546,22 +604,6 @@ backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Backw
       __syncwarp();
       if (elect_one()) ptx::mbar_arrive(BAR(bar));
     };
-    // 16 bf16 values to 32 bytes at dst (16-byte aligned)
-    auto store16 = [&](__nv_bfloat16* dst, const uint32_t* v) {
-      reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-    };
-    // 32 accumulator columns as bf16
-    auto read32 = [&](uint32_t col, float mul, uint32_t* out16) {
-      uint32_t a[32];
-      ptx::tmem_ld32(tmem + lane_base + col, a);
-      ptx::tmem_wait_ld();
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(a[2 * e]) * mul, __uint_as_float(a[2 * e + 1]) * mul);
-        out16[e] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-    };
     while (ok && next_warp(w, t, head0)) {
       const size_t row = static_cast<size_t>(t.r0) + r;
       const bool mine = r < t.rows;
@@ -570,138 +612,76 @@ backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Backw
         float row_lse = 0.f, row_delta = 0.f;
         if constexpr (!kKeys) {
           const float* st = reinterpret_cast<const float*>(p.ws + L.stats) + (static_cast<size_t>(t.stat) * kHeads + head) * 2 * kTile;
-          row_lse = st[r];
-          row_delta = st[kTile + r];
+          row_lse = __ldcg(st + r);
+          row_delta = __ldcg(st + kTile + r);
         }
         for (int i = 0; i < t.steps; ++i, ++n) {
           const uint32_t buf = n & 1u;
-          // columns [lo, hi) of this thread's 64 are seen
-          const int at = (t.first + i) * kTile + 64 * half;
+          // columns [lo, hi) of this thread's 32 are seen
+          const int at = (t.first + i) * kTile + kCols * quarter;
           int lo = 0, hi = t.nc - at;
           if (causal) {
             if constexpr (kKeys) lo = t.lim + r - at;
             else hi = min(hi, t.lim + r - at);
           }
-          const bool all = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
+          const bool all = __all_sync(0xffffffffu, lo <= 0 && hi >= kCols);
           ok = wait_cta_warp(BAR(SFULL), n & 1u, quit);
-          if (ok && kKeys) ok = wait_cta_warp(BAR(C1FULL + buf), (n >> 1) & 1u, quit);   // the statistics
           if (!ok) break;
           ptx::tc_fence_after();
-          uint32_t s[64], pk[32];
+          uint32_t s[kCols], pk[kCols / 2];
           ptx::tmem_ld32(x_addr, s);
-          ptx::tmem_ld32(x_addr + 32u, s + 32);
           ptx::tmem_wait_ld();
           arrive(SREAD);
-          const float4* lse4 = reinterpret_cast<const float4*>(smem + kOffStats + buf * kStatBytes) + 16 * half;
-#pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            float4 l = make_float4(row_lse, row_lse, row_lse, row_lse);
-            if constexpr (kKeys) l = lse4[e / 4];
-            s[e] = __float_as_uint(fast_exp2(fmaf(__uint_as_float(s[e]), c, -l.x)));
-            s[e + 1] = __float_as_uint(fast_exp2(fmaf(__uint_as_float(s[e + 1]), c, -l.y)));
-            s[e + 2] = __float_as_uint(fast_exp2(fmaf(__uint_as_float(s[e + 2]), c, -l.z)));
-            s[e + 3] = __float_as_uint(fast_exp2(fmaf(__uint_as_float(s[e + 3]), c, -l.w)));
-          }
-          if (!all) {
-#pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (e < lo || e >= hi) s[e] = 0u;
-          }
+          const float4* lse4 = reinterpret_cast<const float4*>(smem + kOffStats + buf * kStatBytes) + kCols / 4 * quarter;
+          probabilities<kKeys>(s, lse4, row_lse, c, all, lo, hi);
           if constexpr (kKeys) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-              pk[e] = *reinterpret_cast<const uint32_t*>(&b);
-            }
+            pack(s, pk);
             // the last step's dS has been read
             if (n > 0) ok = wait_cta_warp(BAR(DSDONE), (n - 1) & 1u, quit);
             if (!ok) break;
             ptx::tc_fence_after();
-            ptx::tmem_st32(y_addr, pk);
+            tmem_st16(y_addr, pk);
             ptx::tmem_wait_st();
             arrive(PREADY);
           }
           ok = wait_cta_warp(BAR(DPFULL), n & 1u, quit);
           if (!ok) break;
           ptx::tc_fence_after();
-          const float4* delta4 = lse4 + kTile / 4;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t d[32];
-            ptx::tmem_ld32(dp_addr + 32u * q, d);
-            ptx::tmem_wait_ld();
-            if (q == 1) arrive(DPREAD);
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              float4 m = make_float4(row_delta, row_delta, row_delta, row_delta);
-              if constexpr (kKeys) m = delta4[8 * q + e / 4];
-              const uint32_t* x = s + 32 * q + e;
-              float y0 = __uint_as_float(x[0]) * (__uint_as_float(d[e]) - m.x), y1 = __uint_as_float(x[1]) * (__uint_as_float(d[e + 1]) - m.y);
-              float y2 = __uint_as_float(x[2]) * (__uint_as_float(d[e + 2]) - m.z), y3 = __uint_as_float(x[3]) * (__uint_as_float(d[e + 3]) - m.w);
-              if (!all) {                    // (0 times what is not finite)
-                const int k = 32 * q + e;
-                if (k < lo || k >= hi) y0 = 0.f;
-                if (k + 1 < lo || k + 1 >= hi) y1 = 0.f;
-                if (k + 2 < lo || k + 2 >= hi) y2 = 0.f;
-                if (k + 3 < lo || k + 3 >= hi) y3 = 0.f;
-              }
-              const __nv_bfloat162 a = __floats2bfloat162_rn(y0, y1), b = __floats2bfloat162_rn(y2, y3);
-              pk[16 * q + e / 2] = *reinterpret_cast<const uint32_t*>(&a);
-              pk[16 * q + e / 2 + 1] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-          }
+          uint32_t d[kCols];
+          ptx::tmem_ld32(dp_addr, d);
+          ptx::tmem_wait_ld();
+          arrive(DPREAD);
+          gradients<kKeys>(s, d, lse4 + kTile / 4, row_delta, all, lo, hi, pk);
           // P (keys), or the last step's dS, has been read
           if (kKeys) ok = wait_cta_warp(BAR(PDONE), n & 1u, quit);
           else if (n > 0) ok = wait_cta_warp(BAR(DSDONE), (n - 1) & 1u, quit);
           if (!ok) break;
           ptx::tc_fence_after();
-          ptx::tmem_st32(y_addr, pk);
+          tmem_st16(y_addr, pk);
           ptx::tmem_wait_st();
           arrive(DSREADY);
         }
         if (!ok) break;
         // results of the head
         const bool last = g == group - 1;
-        uint32_t nope[32], second[32], rope[32];
+        uint32_t nope[16], second[16], rope[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) nope[e] = second[e] = rope[e] = 0;
+        for (int e = 0; e < 16; ++e) nope[e] = second[e] = rope[e] = 0;
         if (t.steps > 0) {
           ok = wait_cta_warp(BAR(DSDONE), (n - 1) & 1u, quit);
           if (!ok) break;
           ptx::tc_fence_after();
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            read32(kAcc1 + 64u * half + 32u * q, p.scale, nope + 16 * q);
-            if constexpr (kKeys) read32(kAcc2 + 64u * half + 32u * q, 1.f, second + 16 * q);
-          }
-          if constexpr (kKeys) {
-            if (last) {
-              ptx::tmem_ld32(tmem + lane_base + kAcc1 + 128u + 32u * half, rope);
-              ptx::tmem_wait_ld();
-            }
-          } else {
-            read32(kAcc1 + 128u + 32u * half, p.scale, rope);
-          }
+          uint32_t a[32], b[32];
+          ptx::tmem_ld32(tmem + lane_base + kAcc1 + 32u * quarter, a);
+          if constexpr (kKeys) ptx::tmem_ld32(tmem + lane_base + kAcc2 + 32u * quarter, b);
+          if (!kKeys || last) ptx::tmem_ld16(tmem + lane_base + kAcc1 + 128u + 16u * quarter, rope);
+          ptx::tmem_wait_ld();
+          to_bf16<16>(a, p.scale, nope);
+          if constexpr (kKeys) to_bf16<16>(b, 1.f, second);
+          else to_bf16<8>(rope, p.scale, rope);
           arrive(ACCFREE);
         }
-        if (mine) {
-          __nv_bfloat16* dst = kKeys ? p.dk_nope + row * p.dkn_t + head * p.dkn_h : p.dq_nope + row * p.dqn_t + head * p.dqn_h;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) store16(dst + 64 * half + 16 * q, nope + 8 * q);
-          if constexpr (kKeys) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) store16(p.dv + row * p.dv_t + head * p.dv_h + 64 * half + 16 * q, second + 8 * q);
-            if (last) {
-              float* part = reinterpret_cast<float*>(p.ws + L.rope) +
-                            (static_cast<size_t>(head0 / group) * p.nk + row) * kDr + 32 * half;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) ptx::st_global_v8(part + 8 * q, rope + 8 * q);
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) store16(p.dq_rope + row * p.dqr_t + head * p.dqr_h + 32 * half + 16 * q, rope + 8 * q);
-          }
-        }
+        if (mine) store_results<kKeys>(p, L, row, head, head0 / group, quarter, last, nope, second, rope);
       }
     }
   }
@@ -709,6 +689,7 @@ backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Backw
   ptx::tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *quit != 0) set_status(&hdr->status, MLA_STATUS_TIMEOUT);
+  if constexpr (kKeys) ptx::grid_dep_wait();   // (see begin_pass)
   if (warp == 2) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
@@ -716,28 +697,54 @@ backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Backw
 }
 
 // ---------------------------------------------------------------- RoPE part of dk
-// The groups' sums of a key tile, in the groups' order; a thread has four values.
+// The sum of the groups, two keys a CTA: 16 threads a key and run of groups with four
+// values each, then over the eight runs, in their order.
 __global__ void __launch_bounds__(256) backward_rope_kernel(const BackwardParams p, const BackwardWs L) {
+  __shared__ float4 s_sum[2][8][16];
   const BackwardPlan* plan = reinterpret_cast<const BackwardPlan*>(p.ws + L.plan);
-  if (static_cast<int>(blockIdx.x) >= plan->tiles[0]) return;
-  const Tile t = reinterpret_cast<const Tile*>(p.ws + L.tiles[0])[blockIdx.x];
-  const int r = blockIdx.y * 16 + (threadIdx.x >> 4), d = 4 * (threadIdx.x & 15);
-  if (r >= t.rows) return;
+  ptx::grid_dep_wait();
+  if (static_cast<int>(blockIdx.y) >= *reinterpret_cast<const volatile int*>(&plan->tiles[0])) return;
+  const Tile t = reinterpret_cast<const Tile*>(p.ws + L.tiles[0])[blockIdx.y];
+  const int k = threadIdx.x >> 7, run = (threadIdx.x >> 4) & 7, lane = threadIdx.x & 15, r = 2 * static_cast<int>(blockIdx.x) + k;
+  if (2 * static_cast<int>(blockIdx.x) >= t.rows) return;
   const size_t row = static_cast<size_t>(t.r0) + r;
-  const float* part = reinterpret_cast<const float*>(p.ws + L.rope) + row * kDr + d;
+  const int groups = kHeads / L.group, per = groups / 8;   // 16 to 128 groups
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r < t.rows) {
+    const float4* part = reinterpret_cast<const float4*>(p.ws + L.rope) + (static_cast<size_t>(run * per) * p.nk + row) * (kDr / 4) + lane;
 #pragma unroll 8
-  for (int g = 0; g < kHeads / L.group; ++g) {
-    const float4 x = *reinterpret_cast<const float4*>(part + static_cast<size_t>(g) * p.nk * kDr);
+    for (int g = 0; g < per; ++g) {
+      const float4 x = __ldcs(part + static_cast<size_t>(g) * p.nk * (kDr / 4));
+      sum.x += x.x;
+      sum.y += x.y;
+      sum.z += x.z;
+      sum.w += x.w;
+    }
+  }
+  s_sum[k][run][lane] = sum;
+  __syncthreads();
+  if (run != 0 || r >= t.rows) return;
+#pragma unroll
+  for (int q = 1; q < 8; ++q) {
+    const float4 x = s_sum[k][q][lane];
     sum.x += x.x;
     sum.y += x.y;
     sum.z += x.z;
     sum.w += x.w;
   }
-  const __nv_bfloat162 a = __floats2bfloat162_rn(sum.x * p.scale, sum.y * p.scale);
-  const __nv_bfloat162 b = __floats2bfloat162_rn(sum.z * p.scale, sum.w * p.scale);
-  *reinterpret_cast<uint2*>(p.dk_rope + row * p.dkr_t + d) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  *reinterpret_cast<uint2*>(p.dk_rope + row * p.dkr_t + 4 * lane) =
+      make_uint2(bf16_pair(sum.x * p.scale, sum.y * p.scale), bf16_pair(sum.z * p.scale, sum.w * p.scale));
+}
+
+// Rows of a query tile: 256, on CTA pairs (backward_pair.cu), unless too many of their
+// rows and columns are masked.  Of an average sequence, a pair's tiles of 256 instead of
+// 128 rows are 64 rows more at its end and, where causal, 64 columns more a row at the
+// diagonal; a pair's query pass is about a sixth faster on full tiles.  (Measured there;
+// 2 x 512 queries over 8,012 keys have a share of 0.13, 8 x up to 1024 tokens 0.37.)
+int backward_rows(const BackwardParams& p) {
+  const double n_q = static_cast<double>(p.nq) / p.batch, n_k = static_cast<double>(p.nk) / p.batch;
+  const double seen = p.causal ? std::fmax(n_k - n_q / 2, 1.0) : std::fmax(n_k, 1.0);
+  return 64.0 / n_q + (p.causal ? 64.0 / seen : 0.0) <= 0.16 ? 2 * kTile : kTile;
 }
 
 }  // namespace
@@ -745,32 +752,34 @@ __global__ void __launch_bounds__(256) backward_rope_kernel(const BackwardParams
 cudaError_t launch_backward(PFN_cuTensorMapEncodeTiled_v12000 encode, const BackwardParams& p, int sms,
                             cudaStream_t stream) {
   const BackwardWs L = backward_ws(p.batch, p.nq, p.nk);
-  Maps maps;
-  // with no row at all nothing is loaded; the maps still need one
-  const int nq = p.nq > 0 ? p.nq : 1, nk = p.nk > 0 ? p.nk : 1;
-  if (!encode_map(encode, &maps.qn, p.q_nope, 128, kHeads, nq, p.qn_t, p.qn_h, kTile) ||
-      !encode_map(encode, &maps.qr, p.q_rope, 64, kHeads, nq, p.qr_t, p.qr_h, kTile) ||
-      !encode_map(encode, &maps.kn, p.k_nope, 128, kHeads, nk, p.kn_t, p.kn_h, kTile) ||
-      !encode_map(encode, &maps.kr, p.k_rope, 64, 1, nk, p.kr_t, 64, kTile) ||
-      !encode_map(encode, &maps.v, p.v, 128, kHeads, nk, p.v_t, p.v_h, kTile) ||
-      !encode_map(encode, &maps.d_out, p.d_out, 128, kHeads, nq, p.do_t, p.do_h, kTile))
-    return cudaErrorInvalidValue;
-  static std::atomic<uint64_t> configured_k{0}, configured_q{0};
-  cudaError_t e = allow_smem(backward_kernel<true>, kSmem, configured_k);
-  if (e == cudaSuccess) e = allow_smem(backward_kernel<false>, kSmem, configured_q);
-  if (e != cudaSuccess) return e;
-  const long long items_k = static_cast<long long>(L.max_tiles[0]) * (kHeads / L.group);
-  const long long items_q = static_cast<long long>(L.max_tiles[1]) * kHeads;
-  const int ctas_k = static_cast<int>(items_k < sms ? items_k : sms), ctas_q = static_cast<int>(items_q < sms ? items_q : sms);
-  e = launch_kernel(backward_plan_kernel, dim3(1), dim3(1024), 0, stream, p, L, ctas_k, ctas_q);
-  if (e == cudaSuccess && ctas_q)
-    e = launch_kernel(backward_delta_kernel, dim3(L.max_tiles[1], kHeads / 8), dim3(256), 0, stream, p, L);
-  if (e == cudaSuccess && ctas_q)
-    e = launch_kernel(backward_kernel<false>, dim3(ctas_q), dim3(kThreads), kSmem, stream, maps, p, L);
-  if (e == cudaSuccess && ctas_k)
-    e = launch_kernel(backward_kernel<true>, dim3(ctas_k), dim3(kThreads), kSmem, stream, maps, p, L);
-  if (e == cudaSuccess && ctas_k)
-    e = launch_kernel(backward_rope_kernel, dim3(L.max_tiles[0], kTile / 16), dim3(256), 0, stream, p, L);
+  const int query_rows = backward_rows(p), most[2] = {sms, sms * kTile / query_rows};
+  int clusters[2];
+  for (int side = 0; side < 2; ++side) {
+    const long long items = static_cast<long long>(L.max_tiles[side]) * (side ? kHeads : kHeads / L.group);
+    clusters[side] = static_cast<int>(items < most[side] ? items : most[side]);
+  }
+  cudaError_t e = launch_kernel(backward_plan_kernel, dim3(1), dim3(1024), 0, stream, p, L, clusters[0], clusters[1], query_rows);
+  PassMaps maps;
+  static std::atomic<uint64_t> configured_q{0}, configured_k{0};
+  if (e == cudaSuccess && clusters[1]) {
+    e = launch_dependent(backward_delta_kernel, dim3(L.max_tiles[1] * (query_rows / kDeltaRows), kHeads / 8), dim3(256), 0, stream,
+                         p, L, query_rows);
+    if (e == cudaSuccess && !pass_maps(encode, p, false, query_rows == kTile ? kTile : kTile / 2, &maps)) e = cudaErrorInvalidValue;
+    if (e == cudaSuccess && query_rows > kTile) {
+      e = launch_backward_pairs(maps, p, L, clusters[1], stream);
+    } else if (e == cudaSuccess) {
+      e = allow_smem(backward_kernel<false>, kSmem, configured_q);
+      if (e == cudaSuccess)
+        e = launch_dependent(backward_kernel<false>, dim3(clusters[1]), dim3(kThreads), kSmem, stream, maps, p, L);
+    }
+  }
+  if (e == cudaSuccess && clusters[0]) {
+    if (!pass_maps(encode, p, true, kTile, &maps)) e = cudaErrorInvalidValue;
+    if (e == cudaSuccess) e = allow_smem(backward_kernel<true>, kSmem, configured_k);
+    if (e == cudaSuccess) e = launch_dependent(backward_kernel<true>, dim3(clusters[0]), dim3(kThreads), kSmem, stream, maps, p, L);
+    if (e == cudaSuccess)
+      e = launch_dependent(backward_rope_kernel, dim3(kTile / 2, L.max_tiles[0]), dim3(256), 0, stream, p, L);
+  }
   return e;
 }
 

@@ -5,8 +5,7 @@
 
 namespace mla {
 
-constexpr int kBackwardTile = 128;   // rows and columns of a step's tile of scores
-constexpr int kMaxRopeGroup = 8;     // heads whose key-RoPE gradients are summed in one work item, at most
+constexpr int kBackwardTile = 128;   // columns of a step's tile of scores, and rows of a CTA's
 
 struct BackwardParams {
   const __nv_bfloat16 *d_out, *q_nope, *q_rope, *k_nope, *k_rope, *v, *out;
@@ -32,13 +31,16 @@ struct BackwardWs {
   size_t plan, base, tiles[2], stats, rope, total;
   int max_tiles[2], group;
 };
-__host__ __device__ inline BackwardWs backward_ws(int batch, int nq, int nk) {
+inline BackwardWs backward_ws(int batch, int nq, int nk) {
   BackwardWs w;
   // every sequence ends at most one tile early
   w.max_tiles[0] = nk / kBackwardTile + (batch < nk ? batch : nk);
   w.max_tiles[1] = nq / kBackwardTile + (batch < nq ? batch : nq);
-  w.group = kMaxRopeGroup;
-  while (w.group > 1 && static_cast<long long>(w.max_tiles[0]) * kHeads / w.group < 8 * 152) w.group /= 2;
+  // eight heads where they still make eight items a CTA (a sixteenth of the keys' whole
+  // gradients in the workspace instead of a quarter), two where they do not: one made
+  // 8 x up to 1024 tokens 669 us instead of 646, four 654; 4096 tokens take the same
+  // with one, two or eight
+  w.group = static_cast<long long>(w.max_tiles[0]) * kHeads / 8 >= 8 * 152 ? 8 : 2;
   w.plan = align256(sizeof(PlanHeader));
   w.base = align256(w.plan + sizeof(BackwardPlan));
   w.tiles[0] = align256(w.base + sizeof(int) * static_cast<size_t>(batch));
@@ -49,6 +51,10 @@ __host__ __device__ inline BackwardWs backward_ws(int batch, int nq, int nk) {
   return w;
 }
 
+// The query pass on CTA pairs, whose row tiles are 256.
+struct PassMaps;
+cudaError_t launch_backward_pairs(const PassMaps& maps, const BackwardParams& p, const BackwardWs& L, int pairs,
+                                  cudaStream_t stream);
 cudaError_t launch_backward(PFN_cuTensorMapEncodeTiled_v12000 encode, const BackwardParams& p, int sms,
                             cudaStream_t stream);
 
