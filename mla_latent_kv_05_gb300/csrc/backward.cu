@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParam
           const int n = min(x, L.max_tiles[side]), ctas = side ? ctas_q : ctas_k, groups = side ? kHeads : kHeads / L.group;
           plan->tiles[side] = n;
           plan->next[side] = ctas;
+          plan->odd[side] = 0;
           // (as in prefill: not where all tiles are about as long)
           const bool even = 2 * s_longest <= 3 * s_shortest;
           plan->tail[side] = even ? 1 : min(groups, (kTailItems * ctas + n - 1) / max(n, 1));
@@ -204,7 +205,7 @@ constexpr int kDeltaRows = 32;
 
 __global__ void __launch_bounds__(256) backward_delta_kernel(const BackwardParams p, const BackwardWs L, int query_rows) {
   __shared__ float s_delta[8][kDeltaRows];
-  const BackwardPlan* plan = reinterpret_cast<const BackwardPlan*>(p.ws + L.plan);
+  BackwardPlan* plan = reinterpret_cast<BackwardPlan*>(p.ws + L.plan);
   const int parts = query_rows / kDeltaRows, i_tile = static_cast<int>(blockIdx.x) / parts, part = static_cast<int>(blockIdx.x) % parts;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
@@ -251,6 +252,9 @@ __global__ void __launch_bounds__(256) backward_delta_kernel(const BackwardParam
     const size_t at = (static_cast<size_t>(t.r0) + r0 + r) * kHeads + h0 + h;
     l = __ldg(p.lse + at) * kLog2e;
     d = s_delta[h][r] - (p.d_lse ? __ldg(p.d_lse + at) : 0.f);
+    // a value of q, d_out or d_lse that is not finite is seen here, in the lse or in
+    // delta; so are, for nothing, queries that see no key
+    if (p.causal && !(isfinite(l) && isfinite(d))) plan->odd[0] = 1;
   }
   stats[0] = l;
   stats[kTile] = d;
@@ -696,55 +700,18 @@ backward_kernel(const __grid_constant__ PassMaps maps, const __grid_constant__ B
   }
 }
 
-// ---------------------------------------------------------------- RoPE part of dk
-// The sum of the groups, two keys a CTA: 16 threads a key and run of groups with four
-// values each, then over the eight runs, in their order.
-__global__ void __launch_bounds__(256) backward_rope_kernel(const BackwardParams p, const BackwardWs L) {
-  __shared__ float4 s_sum[2][8][16];
-  const BackwardPlan* plan = reinterpret_cast<const BackwardPlan*>(p.ws + L.plan);
-  ptx::grid_dep_wait();
-  if (static_cast<int>(blockIdx.y) >= *reinterpret_cast<const volatile int*>(&plan->tiles[0])) return;
-  const Tile t = reinterpret_cast<const Tile*>(p.ws + L.tiles[0])[blockIdx.y];
-  const int k = threadIdx.x >> 7, run = (threadIdx.x >> 4) & 7, lane = threadIdx.x & 15, r = 2 * static_cast<int>(blockIdx.x) + k;
-  if (2 * static_cast<int>(blockIdx.x) >= t.rows) return;
-  const size_t row = static_cast<size_t>(t.r0) + r;
-  const int groups = kHeads / L.group, per = groups / 8;   // 16 to 128 groups
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (r < t.rows) {
-    const float4* part = reinterpret_cast<const float4*>(p.ws + L.rope) + (static_cast<size_t>(run * per) * p.nk + row) * (kDr / 4) + lane;
-#pragma unroll 8
-    for (int g = 0; g < per; ++g) {
-      const float4 x = __ldcs(part + static_cast<size_t>(g) * p.nk * (kDr / 4));
-      sum.x += x.x;
-      sum.y += x.y;
-      sum.z += x.z;
-      sum.w += x.w;
-    }
-  }
-  s_sum[k][run][lane] = sum;
-  __syncthreads();
-  if (run != 0 || r >= t.rows) return;
-#pragma unroll
-  for (int q = 1; q < 8; ++q) {
-    const float4 x = s_sum[k][q][lane];
-    sum.x += x.x;
-    sum.y += x.y;
-    sum.z += x.z;
-    sum.w += x.w;
-  }
-  *reinterpret_cast<uint2*>(p.dk_rope + row * p.dkr_t + 4 * lane) =
-      make_uint2(bf16_pair(sum.x * p.scale, sum.y * p.scale), bf16_pair(sum.z * p.scale, sum.w * p.scale));
-}
-
 // Rows of a query tile: 256, on CTA pairs (backward_pair.cu), unless too many of their
 // rows and columns are masked.  Of an average sequence, a pair's tiles of 256 instead of
 // 128 rows are 64 rows more at its end and, where causal, 64 columns more a row at the
-// diagonal; a pair's query pass is about a sixth faster on full tiles.  (Measured there;
-// 2 x 512 queries over 8,012 keys have a share of 0.13, 8 x up to 1024 tokens 0.37.)
+// diagonal; a pair's query pass is about a sixth faster on full tiles.  Shares, and us a
+// call with tiles of 128 and of 256: 2 x 512 over 8,012 keys 0.13, 1,808 and 1,686;
+// 2 x 800 over 1,200 0.16, 497 and 497; 4 x 1024 causal 0.19, 716 and 702; 4 x 300 over
+// 4,300 0.23, 1,782 and 1,808; 4 x 300 full 0.21, 235 and 243; 8 x up to 1024 0.37, 611
+// and 648.
 int backward_rows(const BackwardParams& p) {
   const double n_q = static_cast<double>(p.nq) / p.batch, n_k = static_cast<double>(p.nk) / p.batch;
   const double seen = p.causal ? std::fmax(n_k - n_q / 2, 1.0) : std::fmax(n_k, 1.0);
-  return 64.0 / n_q + (p.causal ? 64.0 / seen : 0.0) <= 0.16 ? 2 * kTile : kTile;
+  return 64.0 / n_q + (p.causal ? 64.0 / seen : 0.0) <= 0.2 ? 2 * kTile : kTile;
 }
 
 }  // namespace
@@ -777,8 +744,7 @@ cudaError_t launch_backward(PFN_cuTensorMapEncodeTiled_v12000 encode, const Back
     if (!pass_maps(encode, p, true, kTile, &maps)) e = cudaErrorInvalidValue;
     if (e == cudaSuccess) e = allow_smem(backward_kernel<true>, kSmem, configured_k);
     if (e == cudaSuccess) e = launch_dependent(backward_kernel<true>, dim3(clusters[0]), dim3(kThreads), kSmem, stream, maps, p, L);
-    if (e == cudaSuccess)
-      e = launch_dependent(backward_rope_kernel, dim3(kTile / 2, L.max_tiles[0]), dim3(256), 0, stream, p, L);
+    if (e == cudaSuccess) e = launch_backward_last(p, L, query_rows, stream);
   }
   return e;
 }

@@ -22,6 +22,7 @@ struct BackwardParams {
 // Behind the plan header.
 struct BackwardPlan {
   int tiles[2], next[2], tail[2];   // [0] key tiles, [1] query tiles
+  int odd[2];                       // where causal, the pass may have results that are not finite
 };
 
 // Workspace: header and plan; the first query tile of each sequence; the key tiles
@@ -55,6 +56,8 @@ inline BackwardWs backward_ws(int batch, int nq, int nk) {
 struct PassMaps;
 cudaError_t launch_backward_pairs(const PassMaps& maps, const BackwardParams& p, const BackwardWs& L, int pairs,
                                   cudaStream_t stream);
+// The sums of the RoPE part of dk, and rows that values outside the mask have spoilt.
+cudaError_t launch_backward_last(const BackwardParams& p, const BackwardWs& L, int query_rows, cudaStream_t stream);
 cudaError_t launch_backward(PFN_cuTensorMapEncodeTiled_v12000 encode, const BackwardParams& p, int sms,
                             cudaStream_t stream);
 

@@ -1,0 +1,226 @@
+// The last kernel of the backward pass (backward.cu): the RoPE part of dk, summed over
+// the groups of heads, and rows that values outside the mask have spoilt.
+//
+// A pair outside the causal mask has P = dS = 0 in its tile, which an infinity or a NaN
+// in its streamed row (the key's K for dq, the query's Q and d_out for dk and dv) turns
+// into NaN.  Looking for such values in every tile at the mask's edge would cost every
+// call.  A query's show in its lse or its delta, which are formed anyway, and a key's in
+// results of the query pass, 24 multiply-adds a thread and item.  (The same in the key
+// pass, 48, cost 2 x 512 queries over 8,012 keys another 9 us.)  Where one has been noted, this kernel looks for results that are not
+// finite and computes their rows again on the CUDA cores, over the pairs that are seen
+// alone; a row that is NaN by rights is so in all its values after a pair or two, and
+// left there.
+//
+// Bound: without such rows the reading of the groups' fp32 sums, 64 (or 16) times 256
+// bytes a key, which the key pass has left in L2.  (The second half's code must not cost
+// the first its occupancy: with 112 registers a thread 2 x 512 queries over 8,012 keys
+// took 1,738 us, with 40, and spills in the second half alone, 1,677.)
+#include "backward_tile.cuh"
+
+namespace mla {
+
+namespace {
+
+using namespace bwd;
+
+constexpr int kUnits = 64;   // CTAs a tile
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ float bf16_value(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+
+// A lane's share of a row of a head: values 4 lane .. of 128, and 2 lane .. of 64.
+__device__ __forceinline__ void load4(const __nv_bfloat16* row, int lane, float* x) {
+  const uint2 w = *reinterpret_cast<const uint2*>(row + 4 * lane);
+  x[0] = __uint_as_float(w.x << 16);
+  x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+  x[2] = __uint_as_float(w.y << 16);
+  x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void load2(const __nv_bfloat16* row, int lane, float* x) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(row + 2 * lane);
+  x[0] = __uint_as_float(w << 16);
+  x[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ void save4(__nv_bfloat16* row, int lane, const float* x, float mul) {
+  *reinterpret_cast<uint2*>(row + 4 * lane) = make_uint2(bf16_pair(x[0] * mul, x[1] * mul), bf16_pair(x[2] * mul, x[3] * mul));
+}
+template <int kN>
+__device__ __forceinline__ bool any_odd(const float* x) {
+  bool odd = false;
+#pragma unroll
+  for (int e = 0; e < kN; ++e) odd |= !isfinite(x[e]);
+  return __any_sync(0xffffffffu, odd);
+}
+
+// One row of a head once more: dk before scaling (128 | 64 values) and dv of a key, or
+// dq, over its seen columns, one warp.
+template <bool kKeys>
+__device__ void row_again(const BackwardParams& p, const BackwardWs& L, const Tile& t, int r, int head, int lane, float* first, float* second) {
+  const size_t row = static_cast<size_t>(t.r0) + r;
+  const float c = p.scale * kLog2e;
+  const float* stats = reinterpret_cast<const float*>(p.ws + L.stats);
+  auto stat = [&](int i) { return stats + (static_cast<size_t>(t.stat + i / kTile) * kHeads + head) * 2 * kTile + i % kTile; };
+  auto q = [&](size_t i, float* x) {
+    load4(p.q_nope + i * p.qn_t + head * p.qn_h, lane, x);
+    load2(p.q_rope + i * p.qr_t + head * p.qr_h, lane, x + 4);
+  };
+  auto k = [&](size_t j, float* x) {
+    load4(p.k_nope + j * p.kn_t + head * p.kn_h, lane, x);
+    load2(p.k_rope + j * p.kr_t, lane, x + 4);
+  };
+  float a[6], b[4], x[6], y[4];
+#pragma unroll
+  for (int e = 0; e < 6; ++e) first[e] = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) second[e] = 0.f;
+  if constexpr (kKeys) {
+    k(row, a);
+    load4(p.v + row * p.v_t + head * p.v_h, lane, b);
+  } else {
+    q(row, a);
+    load4(p.d_out + row * p.do_t + head * p.do_h, lane, b);
+  }
+  const int from = kKeys ? max(0, t.lim + r) : 0, to = kKeys ? t.nc : min(t.nc, t.lim + r);
+  for (int i = from; i < to; ++i) {
+    const size_t col = static_cast<size_t>(t.c0) + i;
+    if constexpr (kKeys) {
+      q(col, x);
+      load4(p.d_out + col * p.do_t + head * p.do_h, lane, y);
+    } else {
+      k(col, x);
+      load4(p.v + col * p.v_t + head * p.v_h, lane, y);
+    }
+    float s = 0.f, dp = 0.f;
+#pragma unroll
+    for (int e = 0; e < 6; ++e) s += a[e] * x[e];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dp += b[e] * y[e];
+    const float* st = stat(kKeys ? i : r);
+    const float pr = fast_exp2(warp_sum(s) * c - __ldcg(st)), ds = bf16_value(pr * (warp_sum(dp) - __ldcg(st + kTile)));
+    bool all_nan = true;
+#pragma unroll
+    for (int e = 0; e < 6; ++e) {
+      first[e] += ds * x[e];
+      all_nan &= isnan(first[e]);
+    }
+    if constexpr (kKeys) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        second[e] += bf16_value(pr) * y[e];
+        all_nan &= isnan(second[e]);
+      }
+    }
+    if (__all_sync(0xffffffffu, all_nan)) break;
+  }
+}
+
+// The rows [r, end) of a tile that are not finite, one warp a row and head, or group of heads.
+__device__ __noinline__ void queries_again(const BackwardParams& p, const BackwardWs& L, const Tile t, int r, int end) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (; r < end; ++r)
+    for (int head = warp; head < kHeads; head += 8) {
+      const size_t row = static_cast<size_t>(t.r0) + r;
+      __nv_bfloat16 *dn = p.dq_nope + row * p.dqn_t + head * p.dqn_h, *dr = p.dq_rope + row * p.dqr_t + head * p.dqr_h;
+      float x[6], unused[4];
+      load4(dn, lane, x);
+      load2(dr, lane, x + 4);
+      if (!any_odd<6>(x)) continue;
+      row_again<false>(p, L, t, r, head, lane, x, unused);
+      save4(dn, lane, x, p.scale);
+      *reinterpret_cast<uint32_t*>(dr + 2 * lane) = bf16_pair(x[4] * p.scale, x[5] * p.scale);
+    }
+}
+__device__ __noinline__ void keys_again(const BackwardParams& p, const BackwardWs& L, const Tile t, int r, int end) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, groups = kHeads / L.group;
+  for (; r < end; ++r)
+    for (int g = warp; g < groups; g += 8) {
+      const size_t row = static_cast<size_t>(t.r0) + r;
+      float* part = reinterpret_cast<float*>(p.ws + L.rope) + (static_cast<size_t>(g) * p.nk + row) * kDr + 2 * lane;
+      float rope[2] = {part[0], part[1]};
+      const bool rope_odd = any_odd<2>(rope);
+      rope[0] = rope[1] = 0.f;
+      for (int head = g * L.group; head < (g + 1) * L.group; ++head) {
+        __nv_bfloat16 *dk = p.dk_nope + row * p.dkn_t + head * p.dkn_h, *dv = p.dv + row * p.dv_t + head * p.dv_h;
+        float x[6], y[4];
+        load4(dk, lane, x);
+        load4(dv, lane, y);
+        const bool k_odd = any_odd<4>(x), v_odd = any_odd<4>(y);
+        if (!rope_odd && !k_odd && !v_odd) continue;
+        row_again<true>(p, L, t, r, head, lane, x, y);
+        if (k_odd) save4(dk, lane, x, p.scale);
+        if (v_odd) save4(dv, lane, y, 1.f);
+        rope[0] += x[4];
+        rope[1] += x[5];
+      }
+      if (rope_odd) {
+        part[0] = rope[0];
+        part[1] = rope[1];
+      }
+    }
+}
+
+// CTAs [0, kUnits key_tiles): two keys of a tile, whose sums 16 threads a key and run of
+// groups with four values each form, then over the eight runs, in their order.  Those
+// behind them, where causal: a 64th of a query tile.
+__global__ void __launch_bounds__(256, 6) backward_last_kernel(const __grid_constant__ BackwardParams p, const __grid_constant__ BackwardWs L, int key_tiles, int query_rows) {
+  __shared__ float4 s_sum[2][8][16];
+  const BackwardPlan* plan = reinterpret_cast<const BackwardPlan*>(p.ws + L.plan);
+  const int i_tile = static_cast<int>(blockIdx.x) / kUnits, unit = static_cast<int>(blockIdx.x) % kUnits;
+  ptx::grid_dep_wait();
+  if (i_tile >= key_tiles) {
+    if (plan->odd[1] == 0 || i_tile - key_tiles >= plan->tiles[1]) return;
+    const Tile t = read_tile(reinterpret_cast<const Tile*>(p.ws + L.tiles[1]) + (i_tile - key_tiles));
+    const int per = query_rows / kUnits;
+    queries_again(p, L, t, per * unit, min(per * unit + per, t.rows));
+    return;
+  }
+  if (i_tile >= plan->tiles[0]) return;
+  const Tile t = read_tile(reinterpret_cast<const Tile*>(p.ws + L.tiles[0]) + i_tile);
+  const int k = threadIdx.x >> 7, run = (threadIdx.x >> 4) & 7, lane = threadIdx.x & 15, r = 2 * unit + k;
+  if (2 * unit >= t.rows) return;
+  if (plan->odd[0] != 0) {
+    keys_again(p, L, t, 2 * unit, min(2 * unit + 2, t.rows));
+    __syncthreads();
+  }
+  const size_t row = static_cast<size_t>(t.r0) + r;
+  const int per = kHeads / L.group / 8;   // 2 or 8 groups a run
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r < t.rows) {
+    const float4* part = reinterpret_cast<const float4*>(p.ws + L.rope) + (static_cast<size_t>(run * per) * p.nk + row) * (kDr / 4) + lane;
+#pragma unroll 8
+    for (int g = 0; g < per; ++g) {
+      const float4 x = __ldcs(part + static_cast<size_t>(g) * p.nk * (kDr / 4));
+      sum.x += x.x;
+      sum.y += x.y;
+      sum.z += x.z;
+      sum.w += x.w;
+    }
+  }
+  s_sum[k][run][lane] = sum;
+  __syncthreads();
+  if (run != 0 || r >= t.rows) return;
+#pragma unroll
+  for (int q = 1; q < 8; ++q) {
+    const float4 x = s_sum[k][q][lane];
+    sum.x += x.x;
+    sum.y += x.y;
+    sum.z += x.z;
+    sum.w += x.w;
+  }
+  *reinterpret_cast<uint2*>(p.dk_rope + row * p.dkr_t + 4 * lane) =
+      make_uint2(bf16_pair(sum.x * p.scale, sum.y * p.scale), bf16_pair(sum.z * p.scale, sum.w * p.scale));
+}
+
+}  // namespace
+
+cudaError_t launch_backward_last(const BackwardParams& p, const BackwardWs& L, int query_rows, cudaStream_t stream) {
+  // (no more query tiles of 256 rows than of 128)
+  const unsigned tiles = static_cast<unsigned>(L.max_tiles[0] + (p.causal ? L.max_tiles[1] : 0));
+  return launch_dependent(backward_last_kernel, dim3(tiles * kUnits), dim3(256), 0, stream, p, L, L.max_tiles[0], query_rows);
+}
+
+}  // namespace mla

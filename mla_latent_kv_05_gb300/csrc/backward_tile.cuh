@@ -233,6 +233,18 @@ template <bool kKeys>
 __device__ __forceinline__ void store_results(const BackwardParams& p, const BackwardWs& L, size_t row, int head, int head_group,
                                               int quarter, bool last, const uint32_t* nope, const uint32_t* second,
                                               const uint32_t* rope) {
+  if (!kKeys && p.causal) {
+    // 0 times every value: not 0 where one is not finite (backward_last.cu)
+    __nv_bfloat162 z[4];
+    const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+#pragma unroll
+    for (int e = 0; e < 24; ++e) {
+      const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(e < 16 ? nope + e : rope + e - 16);
+      z[e & 3] = e < 4 ? __hmul2(x, zero) : __hfma2(x, zero, z[e & 3]);
+    }
+    z[0] = __hadd2(__hadd2(z[0], z[1]), __hadd2(z[2], z[3]));
+    if ((*reinterpret_cast<const uint32_t*>(z) & 0x7FFF7FFFu) != 0) reinterpret_cast<BackwardPlan*>(p.ws + L.plan)->odd[1] = 1;
+  }
   __nv_bfloat16* dst = (kKeys ? p.dk_nope + row * p.dkn_t + head * p.dkn_h : p.dq_nope + row * p.dqn_t + head * p.dqn_h) + 32 * quarter;
   store16(dst, nope);
   store16(dst + 16, nope + 8);
