@@ -532,6 +532,13 @@ _RopeStrides = ctypes.c_size_t * 4
 
 def _vectors_arg(t, name: str, shape=None):
     """Address, token and head stride of a checked [rows, 64] or [rows, heads, 64] bf16 tensor or view."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda:     # (as _rows_arg)
+        size = t.shape
+        if len(size) == 3 and size[2] == 64 and size[0] > 1 and size[1] > 1 and (shape is None or size == shape):
+            s0, s1, s2 = t.stride()
+            at = t.data_ptr()
+            if s2 == 1 and s0 > 0 and s1 > 0 and s0 % 8 == 0 and s1 % 8 == 0 and at % 16 == 0:
+                return at, s0, s1
     if isinstance(t, torch.Tensor) and t.dim() not in (2, 3):
         raise ValueError(f"{name} must be [rows, 64] or [rows, heads, 64], got {tuple(t.shape)}")
     if isinstance(t, torch.Tensor) and shape is not None and t.shape != shape:
@@ -551,13 +558,19 @@ def mla_rope_bf16(x, positions, rope, out=None, inverse=False, stream=None):
     another that does not overlap x.  Returns out."""
     at, x_t, x_h = _vectors_arg(x, "x")
     table = _rope_arg(rope)
-    rows, heads = x.shape[0], x.shape[1] if x.dim() == 3 else 1
+    shape = x.shape
+    rows, heads = shape[0], shape[1] if len(shape) == 3 else 1
     _check(positions, "positions", torch.int32, (rows,))
+    device = x.device
     if out is None:
-        out = _new(stream, torch.empty, x.shape, dtype=torch.bfloat16, device=x.device)
-    to, o_t, o_h = (at, x_t, x_h) if out is x else _vectors_arg(out, "out", x.shape)
+        out = x.new_empty(shape) if stream is None else _new(stream, torch.empty, shape, dtype=torch.bfloat16, device=device)
+        to, o_t, o_h = out.data_ptr(), 64 * heads, 64
+    elif out is x:
+        to, o_t, o_h = at, x_t, x_h
+    else:
+        to, o_t, o_h = _vectors_arg(out, "out", shape)
     dev = torch.cuda.current_device()
-    if not (x.device == positions.device == out.device and x.device.index == dev):
+    if not (device == positions.device == out.device and device.index == dev):
         _same_device(dict(x=x, positions=positions, out=out), dev)
     if rows == 0 or heads == 0:
         return out
