@@ -10,12 +10,17 @@
 // and head, so the tensor cores bound it.  dk and dv are sums over queries, dq
 // over keys.  One pass would add dq tiles into global memory from every key tile,
 // with an order that changes from run to run and 98 KiB of fp32 traffic a tile.
-// Here two passes of one kernel compute S and dO V^T each: one holds 128 keys of
-// a head and streams its queries (dk and dv stay in tensor memory), the other
-// holds 128 queries and streams the keys (dq stays).  That is 640 + 512 units of
-// MMAs where 832 would be the least, every sum has a fixed order, and nothing is
-// added to global memory.  In the first the rope part of dk stays in tensor memory
-// over a group of heads; the groups' sums are added by a last small kernel.
+// Here the key pass holds 128 keys of a head and streams its queries (dk and dv stay in
+// tensor memory), and stores each dS tile, 32 KiB of bf16; backward_dq.cu multiplies
+// those with K.  Every sum has a fixed order, and nothing is added to global memory.  The
+// rope part of dk stays in tensor memory over a group of heads; backward_last.cu adds
+// the groups' sums.  The products are the least there are, 832 units of MMAs.
+// Where the workspace has no room for all dS tiles (4 GiB, 1024 tiles of every head; the
+// plan kernel counts them), the query pass computes dq instead: it holds 128 queries (or
+// 256, backward_pair.cu) and streams the keys, for S and dO V^T once more, 512 units
+// instead of 192.  Both sides measured: 4096 causal tokens (528 tiles) 1,493 us and
+// 1,600, 3 x 777 full 542 and 595, 8 x up to 1024 557 and 617, 2 x 512 queries over 8,012
+// keys 1,660 and 1,683, 5 x up to 33 64.7 and 66.7.
 //
 // One step is a 128 x 128 tile, rows = what is held, columns = what is streamed:
 //     S = R1 C1^T, dP = R2 C2^T (R1, C1: 192 values, R2, C2: 128), then
@@ -33,17 +38,18 @@
 //   P and dS (thread = a quarter row of 32 columns) and write the results.  S of the
 //   next step runs while dS of this one is computed, and the second products of this
 //   one while the next one's P is.
-// Long sequences' query pass runs on CTA pairs instead (backward_pair.cu).
-//
 // Measured (4096 causal tokens, 1.79 TFLOP of the five products, 952 us at the peak):
-// 1,598 us, 1,120 TFLOP/s; 3 x 777 full 595 (a floor of 205), 8 x up to 1024 613 (162),
-// 2 x 512 queries over 8,012 keys 1,676 (900), 5 x up to 33 66.7.  The key pass takes 940
-// of the first, of 599 that its MMAs need: S, its reading, dP and its reading follow one
-// another in one place of tensor memory, and S's MMAs find shared memory busy with the
-// copies (1,150 cycles of 768).  Tried for it and slower: two sets of eight warps on
-// alternate steps (2,110), streamed tiles multicast to clusters of two (1,830 instead of
-// 1,765), reading S and dP together (1,836 instead of 1,770), one warp that issues all
-// products (1,672 instead of 1,605).
+// 1,493 us, 1,200 TFLOP/s; 3 x 777 full 542 (a floor of 205), 8 x up to 1024 557 (162),
+// 2 x 512 queries over 8,012 keys 1,660 (900), 5 x up to 33 64.7.  The key pass takes
+// 1,017 of the first, of 599 that its MMAs need: S, its reading, dP and its reading
+// follow one another in one place of tensor memory, S's MMAs find shared memory busy with
+// the copies (1,150 cycles of 768), and storing dS costs 125.  Tried for it and slower:
+// two sets of eight warps on alternate steps (2,110 instead of 1,770 for the call),
+// streamed tiles multicast to clusters of two (1,830 instead of 1,765), reading S and dP
+// together (1,836 instead of 1,770), one warp that issues all products (1,672 instead of
+// 1,605), one thread instead of a warp that waits and issues (1,645 instead of 1,609),
+// chunks of R1 and R2 loaded one by one (1,705 instead of 1,600), four warps of their
+// own that store dS (1,510 instead of 1,494).
 //
 // Every wait is bounded, as in prefill.cu.
 #include <cmath>
@@ -69,7 +75,7 @@ enum Bar {
 constexpr uint32_t kOffTmem = kOffBar + 8 * NBAR;
 constexpr uint32_t kOffQuit = kOffTmem + 4;
 constexpr uint32_t kOffItems = (kOffQuit + 4 + 15) & ~15u;
-constexpr uint32_t kSmem = kOffItems + 48 * kItemSlots;
+constexpr uint32_t kSmem = kOffItems + kItemBytes * kItemSlots;
 static_assert(kSmem <= 232448, "shared memory budget");
 
 constexpr uint32_t kIdescS = ptx::idesc_bf16(128, 128, 0, 0);    // both K-major
@@ -82,11 +88,13 @@ constexpr uint32_t kIdesc192 = ptx::idesc_bf16(128, 192, 0, 1), kIdesc128 = ptx:
 constexpr int kClasses = 1024;
 constexpr int kTailItems = 5;   // items per CTA of the heads that are taken together at the end
 
-__global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParams p, const BackwardWs L, int ctas_k, int ctas_q, int query_rows) {
+__global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParams p, const BackwardWs L, int ctas_k, int ctas_q, int ctas_dq, int query_rows) {
   __shared__ int s_count[kClasses], s_warp[32], s_longest, s_shortest;
+  __shared__ unsigned long long s_slots;
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws);
   BackwardPlan* plan = reinterpret_cast<BackwardPlan*>(p.ws + L.plan);
-  int* base = reinterpret_cast<int*>(p.ws + L.base);
+  int *base_k = reinterpret_cast<int*>(p.ws + L.base[0]), *base = reinterpret_cast<int*>(p.ws + L.base[1]);
+  int* slots = reinterpret_cast<int*>(p.ws + L.slots);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ptx::grid_dep_launch();   // (what follows waits for this grid before it reads the plan)
   // inclusive sum over the CTA
@@ -107,21 +115,24 @@ __global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParam
     const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1), k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
     return Seq{q0, k0, q1 - q0, k1 - k0, q0 >= 0 && q1 >= q0 && q1 <= p.nq && k0 >= 0 && k1 >= k0 && k1 <= p.nk};
   };
-  int before = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += 1024) {
-    int tiles = 0;
-    if (b0 + tid < p.batch) {
-      const Seq s = sequence(b0 + tid);
-      if (s.ok) tiles = (s.nq + kTile - 1) / kTile;
-      else set_status(&hdr->status, MLA_STATUS_BAD_SEQ_LEN);
+  for (int side = 0; side < 2; ++side) {
+    int before = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 1024) {
+      int tiles = 0;
+      if (b0 + tid < p.batch) {
+        const Seq s = sequence(b0 + tid);
+        if (s.ok) tiles = ((side ? s.nq : s.nk) + kTile - 1) / kTile;
+        else set_status(&hdr->status, MLA_STATUS_BAD_SEQ_LEN);
+      }
+      const int sum = scan(tiles);
+      if (b0 + tid < p.batch) (side ? base : base_k)[b0 + tid] = before + sum - tiles;
+      __syncthreads();
+      if (tid == 1023) s_warp[0] = sum;
+      __syncthreads();
+      before += s_warp[0];
     }
-    const int sum = scan(tiles);
-    if (b0 + tid < p.batch) base[b0 + tid] = before + sum - tiles;
-    __syncthreads();
-    if (tid == 1023) s_warp[0] = sum;
-    __syncthreads();
-    before += s_warp[0];
   }
+  bool from_ds = false;   // (known after the key tiles' first count)
   for (int side = 0; side < 2; ++side) {
     Tile* tiles = reinterpret_cast<Tile*>(p.ws + L.tiles[side]);
     __syncthreads();
@@ -129,16 +140,20 @@ __global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParam
     if (tid == 0) {
       s_longest = 0;
       s_shortest = kClasses;
+      s_slots = 0;
     }
     __syncthreads();
     for (int pass = 0; pass < 2; ++pass) {
       for (int b = warp; b < p.batch; b += 32) {
         const Seq s = sequence(b);
         if (!s.ok) continue;
-        const int n = side ? s.nq : s.nk, rows = side ? query_rows : kTile, off = s.nk - s.nq;
-        for (int i = lane; i * rows < n; i += 32) {
+        const int n = side ? s.nq : s.nk, rows = side && !from_ds ? query_rows : kTile, off = s.nk - s.nq;
+        // (beyond the lists: overlapping sequences, cu decreased somewhere)
+        const bool fits = base[b] + (s.nq + kTile - 1) / kTile <= L.max_tiles[1] && base_k[b] + (s.nk + kTile - 1) / kTile <= L.max_tiles[0];
+        for (int i0 = 0; i0 * rows < n; i0 += 32) {
           Tile t;
-          const int at = i * rows;
+          const int i = i0 + lane, at = i * rows;
+          const bool tile = at < n;
           t.rows = min(rows, n - at);
           t.first = 0;
           if (side == 0) {
@@ -149,6 +164,18 @@ __global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParam
             if (p.causal) t.first = max(0, t.lim) / kTile;
             t.steps = max(0, (s.nq + kTile - 1) / kTile - t.first);
             t.stat = base[b];
+            // places of dS tiles, for 32 key tiles at once
+            const int mine = tile && fits ? t.steps : 0;
+            int sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int y = __shfl_up_sync(0xffffffffu, sum, o);
+              if (lane >= o) sum += y;
+            }
+            unsigned long long from = 0;
+            if (lane == 31) from = atomicAdd(&s_slots, static_cast<unsigned long long>(sum));
+            t.slot = static_cast<int>(__shfl_sync(0xffffffffu, from, 31)) + sum - mine - t.first;
+            if (pass == 1 && tile && fits) slots[base_k[b] + i] = t.slot;
           } else {
             t.r0 = s.q0 + at;
             t.c0 = s.k0;
@@ -157,7 +184,10 @@ __global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParam
             const int sees = p.causal ? max(0, min(s.nk, t.lim + t.rows - 1)) : s.nk;   // its last row
             t.steps = (sees + kTile - 1) / kTile;
             t.stat = base[b] + at / kTile;
+            t.slot = base_k[b];
           }
+          t.tile = i;
+          if (!tile) continue;
           const int steps = min(kClasses - 1, t.steps), c = kClasses - 1 - steps;
           if (pass == 0) {
             atomicMax(&s_longest, steps);
@@ -165,8 +195,7 @@ __global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParam
           }
           const int pos = atomicAdd(&s_count[c], 1);
           if (pass == 1) {
-            // (beyond the list: overlapping sequences, cu decreased somewhere)
-            if (pos < L.max_tiles[side] && base[b] + (s.nq + kTile - 1) / kTile <= L.max_tiles[1]) tiles[pos] = t;
+            if (pos < L.max_tiles[side] && fits) tiles[pos] = t;
             else {
               if (pos < L.max_tiles[side]) {
                 t.rows = t.steps = 0;
@@ -179,14 +208,18 @@ __global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParam
       }
       __syncthreads();
       if (pass == 0) {
+        if (side == 0) from_ds = ctas_k > 0 && s_slots <= static_cast<unsigned long long>(L.ds_tiles);
         // exclusive scan: s_count[c] becomes the first position of class c
         const int v = s_count[tid], x = scan(v);
         s_count[tid] = x - v;
+        if (tid == 0) s_slots = 0;   // (all have read it: scan's barriers)
         if (tid == 1023) {
-          const int n = min(x, L.max_tiles[side]), ctas = side ? ctas_q : ctas_k, groups = side ? kHeads : kHeads / L.group;
+          const int n = min(x, L.max_tiles[side]), ctas = side ? (from_ds ? ctas_dq : ctas_q) : ctas_k, groups = side ? kHeads : kHeads / L.group;
           plan->tiles[side] = n;
           plan->next[side] = ctas;
           plan->odd[side] = 0;
+          plan->stored = from_ds;
+          plan->query_rows = from_ds ? kTile : query_rows;
           // (as in prefill: not where all tiles are about as long)
           const bool even = 2 * s_longest <= 3 * s_shortest;
           plan->tail[side] = even ? 1 : min(groups, (kTailItems * ctas + n - 1) / max(n, 1));
@@ -203,12 +236,13 @@ __global__ void __launch_bounds__(1024) backward_plan_kernel(const BackwardParam
 // CTA, 16 threads a row and head, whose loads are all in flight together.
 constexpr int kDeltaRows = 32;
 
-__global__ void __launch_bounds__(256) backward_delta_kernel(const BackwardParams p, const BackwardWs L, int query_rows) {
+__global__ void __launch_bounds__(256) backward_delta_kernel(const BackwardParams p, const BackwardWs L) {
   __shared__ float s_delta[8][kDeltaRows];
   BackwardPlan* plan = reinterpret_cast<BackwardPlan*>(p.ws + L.plan);
-  const int parts = query_rows / kDeltaRows, i_tile = static_cast<int>(blockIdx.x) / parts, part = static_cast<int>(blockIdx.x) % parts;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
+  const int parts = *reinterpret_cast<const volatile int*>(&plan->query_rows) / kDeltaRows;
+  const int i_tile = static_cast<int>(blockIdx.x) / parts, part = static_cast<int>(blockIdx.x) % parts;
   if (i_tile >= *reinterpret_cast<const volatile int*>(&plan->tiles[1])) return;
   const Tile t = reinterpret_cast<const Tile*>(p.ws + L.tiles[1])[i_tile];
   // (a stat tile is 128 rows: those past the sequence's end get zeros)
@@ -261,13 +295,6 @@ __global__ void __launch_bounds__(256) backward_delta_kernel(const BackwardParam
 }
 
 // ---------------------------------------------------------------- the two passes
-// (Without a cache hint, with which concurrent copies of all SMs reached 110 GB/s an SM
-// instead of 190.)
-__device__ __forceinline__ void load_4d(uint32_t dst, const void* tmap, uint32_t bar, int x, int row, int chunk, int head) {
-  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
-               :: "r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(row), "r"(chunk), "r"(head) : "memory");
-}
-
 // kKeys: rows are keys (dk, dv), else queries (dq).
 template <bool kKeys>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -306,12 +333,13 @@ backward_kernel(const __grid_constant__ PassMaps maps, const __grid_constant__ B
   const bool smem_ok = (sbase & 1023u) == 0;
   if (threadIdx.x == 0 && !smem_ok) set_status(&hdr->status, MLA_ERR_UNSUPPORTED);
   const int causal = p.causal;
+  const bool keep = kKeys && stored(plan);   // dS, for dq
 
   struct Walk { int slot = 0; uint32_t phase = 0; };
   // The next item of this role's walk: its tile and first head, false when there is none.
   auto next_warp = [&](Walk& w, Tile& t, int& head) {
     if (!wait_cta_warp(BAR(IFULL + w.slot), w.phase, quit)) return false;
-    read_item(smem + kOffItems + 48 * w.slot, t, head);
+    read_item(smem + kOffItems + kItemBytes * w.slot, t, head);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(BAR(IEMPTY + w.slot));
     if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
@@ -341,13 +369,13 @@ backward_kernel(const __grid_constant__ PassMaps maps, const __grid_constant__ B
     regs_issue();
     if (elect_one()) {
       const Tile* tiles = reinterpret_cast<const Tile*>(p.ws + L.tiles[kSide]);
-      const Schedule sched(plan, kSide, groups);
+      const Schedule sched(plan, kSide, groups, !kKeys && stored(plan));
       Walk w;
       uint32_t loads = 0, loads2 = 0;
       bool ok = true;
       int item = static_cast<int>(blockIdx.x);
       while (ok) {
-        Tile t = {0, 0, 0, 0, 0, 0, 0, 0};
+        Tile t = {};
         int tile, head0 = -1;
         if (sched.find(item, tile, head0)) {
           t = read_tile(tiles + tile);
@@ -355,7 +383,7 @@ backward_kernel(const __grid_constant__ PassMaps maps, const __grid_constant__ B
         }
         ok = wait_cta(BAR(IEMPTY + w.slot), w.phase ^ 1u, quit);
         if (!ok) break;
-        write_item(smem + kOffItems + 48 * w.slot, t, head0);
+        write_item(smem + kOffItems + kItemBytes * w.slot, t, head0);
         ptx::mbar_arrive(BAR(IFULL + w.slot));
         if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
         if (head0 < 0) break;
@@ -664,6 +692,13 @@ backward_kernel(const __grid_constant__ PassMaps maps, const __grid_constant__ B
           tmem_st16(y_addr, pk);
           ptx::tmem_wait_st();
           arrive(DSREADY);
+          if (kKeys && keep) {
+            if (!mine) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = 0;
+            }
+            store_ds(p.ws + L.ds + (static_cast<size_t>(t.slot + t.first + i) * kHeads + head) * kDsTile, r, quarter, pk);
+          }
         }
         if (!ok) break;
         // results of the head
@@ -716,35 +751,39 @@ int backward_rows(const BackwardParams& p) {
 
 }  // namespace
 
-cudaError_t launch_backward(PFN_cuTensorMapEncodeTiled_v12000 encode, const BackwardParams& p, int sms,
-                            cudaStream_t stream) {
+cudaError_t launch_backward(PFN_cuTensorMapEncodeTiled_v12000 encode, BackwardParams p, int sms, cudaStream_t stream) {
   const BackwardWs L = backward_ws(p.batch, p.nq, p.nk);
-  const int query_rows = backward_rows(p), most[2] = {sms, sms * kTile / query_rows};
-  int clusters[2];
-  for (int side = 0; side < 2; ++side) {
+  const int query_rows = backward_rows(p);
+  auto ctas = [&](int side, int most) {
     const long long items = static_cast<long long>(L.max_tiles[side]) * (side ? kHeads : kHeads / L.group);
-    clusters[side] = static_cast<int>(items < most[side] ? items : most[side]);
-  }
-  cudaError_t e = launch_kernel(backward_plan_kernel, dim3(1), dim3(1024), 0, stream, p, L, clusters[0], clusters[1], query_rows);
+    return static_cast<int>(items < most ? items : most);
+  };
+  const int keys = ctas(0, sms), queries = ctas(1, sms * kTile / query_rows), dq = ctas(1, sms);
+  // the query pass is needed where not all dS tiles may find room, or there is no key pass
+  const bool query_pass = queries > 0 && (!L.ds_always || keys == 0);
+  p.key_waits = !query_pass;
+  cudaError_t e = launch_kernel(backward_plan_kernel, dim3(1), dim3(1024), 0, stream, p, L, keys, queries, dq, query_rows);
   PassMaps maps;
   static std::atomic<uint64_t> configured_q{0}, configured_k{0};
-  if (e == cudaSuccess && clusters[1]) {
+  if (e == cudaSuccess && queries)
     e = launch_dependent(backward_delta_kernel, dim3(L.max_tiles[1] * (query_rows / kDeltaRows), kHeads / 8), dim3(256), 0, stream,
-                         p, L, query_rows);
-    if (e == cudaSuccess && !pass_maps(encode, p, false, query_rows == kTile ? kTile : kTile / 2, &maps)) e = cudaErrorInvalidValue;
+                         p, L);
+  if (e == cudaSuccess && query_pass) {
+    if (!pass_maps(encode, p, false, query_rows == kTile ? kTile : kTile / 2, &maps)) e = cudaErrorInvalidValue;
     if (e == cudaSuccess && query_rows > kTile) {
-      e = launch_backward_pairs(maps, p, L, clusters[1], stream);
+      e = launch_backward_pairs(maps, p, L, queries, stream);
     } else if (e == cudaSuccess) {
       e = allow_smem(backward_kernel<false>, kSmem, configured_q);
       if (e == cudaSuccess)
-        e = launch_dependent(backward_kernel<false>, dim3(clusters[1]), dim3(kThreads), kSmem, stream, maps, p, L);
+        e = launch_dependent(backward_kernel<false>, dim3(queries), dim3(kThreads), kSmem, stream, maps, p, L);
     }
   }
-  if (e == cudaSuccess && clusters[0]) {
+  if (e == cudaSuccess && keys) {
     if (!pass_maps(encode, p, true, kTile, &maps)) e = cudaErrorInvalidValue;
     if (e == cudaSuccess) e = allow_smem(backward_kernel<true>, kSmem, configured_k);
-    if (e == cudaSuccess) e = launch_dependent(backward_kernel<true>, dim3(clusters[0]), dim3(kThreads), kSmem, stream, maps, p, L);
-    if (e == cudaSuccess) e = launch_backward_last(p, L, query_rows, stream);
+    if (e == cudaSuccess) e = launch_dependent(backward_kernel<true>, dim3(keys), dim3(kThreads), kSmem, stream, maps, p, L);
+    if (e == cudaSuccess && queries) e = launch_backward_dq(encode, p, L, dq, stream);
+    if (e == cudaSuccess) e = launch_backward_last(p, L, stream);
   }
   return e;
 }

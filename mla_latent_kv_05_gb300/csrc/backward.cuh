@@ -17,20 +17,27 @@ struct BackwardParams {
   __nv_bfloat16 *dq_nope, *dq_rope, *dk_nope, *dk_rope, *dv;
   long long dqn_t, dqn_h, dqr_t, dqr_h, dkn_t, dkn_h, dkr_t, dv_t, dv_h;
   uint8_t* ws;
+  int key_waits;   // the key pass follows a kernel of this call that it has to wait for (begin_pass)
 };
 
 // Behind the plan header.
 struct BackwardPlan {
   int tiles[2], next[2], tail[2];   // [0] key tiles, [1] query tiles
+  int stored, query_rows;           // dq comes from stored dS tiles; rows of a query tile
   int odd[2];                       // where causal, the pass may have results that are not finite
 };
 
 // Workspace: header and plan; the first query tile of each sequence; the key tiles
 // and the query tiles; per query tile and head 128 values lse log2(e) and 128 values
-// of sum(d_out out) - d_lse; the key-RoPE gradients of `group` heads each, fp32.
+// of sum(d_out out) - d_lse; the key-RoPE gradients of `group` heads each, fp32; the
+// place of each key tile's first dS tile, and the dS tiles of all heads.
+constexpr size_t kDsTile = 2 * kBackwardTile * kBackwardTile;   // bytes
+constexpr long long kMaxDsTiles = 1024;                         // 4 GiB with all heads
+constexpr size_t kTileBytes = 48;
 struct BackwardWs {
-  size_t plan, base, tiles[2], stats, rope, total;
-  int max_tiles[2], group;
+  size_t plan, base[2], tiles[2], stats, rope, slots, ds, total;
+  int max_tiles[2], group, ds_tiles;
+  bool ds_always;   // there is room for all tiles, whatever the sequences' lengths
 };
 inline BackwardWs backward_ws(int batch, int nq, int nk) {
   BackwardWs w;
@@ -43,12 +50,20 @@ inline BackwardWs backward_ws(int batch, int nq, int nk) {
   // with one, two or eight
   w.group = static_cast<long long>(w.max_tiles[0]) * kHeads / 8 >= 8 * 152 ? 8 : 2;
   w.plan = align256(sizeof(PlanHeader));
-  w.base = align256(w.plan + sizeof(BackwardPlan));
-  w.tiles[0] = align256(w.base + sizeof(int) * static_cast<size_t>(batch));
-  w.tiles[1] = align256(w.tiles[0] + 32 * static_cast<size_t>(w.max_tiles[0]));
-  w.stats = align256(w.tiles[1] + 32 * static_cast<size_t>(w.max_tiles[1]));
+  w.base[0] = align256(w.plan + sizeof(BackwardPlan));
+  w.base[1] = align256(w.base[0] + sizeof(int) * static_cast<size_t>(batch));
+  w.tiles[0] = align256(w.base[1] + sizeof(int) * static_cast<size_t>(batch));
+  w.tiles[1] = align256(w.tiles[0] + kTileBytes * static_cast<size_t>(w.max_tiles[0]));
+  w.stats = align256(w.tiles[1] + kTileBytes * static_cast<size_t>(w.max_tiles[1]));
   w.rope = align256(w.stats + sizeof(float) * 2 * kBackwardTile * kHeads * static_cast<size_t>(w.max_tiles[1]));
-  w.total = align256(w.rope + sizeof(float) * kDr * (kHeads / w.group) * static_cast<size_t>(nk));
+  w.slots = align256(w.rope + sizeof(float) * kDr * (kHeads / w.group) * static_cast<size_t>(nk));
+  w.ds = align256(w.slots + sizeof(int) * static_cast<size_t>(w.max_tiles[0]));
+  // a sequence has no more tiles along one axis than all tokens would have together
+  const long long by_q = (nq + kBackwardTile - 1ll) / kBackwardTile * w.max_tiles[0],
+                  by_k = (nk + kBackwardTile - 1ll) / kBackwardTile * w.max_tiles[1], most = by_q < by_k ? by_q : by_k;
+  w.ds_always = most <= kMaxDsTiles;
+  w.ds_tiles = static_cast<int>(w.ds_always ? most : kMaxDsTiles);
+  w.total = align256(w.ds + kDsTile * kHeads * static_cast<size_t>(w.ds_tiles));
   return w;
 }
 
@@ -56,9 +71,11 @@ inline BackwardWs backward_ws(int batch, int nq, int nk) {
 struct PassMaps;
 cudaError_t launch_backward_pairs(const PassMaps& maps, const BackwardParams& p, const BackwardWs& L, int pairs,
                                   cudaStream_t stream);
+// dq from stored dS tiles.
+cudaError_t launch_backward_dq(PFN_cuTensorMapEncodeTiled_v12000 encode, const BackwardParams& p, const BackwardWs& L, int ctas,
+                               cudaStream_t stream);
 // The sums of the RoPE part of dk, and rows that values outside the mask have spoilt.
-cudaError_t launch_backward_last(const BackwardParams& p, const BackwardWs& L, int query_rows, cudaStream_t stream);
-cudaError_t launch_backward(PFN_cuTensorMapEncodeTiled_v12000 encode, const BackwardParams& p, int sms,
-                            cudaStream_t stream);
+cudaError_t launch_backward_last(const BackwardParams& p, const BackwardWs& L, cudaStream_t stream);
+cudaError_t launch_backward(PFN_cuTensorMapEncodeTiled_v12000 encode, BackwardParams p, int sms, cudaStream_t stream);
 
 }  // namespace mla

@@ -166,7 +166,7 @@ __device__ __noinline__ void keys_again(const BackwardParams& p, const BackwardW
 // CTAs [0, kUnits key_tiles): two keys of a tile, whose sums 16 threads a key and run of
 // groups with four values each form, then over the eight runs, in their order.  Those
 // behind them, where causal: a 64th of a query tile.
-__global__ void __launch_bounds__(256, 6) backward_last_kernel(const __grid_constant__ BackwardParams p, const __grid_constant__ BackwardWs L, int key_tiles, int query_rows) {
+__global__ void __launch_bounds__(256, 6) backward_last_kernel(const __grid_constant__ BackwardParams p, const __grid_constant__ BackwardWs L, int key_tiles) {
   __shared__ float4 s_sum[2][8][16];
   const BackwardPlan* plan = reinterpret_cast<const BackwardPlan*>(p.ws + L.plan);
   const int i_tile = static_cast<int>(blockIdx.x) / kUnits, unit = static_cast<int>(blockIdx.x) % kUnits;
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(256, 6) backward_last_kernel(const __grid_cons
   if (i_tile >= key_tiles) {
     if (plan->odd[1] == 0 || i_tile - key_tiles >= plan->tiles[1]) return;
     const Tile t = read_tile(reinterpret_cast<const Tile*>(p.ws + L.tiles[1]) + (i_tile - key_tiles));
-    const int per = query_rows / kUnits;
+    const int per = plan->query_rows / kUnits;
     queries_again(p, L, t, per * unit, min(per * unit + per, t.rows));
     return;
   }
@@ -217,10 +217,10 @@ __global__ void __launch_bounds__(256, 6) backward_last_kernel(const __grid_cons
 
 }  // namespace
 
-cudaError_t launch_backward_last(const BackwardParams& p, const BackwardWs& L, int query_rows, cudaStream_t stream) {
+cudaError_t launch_backward_last(const BackwardParams& p, const BackwardWs& L, cudaStream_t stream) {
   // (no more query tiles of 256 rows than of 128)
   const unsigned tiles = static_cast<unsigned>(L.max_tiles[0] + (p.causal ? L.max_tiles[1] : 0));
-  return launch_dependent(backward_last_kernel, dim3(tiles * kUnits), dim3(256), 0, stream, p, L, L.max_tiles[0], query_rows);
+  return launch_dependent(backward_last_kernel, dim3(tiles * kUnits), dim3(256), 0, stream, p, L, L.max_tiles[0]);
 }
 
 }  // namespace mla

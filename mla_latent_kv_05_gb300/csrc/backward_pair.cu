@@ -1,4 +1,4 @@
-// The query pass of the backward pass (backward.cu) on CTA pairs: dq.
+// The query pass of the backward pass (backward.cu) on CTA pairs: dq, where dS is not stored.
 //
 // A pair holds 256 queries, 128 in each CTA, and streams tiles of 128 keys past them
 // with cta_group::2 MMAs, each of which reads its second operand half from either
@@ -6,8 +6,8 @@
 // dP (all that shared memory gives in that time, and the copies come on top: an S
 // took 1200 cycles instead of 768), each CTA of a pair reads 6, and 3 instead of 6
 // for dq; and the streamed tiles' shares are small enough to be held twice.
-// Measured: 2,580 cycles a step against 3,450 (of 2,048 of MMAs), 4096 causal tokens
-// 1,605 us a call against 1,695; 3 x 777 full 597 and 615, 2 x 512 queries over 7,500
+// Measured, with nothing stored: 2,580 cycles a step against 3,450 (of 2,048 of MMAs),
+// 4096 causal tokens 1,605 us a call against 1,695; 3 x 777 full 597 and 615, 2 x 512 queries over 7,500
 // keys more 1,686 and 1,808.  Not for short sequences (backward_rows): a pair's tiles
 // of 256 rows are half empty in them (8 x up to 1024 tokens 648 us instead of 611).
 // Nor for the key pass, whose S and dP share one place in tensor memory: every
@@ -58,7 +58,7 @@ enum Bar {
 constexpr uint32_t kOffTmem = kOffBar + 8 * NBAR;
 constexpr uint32_t kOffNext = kOffTmem + 4;                      // item numbers for rank 1
 constexpr uint32_t kOffItems = (kOffNext + 4 * kItemSlots + 15) & ~15u;
-constexpr uint32_t kSmem = kOffItems + 48 * kItemSlots;
+constexpr uint32_t kSmem = kOffItems + kItemBytes * kItemSlots;
 static_assert(kSmem <= 232448, "shared memory budget");
 
 constexpr uint32_t kIdescS = ptx::idesc_bf16(256, 128, 0, 0);    // both K-major
@@ -118,7 +118,7 @@ backward_pair_kernel(const __grid_constant__ PassMaps maps, const __grid_constan
   // The next item of this role's walk: its tile and first head, false when there is none.
   auto next_warp = [&](Walk& w, Tile& t, int& head) {
     if (!wait_short_warp(BAR(IFULL + w.slot), w.phase, hdr)) return false;
-    read_item(smem + kOffItems + 48 * w.slot, t, head);
+    read_item(smem + kOffItems + kItemBytes * w.slot, t, head);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(BAR(IEMPTY + w.slot));
     if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
@@ -158,7 +158,7 @@ backward_pair_kernel(const __grid_constant__ PassMaps maps, const __grid_constan
     regs_issue();
     if (elect_one()) {
       const Tile* tiles = reinterpret_cast<const Tile*>(p.ws + L.tiles[1]);
-      const Schedule sched(plan, 1, kHeads);
+      const Schedule sched(plan, 1, kHeads, stored(plan));
       Walk w;
       uint32_t loads = 0;
       bool ok = true;
@@ -177,12 +177,12 @@ backward_pair_kernel(const __grid_constant__ PassMaps maps, const __grid_constan
           item = *reinterpret_cast<volatile int*>(smem + kOffNext + 4 * w.slot);
           ptx::mbar_arrive_remote(LEAD(ITEMACK + w.slot));
         }
-        Tile t = {0, 0, 0, 0, 0, 0, 0, 0};
+        Tile t = {};
         int tile, head = -1;
         if (sched.find(item, tile, head)) t = read_tile(tiles + tile);
         ok = wait_short(BAR(IEMPTY + w.slot), w.phase ^ 1u, hdr);
         if (!ok) break;
-        write_item(smem + kOffItems + 48 * w.slot, t, head);
+        write_item(smem + kOffItems + kItemBytes * w.slot, t, head);
         ptx::mbar_arrive(BAR(IFULL + w.slot));
         if (++w.slot == kItemSlots) { w.slot = 0; w.phase ^= 1u; }
         if (head < 0) break;

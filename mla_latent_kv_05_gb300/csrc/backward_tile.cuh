@@ -6,14 +6,14 @@
 namespace mla {
 namespace bwd {
 
-// Everything before it overlaps what precedes the pass in the stream.  The query pass
-// waits for the statistics and then lets the key pass begin where one of its CTAs has
-// left: that one needs the statistics too, which are complete by then, and nothing of
-// the query pass.  It waits for it at its own end, so that the call is over when both
-// are.
+// Everything before it overlaps what precedes the pass in the stream.  The query pass,
+// where there is one, waits for the statistics and then lets the key pass begin where
+// one of its CTAs has left: that one needs the statistics too, which are complete by
+// then, and nothing of the query pass.  It waits for it at its own end, so that the call
+// is over when both are.
 template <bool kKeys>
 __device__ __forceinline__ void begin_pass(const BackwardParams& p) {
-  if (!kKeys || p.nq == 0) ptx::grid_dep_wait();   // (without queries nothing lies between plan and key pass)
+  if (!kKeys || p.key_waits) ptx::grid_dep_wait();   // (where no query pass lies between)
   ptx::grid_dep_launch();
 }
 
@@ -48,8 +48,12 @@ struct Tile {
   int first;      // first column tile
   int steps;      // column tiles
   int stat;       // query tile (of 128) of column tile 0 (keys), or of the rows' first (queries)
+  int slot;       // place of the dS tile of column tile 0 (keys), or the sequence's first key tile (queries)
+  int tile;       // of its sequence
+  int unused[2];
 };
-static_assert(sizeof(Tile) == 32, "tile record");
+static_assert(sizeof(Tile) == kTileBytes, "tile record");
+constexpr uint32_t kItemBytes = 64;
 
 }  // namespace bwd
 
@@ -104,7 +108,8 @@ inline bool pass_maps(PFN_cuTensorMapEncodeTiled_v12000 encode, const BackwardPa
 // and the statistics, which are complete by then.)
 __device__ __forceinline__ Tile read_tile(const Tile* at) {
   const int4 a = __ldcg(reinterpret_cast<const int4*>(at)), b = __ldcg(reinterpret_cast<const int4*>(at) + 1);
-  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const int2 c = __ldcg(reinterpret_cast<const int2*>(at) + 4);
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y};
 }
 
 // An item in shared memory: its tile, and its first head (-1: no more items).
@@ -113,22 +118,35 @@ __device__ __forceinline__ void write_item(uint8_t* at, const Tile& t, int head)
   dst[0] = t.r0; dst[1] = t.rows; dst[2] = t.c0; dst[3] = t.nc; dst[4] = t.lim; dst[5] = t.first; dst[6] = t.steps;
   dst[7] = t.stat;
   dst[8] = head;
+  dst[9] = t.slot;
+  dst[10] = t.tile;
 }
 __device__ __forceinline__ void read_item(const uint8_t* at, Tile& t, int& head) {
   const volatile int* src = reinterpret_cast<const volatile int*>(at);
   t.r0 = src[0]; t.rows = src[1]; t.c0 = src[2]; t.nc = src[3]; t.lim = src[4]; t.first = src[5]; t.steps = src[6];
   t.stat = src[7];
   head = src[8];
+  t.slot = src[9];
+  t.tile = src[10];
+}
+
+__device__ __forceinline__ bool stored(const BackwardPlan* plan) { return *reinterpret_cast<const volatile int*>(&plan->stored) != 0; }
+
+// (Without a cache hint, with which concurrent copies of all SMs reached 110 GB/s an SM
+// instead of 190.)
+__device__ __forceinline__ void load_4d(uint32_t dst, const void* tmap, uint32_t bar, int x, int row, int chunk, int head) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+               :: "r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(row), "r"(chunk), "r"(head) : "memory");
 }
 
 // Items in the order in which they are handed out: head group by head group, and
 // the last groups tile by tile (as in prefill).
 struct Schedule {
   int n_tiles, tail, groups, items, first_late;
-  __device__ Schedule(const BackwardPlan* plan, int side, int groups) : groups(groups) {
+  __device__ Schedule(const BackwardPlan* plan, int side, int groups, bool off) : groups(groups) {
     n_tiles = *reinterpret_cast<const volatile int*>(&plan->tiles[side]);
     tail = *reinterpret_cast<const volatile int*>(&plan->tail[side]);
-    items = n_tiles * groups;
+    items = off ? 0 : n_tiles * groups;
     first_late = items - n_tiles * tail;
   }
   __device__ bool find(int item, int& tile, int& head_group) const {
@@ -225,6 +243,18 @@ __device__ __forceinline__ void regs_compute() { asm volatile("setmaxnreg.inc.sy
 __device__ __forceinline__ void store16(__nv_bfloat16* dst, const uint32_t* v) {
   reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+}
+
+// A quarter row of dS, 32 columns of key r, to its place in the tile that the product with
+// K reads: halves of 64 keys, of which each has 16 columns of 8 queries, a key's 16 bytes
+// behind the last key's (MN-major without swizzle, so that a warp writes 512 bytes in a
+// row: the key pass of 4096 tokens takes 1,017 us; as 128-byte rows in the swizzled order
+// 1,080, without storing 890).  Written to leave L2 first: 1,660 us instead of 1,674 for
+// 2 x 512 queries over 8,012 keys.
+__device__ __forceinline__ void store_ds(uint8_t* tile, int r, int quarter, const uint32_t* pk) {
+  uint4* at = reinterpret_cast<uint4*>(tile + (r >> 6) * 16384 + quarter * 4096 + (r & 63) * 16);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) __stcs(at + 64 * e, make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]));
 }
 
 // A quarter row of a head's results: 32 values of dk (or dq) and of dv as bf16, 16 of

@@ -23,10 +23,10 @@ def stall_lib():
                                      out_dir=d))
 
 
-@pytest.mark.parametrize("nq", [[300, 7], [1300]], ids=["one CTA", "pairs"])
-def test_a_wait_that_runs_out_ends_the_call_with_timeout_status(cuda_device, stall_lib, nq):
-    d = make(nq, nq, seed=31)
-    ws = binding.alloc_workspace_prefill_backward(len(nq), sum(nq), sum(nq))
+@pytest.mark.parametrize("nq,nk", [([300, 7], [300, 7]), ([300], [45000]), ([520], [33000])], ids=["stored", "128", "256"])
+def test_a_wait_that_runs_out_ends_the_call_with_timeout_status(cuda_device, stall_lib, nq, nk):
+    d = make(nq, nk, seed=31)
+    ws = binding.alloc_workspace_prefill_backward(len(nq), sum(nq), sum(nk))
     want = run(d, workspace=ws)
     assert binding.mla_get_status(ws) == 0
     normal = binding.load()

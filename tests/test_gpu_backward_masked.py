@@ -98,11 +98,11 @@ def test_all_of_a_sequence_not_finite(cuda_device):
     check_rows(got, d, NAMES, list(range(200, 500)), "finite")
 
 
-# both query forms by their sequences' lengths
+# lengths for which tiles of 256 queries would do, and others, with dS stored
 @pytest.mark.parametrize("nq,nk,causal", [([1300], [1300], True), ([900, 1, 600], [1000, 3000, 2600], True),
                                           ([420, 410], [77, 1000], False), ([1, 900], [2, 900], False), ([385], [7000], True)],
                          ids=["1300", "mixed", "full", "one and 900", "385 of 7000"])
-def test_gradients_on_both_query_forms(cuda_device, nq, nk, causal):
+def test_gradients_of_stored_scores(cuda_device, nq, nk, causal):
     d = make(nq, nk, seed=25, causal=causal)
     ws = binding.alloc_workspace_prefill_backward(len(nq), sum(nq), sum(nk))
     got = run(d, causal, workspace=ws)
@@ -110,3 +110,42 @@ def test_gradients_on_both_query_forms(cuda_device, nq, nk, causal):
     for a, b in zip(run(d, causal, workspace=ws), got):
         assert torch.equal(a, b)
     assert binding.mla_get_status(ws) == 0
+
+
+# more than 1024 tiles of scores, which find no room in the workspace: query tiles of 256 and of 128; and just 1024
+LONG = [([520, 7], [33000, 70], True), ([520, 7], [33000, 70], False), ([300], [45000], True), ([140, 30], [60000, 18000], False),
+        ([512], [32768], False)]
+
+
+@pytest.mark.parametrize("nq,nk,causal", LONG, ids=["520 causal", "520 full", "300 causal", "140 and 30 full", "1024 tiles"])
+def test_gradients_without_stored_scores(cuda_device, nq, nk, causal):
+    d = make(nq, nk, seed=26, causal=causal)
+    ws = binding.alloc_workspace_prefill_backward(len(nq), sum(nq), sum(nk))
+    got = run(d, causal, workspace=ws)
+    check(got, d, causal, SCALE)
+    for a, b in zip(run(d, causal, workspace=ws), got):
+        assert torch.equal(a, b)
+    # the same workspace for short sequences, and back
+    e = make([40, 200], [40, 250], seed=27)
+    check(run(e, workspace=ws), e, True, SCALE)
+    for a, b in zip(run(d, causal, workspace=ws), got):
+        assert torch.equal(a, b)
+    assert binding.mla_get_status(ws) == 0
+
+
+@pytest.mark.parametrize("nq,nk", [(520, 33000), (300, 45000)], ids=["256", "128"])
+@pytest.mark.parametrize("key", ["k_nope", "q_nope", "d_out"])
+def test_masked_rows_without_stored_scores(cuda_device, nq, nk, key):
+    d = make([nq], [nk], seed=28)
+    row = 150
+    if key == "k_nope":
+        d[key][nk - nq + row] = NAN
+    else:
+        d[key][row] = NAN
+    d["out"], d["lse"] = binding.mla_prefill_bf16(d["q_nope"], d["q_rope"], d["k_nope"], d["k_rope"], d["v"], d["cu_q"],
+                                                  d["cu_k"], SCALE)
+    got = run(d)
+    check_rows(got, d, NAMES[:2], list(range(row)), key)
+    if key in ("q_nope", "d_out"):
+        check_rows(got, d, NAMES[:2], list(range(row + 1, nq)), key)
+        check_rows(got, d, NAMES[2:], list(range(nk - nq + row + 1, nk)), key)
