@@ -754,6 +754,12 @@ int mla_prefill_backward_bf16(const uint16_t* d_out, const float* d_lse, const u
     return MLA_ERR_INVALID_ARG;
   if (workspace_bytes < backward_ws(batch, num_q, num_k).total) return MLA_ERR_WORKSPACE;
   if (batch == 0 || (num_q == 0 && num_k == 0)) return MLA_OK;
+  // in place, or two results in one place (other overlaps of views are the caller's to avoid)
+  const uint16_t* const tensors[12] = {dq_nope, dq_rope, dk_nope, dk_rope, dv, d_out, q_nope, q_rope, k_nope, k_rope, v, out};
+  const int rows_of[12] = {num_q, num_q, num_k, num_k, num_k, num_q, num_q, num_q, num_k, num_k, num_k, num_q};
+  for (int i = 0; i < 5; ++i)
+    for (int j = i + 1; j < 12; ++j)
+      if (rows_of[i] > 0 && rows_of[j] > 0 && tensors[i] == tensors[j]) return MLA_ERR_INVALID_ARG;
   auto fn = encode_fn();
   const int sms = sm_count();
   if (!fn || sms <= 0) return MLA_ERR_CUDA;

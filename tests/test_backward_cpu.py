@@ -150,6 +150,7 @@ def test_backward_entry_refuses_on_the_host(lib):
     assert lib.mla_workspace_size_prefill_backward(2, 300, 300, ctypes.byref(n)) == 0
     assert call(n=n.value - 1) == -3
     assert call(batch=0) == 0 and call(num_q=0, num_k=0) == 0
+    assert call() == -1                      # results in the place of inputs and of one another
     assert lib.mla_workspace_size_prefill_backward(2, 300, 300, None) == -1
     assert lib.mla_workspace_size_prefill_backward(-1, 300, 300, ctypes.byref(n)) == -1
     assert lib.mla_workspace_size_prefill_backward(1 << 17, 300, 300, ctypes.byref(n)) == -2

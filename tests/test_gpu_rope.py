@@ -285,3 +285,49 @@ def test_append_in_a_captured_graph_and_on_another_stream(cuda_device, fmt):
     t.scale = 1.0
     assert torch.equal(cache.cpu(), want)
     assert torch.equal(y, binding.mla_rope_bf16(q, pos, t))
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_a_prompt_and_drafted_nodes_as_they_are_served(cuda_device, interleaved):
+    """Rotation, append, gather, expansion, prefill and tree decode in a row, against the oracles on exactly rotated rows."""
+    from oracle import expanded, mla_oracle
+    g = torch.Generator().manual_seed(40)
+    n, t, scale = 70, 4, 192 ** -0.5
+    f = rope.frequencies(factor=40.0)
+    table = binding.mla_rope_init(f, interleaved=interleaved)
+
+    def bf16(*shape):
+        return torch.randn(shape, generator=g).to(torch.bfloat16)
+
+    def ints(*x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    c, kr, qn, qr, w_uk, w_uv = bf16(n + t, 512), bf16(n + t, 64), bf16(n, 128, 128), bf16(n, 128, 64), bf16(128, 128, 512), bf16(128, 128, 512)
+    w_uk, w_uv = w_uk * 0.0625, w_uv * 0.0625          # (powers of two: exact)
+    qa, qt, parents = bf16(1, t, 128, 512) * 0.25, bf16(1, t, 128, 64), [-1, 0, 0, 1]
+    at = np.array([n, n + 1, n + 1, n + 2])            # a node's position is its depth's, not its place in the cache
+    cache, pages = torch.zeros((2, 64, 576), dtype=torch.bfloat16, device="cuda"), ints(1, 0)[None].contiguous()
+    binding.mla_cache_append_rope_bf16(c[:n].cuda(), kr[:n].cuda(), table, cache, pages, ints(n), ints(0, n))
+    q_rot = binding.mla_rope_bf16(qr.cuda(), torch.arange(n, dtype=torch.int32, device="cuda"), table)
+    rows = binding.mla_cache_gather_bf16(cache, pages, ints(n), ints(0, n), n)
+    k, v = binding.mla_expand_kv(rows[:, :512], w_uk.cuda(), w_uv.cuda())
+    out, lse = binding.mla_prefill_bf16(qn.cuda(), q_rot, k, rows[:, 512:], v, ints(0, n), ints(0, n), scale)
+    exact_k = round_bf16(rope.rotate(kr[:n].double().numpy(), np.arange(n), f, interleaved))
+    assert torch.equal(rows.cpu(), torch.cat([c[:n], exact_k], 1))
+    for h in (0, 77):
+        q = np.concatenate([qn[:, h].double().numpy(),
+                            round_bf16(rope.rotate(qr[:, h].double().numpy(), np.arange(n), f, interleaved)).double().numpy()], 1)
+        kk = np.concatenate([k[:, h].double().cpu().numpy(), exact_k.double().numpy()], 1)
+        o, l, _ = expanded.attend(q, kk, v[:, h].double().cpu().numpy(), np.tril(np.ones((n, n), dtype=bool)), scale)
+        assert np.abs(out[:, h].double().cpu().numpy() - o).max() <= 1e-2 * np.abs(o).max()
+        assert np.abs(lse[:, h].double().cpu().numpy() - l).max() <= 1e-3
+    binding.mla_cache_append_rope_bf16(c[n:].cuda(), kr[n:].cuda(), table, cache, pages, ints(n + t), ints(0, t), positions=ints(*at))
+    qt_rot = binding.mla_rope_bf16(qt[0].cuda(), ints(*at), table)[None]
+    to, tl = binding.mla_decode_tree_bf16(qa.cuda(), qt_rot, cache, pages, ints(n + t), ints(*parents)[None].contiguous(), scale)
+    k_all = torch.cat([exact_k, round_bf16(rope.rotate(kr[n:].double().numpy(), at, f, interleaved))])
+    latent = torch.cat([c, k_all], 1).double().numpy()
+    for i in range(t):
+        q = round_bf16(rope.rotate(qt[0, i].double().numpy(), np.full(128, at[i]), f, interleaved)).double().numpy()
+        o, l = mla_oracle.attend_latent(qa[0, i].double().numpy(), q, latent[expanded.tree_sees(parents, t, i, n)], scale)
+        assert np.abs(to[0, i].double().cpu().numpy() - o).max() <= 1e-2 * np.abs(o).max()
+        assert np.abs(tl[0, i].double().cpu().numpy() - l).max() <= 1e-3
