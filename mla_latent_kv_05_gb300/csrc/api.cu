@@ -637,6 +637,8 @@ int mla_rope_bf16(const uint16_t* x, const size_t* strides, const int32_t* posit
     if (!stride_ok(strides[i])) return MLA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(out, 16) || !aligned(positions, 4)) return MLA_ERR_INVALID_ARG;
   if (rows == 0 || heads == 0) return MLA_OK;
+  // in place every vector stays where it is
+  if (x == out && ((rows > 1 && strides[0] != strides[2]) || (heads > 1 && strides[1] != strides[3]))) return MLA_ERR_INVALID_ARG;
   RopeParams p;
   p.x = reinterpret_cast<const __nv_bfloat16*>(x);
   p.x_t = static_cast<long long>(strides[0]);

@@ -114,6 +114,7 @@ def test_rope_entry_refuses_on_the_host(lib):
             assert call(strides=s) == -1
     assert call(x=ctypes.c_void_p(0x1008)) == -1 and call(out=ctypes.c_void_p(0x1002)) == -1
     assert call(positions=ctypes.c_void_p(0x1002)) == -1
+    assert call(strides=(8192, 64, 8192, 128)) == -1 and call(strides=(8192, 64, 16384, 64)) == -1     # in place, elsewhere
     assert call(rows=0) == 0 and call(heads=0) == 0
     t.scale = float("inf")
     assert call() == -1
