@@ -563,7 +563,10 @@ def mla_rope_bf16(x, positions, rope, out=None, inverse=False, stream=None):
     _check(positions, "positions", torch.int32, (rows,))
     device = x.device
     if out is None:
-        out = x.new_empty(shape) if stream is None else _new(stream, torch.empty, shape, dtype=torch.bfloat16, device=device)
+        if stream is None:      # (empty_like costs the host half of new_empty)
+            out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
+        else:
+            out = _new(stream, torch.empty, shape, dtype=torch.bfloat16, device=device)
         to, o_t, o_h = out.data_ptr(), 64 * heads, 64
     elif out is x:
         to, o_t, o_h = at, x_t, x_h
@@ -967,10 +970,13 @@ def mla_workspace_size_prefill_backward(batch: int, num_q: int, num_k: int) -> i
 
 
 def alloc_workspace_prefill_backward(batch: int, num_q: int, num_k: int, device=None) -> torch.Tensor:
-    """A zeroed workspace buffer (uint8) for the gradients of a prefill of
-    `batch` sequences with `num_q` queries and `num_k` keys together."""
-    return torch.zeros(mla_workspace_size_prefill_backward(batch, num_q, num_k), dtype=torch.uint8,
-                       device=device or "cuda")
+    """A workspace buffer (uint8) for the gradients of a prefill of `batch`
+    sequences with `num_q` queries and `num_k` keys together, its first 256 bytes
+    zeroed (up to 4 GiB of it hold scores' gradients, so it is worth keeping)."""
+    workspace = torch.empty(mla_workspace_size_prefill_backward(batch, num_q, num_k), dtype=torch.uint8,
+                            device=device or "cuda")
+    workspace[:256].zero_()
+    return workspace
 
 
 def mla_prefill_backward_bf16(d_out, q_nope, q_rope, k_nope, k_rope, v, out, lse, cu_q, cu_k, scale, causal=True,

@@ -6,10 +6,13 @@
 // into NaN.  Looking for such values in every tile at the mask's edge would cost every
 // call.  A query's show in its lse or its delta, which are formed anyway, and a key's in
 // results of the query pass, 24 multiply-adds a thread and item.  (The same in the key
-// pass, 48, cost 2 x 512 queries over 8,012 keys another 9 us.)  Where one has been noted, this kernel looks for results that are not
-// finite and computes their rows again on the CUDA cores, over the pairs that are seen
-// alone; a row that is NaN by rights is so in all its values after a pair or two, and
-// left there.
+// pass, 48, cost 2 x 512 queries over 8,012 keys another 9 us.)  Where one has been
+// noted, this kernel looks for results that are not finite.  Where a hidden column of
+// their edge tiles is not either, their rows are computed again on the CUDA cores, over
+// the pairs that are seen alone; a value that is NaN by rights is so again, and once all
+// that matter are, the row is left.  (Without the look at the hidden columns one NaN in
+// d_out, at token 4000 of 4096 in every head, took 480 ms: every key before it is NaN by
+// rights.)
 //
 // Bound: without such rows the reading of the groups' fp32 sums, 64 (or 16) times 256
 // bytes a key, which the key pass has left in L2.  (The second half's code must not cost
@@ -45,21 +48,31 @@ __device__ __forceinline__ void load2(const __nv_bfloat16* row, int lane, float*
   x[0] = __uint_as_float(w << 16);
   x[1] = __uint_as_float(w & 0xFFFF0000u);
 }
-__device__ __forceinline__ void save4(__nv_bfloat16* row, int lane, const float* x, float mul) {
-  *reinterpret_cast<uint2*>(row + 4 * lane) = make_uint2(bf16_pair(x[0] * mul, x[1] * mul), bf16_pair(x[2] * mul, x[3] * mul));
+__device__ __forceinline__ void save4(__nv_bfloat16* row, int lane, const float* x) {
+  *reinterpret_cast<uint2*>(row + 4 * lane) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
 }
+// A bit for each of a lane's values that is not finite.
 template <int kN>
-__device__ __forceinline__ bool any_odd(const float* x) {
-  bool odd = false;
+__device__ __forceinline__ uint32_t odd_values(const float* x) {
+  uint32_t odd = 0;
 #pragma unroll
-  for (int e = 0; e < kN; ++e) odd |= !isfinite(x[e]);
-  return __any_sync(0xffffffffu, odd);
+  for (int e = 0; e < kN; ++e) odd |= isfinite(x[e]) ? 0u : 1u << e;
+  return odd;
+}
+// The values of the bits from the first, times mul, into those of the second.
+template <int kN>
+__device__ __forceinline__ void replace(uint32_t bits, const float* from, float mul, float* to) {
+#pragma unroll
+  for (int e = 0; e < kN; ++e)
+    if (bits >> e & 1u) to[e] = from[e] * mul;
 }
 
 // One row of a head once more: dk before scaling (128 | 64 values) and dv of a key, or
-// dq, over its seen columns, one warp.
+// dq, over its seen columns, one warp.  need: the values that matter, a lane's bits for
+// first and behind them for second; when all of them are NaN, the rest of the row cannot
+// change that.
 template <bool kKeys>
-__device__ void row_again(const BackwardParams& p, const BackwardWs& L, const Tile& t, int r, int head, int lane, float* first, float* second) {
+__device__ void row_again(const BackwardParams& p, const BackwardWs& L, const Tile& t, int r, int head, int lane, uint32_t need, float* first, float* second) {
   const size_t row = static_cast<size_t>(t.r0) + r;
   const float c = p.scale * kLog2e;
   const float* stats = reinterpret_cast<const float*>(p.ws + L.stats);
@@ -101,21 +114,44 @@ __device__ void row_again(const BackwardParams& p, const BackwardWs& L, const Ti
     for (int e = 0; e < 4; ++e) dp += b[e] * y[e];
     const float* st = stat(kKeys ? i : r);
     const float pr = fast_exp2(warp_sum(s) * c - __ldcg(st)), ds = bf16_value(pr * (warp_sum(dp) - __ldcg(st + kTile)));
-    bool all_nan = true;
+    bool open = false;
 #pragma unroll
     for (int e = 0; e < 6; ++e) {
       first[e] += ds * x[e];
-      all_nan &= isnan(first[e]);
+      open |= (need >> e & 1u) && !isnan(first[e]);
     }
     if constexpr (kKeys) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         second[e] += bf16_value(pr) * y[e];
-        all_nan &= isnan(second[e]);
+        open |= (need >> (6 + e) & 1u) && !isnan(second[e]);
       }
     }
-    if (__all_sync(0xffffffffu, all_nan)) break;
+    if (!__any_sync(0xffffffffu, open)) break;
   }
+}
+
+// Whether a column that the row does not see, in a tile that the pass has computed, has
+// a value that is not finite; without one the row's results are what the formula gives.
+template <bool kKeys>
+__device__ bool hidden_odd(const BackwardParams& p, const Tile& t, int r, int head, int lane) {
+  const int from = kKeys ? t.first * kTile : max(0, t.lim + r), to = kKeys ? min(t.nc, t.lim + r) : min(t.nc, t.steps * kTile);
+  uint32_t odd = 0;
+  for (int i = from; i < to; ++i) {
+    const size_t col = static_cast<size_t>(t.c0) + i;
+    float x[6], y[4];
+    if constexpr (kKeys) {
+      load4(p.q_nope + col * p.qn_t + head * p.qn_h, lane, x);
+      load2(p.q_rope + col * p.qr_t + head * p.qr_h, lane, x + 4);
+      load4(p.d_out + col * p.do_t + head * p.do_h, lane, y);
+      odd |= odd_values<4>(y);
+    } else {
+      load4(p.k_nope + col * p.kn_t + head * p.kn_h, lane, x);
+      load2(p.k_rope + col * p.kr_t, lane, x + 4);
+    }
+    odd |= odd_values<6>(x);
+  }
+  return __any_sync(0xffffffffu, odd != 0);
 }
 
 // The rows [r, end) of a tile that are not finite, one warp a row and head, or group of heads.
@@ -125,13 +161,15 @@ __device__ __noinline__ void queries_again(const BackwardParams& p, const Backwa
     for (int head = warp; head < kHeads; head += 8) {
       const size_t row = static_cast<size_t>(t.r0) + r;
       __nv_bfloat16 *dn = p.dq_nope + row * p.dqn_t + head * p.dqn_h, *dr = p.dq_rope + row * p.dqr_t + head * p.dqr_h;
-      float x[6], unused[4];
+      float x[6], again[6], unused[4];
       load4(dn, lane, x);
       load2(dr, lane, x + 4);
-      if (!any_odd<6>(x)) continue;
-      row_again<false>(p, L, t, r, head, lane, x, unused);
-      save4(dn, lane, x, p.scale);
-      *reinterpret_cast<uint32_t*>(dr + 2 * lane) = bf16_pair(x[4] * p.scale, x[5] * p.scale);
+      const uint32_t need = odd_values<6>(x);
+      if (!__any_sync(0xffffffffu, need != 0) || !hidden_odd<false>(p, t, r, head, lane)) continue;
+      row_again<false>(p, L, t, r, head, lane, need, again, unused);
+      replace<6>(need, again, p.scale, x);
+      save4(dn, lane, x);
+      *reinterpret_cast<uint32_t*>(dr + 2 * lane) = bf16_pair(x[4], x[5]);
     }
 }
 __device__ __noinline__ void keys_again(const BackwardParams& p, const BackwardWs& L, const Tile t, int r, int end) {
@@ -140,26 +178,34 @@ __device__ __noinline__ void keys_again(const BackwardParams& p, const BackwardW
     for (int g = warp; g < groups; g += 8) {
       const size_t row = static_cast<size_t>(t.r0) + r;
       float* part = reinterpret_cast<float*>(p.ws + L.rope) + (static_cast<size_t>(g) * p.nk + row) * kDr + 2 * lane;
-      float rope[2] = {part[0], part[1]};
-      const bool rope_odd = any_odd<2>(rope);
-      rope[0] = rope[1] = 0.f;
+      const float old[2] = {part[0], part[1]};
+      const uint32_t rope_need = odd_values<2>(old);
+      const bool rope_odd = __any_sync(0xffffffffu, rope_need != 0);
+      bool hidden = false;
+      for (int head = g * L.group; head < (g + 1) * L.group && !hidden; ++head) {
+        float x[4], y[4];
+        load4(p.dk_nope + row * p.dkn_t + head * p.dkn_h, lane, x);
+        load4(p.dv + row * p.dv_t + head * p.dv_h, lane, y);
+        if (rope_odd || __any_sync(0xffffffffu, (odd_values<4>(x) | odd_values<4>(y)) != 0)) hidden = hidden_odd<true>(p, t, r, head, lane);
+      }
+      if (!hidden) continue;
+      float rope[2] = {0.f, 0.f};
       for (int head = g * L.group; head < (g + 1) * L.group; ++head) {
         __nv_bfloat16 *dk = p.dk_nope + row * p.dkn_t + head * p.dkn_h, *dv = p.dv + row * p.dv_t + head * p.dv_h;
-        float x[6], y[4];
+        float x[4], y[4], first[6], second[4];
         load4(dk, lane, x);
         load4(dv, lane, y);
-        const bool k_odd = any_odd<4>(x), v_odd = any_odd<4>(y);
-        if (!rope_odd && !k_odd && !v_odd) continue;
-        row_again<true>(p, L, t, r, head, lane, x, y);
-        if (k_odd) save4(dk, lane, x, p.scale);
-        if (v_odd) save4(dv, lane, y, 1.f);
-        rope[0] += x[4];
-        rope[1] += x[5];
+        const uint32_t k_need = odd_values<4>(x), v_need = odd_values<4>(y);
+        if (!rope_odd && !__any_sync(0xffffffffu, (k_need | v_need) != 0)) continue;
+        row_again<true>(p, L, t, r, head, lane, k_need | rope_need << 4 | v_need << 6, first, second);
+        replace<4>(k_need, first, p.scale, x);
+        replace<4>(v_need, second, 1.f, y);
+        save4(dk, lane, x);
+        save4(dv, lane, y);
+        rope[0] += first[4];
+        rope[1] += first[5];
       }
-      if (rope_odd) {
-        part[0] = rope[0];
-        part[1] = rope[1];
-      }
+      replace<2>(rope_need, rope, 1.f, part);
     }
 }
 

@@ -42,6 +42,19 @@ def test_a_wait_that_runs_out_ends_the_call_with_timeout_status(cuda_device, sta
     assert binding.mla_get_status(ws) == 0
 
 
+@pytest.mark.parametrize("nq,nk", [([300, 7], [300, 70]), ([300], [45000])], ids=["stored", "not stored"])
+def test_what_a_workspace_held_does_not_matter(cuda_device, nq, nk):
+    d = make(nq, nk, seed=36)
+    ws = binding.alloc_workspace_prefill_backward(len(nq), sum(nq), sum(nk))
+    ws[256:] = 0
+    want = run(d, workspace=ws)
+    for byte in (0xFF, 0x7F):
+        ws[256:] = byte
+        for a, b in zip(run(d, workspace=ws), want):
+            assert torch.equal(a, b)
+    assert binding.mla_get_status(ws) == 0
+
+
 @pytest.mark.parametrize("n", [1, 3, 200])
 @pytest.mark.parametrize("name", ["d_out", "q_nope", "q_rope", "k_nope", "k_rope", "v", *NAMES])
 def test_tensors_at_the_end_of_the_memory(cuda_device, n, name):
