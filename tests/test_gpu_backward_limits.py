@@ -55,6 +55,20 @@ def test_what_a_workspace_held_does_not_matter(cuda_device, nq, nk):
     assert binding.mla_get_status(ws) == 0
 
 
+def test_a_captured_call_with_a_workspace_of_its_own(cuda_device):
+    d = make([150, 33], [150, 60], seed=37)
+    want = run(d)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(d)
+    for _ in range(2):
+        for x in got:
+            x.fill_(7)
+        graph.replay()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("n", [1, 3, 200])
 @pytest.mark.parametrize("name", ["d_out", "q_nope", "q_rope", "k_nope", "k_rope", "v", *NAMES])
 def test_tensors_at_the_end_of_the_memory(cuda_device, n, name):
