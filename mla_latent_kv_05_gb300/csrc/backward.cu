@@ -735,14 +735,14 @@ backward_kernel(const __grid_constant__ PassMaps maps, const __grid_constant__ B
   }
 }
 
-// Rows of a query tile: 256, on CTA pairs (backward_pair.cu), unless too many of their
-// rows and columns are masked.  Of an average sequence, a pair's tiles of 256 instead of
-// 128 rows are 64 rows more at its end and, where causal, 64 columns more a row at the
-// diagonal; a pair's query pass is about a sixth faster on full tiles.  Shares, and us a
-// call with tiles of 128 and of 256: 2 x 512 over 8,012 keys 0.13, 1,808 and 1,686;
-// 2 x 800 over 1,200 0.16, 497 and 497; 4 x 1024 causal 0.19, 716 and 702; 4 x 300 over
-// 4,300 0.23, 1,782 and 1,808; 4 x 300 full 0.21, 235 and 243; 8 x up to 1024 0.37, 611
-// and 648.
+// Rows of a query tile in the query pass: 256, on CTA pairs (backward_pair.cu), unless
+// too many of their rows and columns are masked.  Of an average sequence, a pair's tiles
+// of 256 instead of 128 rows are 64 rows more at its end and, where causal, 64 columns
+// more a row at the diagonal; a pair's query pass is about a sixth faster on full tiles.
+// Shares, and us a call that stores nothing with tiles of 128 and of 256: 2 x 512 over
+// 8,012 keys 0.13, 1,808 and 1,686; 2 x 800 over 1,200 0.16, 497 and 497; 4 x 1024 causal
+// 0.19, 716 and 702; 4 x 300 over 4,300 0.23, 1,782 and 1,808; 4 x 300 full 0.21, 235 and
+// 243; 8 x up to 1024 0.37, 611 and 648.
 int backward_rows(const BackwardParams& p) {
   const double n_q = static_cast<double>(p.nq) / p.batch, n_k = static_cast<double>(p.nk) / p.batch;
   const double seen = p.causal ? std::fmax(n_k - n_q / 2, 1.0) : std::fmax(n_k, 1.0);

@@ -69,7 +69,7 @@ namespace bwd {
 
 // 128 (chunks = 2) or 64 values of tokens and heads; boxes of box_chunks x rows x 64
 // values of a head, in that order, so that one copy brings both chunks of an operand
-// (a copy costs its SM about 400 cycles, whatever its size).  Strides in values.
+// (a copy costs its thread about 160 cycles, whatever its size).  Strides in values.
 inline bool encode_chunks(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* base, int chunks, int heads,
                           int tokens, long long stride_t, long long stride_h, unsigned rows, unsigned box_chunks) {
   // (spans.cuh; 128 values of 128 heads span enough from the fourth token on)
@@ -233,7 +233,7 @@ __device__ __forceinline__ void to_bf16(const uint32_t* a, float mul, uint32_t* 
   for (int e = 0; e < kPairs; ++e) out[e] = bf16_pair(__uint_as_float(a[2 * e]) * mul, __uint_as_float(a[2 * e + 1]) * mul);
 }
 
-// Registers on pairs (80 a thread at launch): 40 for the eight warps that load and
+// Registers (80 a thread at launch): 40 for the eight warps that load and
 // issue, 96 for the sixteen others (8 * 40 + 16 * 96 <= 24 * 80), each role's branch
 // setting its own.
 __device__ __forceinline__ void regs_issue() { asm volatile("setmaxnreg.dec.sync.aligned.u32 40;"); }
