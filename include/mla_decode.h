@@ -493,7 +493,8 @@ int mla_prefill_bf16(const uint16_t* q_nope, const uint16_t* q_rope, const uint1
  * another.  Limits and device status as for mla_prefill_bf16.
  * workspace: mla_workspace_size_prefill_backward(...) bytes, the first 256 zeroed
  * before its first use, 256-byte aligned, not shared with a call that may run
- * concurrently.
+ * concurrently.  The size grows with each of the three counts, so a workspace for
+ * the largest serves all calls.
  * Up to 4 GiB of it hold ds of all heads, 4 MiB for every tile of 128 x 128 scores
  * that these counts could have; with more tiles than that dq takes longer. */
 int mla_workspace_size_prefill_backward(int batch, int num_q, int num_k, size_t* bytes);

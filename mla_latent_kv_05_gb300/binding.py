@@ -972,7 +972,8 @@ def mla_workspace_size_prefill_backward(batch: int, num_q: int, num_k: int) -> i
 def alloc_workspace_prefill_backward(batch: int, num_q: int, num_k: int, device=None) -> torch.Tensor:
     """A workspace buffer (uint8) for the gradients of a prefill of `batch`
     sequences with `num_q` queries and `num_k` keys together, its first 256 bytes
-    zeroed (up to 4 GiB of it hold scores' gradients, so it is worth keeping)."""
+    zeroed (up to 4 GiB of it hold scores' gradients, so it is worth keeping; one
+    for the largest counts serves every call of smaller ones)."""
     workspace = torch.empty(mla_workspace_size_prefill_backward(batch, num_q, num_k), dtype=torch.uint8,
                             device=device or "cuda")
     workspace[:256].zero_()

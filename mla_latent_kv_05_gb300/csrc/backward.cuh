@@ -34,6 +34,8 @@ struct BackwardPlan {
 constexpr size_t kDsTile = 2 * kBackwardTile * kBackwardTile;   // bytes
 constexpr long long kMaxDsTiles = 1024;                         // 4 GiB with all heads
 constexpr size_t kTileBytes = 48;
+constexpr int kCtas = 152;            // CTAs of the passes, one an SM; sizes do not depend on the device that is current
+// Every part grows with each of the three counts, and so does the total.
 struct BackwardWs {
   size_t plan, base[2], tiles[2], stats, rope, slots, ds, total;
   int max_tiles[2], group, ds_tiles;
@@ -48,7 +50,8 @@ inline BackwardWs backward_ws(int batch, int nq, int nk) {
   // gradients in the workspace instead of a quarter), two where they do not: one made
   // 8 x up to 1024 tokens 669 us instead of 646, four 654; 4096 tokens take the same
   // with one, two or eight
-  w.group = static_cast<long long>(w.max_tiles[0]) * kHeads / 8 >= 8 * 152 ? 8 : 2;
+  constexpr int kEightFrom = 8 * kCtas / (kHeads / 8);   // key tiles
+  w.group = w.max_tiles[0] >= kEightFrom ? 8 : 2;
   w.plan = align256(sizeof(PlanHeader));
   w.base[0] = align256(w.plan + sizeof(BackwardPlan));
   w.base[1] = align256(w.base[0] + sizeof(int) * static_cast<size_t>(batch));
@@ -56,7 +59,11 @@ inline BackwardWs backward_ws(int batch, int nq, int nk) {
   w.tiles[1] = align256(w.tiles[0] + kTileBytes * static_cast<size_t>(w.max_tiles[0]));
   w.stats = align256(w.tiles[1] + kTileBytes * static_cast<size_t>(w.max_tiles[1]));
   w.rope = align256(w.stats + sizeof(float) * 2 * kBackwardTile * kHeads * static_cast<size_t>(w.max_tiles[1]));
-  w.slots = align256(w.rope + sizeof(float) * kDr * (kHeads / w.group) * static_cast<size_t>(nk));
+  // a call of fewer keys may take two heads, four times the sums a key: there is room for
+  // those too, so that a workspace for a larger call serves every smaller one
+  const size_t row = sizeof(float) * kDr, own = row * (kHeads / w.group) * static_cast<size_t>(nk),
+               fewer = row * (kHeads / 2) * static_cast<size_t>(nk < kEightFrom * kBackwardTile ? nk : kEightFrom * kBackwardTile);
+  w.slots = align256(w.rope + (own > fewer ? own : fewer));
   w.ds = align256(w.slots + sizeof(int) * static_cast<size_t>(w.max_tiles[0]));
   // a sequence has no more tiles along one axis than all tokens would have together
   const long long by_q = (nq + kBackwardTile - 1ll) / kBackwardTile * w.max_tiles[0],
