@@ -65,9 +65,14 @@ inline BackwardWs backward_ws(int batch, int nq, int nk) {
                fewer = row * (kHeads / 2) * static_cast<size_t>(nk < kEightFrom * kBackwardTile ? nk : kEightFrom * kBackwardTile);
   w.slots = align256(w.rope + (own > fewer ? own : fewer));
   w.ds = align256(w.slots + sizeof(int) * static_cast<size_t>(w.max_tiles[0]));
-  // a sequence has no more tiles along one axis than all tokens would have together
-  const long long by_q = (nq + kBackwardTile - 1ll) / kBackwardTile * w.max_tiles[0],
-                  by_k = (nk + kBackwardTile - 1ll) / kBackwardTile * w.max_tiles[1], most = by_q < by_k ? by_q : by_k;
+  // Tiles of scores: sum over the sequences of ceil(q / 128) ceil(k / 128).  A sequence has
+  // no more along one axis than all tokens would have together; and its tiles are at most
+  // (q + 127) (k + 127) / 128^2, where the products q k sum to at most nq nk.
+  constexpr long long kT = kBackwardTile;
+  const long long q = nq, k = nk, some = batch < nq ? (batch < nk ? batch : nk) : (nq < nk ? nq : nk),   // sequences with both
+                  by_q = (q + kT - 1) / kT * w.max_tiles[0], by_k = (k + kT - 1) / kT * w.max_tiles[1],
+                  by_area = (q * k + (kT - 1) * (q + k) + (kT - 1) * (kT - 1) * some) / (kT * kT),
+                  by_axis = by_q < by_k ? by_q : by_k, most = by_axis < by_area ? by_axis : by_area;
   w.ds_always = most <= kMaxDsTiles;
   w.ds_tiles = static_cast<int>(w.ds_always ? most : kMaxDsTiles);
   w.total = align256(w.ds + kDsTile * kHeads * static_cast<size_t>(w.ds_tiles));

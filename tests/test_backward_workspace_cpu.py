@@ -43,3 +43,38 @@ def test_sizes_never_fall_from_one_key_to_the_next(size, batch):
             n = size(batch, nq, nk)
             assert n >= last, (batch, nq, nk)
             last = n
+
+
+TILE = 128 * 2 * 128 * 128   # bytes of a tile of scores' gradients, all heads
+
+
+def tiles(nq, nk):
+    return sum(-(-q // 128) * -(-k // 128) for q, k in zip(nq, nk))
+
+
+# what the gradients of scores may take beyond what these lengths need: the counts do not tell the lengths
+@pytest.mark.parametrize("nq,nk,most", [([100] * 16, [100] * 16, 200), ([33, 7, 1, 20, 5], [33, 7, 1, 20, 5], 5), ([1] * 64, [500] * 64, 256),
+                                        ([777] * 3, [777] * 3, 384), ([4096], [4096], 1024)],
+                         ids=["16 x 100", "short", "64 queries", "777", "4096"])
+def test_room_for_scores_is_near_what_the_counts_can_need(size, nq, nk, most):
+    n = size(len(nq), sum(nq), sum(nk))
+    # the rest: fp32 sums of the RoPE part (16 KiB a key), statistics (128 KiB a tile of queries), lists
+    rest = 16384 * sum(nk) + 131072 * (sum(nq) // 128 + len(nq)) + 65536
+    assert tiles(nq, nk) * TILE <= n <= most * TILE + rest
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_room_for_scores_is_enough(size, seed):
+    r = random.Random(seed)
+
+    def lengths(n, top):
+        return [r.choice((0, 1, 127, 128, 129, round(2 ** r.uniform(0, top)))) for _ in range(n)]
+
+    for _ in range(3000):
+        n = round(2 ** r.uniform(0, 7))
+        top = r.uniform(1, 12)
+        nq, nk = lengths(n, top), lengths(n, top)
+        if r.random() < 0.3:
+            nk = nq
+        rest = size(n, sum(nq), 0) + size(0, 0, sum(nk))   # no scores at all (each has a header of under 4 KiB)
+        assert size(n, sum(nq), sum(nk)) >= min(tiles(nq, nk), 1024) * TILE + rest - 4096 - 16 * n, (nq, nk)
