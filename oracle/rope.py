@@ -45,3 +45,19 @@ def rotate(x, positions, inv_freq, interleaved, scale=1.0, inverse=False):
         out[..., first] = x[..., first] * c - x[..., second] * s
         out[..., second] = x[..., first] * s + x[..., second] * c
     return out
+
+
+def to_bf16(x):
+    """float64 -> the nearest bf16 value, ties to even, in one rounding (normal numbers)."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.round(np.ldexp(m, 8)), e - 8)
+
+
+def fp32_bound(x, want, interleaved, scale=1.0):
+    """How far bf16 values may be off `want` = rotate(x, ...) that were rotated in fp32 and rounded once.  Cosine and sine
+    times the scale are off by 2^-23 of it, the two products and their sum by 2^-24 each of the pair's |a| + |b|: together
+    under 2^-21; half a bf16 step is 2^-8 of the value at most."""
+    a, b = (np.abs(x[..., 0::2]), np.abs(x[..., 1::2])) if interleaved else (np.abs(x[..., :32]), np.abs(x[..., 32:]))
+    pair = np.repeat(a + b, 2, -1) if interleaved else np.concatenate([a + b, a + b], -1)
+    fp32 = 2.0 ** -21 * abs(scale) * pair
+    return fp32 + 2.0 ** -8 * (np.abs(want) + fp32)
