@@ -324,6 +324,10 @@ append_rope_kernel(const RowsParams p, const __grid_constant__ RowsRope rope) {
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     const int at = g * kGroupRows + r, slot = s_slot[at];
+    if (F == RowFormat::kBf16 && j < kLatentPieces) {   // as they are, a NaN's bits too
+      if (slot >= 0) *reinterpret_cast<uint4*>(p.cache + static_cast<size_t>(slot) * Fmt<F>::kBytes + j * 16) = v[g];
+      continue;
+    }
     float x[kPiece];
     const uint32_t w[4] = {v[g].x, v[g].y, v[g].z, v[g].w};
 #pragma unroll
