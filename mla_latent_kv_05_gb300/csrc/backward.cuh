@@ -86,7 +86,7 @@ cudaError_t launch_backward_pairs(const PassMaps& maps, const BackwardParams& p,
 // dq from stored dS tiles.
 cudaError_t launch_backward_dq(PFN_cuTensorMapEncodeTiled_v12000 encode, const BackwardParams& p, const BackwardWs& L, int ctas,
                                cudaStream_t stream);
-// The sums of the RoPE part of dk, and rows that values outside the mask have spoilt.
+// The sums of the RoPE part of dk, and what values outside the mask would spoil.
 cudaError_t launch_backward_last(const BackwardParams& p, const BackwardWs& L, cudaStream_t stream);
 cudaError_t launch_backward(PFN_cuTensorMapEncodeTiled_v12000 encode, BackwardParams p, int sms, cudaStream_t stream);
 

@@ -1,18 +1,25 @@
 // The last kernel of the backward pass (backward.cu): the RoPE part of dk, summed over
-// the groups of heads, and rows that values outside the mask have spoilt.
+// the groups of heads, and what values outside the mask would spoil.
 //
 // A pair outside the causal mask has P = dS = 0 in its tile, which an infinity or a NaN
 // in its streamed row (the key's K for dq, the query's Q and d_out for dk and dv) turns
 // into NaN.  Looking for such values in every tile at the mask's edge would cost every
 // call.  A query's show in its lse or its delta, which are formed anyway, and a key's in
 // results of the query pass, 24 multiply-adds a thread and item.  (The same in the key
-// pass, 48, cost 2 x 512 queries over 8,012 keys another 9 us.)  Where one has been
-// noted, this kernel looks for results that are not finite.  Where a hidden column of
-// their edge tiles is not either, their rows are computed again on the CUDA cores, over
-// the pairs that are seen alone; a value that is NaN by rights is so again, and once all
-// that matter are, the row is left.  (Without the look at the hidden columns one NaN in
-// d_out, at token 4000 of 4096 in every head, took 480 ms: every key before it is NaN by
-// rights.)
+// pass, 48, cost 2 x 512 queries over 8,012 keys another 9 us.)
+//
+// Where a query's has been noted, the key pass takes such values of its tiles at the edge
+// as 0 in the sums.  For dk that is all: a query whose Q is not finite has a NaN for p and
+// ds of every key that it sees (its lse is NaN, or it is -inf as every score of it).  For
+// dv the terms p d_out of seen pairs of those tiles are missing, each an infinity or a
+// NaN; this kernel adds them to the results, over the at most 255 columns of these tiles.
+// (With every sum that was not finite computed again over all its columns, a column of
+// d_out that is +inf in all of 4096 rows took 420 ms a call instead of 11.)
+//
+// Where a key's has been noted, it looks for results of dq that are not finite.  Where a
+// hidden column of their edge tiles is not either, their rows are computed again on the
+// CUDA cores, over the pairs that are seen alone; a value that is NaN by rights is so
+// again, and once all that matter are, the row is left.
 //
 // Bound: without such rows the reading of the groups' fp32 sums, 64 (or 16) times 256
 // bytes a key, which the key pass has left in L2.  (The second half's code must not cost
@@ -67,145 +74,122 @@ __device__ __forceinline__ void replace(uint32_t bits, const float* from, float 
     if (bits >> e & 1u) to[e] = from[e] * mul;
 }
 
-// One row of a head once more: dk before scaling (128 | 64 values) and dv of a key, or
-// dq, over its seen columns, one warp.  need: the values that matter, a lane's bits for
-// first and behind them for second; when all of them are NaN, the rest of the row cannot
-// change that.
-template <bool kKeys>
-__device__ void row_again(const BackwardParams& p, const BackwardWs& L, const Tile& t, int r, int head, int lane, uint32_t need, float* first, float* second) {
+// A lane's share of a query's and of a key's 192 values.
+__device__ __forceinline__ void load_q(const BackwardParams& p, size_t i, int head, int lane, float* x) {
+  load4(p.q_nope + i * p.qn_t + head * p.qn_h, lane, x);
+  load2(p.q_rope + i * p.qr_t + head * p.qr_h, lane, x + 4);
+}
+__device__ __forceinline__ void load_k(const BackwardParams& p, size_t j, int head, int lane, float* x) {
+  load4(p.k_nope + j * p.kn_t + head * p.kn_h, lane, x);
+  load2(p.k_rope + j * p.kr_t, lane, x + 4);
+}
+// lse log2(e) of a sequence's query i, and kTile values on its delta.
+__device__ __forceinline__ const float* stats_of(const BackwardParams& p, const BackwardWs& L, const Tile& t, int i, int head) {
+  return reinterpret_cast<const float*>(p.ws + L.stats) + (static_cast<size_t>(t.stat + i / kTile) * kHeads + head) * 2 * kTile + i % kTile;
+}
+__device__ __forceinline__ float probability(const BackwardParams& p, const float* a, const float* x, float lse) {
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < 6; ++e) s += a[e] * x[e];
+  return fast_exp2(warp_sum(s) * (p.scale * kLog2e) - lse);
+}
+
+// dq of a row of a head before scaling once more, over its seen columns, one warp.  need:
+// the values that matter; when all of them are NaN, the rest of the row cannot change that.
+__device__ void row_again(const BackwardParams& p, const BackwardWs& L, const Tile& t, int r, int head, int lane, uint32_t need, float* dq) {
   const size_t row = static_cast<size_t>(t.r0) + r;
-  const float c = p.scale * kLog2e;
-  const float* stats = reinterpret_cast<const float*>(p.ws + L.stats);
-  auto stat = [&](int i) { return stats + (static_cast<size_t>(t.stat + i / kTile) * kHeads + head) * 2 * kTile + i % kTile; };
-  auto q = [&](size_t i, float* x) {
-    load4(p.q_nope + i * p.qn_t + head * p.qn_h, lane, x);
-    load2(p.q_rope + i * p.qr_t + head * p.qr_h, lane, x + 4);
-  };
-  auto k = [&](size_t j, float* x) {
-    load4(p.k_nope + j * p.kn_t + head * p.kn_h, lane, x);
-    load2(p.k_rope + j * p.kr_t, lane, x + 4);
-  };
+  const float* st = stats_of(p, L, t, r, head);
+  const float lse = __ldcg(st), delta = __ldcg(st + kTile);
   float a[6], b[4], x[6], y[4];
 #pragma unroll
-  for (int e = 0; e < 6; ++e) first[e] = 0.f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) second[e] = 0.f;
-  if constexpr (kKeys) {
-    k(row, a);
-    load4(p.v + row * p.v_t + head * p.v_h, lane, b);
-  } else {
-    q(row, a);
-    load4(p.d_out + row * p.do_t + head * p.do_h, lane, b);
-  }
-  const int from = kKeys ? max(0, t.lim + r) : 0, to = kKeys ? t.nc : min(t.nc, t.lim + r);
-  for (int i = from; i < to; ++i) {
+  for (int e = 0; e < 6; ++e) dq[e] = 0.f;
+  load_q(p, row, head, lane, a);
+  load4(p.d_out + row * p.do_t + head * p.do_h, lane, b);
+  const int to = min(t.nc, t.lim + r);
+  for (int i = 0; i < to; ++i) {
     const size_t col = static_cast<size_t>(t.c0) + i;
-    if constexpr (kKeys) {
-      q(col, x);
-      load4(p.d_out + col * p.do_t + head * p.do_h, lane, y);
-    } else {
-      k(col, x);
-      load4(p.v + col * p.v_t + head * p.v_h, lane, y);
-    }
-    float s = 0.f, dp = 0.f;
-#pragma unroll
-    for (int e = 0; e < 6; ++e) s += a[e] * x[e];
+    load_k(p, col, head, lane, x);
+    load4(p.v + col * p.v_t + head * p.v_h, lane, y);
+    float dp = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) dp += b[e] * y[e];
-    const float* st = stat(kKeys ? i : r);
-    const float pr = fast_exp2(warp_sum(s) * c - __ldcg(st)), ds = bf16_value(pr * (warp_sum(dp) - __ldcg(st + kTile)));
+    const float ds = bf16_value(probability(p, a, x, lse) * (warp_sum(dp) - delta));
     bool open = false;
 #pragma unroll
     for (int e = 0; e < 6; ++e) {
-      first[e] += ds * x[e];
-      open |= (need >> e & 1u) && !isnan(first[e]);
-    }
-    if constexpr (kKeys) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        second[e] += bf16_value(pr) * y[e];
-        open |= (need >> (6 + e) & 1u) && !isnan(second[e]);
-      }
+      dq[e] += ds * x[e];
+      open |= (need >> e & 1u) && !isnan(dq[e]);
     }
     if (!__any_sync(0xffffffffu, open)) break;
   }
 }
 
-// Whether a column that the row does not see, in a tile that the pass has computed, has
-// a value that is not finite; without one the row's results are what the formula gives.
-template <bool kKeys>
+// Whether a key that the row does not see, in a tile that the pass has computed, has a
+// value that is not finite; without one the row's results are what the formula gives.
 __device__ bool hidden_odd(const BackwardParams& p, const Tile& t, int r, int head, int lane) {
-  const int from = kKeys ? t.first * kTile : max(0, t.lim + r), to = kKeys ? min(t.nc, t.lim + r) : min(t.nc, t.steps * kTile);
+  const int from = max(0, t.lim + r), to = min(t.nc, t.steps * kTile);
   uint32_t odd = 0;
   for (int i = from; i < to; ++i) {
-    const size_t col = static_cast<size_t>(t.c0) + i;
-    float x[6], y[4];
-    if constexpr (kKeys) {
-      load4(p.q_nope + col * p.qn_t + head * p.qn_h, lane, x);
-      load2(p.q_rope + col * p.qr_t + head * p.qr_h, lane, x + 4);
-      load4(p.d_out + col * p.do_t + head * p.do_h, lane, y);
-      odd |= odd_values<4>(y);
-    } else {
-      load4(p.k_nope + col * p.kn_t + head * p.kn_h, lane, x);
-      load2(p.k_rope + col * p.kr_t, lane, x + 4);
-    }
+    float x[6];
+    load_k(p, static_cast<size_t>(t.c0) + i, head, lane, x);
     odd |= odd_values<6>(x);
   }
   return __any_sync(0xffffffffu, odd != 0);
 }
 
-// The rows [r, end) of a tile that are not finite, one warp a row and head, or group of heads.
+// The rows [r, end) of a query tile whose dq is not finite, one warp a row and head.
 __device__ __noinline__ void queries_again(const BackwardParams& p, const BackwardWs& L, const Tile t, int r, int end) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (; r < end; ++r)
     for (int head = warp; head < kHeads; head += 8) {
       const size_t row = static_cast<size_t>(t.r0) + r;
       __nv_bfloat16 *dn = p.dq_nope + row * p.dqn_t + head * p.dqn_h, *dr = p.dq_rope + row * p.dqr_t + head * p.dqr_h;
-      float x[6], again[6], unused[4];
+      float x[6], again[6];
       load4(dn, lane, x);
       load2(dr, lane, x + 4);
       const uint32_t need = odd_values<6>(x);
-      if (!__any_sync(0xffffffffu, need != 0) || !hidden_odd<false>(p, t, r, head, lane)) continue;
-      row_again<false>(p, L, t, r, head, lane, need, again, unused);
+      if (!__any_sync(0xffffffffu, need != 0) || !hidden_odd(p, t, r, head, lane)) continue;
+      row_again(p, L, t, r, head, lane, need, again);
       replace<6>(need, again, p.scale, x);
       save4(dn, lane, x);
       *reinterpret_cast<uint32_t*>(dr + 2 * lane) = bf16_pair(x[4], x[5]);
     }
 }
+
+// dv of the keys [r, end) of a tile: the terms of seen pairs whose d_out the key pass has
+// taken as 0, one warp a row and head.  Such a query's delta is not finite.
 __device__ __noinline__ void keys_again(const BackwardParams& p, const BackwardWs& L, const Tile t, int r, int end) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, groups = kHeads / L.group;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int to = min(t.nc, (max(0, mask_end(t)) + kTile - 1) / kTile * kTile);   // the last tile with hidden pairs
   for (; r < end; ++r)
-    for (int g = warp; g < groups; g += 8) {
+    for (int head = warp; head < kHeads; head += 8) {
       const size_t row = static_cast<size_t>(t.r0) + r;
-      float* part = reinterpret_cast<float*>(p.ws + L.rope) + (static_cast<size_t>(g) * p.nk + row) * kDr + 2 * lane;
-      const float old[2] = {part[0], part[1]};
-      const uint32_t rope_need = odd_values<2>(old);
-      const bool rope_odd = __any_sync(0xffffffffu, rope_need != 0);
-      bool hidden = false;
-      for (int head = g * L.group; head < (g + 1) * L.group && !hidden; ++head) {
-        float x[4], y[4];
-        load4(p.dk_nope + row * p.dkn_t + head * p.dkn_h, lane, x);
-        load4(p.dv + row * p.dv_t + head * p.dv_h, lane, y);
-        if (rope_odd || __any_sync(0xffffffffu, (odd_values<4>(x) | odd_values<4>(y)) != 0)) hidden = hidden_odd<true>(p, t, r, head, lane);
+      __nv_bfloat16* dv = p.dv + row * p.dv_t + head * p.dv_h;
+      float a[6], sum[4];
+      bool some = false;
+      for (int i0 = max(0, t.lim + r); i0 < to; i0 += 32) {
+        const int mine = i0 + lane;
+        uint32_t columns = __ballot_sync(0xffffffffu, mine < to && !isfinite(__ldcg(stats_of(p, L, t, mine, head) + kTile)));
+        for (; columns != 0; columns &= columns - 1) {
+          const int i = i0 + __ffs(static_cast<int>(columns)) - 1;
+          const size_t col = static_cast<size_t>(t.c0) + i;
+          float x[6], y[4];
+          load4(p.d_out + col * p.do_t + head * p.do_h, lane, y);
+          const uint32_t odd = odd_values<4>(y);
+          if (!__any_sync(0xffffffffu, odd != 0)) continue;
+          if (!some) {
+            load_k(p, row, head, lane, a);
+            load4(dv, lane, sum);
+            some = true;
+          }
+          load_q(p, col, head, lane, x);
+          const float pr = bf16_value(probability(p, a, x, __ldcg(stats_of(p, L, t, i, head))));
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (odd >> e & 1u) sum[e] += pr * y[e];
+        }
       }
-      if (!hidden) continue;
-      float rope[2] = {0.f, 0.f};
-      for (int head = g * L.group; head < (g + 1) * L.group; ++head) {
-        __nv_bfloat16 *dk = p.dk_nope + row * p.dkn_t + head * p.dkn_h, *dv = p.dv + row * p.dv_t + head * p.dv_h;
-        float x[4], y[4], first[6], second[4];
-        load4(dk, lane, x);
-        load4(dv, lane, y);
-        const uint32_t k_need = odd_values<4>(x), v_need = odd_values<4>(y);
-        if (!rope_odd && !__any_sync(0xffffffffu, (k_need | v_need) != 0)) continue;
-        row_again<true>(p, L, t, r, head, lane, k_need | rope_need << 4 | v_need << 6, first, second);
-        replace<4>(k_need, first, p.scale, x);
-        replace<4>(v_need, second, 1.f, y);
-        save4(dk, lane, x);
-        save4(dv, lane, y);
-        rope[0] += first[4];
-        rope[1] += first[5];
-      }
-      replace<2>(rope_need, rope, 1.f, part);
+      if (some) save4(dv, lane, sum);
     }
 }
 
@@ -228,10 +212,7 @@ __global__ void __launch_bounds__(256, 6) backward_last_kernel(const __grid_cons
   const Tile t = read_tile(reinterpret_cast<const Tile*>(p.ws + L.tiles[0]) + i_tile);
   const int k = threadIdx.x >> 7, run = (threadIdx.x >> 4) & 7, lane = threadIdx.x & 15, r = 2 * unit + k;
   if (2 * unit >= t.rows) return;
-  if (plan->odd[0] != 0) {
-    keys_again(p, L, t, 2 * unit, min(2 * unit + 2, t.rows));
-    __syncthreads();
-  }
+  if (plan->odd[0] != 0) keys_again(p, L, t, 2 * unit, min(2 * unit + 2, t.rows));
   const size_t row = static_cast<size_t>(t.r0) + r;
   const int per = kHeads / L.group / 8;   // 2 or 8 groups a run
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -53,6 +53,8 @@ struct Tile {
   int unused[2];
 };
 static_assert(sizeof(Tile) == kTileBytes, "tile record");
+// Keys, causal: the columns from here on are seen by all rows.
+__device__ __forceinline__ int mask_end(const Tile& t) { return t.lim + t.rows - 1; }
 constexpr uint32_t kItemBytes = 64;
 
 }  // namespace bwd
