@@ -381,10 +381,15 @@ int mla_rope_init(mla_rope* rope, const double* inv_freq, float scale, int inter
  * times the original_tokens a model was trained on (YaRN): with r(n) =
  * 64 ln(original_tokens / (2 pi n)) / (2 ln base) the pair that turns n times
  * over them, pairs up to floor(r(beta_fast)) keep their frequency, pairs from
- * ceil(r(beta_slow)) have it divided by factor, and a linear ramp joins them.
+ * ceil(r(beta_slow)) have it divided by factor, and a linear ramp joins them
+ * (limits below 0 count as 0; where both are one pair, it keeps its frequency).
  * base > 1, factor >= 1, beta_fast > beta_slow > 0. */
 int mla_rope_frequencies(float base, float factor, int original_tokens, float beta_fast, float beta_slow,
                          double* inv_freq);
+/* The same in 64 bits: scaling[4] (host) holds base, factor, beta_fast, beta_slow.
+ * A base or factor that fp32 does not hold is off by up to 2^-25 of it above, which
+ * turns a pair by 4e-3 at position 160,000. */
+int mla_rope_frequencies_f64(const double* scaling, int original_tokens, double* inv_freq);
 
 /* Rotate packed vectors: x [rows, heads, 64] bf16 (a query's q_rope, a part of
  * wider heads through its strides, or with one head k_rope) by positions[row]

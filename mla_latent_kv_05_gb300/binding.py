@@ -59,6 +59,7 @@ SIGNATURES = {
        for f in ("bf16", "fp8", "fp4", "fp8_v41", "fp4_v41")},
     "mla_rope_init": (_I, [_P, _P, ctypes.c_float, _I]),
     "mla_rope_frequencies": (_I, [ctypes.c_float, ctypes.c_float, _I, ctypes.c_float, ctypes.c_float, _P]),
+    "mla_rope_frequencies_f64": (_I, [_P, _I, _P]),
     "mla_rope_bf16": (_I, [_P, ctypes.POINTER(_Z), _P, _I, _I, _P, _I, _P, _P]),
     **{"mla_cache_append_rope_" + f: (_I, [_P, _Z, _P, _Z, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _Z, _P])
        for f in ("bf16", "fp8", "fp4", "fp8_v41", "fp4_v41")},
@@ -500,8 +501,8 @@ def mla_rope_frequencies(base: float = 10000.0, factor: float = 1.0, original_to
     """The 32 frequencies (radians a token) base^(-i/32), for factor > 1 scaled
     (YaRN) to contexts `factor` times the original_tokens."""
     f = (ctypes.c_double * 32)()
-    rc = load().mla_rope_frequencies(float(base), float(factor), int(original_tokens), float(beta_fast),
-                                     float(beta_slow), f)
+    scaling = (ctypes.c_double * 4)(float(base), float(factor), float(beta_fast), float(beta_slow))
+    rc = load().mla_rope_frequencies_f64(scaling, int(original_tokens), f)
     if rc != MLA_OK:
         raise MLAError(rc, "mla_rope_frequencies")
     return list(f)

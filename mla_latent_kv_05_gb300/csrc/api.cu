@@ -613,10 +613,17 @@ int mla_rope_init(mla_rope* rope, const double* inv_freq, float scale, int inter
 
 int mla_rope_frequencies(float base, float factor, int original_tokens, float beta_fast, float beta_slow,
                          double* inv_freq) {
-  if (!inv_freq || !(base > 1.f) || !std::isfinite(base) || !(factor >= 1.f) || !std::isfinite(factor) ||
-      original_tokens <= 0 || !(beta_slow > 0.f) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast))
+  const double scaling[4] = {base, factor, beta_fast, beta_slow};
+  return mla_rope_frequencies_f64(scaling, original_tokens, inv_freq);
+}
+
+int mla_rope_frequencies_f64(const double* scaling, int original_tokens, double* inv_freq) {
+  if (!scaling || !inv_freq) return MLA_ERR_INVALID_ARG;
+  const double base = scaling[0], factor = scaling[1], beta_fast = scaling[2], beta_slow = scaling[3];
+  if (!(base > 1.0) || !std::isfinite(base) || !(factor >= 1.0) || !std::isfinite(factor) ||
+      original_tokens <= 0 || !(beta_slow > 0.0) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast))
     return MLA_ERR_INVALID_ARG;
-  const double ln_base = std::log(static_cast<double>(base));
+  const double ln_base = std::log(base);
   // the pair that turns `n` times over the original length
   auto pair = [&](double n) { return kDr * std::log(original_tokens / (n * 6.283185307179586)) / (2 * ln_base); };
   const double low = std::fmax(std::floor(pair(beta_fast)), 0.0);
