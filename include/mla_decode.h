@@ -393,7 +393,8 @@ int mla_rope_frequencies_f64(const double* scaling, int original_tokens, double*
 
 /* Rotate packed vectors: x [rows, heads, 64] bf16 (a query's q_rope, a part of
  * wider heads through its strides, or with one head k_rope) by positions[row]
- * (int32 [rows], device, any value) into out, rounded to nearest.  inverse != 0
+ * (int32 [rows], device, any value) into out, in fp32 (to 2^-21 of the pair) and
+ * then rounded to nearest.  inverse != 0
  * negates the angles: the gradient of the rotation, and for scale 1 its
  * inverse.  strides (host memory, values, positive multiples of 8): token and
  * head stride of x, then of out.  x and out are 16-byte aligned; they may be the
@@ -404,8 +405,9 @@ int mla_rope_bf16(const uint16_t* x, const size_t* strides, const int32_t* posit
 
 /* mla_cache_append_* with k_rope arriving unrotated: row i's 64 values are
  * rotated by positions[i] (int32 [rows], device, any value; NULL: the row's
- * token index) and rounded once, to bf16 or straight to the codes (as the exact
- * rotated values would be, to about 2^-40 of their pair).  A drafted tree's rows
+ * token index) and rounded once, to bf16 or straight to the codes: as the exact
+ * rotated values would be, to 2^-37 of their pair (|a| + |b|) and the angle's error,
+ * |position| 2^-62.  A drafted tree's rows
  * stand at token indexes that are not their positions, and need the array.
  * Everything else is as for mla_cache_append_*. */
 int mla_cache_append_rope_bf16(const uint16_t* c_kv, size_t c_stride, const uint16_t* k_rope, size_t r_stride,

@@ -5,16 +5,17 @@
 // table holds f_i / (2 pi) as a 64-bit fraction of a turn, so p times it,
 // modulo 2^64, is the angle's fraction of a turn with no rounding at all: far
 // positions lose nothing (in fp32 an angle of 10^5 radians is known to 2^-8).
-// The error is the table's own, p 2^-65 turns.
+// The error is the table's own, |p| 2^-65 turns (|p| 2^-62.3 rad).
 //
 // Sine and cosine come from the addition theorems: the fraction is split into
 // the nearest 64th of a turn, whose values a table holds, and a rest d of at
 // most a 128th (0.049 rad), whose sine and cosine are the first terms of their
 // Taylor series.  Everything that matters is kept as an unevaluated sum of two
 // floats (products and sums by the error-free transformations of Dekker and
-// Knuth, with fma), so that a rotated value is known to about 2^-40 of its pair
-// and can be rounded to a cache's codes as the exact value would be; one in fp32
-// lands on the other side of a border for about one value in 2^19.
+// Knuth, with fma), so that a rotated value is known to 2^-37 of its pair (the cube of
+// d, up to 2e-5, is a product of fp32 roundings) besides the angle's error, and can be rounded to a cache's codes as the exact value would be; one in fp32
+// lands on the other side of a border for about one value in 2^19.  The rotation on
+// its own (rope.cu) takes the high parts and multiplies in fp32.
 #pragma once
 #include <cuda_bf16.h>
 
