@@ -488,7 +488,9 @@ int mla_prefill_bf16(const uint16_t* q_nope, const uint16_t* q_rope, const uint1
  * where q, k are the 192 values of both parts, and the RoPE part of dk is summed
  * over the heads.  p and ds are rounded to bf16 for the products, all sums are
  * fp32, results rounded to nearest; the order of every sum is fixed, so equal
- * calls give equal bits.  out and lse are what the forward call gave for the same
+ * calls give equal bits.  Calls whose rows hold infinities or NaN take longer (4096
+ * causal tokens with a column of d_out that is infinite in all of them 11 ms instead
+ * of 1.5).  out and lse are what the forward call gave for the same
  * inputs, cu_q, cu_k, causal and scale.  A pair outside the mask takes no part,
  * whatever its rows hold (including NaN); a query that sees no key, and a key that
  * no query sees, get zeros.  Rows of no sequence are left alone.

@@ -39,9 +39,11 @@
 //   next step runs while dS of this one is computed, and the second products of this
 //   one while the next one's P is.
 // Measured (4096 causal tokens, 1.79 TFLOP of the five products, 952 us at the peak):
-// 1,493 us, 1,200 TFLOP/s; 3 x 777 full 542 (a floor of 205), 8 x up to 1024 557 (162),
-// 2 x 512 queries over 8,012 keys 1,660 (900), 5 x up to 33 64.7.  The key pass takes
-// 1,017 of the first, of 599 that its MMAs need: S, its reading, dP and its reading
+// 1,481 us, 1,207 TFLOP/s; 3 x 777 full 542 (a floor of 205), 8 x up to 1024 550 (162),
+// 2 x 512 queries over 8,012 keys 1,646 (900), 5 x up to 33 64.7.  With the query pass:
+// 8192 causal tokens 5,950 (3,803), 32,768 90 ms (60.8), 1,024 queries over 30,000 keys
+// 5,400 (3,422), 8 x 200 over 9,000 5,410 (1,614).  The key pass takes 995 of the first,
+// of 754 that its MMAs need at the same peak: S, its reading, dP and its reading
 // follow one another in one place of tensor memory, S's MMAs find shared memory busy with
 // the copies (1,150 cycles of 768), and storing dS costs 125.  Tried for it and slower:
 // two sets of eight warps on alternate steps (2,110 instead of 1,770 for the call),

@@ -190,6 +190,11 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+// P and dS as the bf16 operands of the second products: half a step, 2^-8 of each.  The
+// MMAs that take fp32 values (tf32) run at half the rate; two bf16 terms for each of P and
+// dS would be another 320 (dk, dv) and 192 (dq) units beside the 832.  Against 64 bits the
+// results' relative error is 2.3e-3, that of exact results rounded to bf16 1.7e-3
+// (1000 causal, 777 full).
 __device__ __forceinline__ void pack(const uint32_t* s, uint32_t* pk) {
 #pragma unroll
   for (int e = 0; e < kCols / 2; ++e) pk[e] = bf16_pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));

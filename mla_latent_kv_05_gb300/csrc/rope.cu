@@ -4,9 +4,10 @@
 // the transposed map and so the gradient.
 //
 // Bound: 256 bytes a vector read and written against 6 operations a pair, so HBM
-// bounds long calls.  A row's 32 cosines and sines (about 70 operations each) are
-// computed once by a CTA for all the heads it takes, while its loads are in
-// flight.  A thread takes two 16-byte pieces of a vector, 64 bytes apart: with
+// bounds long calls of many heads (8192 rows of 128 heads 42 us, 6,400 GB/s).  A row's
+// 32 cosines and sines (about 70 operations each) are computed once by a CTA for all the
+// heads it takes, while its loads are in flight; with one head a row they bound the call
+// (262,144 keys 67 us, 1,010 GB/s; 16,384 7.1).  A thread takes two 16-byte pieces of a vector, 64 bytes apart: with
 // both layouts the pieces hold whole pairs, so a vector may be rotated in place.
 // A CTA takes 64 vectors a step (64 heads of a row, or fewer heads of more rows)
 // and kSteps steps, whose loads are all issued before the first result is needed.

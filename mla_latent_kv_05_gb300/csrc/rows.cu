@@ -35,7 +35,10 @@
 // The append may rotate the RoPE values on their way (rope.cuh): the CTA's rows
 // have 32 pairs each, which its threads take in turn into shared memory, as floats
 // that round to the cache's format as the exact rotated values would.  They are
-// rounded once, straight to bf16 or to the codes.
+// rounded once, straight to bf16 or to the codes.  The cosines and sines bound long
+// calls, by their instructions: 262,144 rows bf16 129 us (4,670 GB/s), fp8 157 (2,920),
+// fp4 156 (2,480), V4.1 rows 136 and 139 (3,230, 2,720); 16,384 rows 11.6 to 13.5 us;
+// 64 rows 3.5 us.
 #include <climits>
 
 #include <cuda_bf16.h>

@@ -13,7 +13,8 @@ namespace mla {
 // the tensor ended less than a box's rows before the end of the mapped memory.)
 //
 // Byte stride of entry 1 for a tensor of `bytes` at `base`: 0 where the map takes
-// no second entry, because it is wide enough or because there is no room.
+// no second entry, because it is wide enough or because there is no room (its boxes
+// then load at the slow rate).
 uint64_t tma_far(const void* base, uint64_t bytes);
 
 }  // namespace mla
